@@ -10,12 +10,14 @@ Two layers:
     place of pointers), for callers that manage their own buffers;
   * ``quantize_1d`` / ``quantize_2d`` / ``rht_quantize`` / ``dequantize`` /
     ``gemm``, which allocate outputs with ``torch.empty`` and return
-    :class:`NVFP4Tensor` operands.
+    :class:`NVFP4Tensor` operands, and the operators at the ends of a training
+    step beside them: ``embed`` / ``embed_grad`` and ``clip_grads``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Union
 
@@ -28,6 +30,8 @@ NVFP4_OK, NVFP4_ERR_NULL, NVFP4_ERR_SHAPE, NVFP4_ERR_ALIGN, NVFP4_ERR_ARG, NVFP4
     0, -1, -2, -3, -4, -5)
 NVFP4_AMAX_COMPUTE, NVFP4_AMAX_GIVEN = 0, 1
 NVFP4_ROWWISE, NVFP4_COLWISE = 0, 1
+NVFP4_TYPE_BF16, NVFP4_TYPE_F32, NVFP4_TYPE_I32, NVFP4_TYPE_I64 = 0, 1, 2, 3
+NVFP4_SUMSQ_WORDS = 512
 
 EXPORTED = ("nvfp4_amax", "nvfp4_amax_rht", "nvfp4_quantize1d_rtn", "nvfp4_quantize1d_sr",
             "nvfp4_quantize2d_rtn", "nvfp4_quantize2d_sr", "nvfp4_rht_quantize",
@@ -36,7 +40,9 @@ EXPORTED = ("nvfp4_amax", "nvfp4_amax_rht", "nvfp4_quantize1d_rtn", "nvfp4_quant
             "nvfp4_gemm_bf16_noalloc_max_bytes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
             "nvfp4_probe_mfma", "nvfp4_probe_scratch_bytes", "nvfp4_amax_both",
             "nvfp4_quantize_row_rht", "nvfp4_amax_rht1d", "nvfp4_rht_quantize1d",
-            "nvfp4_probe_clock", "nvfp4_probe_clock_bytes", "nvfp4_probe_copy")
+            "nvfp4_probe_clock", "nvfp4_probe_clock_bytes", "nvfp4_probe_copy",
+            "nvfp4_embed", "nvfp4_embed_grad", "nvfp4_embed_grad_workspace_bytes",
+            "nvfp4_grad_sumsq", "nvfp4_grad_clip")
 
 
 class NVFP4Error(RuntimeError):
@@ -61,6 +67,12 @@ class c_mx_operand(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
+class c_grad(ctypes.Structure):
+    """Mirror of ``nvfp4_grad``."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("in_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -73,8 +85,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"{path} is missing: build it with "
                            f"`python -m bit_microscaled_numerics_amd.build`")
     lib = ctypes.CDLL(path)
-    vp, i64, u64, u32, i32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64,
-                              ctypes.c_uint32, ctypes.c_int)
+    vp, i64, u64, u32, i32, f32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64,
+                                   ctypes.c_uint32, ctypes.c_int, ctypes.c_float)
     sigs = {
         "nvfp4_amax": [vp, i64, i64, vp, vp],
         "nvfp4_amax_rht": [vp, i64, i64, u64, vp, vp],
@@ -100,6 +112,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "nvfp4_probe_mfma": [i32, i32, vp, i64, vp],
         "nvfp4_probe_clock": [vp, i64, vp],
         "nvfp4_probe_copy": [vp, vp, i64, vp],
+        "nvfp4_embed": [vp, i32, i64, vp, i32, i64, i64, i64, f32, vp, i32, i64, vp],
+        "nvfp4_embed_grad": [vp, i32, i64, vp, i32, i64, i64, i64, f32, vp, i32, i64, i32, vp, i64,
+                             vp],
+        "nvfp4_grad_sumsq": [vp, i64, vp, vp],
+        "nvfp4_grad_clip": [vp, i64, vp, ctypes.c_double, vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -115,6 +132,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_int64
     lib.nvfp4_gemm_bf16_workspace_bytes.argtypes = [i64, i64, i64]
     lib.nvfp4_gemm_bf16_workspace_bytes.restype = ctypes.c_int64
+    lib.nvfp4_embed_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.nvfp4_embed_grad_workspace_bytes.restype = ctypes.c_int64
     _lib = lib
     return lib
 
@@ -497,6 +516,160 @@ def mx_gemm(a: MXFP4Tensor, b: MXFP4Tensor, out: Optional[torch.Tensor] = None) 
         out = _empty(a.rows, b.rows, dtype=torch.float32, device=a.codes.device)
     mxfp4_gemm(a, b, out, out.stride(0))
     return out
+
+
+# ------------------------------------------------- the ends of a training step
+_FLOATS = {torch.bfloat16: NVFP4_TYPE_BF16, torch.float32: NVFP4_TYPE_F32}
+_INDEXES = {torch.int32: NVFP4_TYPE_I32, torch.int64: NVFP4_TYPE_I64}
+
+
+def _dev_matrix(x: torch.Tensor, name: str) -> int:
+    """The type of a 2-D bf16 or float32 GPU tensor with contiguous rows."""
+    if not x.is_cuda or x.dtype not in _FLOATS or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D bf16 or float32 CUDA tensor")
+    if x.stride(1) != 1 and x.shape[1] > 1 and x.shape[0] > 0:
+        raise ValueError(f"{name} must have contiguous rows")
+    return _FLOATS[x.dtype]
+
+
+def _pitch(x: torch.Tensor, name: str) -> int:
+    """Row pitch of a matrix.  torch leaves the row stride of a single row (or
+    none) free; the library wants at least the row's length."""
+    if x.shape[0] <= 1:
+        return x.shape[1]
+    if x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name} must not have overlapping (expanded) rows")
+    return x.stride(0)
+
+
+def _dev_ids(ids: torch.Tensor, name: str) -> int:
+    if not ids.is_cuda or ids.dtype not in _INDEXES or not ids.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 or int64 CUDA tensor")
+    return _INDEXES[ids.dtype]
+
+
+def nvfp4_embed(ids, w, scale, out, stream=None):
+    it, wt, ot = _dev_ids(ids, "ids"), _dev_matrix(w, "w"), _dev_matrix(out, "out")
+    if out.shape[0] != ids.numel() or out.shape[1] != w.shape[1]:
+        raise ValueError("out must be [number of ids][columns of w]")
+    _check(load_library().nvfp4_embed(_p(ids), it, ids.numel(), _p(w), wt, w.shape[0], w.shape[1],
+                                      _pitch(w, "w"), scale, _p(out), ot, _pitch(out, "out"),
+                                      _stream(stream)))
+
+
+def nvfp4_embed_grad_workspace_bytes(n: int, vocab: int, dim: int) -> int:
+    b = int(load_library().nvfp4_embed_grad_workspace_bytes(n, vocab, dim))
+    if b < 0:
+        _check(b)
+    return b
+
+
+def nvfp4_embed_grad(ids, dy, scale, dw, accumulate, workspace, stream=None):
+    it, yt, wt = _dev_ids(ids, "ids"), _dev_matrix(dy, "dy"), _dev_matrix(dw, "dw")
+    if dy.shape[0] != ids.numel() or dy.shape[1] != dw.shape[1]:
+        raise ValueError("dy must be [number of ids][columns of dw]")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().nvfp4_embed_grad(_p(ids), it, ids.numel(), _p(dy), yt, _pitch(dy, "dy"),
+                                           dw.shape[0], dw.shape[1], scale, _p(dw), wt, _pitch(dw, "dw"),
+                                           int(accumulate), _p(workspace), nbytes,
+                                           _stream(stream)))
+
+
+def embed(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
+          dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """scale * w[ids] as [number of ids][columns] of dtype (w's if None).  An
+    id outside 0 .. rows-1 gives a row of zeros."""
+    _dev_matrix(w, "w")
+    out = _empty(ids.numel(), w.shape[1], dtype=w.dtype if dtype is None else dtype,
+                 device=w.device)
+    nvfp4_embed(ids, w, scale, out)
+    return out
+
+
+def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1.0,
+               dtype: Optional[torch.dtype] = None,
+               accumulate_into: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of ``embed`` with respect to w, [vocab][columns of dy] of
+    dtype (dy's if None): row v is scale times the sum of dy's rows whose id
+    is v, in ascending order.  accumulate_into: a gradient that is added to in
+    place and returned."""
+    _dev_matrix(dy, "dy")
+    dw = accumulate_into
+    if dw is None:
+        dw = _empty(vocab, dy.shape[1], dtype=dy.dtype if dtype is None else dtype,
+                    device=dy.device)
+    elif dw.shape[0] != vocab or (dtype is not None and dw.dtype != dtype):
+        raise ValueError("accumulate_into must be [vocab][columns of dy] of the given dtype")
+    n = nvfp4_embed_grad_workspace_bytes(ids.numel(), vocab, dy.shape[1])
+    ws = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+    nvfp4_embed_grad(ids, dy, scale, dw, accumulate_into is not None, ws)
+    return dw
+
+
+def _grad_list(grads, outs):
+    """The nvfp4_grad array of a list of gradients (and outputs)."""
+    words = []
+    for g, o in zip(grads, outs):
+        gt, ot = _FLOATS.get(g.dtype), _FLOATS.get(o.dtype)
+        if gt is None or ot is None or not g.is_cuda or not o.is_cuda:
+            raise ValueError("gradients must be bf16 or float32 CUDA tensors")
+        if not g.is_contiguous() or not o.is_contiguous() or o.shape != g.shape:
+            raise ValueError("gradients and outputs must be contiguous and of equal shapes")
+        words += (g.data_ptr(), o.data_ptr(), g.numel(), gt | ot << 32)
+    return struct.pack(f"{len(words)}q", *words), len(words) // 4
+
+
+def nvfp4_grad_sumsq(grads, partials, stream=None):
+    lst, n = _grad_list(grads, grads)
+    _dev_partials(partials)
+    _check(load_library().nvfp4_grad_sumsq(lst, n, _p(partials), _stream(stream)))
+
+
+def nvfp4_grad_clip(grads, outs, partials, max_norm, norm_out, stream=None):
+    lst, n = _grad_list(grads, outs)
+    _dev_partials(partials)
+    _check(load_library().nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm_out),
+                                          _stream(stream)))
+
+
+def _dev_partials(partials):
+    if (not partials.is_cuda or partials.dtype != torch.float64 or not partials.is_contiguous()
+            or partials.numel() != NVFP4_SUMSQ_WORDS):
+        raise ValueError(f"partials must be {NVFP4_SUMSQ_WORDS} contiguous float64 CUDA values")
+
+
+def grad_sumsq(grads) -> torch.Tensor:
+    """Partial sums of the squares of all gradients (float64, on the GPU);
+    their total is the squared global norm.  Over several processes, add them
+    up (``all_reduce``) before ``clip_grads``."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    partials = _empty(NVFP4_SUMSQ_WORDS, dtype=torch.float64, device=grads[0].device)
+    nvfp4_grad_sumsq(grads, partials)
+    return partials
+
+
+def clip_grads(grads, max_norm: float, out=None, partials: Optional[torch.Tensor] = None
+               ) -> torch.Tensor:
+    """Scale the gradients by min(1, max_norm / (norm + 1e-6)), norm their
+    global 2-norm, in place or into the tensors of ``out`` (bf16 or float32,
+    whatever the gradients' type).  Returns norm (float32 [1], on the GPU,
+    without waiting for it).  partials: ``grad_sumsq``'s, if already taken."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads or len(outs) != len(grads):
+        raise ValueError("one output for each gradient, and at least one gradient")
+    lst, n = _grad_list(grads, outs)
+    dev = grads[0].device
+    norm = _empty(1, dtype=torch.float32, device=dev)
+    lib, s = load_library(), _stream(None)
+    if partials is None:
+        partials = torch.empty(NVFP4_SUMSQ_WORDS, dtype=torch.float64, device=dev)
+        _check(lib.nvfp4_grad_sumsq(lst, n, _p(partials), s))
+    _dev_partials(partials)
+    _check(lib.nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm), s))
+    return norm
 
 
 PROBE_ZEROS, PROBE_NVFP4_LIKE, PROBE_UNIFORM = 0, 1, 2

@@ -1,0 +1,33 @@
+// lm_kernels.h -- launch functions of the embedding, gradient-clipping and
+// cross-entropy kernels (internal to libnvfp4.so; the public interface is
+// include/nvfp4.h).  Types are the public NVFP4_TYPE_* values.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+#include "../../include/nvfp4.h"
+
+namespace nvfp4 {
+
+struct EmbedArgs {
+  const void* ids;
+  int ids_type;
+  int64_t n, vocab, dim;
+  float scale;
+};
+
+hipError_t launch_embed(const EmbedArgs& a, const void* w, int w_type, int64_t ldw, void* out,
+                        int out_type, int64_t ldo, hipStream_t s);
+
+int64_t embed_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+hipError_t launch_embed_grad(const EmbedArgs& a, const void* dy, int dy_type, int64_t ld_dy,
+                             void* dw, int dw_type, int64_t ld_dw, bool accumulate, void* ws,
+                             hipStream_t s);
+
+hipError_t launch_grad_sumsq(const nvfp4_grad* list, int64_t count, double* partials,
+                             hipStream_t s);
+hipError_t launch_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials,
+                            double max_norm, float* norm_out, hipStream_t s);
+
+}  // namespace nvfp4

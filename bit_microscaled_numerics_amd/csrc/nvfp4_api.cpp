@@ -6,32 +6,13 @@
 #include <hip/hip_runtime_api.h>
 
 #include <atomic>
-#include <cstdarg>
-#include <cstdio>
-#include <cstdlib>
-#include <cstring>
 
+#include "api_common.h"
 #include "nvfp4_kernels.h"
 
+using namespace nvfp4::api;
+
 namespace {
-
-thread_local char g_last_error[256] = "";
-
-// No tensor or buffer the library touches may exceed 2^40 elements or bytes
-// (far beyond the 288 GB of one MI355X): with that bound every size, offset
-// and grid computation here and in the launchers stays within int64 (and the
-// grids within their 32-bit dimensions).
-constexpr int64_t kMaxElems = int64_t(1) << 40;
-
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
-  va_end(ap);
-  return status;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_tensor(const void* x, int64_t rows, int64_t cols, const char* name) {
   if (x == nullptr) return fail(NVFP4_ERR_NULL, "%s is NULL", name);
@@ -57,14 +38,6 @@ int check_outputs(const void* codes, const void* scales, const float* amax_io,
     return fail(NVFP4_ERR_ALIGN, "amax_io / tensor_scale_out must be 4-byte aligned");
   return NVFP4_OK;
 }
-
-int launched(hipError_t e) {
-  if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
-  g_last_error[0] = '\0';
-  return NVFP4_OK;
-}
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 int check_operand(const nvfp4_operand* q, const char* name) {
   if (q == nullptr) return fail(NVFP4_ERR_NULL, "%s is NULL", name);

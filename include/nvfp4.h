@@ -31,9 +31,10 @@
  * are unspecified, and never out of bounds).
  *
  * Conventions (all entry points):
- *  - Every pointer is DEVICE memory owned by the caller; the library never
- *    allocates, frees or synchronises.  `stream` is a hipStream_t (NULL = the
- *    default stream); all work is enqueued on it, in order.
+ *  - Every pointer is DEVICE memory owned by the caller (descriptors and
+ *    lists of them are host memory); the library never allocates, frees or
+ *    synchronises.  `stream` is a hipStream_t (NULL = the default stream); all
+ *    work is enqueued on it, in order.
  *  - bf16 inputs are row-major [rows][cols] with 16-byte aligned base
  *    pointers; rows and cols are positive multiples of 16, and cols is at
  *    most 2^28 (16 rows of packed codes then span less than 2^32 bytes).
@@ -304,6 +305,63 @@ int mxfp4_dequantize(const mxfp4_operand* q, float* out, void* stream);
  * only rounding is the FP32 accumulation. */
 int mxfp4_gemm(const mxfp4_operand* a, const mxfp4_operand* b, float* c, int64_t ldc,
                void* stream);
+
+/* ------------------------------------------------------------------------
+ * The ends of a language model's training step, beside its NVFP4 linear
+ * layers: token embedding, output head with softmax cross entropy, and the
+ * gradient norm.  The recipe leaves these in higher precision ("Pretraining
+ * Large Language Models with NVFP4", summary page, recipe paragraph); values
+ * are BF16 or FP32, sums FP32 or wider.  Matrices are row-major with a row
+ * pitch (ld, in elements) of at least their columns.  Sizes may be odd and
+ * rows need only their elements' alignment, unless said otherwise.  No
+ * workspace content matters on entry; calls that use one workspace at the
+ * same time race.
+ * ------------------------------------------------------------------------ */
+enum { NVFP4_TYPE_BF16 = 0, NVFP4_TYPE_F32 = 1, NVFP4_TYPE_I32 = 2, NVFP4_TYPE_I64 = 3 };
+
+/* out[t] = scale * w[ids[t]] for t < n: w [vocab][dim], out [n][dim], each BF16
+ * or F32; ids I32 or I64.  An id outside 0 .. vocab-1 (a padding mark such as
+ * -1) gives a row of zeros.  n may be 0. */
+int nvfp4_embed(const void* ids, int ids_type, int64_t n, const void* w, int w_type, int64_t vocab,
+                int64_t dim, int64_t ldw, float scale, void* out, int out_type, int64_t ldo,
+                void* stream);
+
+/* The gradient of nvfp4_embed: dw[v] = scale * sum of dy[t] over the tokens t
+ * with ids[t] == v, an FP32 sum in ascending t (the same bits every time),
+ * rounded once.  Rows of absent words are zeros.  accumulate = 1: added to
+ * dw's own rows instead (rows of absent words are not touched).  Ids outside
+ * 0 .. vocab-1 take no gradient.  workspace: 256-byte aligned, of at least
+ * nvfp4_embed_grad_workspace_bytes(n, vocab, dim). */
+int64_t nvfp4_embed_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+int nvfp4_embed_grad(const void* ids, int ids_type, int64_t n, const void* dy, int dy_type,
+                     int64_t ld_dy, int64_t vocab, int64_t dim, float scale, void* dw, int dw_type,
+                     int64_t ld_dw, int accumulate, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/* One gradient tensor of a list (contiguous).  The list itself is HOST
+ * memory, read before the call returns; in and out are device memory.  out
+ * may equal in (in place, same type); other overlaps race. */
+typedef struct {
+  const void* in;
+  void* out;           /* nvfp4_grad_clip only */
+  int64_t numel;       /* may be 0 */
+  int32_t in_type, out_type;   /* NVFP4_TYPE_BF16 or NVFP4_TYPE_F32 */
+} nvfp4_grad;
+
+/* The squares of all elements of a list of gradients, summed in FP64 into
+ * NVFP4_SUMSQ_WORDS partial sums (device memory) whose total is the square of
+ * the global norm.  Partial sums of several processes may be added word by
+ * word before nvfp4_grad_clip. */
+enum { NVFP4_SUMSQ_WORDS = 512 };
+int nvfp4_grad_sumsq(const nvfp4_grad* list, int64_t count, double* partials, void* stream);
+
+/* out = in * min(1, max_norm / (norm + 1e-6)) for every tensor of the list, with
+ * norm = sqrt(sum of partials); *norm_out = norm (nullable).  A NaN norm makes
+ * every output NaN; an infinite one makes finite elements 0.  max_norm is 0 or
+ * more (infinity: only convert or copy).  In place with a factor of 1 nothing
+ * is written. */
+int nvfp4_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials, double max_norm,
+                    float* norm_out, void* stream);
 
 /* ------------------------------------------------------------------------
  * Measurement support (not part of the quantize / GEMM path): the sustained

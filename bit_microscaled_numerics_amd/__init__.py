@@ -11,7 +11,8 @@ Two layers:
   * ``quantize_1d`` / ``quantize_2d`` / ``rht_quantize`` / ``dequantize`` /
     ``gemm``, which allocate outputs with ``torch.empty`` and return
     :class:`NVFP4Tensor` operands, and the operators at the ends of a training
-    step beside them: ``embed`` / ``embed_grad`` and ``clip_grads``.
+    step beside them: ``embed`` / ``embed_grad``, ``linear_ce`` /
+    ``linear_ce_grad`` and ``clip_grads``.
 """
 from __future__ import annotations
 
@@ -42,7 +43,8 @@ EXPORTED = ("nvfp4_amax", "nvfp4_amax_rht", "nvfp4_quantize1d_rtn", "nvfp4_quant
             "nvfp4_quantize_row_rht", "nvfp4_amax_rht1d", "nvfp4_rht_quantize1d",
             "nvfp4_probe_clock", "nvfp4_probe_clock_bytes", "nvfp4_probe_copy",
             "nvfp4_embed", "nvfp4_embed_grad", "nvfp4_embed_grad_workspace_bytes",
-            "nvfp4_grad_sumsq", "nvfp4_grad_clip")
+            "nvfp4_grad_sumsq", "nvfp4_grad_clip", "nvfp4_linear_ce", "nvfp4_linear_ce_grad",
+            "nvfp4_linear_ce_workspace_bytes")
 
 
 class NVFP4Error(RuntimeError):
@@ -115,6 +117,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "nvfp4_embed": [vp, i32, i64, vp, i32, i64, i64, i64, f32, vp, i32, i64, vp],
         "nvfp4_embed_grad": [vp, i32, i64, vp, i32, i64, i64, i64, f32, vp, i32, i64, i32, vp, i64,
                              vp],
+        "nvfp4_linear_ce": [vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp],
+        "nvfp4_linear_ce_grad": [vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, vp, vp, vp, i64,
+                                 vp, i64, vp, i64, vp],
         "nvfp4_grad_sumsq": [vp, i64, vp, vp],
         "nvfp4_grad_clip": [vp, i64, vp, ctypes.c_double, vp, vp],
     }
@@ -134,6 +139,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.nvfp4_gemm_bf16_workspace_bytes.restype = ctypes.c_int64
     lib.nvfp4_embed_grad_workspace_bytes.argtypes = [i64, i64, i64]
     lib.nvfp4_embed_grad_workspace_bytes.restype = ctypes.c_int64
+    lib.nvfp4_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, i32, i64]
+    lib.nvfp4_linear_ce_workspace_bytes.restype = ctypes.c_int64
     _lib = lib
     return lib
 
@@ -542,6 +549,10 @@ def _pitch(x: torch.Tensor, name: str) -> int:
     return x.stride(0)
 
 
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _dev_ids(ids: torch.Tensor, name: str) -> int:
     if not ids.is_cuda or ids.dtype not in _INDEXES or not ids.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 or int64 CUDA tensor")
@@ -568,10 +579,9 @@ def nvfp4_embed_grad(ids, dy, scale, dw, accumulate, workspace, stream=None):
     it, yt, wt = _dev_ids(ids, "ids"), _dev_matrix(dy, "dy"), _dev_matrix(dw, "dw")
     if dy.shape[0] != ids.numel() or dy.shape[1] != dw.shape[1]:
         raise ValueError("dy must be [number of ids][columns of dw]")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().nvfp4_embed_grad(_p(ids), it, ids.numel(), _p(dy), yt, _pitch(dy, "dy"),
                                            dw.shape[0], dw.shape[1], scale, _p(dw), wt, _pitch(dw, "dw"),
-                                           int(accumulate), _p(workspace), nbytes,
+                                           int(accumulate), _p(workspace), _nbytes(workspace),
                                            _stream(stream)))
 
 
@@ -604,6 +614,86 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1
     ws = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
     nvfp4_embed_grad(ids, dy, scale, dw, accumulate_into is not None, ws)
     return dw
+
+
+def nvfp4_linear_ce_workspace_bytes(T: int, V: int, D: int, grad: bool,
+                                    piece_tokens: int = 0) -> int:
+    n = int(load_library().nvfp4_linear_ce_workspace_bytes(T, V, D, int(grad), piece_tokens))
+    if n < 0:
+        _check(n)
+    return n
+
+
+def _ce_inputs(h, w, targets):
+    """Checked (h pitch, w pitch, T, V, D, targets type)."""
+    for x, name in ((h, "h"), (w, "w")):
+        if _dev_matrix(x, name) != NVFP4_TYPE_BF16:
+            raise ValueError(f"{name} must be bf16")
+    if h.shape[1] != w.shape[1]:
+        raise ValueError("h and w must have the same number of columns")
+    tt = _dev_ids(targets, "targets")
+    if targets.numel() != h.shape[0]:
+        raise ValueError("one target for each row of h")
+    return _pitch(h, "h"), _pitch(w, "w"), h.shape[0], w.shape[0], h.shape[1], tt
+
+
+def _dev_f32(x, n, name):
+    if x is not None and (not x.is_cuda or x.dtype != torch.float32 or not x.is_contiguous()
+                          or x.numel() != n):
+        raise ValueError(f"{name} must be {n} contiguous float32 CUDA values")
+
+
+def nvfp4_linear_ce(h, w, targets, loss, lse, workspace, stream=None):
+    ldh, ldw, T, V, D, tt = _ce_inputs(h, w, targets)
+    _dev_f32(loss, T, "loss")
+    _dev_f32(lse, T, "lse")
+    _check(load_library().nvfp4_linear_ce(_p(h), ldh, _p(w), ldw, T, V, D, _p(targets), tt,
+                                          _p(loss), _p(lse), _p(workspace), _nbytes(workspace),
+                                          _stream(stream)))
+
+
+def nvfp4_linear_ce_grad(h, w, targets, row_weight, piece_tokens, loss, lse, dh, dw, workspace,
+                         stream=None):
+    ldh, ldw, T, V, D, tt = _ce_inputs(h, w, targets)
+    for x, n, name in ((row_weight, T, "row_weight"), (loss, T, "loss"), (lse, T, "lse")):
+        _dev_f32(x, n, name)
+    for x, like, name in ((dh, h, "dh"), (dw, w, "dw")):
+        if _dev_matrix(x, name) != NVFP4_TYPE_BF16 or x.shape != like.shape:
+            raise ValueError(f"{name} must be bf16 of its input's shape")
+    _check(load_library().nvfp4_linear_ce_grad(
+        _p(h), ldh, _p(w), ldw, T, V, D, _p(targets), tt, _p(row_weight), piece_tokens, _p(loss),
+        _p(lse), _p(dh), _pitch(dh, "dh"), _p(dw), _pitch(dw, "dw"), _p(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
+    """(loss, lse) of the output head z = h w^T, float32 [rows of h]: lse the
+    log of the sum of exponentials of a row's logits, loss lse minus the
+    target's logit (0 where the target is outside 0 .. rows of w - 1)."""
+    T, V, D = _ce_inputs(h, w, targets)[2:5]
+    loss = _empty(T, dtype=torch.float32, device=h.device)
+    lse = _empty(T, dtype=torch.float32, device=h.device)
+    ws = torch.empty(nvfp4_linear_ce_workspace_bytes(T, V, D, False), dtype=torch.uint8,
+                     device=h.device)
+    nvfp4_linear_ce(h, w, targets, loss, lse, ws)
+    return loss, lse
+
+
+def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                   row_weight: Optional[torch.Tensor] = None, piece_tokens: int = 0):
+    """(loss, lse, dh, dw): ``linear_ce`` and the gradient of the sum of
+    row_weight * loss (of the mean over the rows that have a target if None).
+    piece_tokens bounds the workspace: about 2 bytes for each of its tokens
+    and each word (0: 4 GiB at most)."""
+    T, V, D = _ce_inputs(h, w, targets)[2:5]
+    loss = _empty(T, dtype=torch.float32, device=h.device)
+    lse = _empty(T, dtype=torch.float32, device=h.device)
+    dh = _empty(T, D, dtype=torch.bfloat16, device=h.device)
+    dw = _empty(V, D, dtype=torch.bfloat16, device=h.device)
+    ws = torch.empty(nvfp4_linear_ce_workspace_bytes(T, V, D, True, piece_tokens),
+                     dtype=torch.uint8, device=h.device)
+    nvfp4_linear_ce_grad(h, w, targets, row_weight, piece_tokens, loss, lse, dh, dw, ws)
+    return loss, lse, dh, dw
 
 
 def _grad_list(grads, outs):

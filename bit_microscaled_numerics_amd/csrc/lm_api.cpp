@@ -67,6 +67,52 @@ int check_workspace(const void* ws, int64_t bytes, int64_t need, const char* que
   return NVFP4_OK;
 }
 
+// The cross-entropy sizes: offsets inside a tile are 32-bit bytes (256 rows of a
+// pitch below 2^22 elements), token and word numbers 32-bit.
+constexpr int64_t kMaxPitch = (int64_t(1) << 22) - 8;
+
+int check_ce_sizes(int64_t T, int64_t V, int64_t D, int grad, int64_t piece) {
+  if (T < 0 || T > kMaxCount - 512)
+    return fail(NVFP4_ERR_SHAPE, "T=%lld must be 0 .. 2^31 - 513", (long long)T);
+  // the code rows of a piece are an operand too: V bounded like a pitch there
+  const int64_t most = grad ? kMaxPitch - 128 : kMaxCount - 512;
+  if (V < 1 || V > most)
+    return fail(NVFP4_ERR_SHAPE, "V=%lld must be 1 .. %lld", (long long)V, (long long)most);
+  if (D < 8 || D % 8 || D > kMaxPitch)
+    return fail(NVFP4_ERR_SHAPE, "D=%lld must be a positive multiple of 8 below 2^22", (long long)D);
+  if (grad != 0 && grad != 1) return fail(NVFP4_ERR_ARG, "grad=%d must be 0 or 1", grad);
+  if (piece < 0)
+    return fail(NVFP4_ERR_SHAPE, "piece_tokens=%lld must be 0 or more", (long long)piece);
+  if (T > 0 && (V > kMaxElems / T || D > kMaxElems / T))
+    return fail(NVFP4_ERR_SHAPE, "T*V or T*D exceeds 2^40");
+  return NVFP4_OK;
+}
+
+// A BF16 operand or result of the products: 16-byte rows.
+int check_rows16(const void* p, int64_t rows, int64_t cols, int64_t ld, const char* name) {
+  int st = check_matrix(p, NVFP4_TYPE_BF16, rows, cols, ld, name);
+  if (st) return st;
+  if (ld > kMaxPitch)
+    return fail(NVFP4_ERR_SHAPE, "%s: row pitch %lld must be below 2^22", name, (long long)ld);
+  if (ld % 8 || (rows > 0 && !aligned(p, 16)))
+    return fail(NVFP4_ERR_ALIGN, "%s: row pitch %lld must be a multiple of 8, the base 16-byte "
+                "aligned", name, (long long)ld);
+  return NVFP4_OK;
+}
+
+int check_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T, int64_t V,
+             int64_t D, const void* targets, int targets_type, const float* loss,
+             const float* lse) {
+  int st = check_rows16(h, T, D, ldh, "h");
+  if (st) return st;
+  if ((st = check_rows16(w, V, D, ldw, "w"))) return st;
+  if ((st = check_ids(targets, targets_type, T, "targets"))) return st;
+  if (T > 0 && loss == nullptr) return fail(NVFP4_ERR_NULL, "loss is NULL");
+  if (!aligned(loss, 4) || !aligned(lse, 4))
+    return fail(NVFP4_ERR_ALIGN, "loss and lse must be 4-byte aligned");
+  return NVFP4_OK;
+}
+
 int check_grads(const nvfp4_grad* list, int64_t count, bool outputs) {
   if (count < 0 || count > kMaxCount)
     return fail(NVFP4_ERR_SHAPE, "count=%lld must be 0 .. 2^31 - 1", (long long)count);
@@ -135,6 +181,76 @@ int nvfp4_embed_grad(const void* ids, int ids_type, int64_t n, const void* dy, i
   return launched(nvfp4::launch_embed_grad(nvfp4::EmbedArgs{ids, ids_type, n, vocab, dim, scale},
                                            dy, dy_type, ld_dy, dw, dw_type, ld_dw,
                                            accumulate == 1, workspace, as_stream(stream)));
+}
+
+int64_t nvfp4_linear_ce_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad,
+                                        int64_t piece_tokens) {
+  const int st = check_ce_sizes(T, V, D, grad, piece_tokens);
+  return st ? st : nvfp4::ce_workspace_bytes(T, V, D, grad == 1, piece_tokens);
+}
+
+int nvfp4_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T, int64_t V,
+                    int64_t D, const void* targets, int targets_type, float* loss, float* lse,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = check_ce_sizes(T, V, D, 0, 0);
+  if (st) return st;
+  if ((st = check_ce(h, ldh, w, ldw, T, V, D, targets, targets_type, loss, lse))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            nvfp4::ce_workspace_bytes(T, V, D, false, 0),
+                            "nvfp4_linear_ce_workspace_bytes")))
+    return st;
+  nvfp4::CeCall c{};
+  c.h = h;
+  c.w = w;
+  c.ldh = ldh;
+  c.ldw = ldw;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.targets = targets;
+  c.targets_type = targets_type;
+  c.loss = loss;
+  c.lse = lse;
+  c.ws = workspace;
+  return launched(nvfp4::launch_ce(c, as_stream(stream)));
+}
+
+int nvfp4_linear_ce_grad(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T,
+                         int64_t V, int64_t D, const void* targets, int targets_type,
+                         const float* row_weight, int64_t piece_tokens, float* loss, float* lse,
+                         void* dh, int64_t ld_dh, void* dw, int64_t ld_dw, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  int st = check_ce_sizes(T, V, D, 1, piece_tokens);
+  if (st) return st;
+  if ((st = check_ce(h, ldh, w, ldw, T, V, D, targets, targets_type, loss, lse))) return st;
+  if (!aligned(row_weight, 4)) return fail(NVFP4_ERR_ALIGN, "row_weight must be 4-byte aligned");
+  if ((st = check_rows16(dh, T, D, ld_dh, "dh"))) return st;
+  if ((st = check_rows16(dw, V, D, ld_dw, "dw"))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            nvfp4::ce_workspace_bytes(T, V, D, true, piece_tokens),
+                            "nvfp4_linear_ce_workspace_bytes")))
+    return st;
+  nvfp4::CeCall c{};
+  c.h = h;
+  c.w = w;
+  c.ldh = ldh;
+  c.ldw = ldw;
+  c.T = T;
+  c.V = V;
+  c.D = D;
+  c.targets = targets;
+  c.targets_type = targets_type;
+  c.row_weight = row_weight;
+  c.piece = piece_tokens;
+  c.loss = loss;
+  c.lse = lse;
+  c.dh = dh;
+  c.dw = dw;
+  c.ld_dh = ld_dh;
+  c.ld_dw = ld_dw;
+  c.grad = true;
+  c.ws = workspace;
+  return launched(nvfp4::launch_ce(c, as_stream(stream)));
 }
 
 int nvfp4_grad_sumsq(const nvfp4_grad* list, int64_t count, double* partials, void* stream) {

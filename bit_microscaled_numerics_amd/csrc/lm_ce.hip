@@ -1,0 +1,682 @@
+// lm_ce.hip -- softmax cross entropy of an output head z = h w^T over a large
+// vocabulary, with its gradient, without the logits:
+//
+//   lse_t  = log sum_v exp(z_tv),   loss_t = lse_t - z_t,target
+//   d_tv   = g_t (exp(z_tv - lse_t) - [v = target_t])
+//   dH     = d W,   dW = d^T H
+//
+// Three matrix products of 2 T V D operations each (one for the loss alone);
+// everything else is fused around them.
+//
+//  k_ce_logits   z tile by tile on the matrix cores (lm_gemm.h).  Per token and
+//                span of 128 words the epilogue leaves the maximum and the sum
+//                of exponentials, and for the gradient a 16-bit code per entry:
+//                how far log2 of its exponential lies below the span's maximum,
+//                in steps of 64/65535 (an absolute step in the logarithm, so a
+//                relative error of at most 3.4e-4 in the exponential, a twelfth
+//                of the BF16 rounding d gets anyway; entries more than 2^-64
+//                below their span's maximum become 0).  FP32 logits would be
+//                twice the bytes, BF16 ones off by 2% at a logit of 10; a
+//                second product to recompute them is a fourth product.
+//  k_ce_rows     the spans' statistics joined into lse_t and loss_t.
+//  k_ce_dlogits  codes -> d in BF16, in place.
+//  k_ce_dh       dH = d W: few tiles, a long sum over the vocabulary, cut in
+//                equal parts when the tiles do not fill the compute units.
+//  k_ce_dw       dW = d^T H.
+//
+// Tokens without a target are taken out first (k_ce_prep, k_ce_gather): they
+// cost nothing in any product, and nothing they hold can reach a gradient.  The
+// number of remaining tokens stays on the device; the products run a fixed grid
+// of one workgroup per compute unit that walks as many tiles as there are.
+// Tokens may be taken in pieces to bound the code buffer; dW is then held in
+// FP32 between pieces.
+#include "gemm_tiles.h"
+#include "lm_gemm.h"
+#include "lm_kernels.h"
+
+namespace nvfp4 {
+
+namespace {
+
+using namespace lm;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kSpan = 128;                 // words per softmax partial (a wave's m range)
+constexpr float kCodeSpan = 64.0f;         // log2 range of a code
+constexpr float kCodeStep = kCodeSpan / 65535.0f;
+constexpr int kMaxItems = 2048;            // parts x tiles of a cut dH product
+
+struct Meta {
+  int n;        // tokens with a target
+  int split;    // parts of the dH product's sum
+};
+
+struct CeArgs {
+  const uint16_t* h;       // [.][ldh]: the tokens themselves, or the gathered ones
+  const uint16_t* w;
+  int64_t ldh, ldw, T, V, D;
+  const Meta* meta;        // null: all T tokens
+  int64_t first, piece;    // this piece's first row and most rows
+  const int32_t* idx;      // row -> token (null: the same)
+  const void* targets;
+  int targets_type;
+  const int32_t* tgt;      // gathered targets
+  const float* weight;     // gathered row weights g
+  float* tlogit;           // [rows] the target's logit
+  float2* stats;           // [piece][spans] (log2 maximum, sum)
+  float* lse2;             // [rows] lse / ln 2
+  float* rloss;            // [rows]
+  uint16_t* codes;         // [piece][ldc] codes, then d
+  int64_t ldc, spans;
+  float* loss;             // by token
+  float* lse;              // by token (nullable)
+  uint16_t* dh;
+  int64_t ld_dh;
+  uint16_t* dw;
+  int64_t ld_dw;
+  float* part;             // FP32 parts of dH, in accumulator order
+  float* dw_acc;           // FP32 dW between pieces, in accumulator order
+  int tiles_dh_m;          // ceil(D / 256)
+  bool keep, add, finish;  // codes wanted; dW adds to dw_acc; dW is written out
+};
+
+__device__ __forceinline__ int64_t piece_rows(const CeArgs& g) {
+  const int64_t n = g.meta == nullptr ? g.T : (int64_t)g.meta->n;
+  const int64_t r = n - g.first;
+  return r < 0 ? 0 : r < g.piece ? r : g.piece;
+}
+
+__device__ __forceinline__ int64_t target_of(const void* t, int type, int64_t i) {
+  return type == NVFP4_TYPE_I64 ? reinterpret_cast<const int64_t*>(t)[i]
+                                : (int64_t) reinterpret_cast<const int32_t*>(t)[i];
+}
+
+// The target of a row (< 0: none).
+__device__ __forceinline__ int row_target(const CeArgs& g, int64_t row) {
+  if (g.tgt != nullptr) return g.tgt[row];
+  const int64_t t = target_of(g.targets, g.targets_type, row);
+  return t >= 0 && t < g.V ? (int)t : -1;
+}
+
+// Round `round` of workgroup blockIdx.x over `total` items; each XCD (workgroups
+// are dealt to the 8 in turn) owns a contiguous range.  False: no more.
+__device__ __forceinline__ bool next_item(int64_t total, int64_t round, int64_t& item) {
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t at = round * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  item = (int64_t)(blockIdx.x % kXcds) * per + at;
+  return at < per && item < total;
+}
+
+template <int WN>
+__device__ __forceinline__ void clear(v16f (&acc)[kWM][WN]) {
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) acc[i][j] = v16f{};
+}
+
+// A wave's 32 n x 128 m half-words staged in its own 8 KiB of LDS, row n in 256
+// bytes, chunk c at c ^ (n & 15): 8-byte writes of 4 consecutive m, 16-byte
+// reads of whole rows.
+__device__ __forceinline__ void stage_put(uint8_t* region, int i, int q, v2u v) {
+  const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
+  *reinterpret_cast<v2u*>(region + n * 256 + (((4 * i + q) ^ (n & 15)) << 4) + half * 8) = v;
+}
+__device__ __forceinline__ v4u stage_get(const uint8_t* region, int r, int c) {
+  return *reinterpret_cast<const v4u*>(region + r * 256 + ((c ^ (r & 15)) << 4));
+}
+__device__ __forceinline__ void wave_lds_done() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  __builtin_amdgcn_wave_barrier();
+}
+
+// ------------------------------------------------------------------- logits
+template <int WN>
+__global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int wm = wave & 1, wn = wave >> 1;
+  const int64_t rows = piece_rows(g);
+  const int64_t tm_all = (g.V + kTM - 1) / kTM, tn_all = (rows + 64 * WN - 1) / (64 * WN);
+  int64_t item;
+  for (int64_t round = 0; next_item(tm_all * tn_all, round, item); ++round) {
+    int64_t tm, tn;
+    grouped(item, tm_all, tn_all, tm, tn);
+    tm = uniform((int)tm);
+    tn = uniform((int)tn);
+    Core<false, false, WN> core;
+    clear<WN>(core.acc);
+    core.a.init(Operand{g.w, g.ldw, g.V}, tm * kTM, g.D, wave, wm * 128);
+    core.b.init(Operand{g.h + g.first * g.ldh, g.ldh, rows}, tn * 64 * WN, g.D, wave, wn * 32 * WN);
+    core.run(a0, b0, a1, b1, wave, 0, g.D);
+
+    const int64_t m0 = tm * kTM + wm * 128;   // the wave's span of words
+    uint8_t* region = a0 + wave * 8192;
+    const bool whole = m0 + kSpan <= g.V;
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      __builtin_amdgcn_sched_barrier(0);   // one block of tokens at a time: registers
+      const int64_t row = tn * 64 * WN + wn * 32 * WN + j * 32 + (lane & 31);
+      if (!whole) {   // words past the vocabulary take no part
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (m0 + acc_m(i, v, half) >= g.V) core.acc[i][j][v] = -__builtin_inff();
+      }
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < kWM; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, core.acc[i][j][v]);
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      // the reference of the span: this binary32 value itself, so its rounding
+      // costs nothing; 0 where every logit is -inf (all exponentials are 0)
+      const float m2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2e;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWM; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          sum += __builtin_amdgcn_exp2f(__builtin_fmaf(core.acc[i][j][v], kLog2e, -m2));
+      sum += __shfl_xor(sum, 32, 64);
+      const bool live = row < rows;
+      if (live && half == 0 && m0 < g.V) g.stats[row * g.spans + m0 / kSpan] = float2{m2, sum};
+      const int target = live ? row_target(g, g.first + row) : -1;
+      const int at = target - (int)m0;   // words below 2^31: no overflow
+      if (__ballot(target >= 0 && at >= 0 && at < kSpan)) {
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (target >= 0 && at == acc_m(i, v, half)) g.tlogit[g.first + row] = core.acc[i][j][v];
+      }
+      if (g.keep) {
+        const float c0 = m2 / kCodeSpan;
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = __builtin_fmaf(core.acc[i][j][4 * q + e], -kLog2e / kCodeSpan, c0);
+            stage_put(region, i, q,
+                      v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[0], x[1])),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[2], x[3]))});
+          }
+        wave_lds_done();
+        if (m0 < g.ldc) {
+          const int64_t r0 = tn * 64 * WN + wn * 32 * WN + j * 32;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const int r = 4 * p + (lane >> 4), c = lane & 15;
+            const v4u val = stage_get(region, r, c);
+            if (r0 + r < rows)
+              *reinterpret_cast<v4u*>(g.codes + (r0 + r) * g.ldc + m0 + 8 * c) = val;
+          }
+        }
+        wave_lds_done();
+      }
+    }
+    // the next tile's loads write the region: every wave is past it
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+}
+
+// ----------------------------------------------------------------- row sums
+// One wave per row: the spans' (maximum, sum) joined; loss in binary64 from
+// there, so that lse - z loses nothing to the size of lse.
+__global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  if (r >= piece_rows(g)) return;
+  const float2* st = g.stats + r * g.spans;
+  float mx = -__builtin_inff();
+  for (int64_t s = lane; s < g.spans; s += 64) mx = fmaxf(mx, st[s].y == 0.0f ? mx : st[s].x);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  float sum = 0.0f;
+  for (int64_t s = lane; s < g.spans; s += 64) {
+    const float2 v = st[s];
+    sum += v.y == 0.0f ? 0.0f : v.y * __builtin_amdgcn_exp2f(v.x - mx);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane != 0) return;
+  const int64_t row = g.first + r;
+  const double lse = (double)mx * (1.0 / (double)kLog2e) + log((double)sum);
+  const int target = row_target(g, row);
+  const float loss = target >= 0 ? (float)(lse - (double)g.tlogit[row]) : 0.0f;
+  const int64_t t = g.idx == nullptr ? row : g.idx[row];
+  g.loss[t] = loss;
+  if (g.lse != nullptr) g.lse[t] = (float)lse;
+  if (g.keep) {
+    g.lse2[row] = (float)(lse * (double)kLog2e);
+    g.rloss[row] = loss;
+  }
+}
+
+// codes -> d = g (p - [target]), BF16, in place.  Each thread 8 entries of a
+// row.  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
+// close to 1.  A weight of 0 gives zeros whatever the row holds.
+__global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
+  const int64_t vecs = g.ldc / 8, rows = piece_rows(g);
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v >= vecs) return;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    uint16_t* p = g.codes + r * g.ldc + v * 8;
+    const float weight = g.weight[g.first + r];
+    const v4u code = *reinterpret_cast<const v4u*>(p);
+    const int64_t span = v * 8 / kSpan;
+    const float base = (span < g.spans ? g.stats[r * g.spans + span].x : 0.0f) - g.lse2[g.first + r];
+    v8f d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t c = i & 1 ? code[i >> 1] >> 16 : code[i >> 1] & 0xFFFFu;
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf((float)c, -kCodeStep, base));
+      d[i] = c == 0xFFFFu && base == base ? 0.0f : e * weight;
+    }
+    const int64_t at = (int64_t)g.tgt[g.first + r] - v * 8;
+    if (at >= 0 && at < 8) {
+      const float own = expm1f(-g.rloss[g.first + r]) * weight;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = i == at ? own : d[i];
+    }
+    *reinterpret_cast<v4u*>(p) = weight == 0.0f ? v4u{} : pack8(d);
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+// A tile of BF16 results, rows n (tile-relative n0 + ..) to out[row_of(n)], m
+// contiguous, through the wave's LDS region.
+template <int WN, class RowOf>
+__device__ __forceinline__ void store_tile(v16f (&acc)[kWM][WN], uint8_t* region, uint16_t* out,
+                                           int64_t ld, int64_t m0, int64_t m_end, int64_t n0,
+                                           int64_t n_end, RowOf row_of) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < WN; ++j) {
+#pragma unroll
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        const f4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                      acc[i][j][4 * q + 3]};
+        stage_put(region, i, q, __builtin_bit_cast(v2u, __builtin_convertvector(v, b4)));
+      }
+    wave_lds_done();
+    const int c = lane & 15;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int r = 4 * p + (lane >> 4);
+      const v4u val = stage_get(region, r, c);
+      const int64_t n = n0 + j * 32 + r;
+      if (n < n_end && m0 + 8 * c < m_end)
+        *reinterpret_cast<v4u*>(out + row_of(n) * ld + m0 + 8 * c) = val;
+    }
+    wave_lds_done();
+  }
+}
+
+// A wave's accumulators in accumulator order: 16-byte pieces, 1 KiB per
+// instruction.
+template <int WN>
+__device__ __forceinline__ void put_acc(v16f (&acc)[kWM][WN], float* p) {
+  v4f* at = reinterpret_cast<v4f*>(p) + (threadIdx.x & 63);
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        at[((i * WN + j) * 4 + q) * 64] = v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                              acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+}
+template <int WN>
+__device__ __forceinline__ void add_acc(v16f (&acc)[kWM][WN], const float* p) {
+  const v4f* at = reinterpret_cast<const v4f*>(p) + (threadIdx.x & 63);
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      __builtin_amdgcn_sched_barrier(0);   // 16 values in flight: registers
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v4f v = at[((i * WN + j) * 4 + q) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+      }
+    }
+}
+constexpr int64_t wave_floats(int wn) { return (int64_t)kWM * wn * 16 * 64; }
+
+// dH tile: m over D (W transposed), n over the piece's rows, k over the words.
+template <int WN>
+__global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
+  const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+  const int64_t rows = piece_rows(g);
+  const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
+  const int64_t tiles = tm_all * tn_all, split = g.meta->split;
+  const int64_t steps = g.ldc / kBK, per = (steps + split - 1) / split;
+  int64_t item;
+  for (int64_t round = 0; next_item(tiles * split, round, item); ++round) {
+    const int64_t part = item / tiles;
+    int64_t tm, tn;
+    grouped(item - part * tiles, tm_all, tn_all, tm, tn);
+    tm = uniform((int)tm);
+    tn = uniform((int)tn);
+    const int64_t s0 = part * per, s1 = s0 + per < steps ? s0 + per : steps;
+    // W's rows end at V: words past it are zero codes in d and read zero in W
+    const int64_t k_end = s1 * kBK;
+    Core<true, false, WN> core;
+    clear<WN>(core.acc);
+    core.a.init(Operand{g.w, g.ldw, g.D}, tm * kTM, k_end < g.V ? k_end : g.V, wave, wm * 128);
+    core.b.init(Operand{g.codes, g.ldc, rows}, tn * 64 * WN, k_end, wave, wn * 32 * WN);
+    core.run(a0, b0, a1, b1, wave, s0, k_end);
+    if (split > 1) {
+      put_acc<WN>(core.acc, g.part + (item * 4 + wave) * wave_floats(WN));
+    } else {
+      store_tile<WN>(core.acc, a0 + wave * 8192, g.dh, g.ld_dh, tm * kTM + wm * 128, g.D,
+                     tn * 64 * WN + wn * 32 * WN, rows,
+                     [&](int64_t n) { return (int64_t)g.idx[g.first + n]; });
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+}
+
+// The parts of a cut dH product added in order and written out.
+template <int WN>
+__global__ __launch_bounds__(kThreads, 1) void k_ce_dh_join(CeArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[32768];
+  const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+  const int64_t rows = piece_rows(g);
+  const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
+  const int64_t tiles = tm_all * tn_all, split = g.meta->split;
+  if (split == 1) return;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int64_t tm, tn;
+    grouped(tile, tm_all, tn_all, tm, tn);
+    v16f acc[kWM][WN];
+    clear<WN>(acc);
+    for (int64_t s = 0; s < split; ++s)
+      add_acc<WN>(acc, g.part + ((s * tiles + tile) * 4 + wave) * wave_floats(WN));
+    store_tile<WN>(acc, lds + wave * 8192, g.dh, g.ld_dh, tm * kTM + wm * 128, g.D,
+                   tn * 64 * WN + wn * 32 * WN, rows,
+                   [&](int64_t n) { return (int64_t)g.idx[g.first + n]; });
+  }
+}
+
+// dW tile: m over D (H transposed), n over the words (d transposed), k over the
+// piece's rows.
+__global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
+  constexpr int WN = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
+  const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+  const int64_t rows = piece_rows(g);
+  if (rows == 0 && g.add && !g.finish) return;   // an empty piece in the middle
+  const int64_t tm_all = (g.D + kTM - 1) / kTM, tn_all = (g.V + 255) / 256;
+  int64_t item;
+  for (int64_t round = 0; next_item(tm_all * tn_all, round, item); ++round) {
+    int64_t tm, tn;
+    grouped(item, tm_all, tn_all, tm, tn);
+    tm = uniform((int)tm);
+    tn = uniform((int)tn);
+    Core<true, true, WN> core;
+    clear<WN>(core.acc);
+    core.a.init(Operand{g.h + g.first * g.ldh, g.ldh, g.D}, tm * kTM, rows, wave, wm * 128);
+    core.b.init(Operand{g.codes, g.ldc, g.ldc}, tn * 256, rows, wave, wn * 128);
+    core.run(a0, b0, a1, b1, wave, 0, rows);
+    float* acc_at = g.dw_acc + ((tn * tm_all + tm) * 4 + wave) * wave_floats(WN);
+    if (g.add) add_acc<WN>(core.acc, acc_at);
+    if (g.finish)
+      store_tile<WN>(core.acc, a0 + wave * 8192, g.dw, g.ld_dw, tm * kTM + wm * 128, g.D,
+                     tn * 256 + wn * 128, g.V, [](int64_t n) { return n; });
+    else
+      put_acc<WN>(core.acc, acc_at);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+}
+
+// -------------------------------------------------------------- preparation
+struct PrepArgs {
+  const void* targets;
+  int targets_type;
+  int64_t T, V, D, piece;
+  const float* row_weight;   // by token, null: 1 / number of targets
+  Meta* meta;
+  int32_t* idx;
+  int32_t* tgt;
+  float* weight;
+  float* loss;
+  float* lse;
+  int cus, rows_per_tile;    // of the dH product
+  int64_t tiles_m, steps, max_items;
+};
+
+constexpr int kPrepThreads = 1024;
+
+// One workgroup: number the tokens that have a target, in order; the others'
+// loss is 0.  Then the dH product's cut: the number of equal parts that lets
+// the compute units finish earliest, counting a fixed cost per part.
+__global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
+  __shared__ uint32_t wave_sum[kPrepThreads / 64];
+  __shared__ unsigned long long best;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t n = 0;
+  for (int64_t t0 = 0; t0 < p.T; t0 += kPrepThreads) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t target = -1;
+    if (t < p.T) target = target_of(p.targets, p.targets_type, t);
+    const bool live = target >= 0 && target < p.V;
+    const uint64_t m = __ballot(live);
+    if (lane == 0) wave_sum[wave] = (uint32_t)__popcll(m);
+    __syncthreads();
+    int64_t at = n + __popcll(m & ((1ull << lane) - 1ull));
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 64; ++w) {
+      at += w < wave ? wave_sum[w] : 0u;
+      n += wave_sum[w];
+    }
+    __syncthreads();
+    if (live) {
+      p.idx[at] = (int32_t)t;
+      p.tgt[at] = (int32_t)target;
+      if (p.row_weight != nullptr) p.weight[at] = p.row_weight[t];
+    } else if (t < p.T) {
+      p.loss[t] = 0.0f;
+      if (p.lse != nullptr) p.lse[t] = 0.0f;
+    }
+  }
+  if (p.row_weight == nullptr)
+    for (int64_t i = threadIdx.x; i < n; i += kPrepThreads) p.weight[i] = 1.0f / (float)n;
+
+  if (threadIdx.x == 0) best = ~0ull;
+  __syncthreads();
+  const int64_t rows = n < p.piece ? n : p.piece;
+  const int64_t tiles = p.tiles_m * ((rows + p.rows_per_tile - 1) / p.rows_per_tile);
+  const int64_t s = threadIdx.x + 1;
+  if (s == 1 || (s * tiles <= p.max_items && p.steps / s >= 8)) {
+    const int64_t rounds = (s * tiles + p.cus - 1) / p.cus;
+    const int64_t cost = rounds * ((p.steps + s - 1) / s + 8);
+    atomicMin(&best, (unsigned long long)cost << 16 | (unsigned long long)s);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.meta->n = (int)n;
+    p.meta->split = (int)(best & 0xFFFFu);
+  }
+}
+
+// hc[r] = h[idx[r]]; the gradient of a token without a target is zero.
+__global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ h, int64_t ldh,
+                                                   uint16_t* __restrict__ hc, int64_t T, int64_t V,
+                                                   int64_t D, const Meta* meta,
+                                                   const int32_t* __restrict__ idx,
+                                                   const void* targets, int targets_type,
+                                                   uint16_t* __restrict__ dh, int64_t ld_dh) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  if (r >= T) return;
+  if (r < meta->n) {
+    const uint16_t* src = h + (int64_t)idx[r] * ldh;
+    for (int64_t c = lane * 8; c < D; c += 512)
+      *reinterpret_cast<v4u*>(hc + r * D + c) = *reinterpret_cast<const v4u*>(src + c);
+  }
+  const int64_t target = target_of(targets, targets_type, r);
+  if (target < 0 || target >= V)
+    for (int64_t c = lane * 8; c < D; c += 512) *reinterpret_cast<v4u*>(dh + r * ld_dh + c) = v4u{};
+}
+
+// ---------------------------------------------------------------- the plan
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Width of a tile of tokens: the narrowest that holds them all, at most 256.
+int tokens_wn(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
+
+struct CePlan {
+  int64_t piece, pieces, spans, ldc, max_items;
+  int wn;
+  // workspace offsets
+  int64_t meta, idx, tgt, weight, tlogit, lse2, rloss, hc, stats, codes, part, dw_acc, total;
+};
+
+constexpr int64_t kCodeBytes = int64_t(4) << 30;   // default bound of the code buffer
+
+CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
+  CePlan p{};
+  p.spans = (V + kSpan - 1) / kSpan;
+  p.ldc = p.spans * kSpan;
+  p.piece = T;
+  if (grad) {
+    if (piece <= 0) {
+      const int64_t fit = kCodeBytes / (2 * p.ldc) / 256 * 256;
+      piece = fit < 256 ? 256 : fit;
+    }
+    if (piece < T) p.piece = piece;
+  }
+  p.pieces = p.piece > 0 ? (T + p.piece - 1) / p.piece : 1;
+  p.wn = tokens_wn(p.piece);
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  p.meta = take(sizeof(Meta));
+  p.tlogit = take(T * 4);
+  p.stats = take(p.piece * p.spans * 8);
+  if (grad) {
+    p.idx = take(T * 4);
+    p.tgt = take(T * 4);
+    p.weight = take(T * 4);
+    p.lse2 = take(T * 4);
+    p.rloss = take(T * 4);
+    p.hc = take(T * D * 2);
+    p.codes = take(p.piece * p.ldc * 2);
+    const int64_t tiles = (D + kTM - 1) / kTM * ((p.piece + 64 * p.wn - 1) / (64 * p.wn));
+    // 0: no token, or more tiles than that: never cut
+    p.max_items = tiles == 0 ? 0 : kMaxItems / tiles * tiles;
+    const int64_t most = p.ldc / kBK / 8 * tiles;
+    if (p.max_items > most) p.max_items = most;
+    p.part = take(p.max_items * 4 * wave_floats(p.wn) * 4);
+    if (p.pieces > 1)
+      p.dw_acc = take((D + kTM - 1) / kTM * ((V + 255) / 256) * 4 * wave_floats(4) * 4);
+  }
+  p.total = at;
+  return p;
+}
+
+template <int WN>
+void products(const CeArgs& a, int cus, hipStream_t s) {
+  const dim3 grid(cus), block(kThreads);
+  hipLaunchKernelGGL(k_ce_logits<WN>, grid, block, 0, s, a);
+  hipLaunchKernelGGL(k_ce_rows, dim3((uint32_t)((a.piece + 3) / 4)), dim3(256), 0, s, a);
+  if (!a.keep) return;
+  const int64_t vecs = a.ldc / 8;
+  hipLaunchKernelGGL(k_ce_dlogits,
+                     dim3((uint32_t)((vecs + 255) / 256),
+                          (uint32_t)(a.piece < 16384 ? a.piece : 16384)),
+                     dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_ce_dh<WN>, grid, block, 0, s, a);
+  hipLaunchKernelGGL(k_ce_dh_join<WN>, grid, block, 0, s, a);
+}
+
+void products(const CeArgs& a, int wn, int cus, hipStream_t s) {
+  if (wn == 1) products<1>(a, cus, s);
+  else if (wn == 2) products<2>(a, cus, s);
+  else products<4>(a, cus, s);
+}
+
+}  // namespace
+
+int64_t ce_workspace_bytes(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
+  return ce_plan(T, V, D, grad, piece).total;
+}
+
+hipError_t launch_ce(const CeCall& c, hipStream_t s) {
+  const CePlan p = ce_plan(c.T, c.V, c.D, c.grad, c.piece);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(c.ws);
+  const int cus = num_cus() / kXcds * kXcds;
+  CeArgs a{};
+  a.h = reinterpret_cast<const uint16_t*>(c.h);
+  a.w = reinterpret_cast<const uint16_t*>(c.w);
+  a.ldh = c.ldh;
+  a.ldw = c.ldw;
+  a.T = c.T;
+  a.V = c.V;
+  a.D = c.D;
+  a.piece = p.piece;
+  a.targets = c.targets;
+  a.targets_type = c.targets_type;
+  a.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
+  a.stats = reinterpret_cast<float2*>(ws + p.stats);
+  a.ldc = p.ldc;
+  a.spans = p.spans;
+  a.loss = c.loss;
+  a.lse = c.lse;
+  if (!c.grad) {
+    if (c.T > 0) products(a, p.wn, cus, s);
+    return hipGetLastError();
+  }
+  Meta* meta = reinterpret_cast<Meta*>(ws + p.meta);
+  a.meta = meta;
+  a.idx = reinterpret_cast<int32_t*>(ws + p.idx);
+  a.tgt = reinterpret_cast<int32_t*>(ws + p.tgt);
+  a.weight = reinterpret_cast<float*>(ws + p.weight);
+  a.lse2 = reinterpret_cast<float*>(ws + p.lse2);
+  a.rloss = reinterpret_cast<float*>(ws + p.rloss);
+  a.codes = reinterpret_cast<uint16_t*>(ws + p.codes);
+  a.dh = reinterpret_cast<uint16_t*>(c.dh);
+  a.ld_dh = c.ld_dh;
+  a.dw = reinterpret_cast<uint16_t*>(c.dw);
+  a.ld_dw = c.ld_dw;
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  a.dw_acc = reinterpret_cast<float*>(ws + p.dw_acc);
+  a.tiles_dh_m = (int)((c.D + kTM - 1) / kTM);
+  a.keep = true;
+  uint16_t* hc = reinterpret_cast<uint16_t*>(ws + p.hc);
+  PrepArgs pa{c.targets, c.targets_type, c.T, c.V, c.D, p.piece, c.row_weight, meta,
+              reinterpret_cast<int32_t*>(ws + p.idx), reinterpret_cast<int32_t*>(ws + p.tgt),
+              reinterpret_cast<float*>(ws + p.weight), c.loss, c.lse, cus, 64 * p.wn,
+              a.tiles_dh_m, p.ldc / kBK, p.max_items};
+  hipLaunchKernelGGL(k_ce_prep, dim3(1), dim3(kPrepThreads), 0, s, pa);
+  if (c.T > 0)
+    hipLaunchKernelGGL(k_ce_gather, dim3((uint32_t)((c.T + 3) / 4)), dim3(256), 0, s, a.h, c.ldh,
+                       hc, c.T, c.V, c.D, meta, a.idx, c.targets, c.targets_type, a.dh, c.ld_dh);
+  a.h = hc;
+  a.ldh = c.D;
+  for (int64_t q = 0; q < p.pieces; ++q) {
+    a.first = q * p.piece;
+    a.add = q > 0;
+    a.finish = q + 1 == p.pieces;
+    if (c.T > 0) products(a, p.wn, cus, s);
+    hipLaunchKernelGGL(k_ce_dw, dim3(cus), dim3(kThreads), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

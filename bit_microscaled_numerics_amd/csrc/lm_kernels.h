@@ -10,6 +10,8 @@
 
 namespace nvfp4 {
 
+int num_cus();  // compute units of the current device
+
 struct EmbedArgs {
   const void* ids;
   int ids_type;
@@ -29,5 +31,26 @@ hipError_t launch_grad_sumsq(const nvfp4_grad* list, int64_t count, double* part
                              hipStream_t s);
 hipError_t launch_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials,
                             double max_norm, float* norm_out, hipStream_t s);
+
+// Softmax cross entropy of a head: loss (and lse) of every token; grad: dh and
+// dw as well.  piece: tokens per piece of the gradient (0: chosen here).
+struct CeCall {
+  const void* h;
+  const void* w;
+  int64_t ldh, ldw, T, V, D;
+  const void* targets;
+  int targets_type;
+  const float* row_weight;
+  int64_t piece;
+  float* loss;
+  float* lse;
+  void* dh;
+  void* dw;
+  int64_t ld_dh, ld_dw;
+  bool grad;
+  void* ws;
+};
+int64_t ce_workspace_bytes(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece);
+hipError_t launch_ce(const CeCall& c, hipStream_t s);
 
 }  // namespace nvfp4

@@ -338,6 +338,44 @@ int nvfp4_embed_grad(const void* ids, int ids_type, int64_t n, const void* dy, i
                      int64_t ld_dw, int accumulate, void* workspace, int64_t workspace_bytes,
                      void* stream);
 
+/* Softmax cross entropy of an output head: with z_tv = sum_k h[t][k] w[v][k]
+ * (FP32 accumulation of exact products),
+ *   lse[t]  = log sum_v exp(z_tv),   loss[t] = lse[t] - z_t,targets[t].
+ * h [T][D] and w [V][D] are BF16 with D and both row pitches multiples of 8
+ * and 16-byte aligned bases; loss and lse (nullable) FP32 [T]; targets I32 or
+ * I64.  A target outside 0 .. V-1 (an ignore mark such as -100) is none: its
+ * loss is 0.  The logits are never stored.  T may be 0.  Rows whose logits are
+ * not all finite give a loss and gradient that are not finite; other rows are
+ * not affected.  workspace: 256-byte aligned, of at least
+ * nvfp4_linear_ce_workspace_bytes(T, V, D, 0, 0). */
+int nvfp4_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T, int64_t V,
+                    int64_t D, const void* targets, int targets_type, float* loss, float* lse,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same with its gradient, from one call: for the sum of
+ * row_weight[t] * loss[t] over the tokens with a target (row_weight NULL: each
+ * 1 / their number, the mean),
+ *   d_tv = row_weight[t] * (exp(z_tv - lse[t]) - [v == targets[t]])
+ *   dh = d w  [T][D],   dw = d^T h  [V][D],
+ * BF16, accumulated in FP32 (d enters the products rounded to BF16).  dh, dw:
+ * row pitches multiples of 8, 16-byte aligned.  A token without a target costs
+ * no arithmetic, has a zero row in dh and an lse of 0, and nothing in its row
+ * of h (infinities, NaN) reaches another result.
+ * Tokens are taken piece_tokens at a time (0: as many as a buffer of 4 GiB
+ * allows at 2 bytes per token and word); the workspace is
+ * nvfp4_linear_ce_workspace_bytes(T, V, D, 1, piece_tokens) bytes.  The result
+ * is the same bits every time. */
+int nvfp4_linear_ce_grad(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T,
+                         int64_t V, int64_t D, const void* targets, int targets_type,
+                         const float* row_weight, int64_t piece_tokens, float* loss, float* lse,
+                         void* dh, int64_t ld_dh, void* dw, int64_t ld_dw, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two calls above (grad 0 or 1); a negative
+ * NVFP4_ERR_* status for sizes they refuse. */
+int64_t nvfp4_linear_ce_workspace_bytes(int64_t T, int64_t V, int64_t D, int grad,
+                                        int64_t piece_tokens);
+
 /* One gradient tensor of a list (contiguous).  The list itself is HOST
  * memory, read before the call returns; in and out are device memory.  out
  * may equal in (in place, same type); other overlaps race. */

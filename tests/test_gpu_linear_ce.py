@@ -1,0 +1,290 @@
+"""Softmax cross entropy of an output head, and its gradient, against binary64.
+
+Tolerances, from the arithmetic (u = 2^-24, one binary32 rounding):
+  logit     products of BF16 are exact in binary32; a sum of D of them is within
+            dz = D u sum_k |h_k w_k| of the exact one
+  lse       each exponential within dz plus 4 u; a span's sum adds 72 terms in
+            sequence and tree, the spans' sum S / 64 + 8 more: relative
+            (80 + S / 64 + 8) u, and the result is rounded once
+  d         the code is within half a step of 64/65535 in log2: 3.4e-4; dz and
+            the lse error enter as relative errors; BF16 rounds by half a step,
+            2^-8.  At the target exp(-loss) - 1 takes the loss's error times
+            exp(-loss) instead of the code's.
+  dh, dw    the errors of d through the product, a binary32 sum of n terms
+            (n u of the sum of magnitudes), half a BF16 step."""
+import pytest
+import torch
+
+import bit_microscaled_numerics_amd as nv
+from parity import say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = 2.0 ** -8
+CODE = 0.5 * 64 / 65535 * 0.6931472 * 1.001
+
+
+class Ref:
+    """The definitions in binary64, and bounds of the kernels' errors."""
+
+    def __init__(self, h, w, t, weight=None):
+        h, w, t = h.cpu().double(), w.cpu().double(), t.cpu().long()
+        T, V, D = h.shape[0], w.shape[0], h.shape[1]
+        self.live = (t >= 0) & (t < V)
+        z = h @ w.t()
+        self.dz = (D * U * (h.abs() @ w.abs().t())).amax(1) if T else torch.zeros(0).double()
+        self.lse = torch.logsumexp(z, 1)
+        at = t.clamp(0, V - 1).unsqueeze(1)
+        raw = self.lse - z.gather(1, at).squeeze(1)
+        self.loss = torch.where(self.live, raw, torch.zeros_like(raw))
+        rel = (80 + V / 128 / 64 + 8) * U + 8 * U
+        self.tol_lse = self.dz + rel + U * self.lse.abs()
+        self.tol_loss = torch.where(self.live, 2 * self.dz + rel + U * raw.abs(), torch.zeros_like(raw))
+        if weight is None:
+            weight = torch.full((T,), 1.0 / max(1, int(self.live.sum())))
+        g = torch.where(self.live, weight.cpu().double(), torch.zeros(T).double()).unsqueeze(1)
+        p = torch.exp(z - self.lse.unsqueeze(1))
+        onehot = torch.zeros_like(p).scatter_(1, at, 1.0)
+        d = g * (p - onehot)
+        ez = (2 * self.dz + rel).unsqueeze(1)
+        err = g.abs() * p * (CODE * (1 - onehot) + 2 * ez + 8 * U) + g.abs() * 1e-18
+        err = err * (1 + HALF) + HALF * d.abs()
+        dead = ~self.live.unsqueeze(1)
+        # a row without a target holds anything
+        h = torch.where(dead, torch.zeros_like(h), h)
+        d, err = torch.where(dead, 0.0, d), torch.where(dead, 0.0, err)
+        self.dh, self.dw = d @ w, d.t() @ h
+        mag = d.abs() + err
+        self.tol_dh = err @ w.abs() + (V + 130) * U * (mag @ w.abs())
+        self.tol_dw = err.t() @ h.abs() + (T + 130) * U * (mag.t() @ h.abs())
+        self.tol_dh += HALF * (self.dh.abs() + self.tol_dh)
+        self.tol_dw += HALF * (self.dw.abs() + self.tol_dw)
+
+
+def _close(got, ref, tol, what):
+    err = (got.cpu().double() - ref).abs()
+    bad = torch.nonzero(~(err <= tol))
+    assert bad.numel() == 0, (what, len(bad), bad[0].tolist(), err[tuple(bad[0])].item(), tol[tuple(bad[0])].item())
+
+
+def _inputs(T, V, D, seed=0, ignored="some", scale=0.3, it=torch.int64):
+    g = torch.Generator().manual_seed(seed + T * 7 + V * 3 + D)
+    h = torch.randn(T, D, generator=g).to(torch.bfloat16)
+    w = (torch.randn(V, D, generator=g) * scale).to(torch.bfloat16)
+    t = torch.randint(0, V, (T,), generator=g)
+    if ignored == "some":
+        r = torch.rand(T, generator=g)
+        t = torch.where(r < 0.1, torch.full_like(t, -100), torch.where(r < 0.2, t + V, t))
+    elif ignored == "all":
+        t = torch.full_like(t, -100)
+    return h.cuda(), w.cuda(), t.to(it).cuda()
+
+
+def _check_all(h, w, t, weight=None, piece=0):
+    ref = Ref(h, w, t, weight)
+    loss, lse = nv.linear_ce(h, w, t)
+    _close(loss, ref.loss, ref.tol_loss, "loss")
+    _close(lse, ref.lse, ref.tol_lse, "lse")
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t, row_weight=weight, piece_tokens=piece)
+    _close(loss, ref.loss, ref.tol_loss, "loss with gradient")
+    _close(lse, ref.lse * ref.live, ref.tol_lse, "lse with gradient")
+    _close(dh, ref.dh, ref.tol_dh, "dh")
+    _close(dw, ref.dw, ref.tol_dw, "dw")
+    return loss, lse, dh, dw
+
+
+# one token, both sides of the token tiles (64, 128, 256), of a span (128) and
+# tile (256) of words, of a step (64) and an instruction (16) of D
+@pytest.mark.parametrize("T", [1, 5, 64, 65, 129, 257])
+@pytest.mark.parametrize("V", [1, 7, 128, 129, 300, 1027])
+@pytest.mark.parametrize("D", [8, 64, 72, 264])
+def test_sizes(T, V, D):
+    say("ce", T, V, D)
+    _check_all(*_inputs(T, V, D, it=torch.int32 if (T + V) % 2 else torch.int64))
+
+
+@pytest.mark.parametrize("T,V,D", [(300, 4099, 520), (520, 33000, 136), (40, 9000, 1032)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_larger(T, V, D, weighted):
+    """Several tiles in each direction, and a dH sum cut into parts."""
+    say("ce", T, V, D, weighted)
+    h, w, t = _inputs(T, V, D, scale=0.1)
+    weight = None
+    if weighted:
+        weight = torch.rand(T, generator=torch.Generator().manual_seed(1)).sub_(0.2).cuda()
+        weight[::5] = 0.0
+    _check_all(h, w, t, weight)
+
+
+@pytest.mark.parametrize("ignored", ["none", "all"])
+@pytest.mark.parametrize("T", [1, 70, 300])
+def test_masks(T, ignored):
+    say("ce mask", T, ignored)
+    h, w, t = _inputs(T, 500, 64, ignored=ignored)
+    _, _, dh, dw = _check_all(h, w, t)
+    if ignored == "all":
+        assert torch.all(dh == 0) and torch.all(dw == 0)
+
+
+def test_no_tokens():
+    h, w, t = _inputs(0, 40, 16)
+    loss, lse = nv.linear_ce(h, w, t)
+    assert loss.shape == (0,) and lse.shape == (0,)
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t)
+    assert loss.shape == (0,) and dh.shape == (0, 16)
+    assert torch.all(dw == 0)
+
+
+@pytest.mark.parametrize("T,piece", [(300, 64), (300, 100), (257, 256), (700, 256)])
+@pytest.mark.parametrize("ignored", ["none", "some", "all"])
+def test_pieces(T, piece, ignored):
+    """dW is added up in FP32 over pieces, the last of them short or empty."""
+    say("ce pieces", T, piece, ignored)
+    h, w, t = _inputs(T, 777, 136, ignored=ignored)
+    if ignored == "some":
+        t[T // 3:] = -100   # whole pieces without a token
+    _check_all(h, w, t, piece=piece)
+
+
+def test_strides_and_neighbours():
+    """Pitches above the width, outputs inside larger buffers."""
+    T, V, D = 77, 333, 72
+    h, w, t = _inputs(T, V, D)
+    hb = torch.full((T + 1, D + 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wb = torch.full((V + 1, D + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    hv, wv = hb[:T, 8:D + 8], wb[:V, :D]
+    hv.copy_(h)
+    wv.copy_(w)
+    dh = torch.full((T, D + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((V, D + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    ws = torch.empty(nv.nvfp4_linear_ce_workspace_bytes(T, V, D, True), dtype=torch.uint8, device="cuda")
+    say("ce strides")
+    nv.nvfp4_linear_ce_grad(hv, wv, t, None, 0, loss, lse, dh[:, :D], dw[:, 8:], ws)
+    ref = Ref(h, w, t)
+    _close(loss, ref.loss, ref.tol_loss, "loss")
+    _close(dh[:, :D], ref.dh, ref.tol_dh, "dh")
+    _close(dw[:, 8:], ref.dw, ref.tol_dw, "dw")
+    assert torch.all(dh[:, D:] == 5.0) and torch.all(dw[:, :8] == 5.0)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nonfinite_rows_without_a_target_reach_nothing(bad):
+    h, w, t = _inputs(100, 300, 64, ignored="none")
+    t[10:20] = -100
+    want = nv.linear_ce_grad(h, w, t)
+    h[10:20] = bad
+    got = nv.linear_ce_grad(h, w, t)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nonfinite_rows_with_a_target_show(bad):
+    h, w, t = _inputs(100, 300, 64, ignored="none")
+    want_loss, want_lse, want_dh, _ = nv.linear_ce_grad(h, w, t)
+    h[33, 5] = bad
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t)
+    assert not torch.isfinite(loss[33]) and not torch.isfinite(dh[33]).any()
+    keep = torch.arange(100, device="cuda") != 33
+    assert torch.equal(loss[keep], want_loss[keep]) and torch.equal(dh[keep], want_dh[keep])
+
+
+@pytest.mark.parametrize("scale", [8.0, 60.0])
+def test_large_logits(scale):
+    """Logits in the hundreds and thousands: nearly all of the mass on one word,
+    most exponentials 0, losses near 0 and large ones side by side."""
+    h, w, t = _inputs(140, 400, 64, ignored="none", scale=scale)
+    best = (h.float() @ w.float().t()).argmax(1)
+    t[::2] = best[::2]
+    _check_all(h, w, t)
+
+
+def test_one_word_and_equal_logits():
+    h = torch.zeros(9, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1000, 16, dtype=torch.bfloat16, device="cuda")
+    t = torch.arange(9, device="cuda")
+    _check_all(h, w, t)
+
+
+def test_gradient_against_differences():
+    """The directional derivative of the weighted loss, by central differences of
+    the binary64 definition, against the kernels' gradient along the same
+    direction (step 1e-4: error 1e-8 of the third derivative)."""
+    T, V, D = 60, 200, 48
+    h, w, t = _inputs(T, V, D)
+    weight = torch.rand(T, generator=torch.Generator().manual_seed(2)).cuda()
+    ref = Ref(h, w, t, weight)
+    _, _, dh, dw = nv.linear_ce_grad(h, w, t, row_weight=weight)
+    g = torch.Generator().manual_seed(3)
+    uh, uw = torch.randn(T, D, generator=g).double(), torch.randn(V, D, generator=g).double()
+
+    def value(eps):
+        r = (h.cpu().double() + eps * uh) @ (w.cpu().double() + eps * uw).t()
+        tt = t.cpu()
+        raw = torch.logsumexp(r, 1) - r.gather(1, tt.clamp(0, V - 1).unsqueeze(1)).squeeze(1)
+        return (raw * weight.cpu().double())[ref.live].sum()
+
+    slope = (value(1e-4) - value(-1e-4)) / 2e-4
+    got = (dh.cpu().double() * uh).sum() + (dw.cpu().double() * uw).sum()
+    tol = (ref.tol_dh * uh.abs()).sum() + (ref.tol_dw * uw.abs()).sum() + 1e-4 * slope.abs()
+    assert abs(got - slope) <= tol
+
+
+def test_same_bits_every_time():
+    h, w, t = _inputs(600, 9001, 200)
+    first = nv.linear_ce_grad(h, w, t)
+    for _ in range(3):
+        for a, b in zip(nv.linear_ce_grad(h, w, t), first):
+            assert torch.equal(a, b)
+
+
+def test_on_another_stream_and_in_a_graph():
+    T, V, D = 200, 1500, 96
+    h, w, t = _inputs(T, V, D)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    ws = torch.empty(nv.nvfp4_linear_ce_workspace_bytes(T, V, D, True), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nv.nvfp4_linear_ce_grad(h, w, t, None, 0, loss, lse, dh, dw, ws, stream=side)
+    side.synchronize()
+    ref = Ref(h, w, t)
+    _close(dw, ref.dw, ref.tol_dw, "dw")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.nvfp4_linear_ce_grad(h, w, t, None, 0, loss, lse, dh, dw, ws)
+    for seed in range(3):
+        h2, _, t2 = _inputs(T, V, D, seed=seed + 1, ignored="none" if seed == 1 else "some")
+        h.copy_(h2)
+        t.copy_(t2)
+        for x in (loss, lse, dh, dw):
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((loss, lse, dh, dw), nv.linear_ce_grad(h, w, t)):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """A vocabulary matrix of 5.2 GB: the last words' logits and gradients."""
+    T, V, D = 8, 320000, 8192
+    say("ce 5.2 GB", T, V, D)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda").normal_(0, 0.01, generator=g)
+    h = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    t = V - 1 - torch.arange(T, device="cuda") * 40000
+    loss, _, dh, dw = nv.linear_ce_grad(h, w, t)
+    z = torch.cat([h.double() @ w[v:v + 16000].double().t() for v in range(0, V, 16000)], 1)
+    p = torch.softmax(z, 1)
+    p[torch.arange(T), t] -= 1
+    ref = torch.logsumexp(z, 1) - z.gather(1, t.unsqueeze(1)).squeeze(1)
+    # |h w| sums to about 0.0064 D = 52: dz = D u 52 = 0.026 is the worst case; rounding errors of
+    # random sign grow as sqrt(D): 3e-4
+    assert torch.all((loss.double() - ref).abs() <= 0.026 * 2)
+    p /= T
+    d_dh = sum(p[:, v:v + 16000] @ w[v:v + 16000].double() for v in range(0, V, 16000))
+    assert (dh.double() - d_dh).norm() <= (2 * HALF + 0.052) * d_dh.norm()
+    last = p[:, V - 300:].t() @ h.double()
+    assert (dw[V - 300:].double() - last).norm() <= (2 * HALF + 0.052) * last.norm()

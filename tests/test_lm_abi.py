@@ -118,3 +118,60 @@ def test_binding_refuses():
         nv._pitch(torch.zeros(1, 4).expand(3, 4), "x")
     assert nv._pitch(torch.zeros(1, 4).expand(1, 4), "x") == 4
     assert nv._pitch(torch.zeros(3, 9)[:, :4], "x") == 9
+
+
+def _ce(lib, grad=True, h=FAKE, ldh=64, w=FAKE, ldw=64, T=4, V=10, D=64, t=FAKE, tt=I8, rw=None,
+        piece=0, loss=FAKE, lse=FAKE, dh=FAKE, ld_dh=64, dw=FAKE, ld_dw=64, ws=FAKE, nb=1 << 40):
+    if not grad:
+        return lib.nvfp4_linear_ce(h, ldh, w, ldw, T, V, D, t, tt, loss, lse, ws, nb, None)
+    return lib.nvfp4_linear_ce_grad(h, ldh, w, ldw, T, V, D, t, tt, rw, piece, loss, lse, dh, ld_dh,
+                                    dw, ld_dw, ws, nb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(h=None), nv.NVFP4_ERR_NULL), (dict(w=None), nv.NVFP4_ERR_NULL),
+    (dict(t=None), nv.NVFP4_ERR_NULL), (dict(loss=None), nv.NVFP4_ERR_NULL),
+    (dict(ws=None), nv.NVFP4_ERR_NULL), (dict(T=-1), nv.NVFP4_ERR_SHAPE),
+    (dict(T=(1 << 31) - 1), nv.NVFP4_ERR_SHAPE), (dict(V=0), nv.NVFP4_ERR_SHAPE),
+    (dict(V=1 << 31), nv.NVFP4_ERR_SHAPE), (dict(D=0), nv.NVFP4_ERR_SHAPE),
+    (dict(D=60), nv.NVFP4_ERR_SHAPE), (dict(ldh=56), nv.NVFP4_ERR_SHAPE),
+    (dict(ldw=56), nv.NVFP4_ERR_SHAPE), (dict(ldw=1 << 22), nv.NVFP4_ERR_SHAPE),
+    (dict(ldh=68), nv.NVFP4_ERR_ALIGN), (dict(w=FAKE + 8), nv.NVFP4_ERR_ALIGN),
+    (dict(lse=FAKE + 2), nv.NVFP4_ERR_ALIGN), (dict(t=FAKE + 4), nv.NVFP4_ERR_ALIGN),
+    (dict(ws=FAKE + 128), nv.NVFP4_ERR_ALIGN), (dict(tt=BF), nv.NVFP4_ERR_ARG),
+    (dict(nb=64), nv.NVFP4_ERR_ARG), (dict(nb=-1), nv.NVFP4_ERR_ARG)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_ce_validation(lib, kw, status, grad):
+    assert _ce(lib, grad=grad, **kw) == status
+    assert lib.nvfp4_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dh=None), nv.NVFP4_ERR_NULL), (dict(dw=None), nv.NVFP4_ERR_NULL),
+    (dict(V=1 << 22), nv.NVFP4_ERR_SHAPE), (dict(piece=-1), nv.NVFP4_ERR_SHAPE),
+    (dict(ld_dh=8), nv.NVFP4_ERR_SHAPE), (dict(ld_dw=70), nv.NVFP4_ERR_ALIGN),
+    (dict(dh=FAKE + 2), nv.NVFP4_ERR_ALIGN), (dict(rw=FAKE + 2), nv.NVFP4_ERR_ALIGN)])
+def test_ce_grad_validation(lib, kw, status):
+    assert _ce(lib, **kw) == status
+
+
+def test_ce_workspace_query(lib):
+    q = lib.nvfp4_linear_ce_workspace_bytes
+    for T in (0, 1, 63, 64, 65, 1000, 100000):
+        for V in (1, 127, 50257, 131072):
+            small = [q(T, V, D, g, 0) for D in (8, 5120) for g in (0, 1)]
+            assert all(0 < b < 1 << 36 for b in small), (T, V, small)
+            assert q(T, V, 512, 1, 256) <= q(T, V, 512, 1, 0) + (V + 256) * 512 * 4 + (1 << 20)
+    assert q(4, 10, 64, 2, 0) == nv.NVFP4_ERR_ARG
+    assert q(4, 10, 63, 1, 0) == nv.NVFP4_ERR_SHAPE
+    assert q(-4, 10, 64, 1, 0) == nv.NVFP4_ERR_SHAPE
+    with pytest.raises(nv.NVFP4Error):
+        nv.nvfp4_linear_ce_workspace_bytes(4, 0, 64, True)
+
+
+def test_ce_binding_refuses():
+    h = torch.zeros(4, 16, dtype=torch.bfloat16)
+    t = torch.zeros(4, dtype=torch.int64)
+    for f in (nv.linear_ce, nv.linear_ce_grad):
+        with pytest.raises(ValueError, match="CUDA"):
+            f(h, h, t)

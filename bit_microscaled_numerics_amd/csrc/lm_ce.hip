@@ -49,6 +49,7 @@ constexpr int kMaxItems = 2048;            // parts x tiles of a cut dH product
 struct Meta {
   int n;        // tokens with a target
   int split;    // parts of the dH product's sum
+  float scale;  // of the row weights: the results are multiplied by it
 };
 
 struct CeArgs {
@@ -61,13 +62,13 @@ struct CeArgs {
   const void* targets;
   int targets_type;
   const int32_t* tgt;      // gathered targets
-  const float* weight;     // gathered row weights g
+  const float* weight;     // gathered row weights g, divided by the scale
   float* tlogit;           // [rows] the target's logit
   float2* stats;           // [piece][spans] (log2 maximum, sum)
   float* lse2;             // [rows] lse / ln 2
   float* rloss;            // [rows]
   uint16_t* codes;         // [piece][ldc] codes, then d
-  int64_t ldc, spans;
+  int64_t ldc, spans, wide;   // pitch of codes, spans, words with their padding (spans * 128)
   float* loss;             // by token
   float* lse;              // by token (nullable)
   uint16_t* dh;
@@ -115,15 +116,29 @@ __device__ __forceinline__ void clear(v16f (&acc)[kWM][WN]) {
     for (int j = 0; j < WN; ++j) acc[i][j] = v16f{};
 }
 
+// The lane number, opaque: epilogue addresses derived from it are formed where
+// they are used.  The compiler otherwise keeps them all across the tile loop,
+// spilled, since the products need every register.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // A wave's 32 n x 128 m half-words staged in its own 8 KiB of LDS, row n in 256
 // bytes, chunk c at c ^ (n & 15): 8-byte writes of 4 consecutive m, 16-byte
 // reads of whole rows.
-__device__ __forceinline__ void stage_put(uint8_t* region, int i, int q, v2u v) {
-  const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
-  *reinterpret_cast<v2u*>(region + n * 256 + (((4 * i + q) ^ (n & 15)) << 4) + half * 8) = v;
+__device__ __forceinline__ uint32_t stage_base(int lane) {
+  const int n = lane & 31;
+  return (uint32_t)(n * 256 + ((n & 15) << 4) + (lane >> 5) * 8);
 }
-__device__ __forceinline__ v4u stage_get(const uint8_t* region, int r, int c) {
-  return *reinterpret_cast<const v4u*>(region + r * 256 + ((c ^ (r & 15)) << 4));
+__device__ __forceinline__ void stage_put(uint8_t* region, uint32_t base, int i, int q, v2u v) {
+  *reinterpret_cast<v2u*>(region + (base ^ (uint32_t)((4 * i + q) << 4))) = v;
+}
+// Piece p of the readback: rows 4 p + lane / 16, chunk lane % 16.
+__device__ __forceinline__ v4u stage_get(const uint8_t* region, int lane, int p) {
+  const int r = 4 * p + (lane >> 4);
+  return *reinterpret_cast<const v4u*>(region + r * 256 + (((lane & 15) ^ (r & 15)) << 4));
 }
 __device__ __forceinline__ void wave_lds_done() {
   __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
@@ -131,10 +146,75 @@ __device__ __forceinline__ void wave_lds_done() {
 }
 
 // ------------------------------------------------------------------- logits
-template <int WN>
+// What the epilogue does with block column j of a wave (32 rows, the 128 words
+// from m0 on); `left` words of the span exist (128 or more: WHOLE).
+template <int WN, bool KEEP, bool WHOLE>
+__device__ __forceinline__ void logits_block(const CeArgs& g, const v16f (&acc)[kWM][WN], int j,
+                                             int left, int64_t m0, int64_t row0, int64_t rows,
+                                             uint8_t* region) {
+  const int lane = fresh_lane(), half = lane >> 5;
+  const int64_t row = row0 + (lane & 31);
+  // words past the vocabulary take no part
+  const auto z = [&](int i, int v) {
+    return WHOLE || acc_m(i, v, half) < left ? acc[i][j][v] : -__builtin_inff();
+  };
+  float mx = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) mx = fmaxf(mx, z(i, v));
+  mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+  // the reference of the span: this binary32 value itself, so its rounding
+  // costs nothing; 0 where every logit is -inf (all exponentials are 0)
+  const float m2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2e;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWM; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+      sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, v), kLog2e, -m2));
+  sum += __shfl_xor(sum, 32, 64);
+  if (row < rows && half == 0) g.stats[row * g.spans + m0 / kSpan] = float2{m2, sum};
+  const int target = row < rows ? row_target(g, g.first + row) : -1;
+  const int at = target < 0 ? -1 : target - (int)m0;
+  if (__ballot(at >= 0 && at < kSpan)) {
+    float own = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) own = at == acc_m(i, v, half) ? acc[i][j][v] : own;
+    if (at >= 0 && at < kSpan && ((at >> 2) & 1) == half) g.tlogit[g.first + row] = own;
+  }
+  if (KEEP) {
+    const float c0 = m2 / kCodeSpan;
+    const uint32_t base = stage_base(lane);
+#pragma unroll
+    for (int i = 0; i < kWM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(z(i, 4 * q + e), -kLog2e / kCodeSpan, c0);
+        stage_put(region, base, i, q,
+                  v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[0], x[1])),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[2], x[3]))});
+      }
+    wave_lds_done();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int r = 4 * p + (lane >> 4), c = lane & 15;
+      const v4u val = stage_get(region, lane, p);
+      if (row0 + r < rows)
+        *reinterpret_cast<v4u*>(g.codes + (row0 + r) * g.ldc + m0 + 8 * c) = val;
+    }
+    wave_lds_done();
+  }
+}
+
+template <int WN, bool KEEP>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = uniform(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   const int64_t rows = piece_rows(g);
   const int64_t tm_all = (g.V + kTM - 1) / kTM, tn_all = (rows + 64 * WN - 1) / (64 * WN);
@@ -151,72 +231,20 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
     core.run(a0, b0, a1, b1, wave, 0, g.D);
 
     const int64_t m0 = tm * kTM + wm * 128;   // the wave's span of words
+    const int64_t row0 = tn * 64 * WN + wn * 32 * WN;
     uint8_t* region = a0 + wave * 8192;
-    const bool whole = m0 + kSpan <= g.V;
+    if (m0 + kSpan <= g.V) {
 #pragma unroll
-    for (int j = 0; j < WN; ++j) {
-      __builtin_amdgcn_sched_barrier(0);   // one block of tokens at a time: registers
-      const int64_t row = tn * 64 * WN + wn * 32 * WN + j * 32 + (lane & 31);
-      if (!whole) {   // words past the vocabulary take no part
-#pragma unroll
-        for (int i = 0; i < kWM; ++i)
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            if (m0 + acc_m(i, v, half) >= g.V) core.acc[i][j][v] = -__builtin_inff();
+      for (int j = 0; j < WN; ++j) {
+        __builtin_amdgcn_sched_barrier(0);   // one block of rows at a time: registers
+        logits_block<WN, KEEP, true>(g, core.acc, j, kSpan, m0, row0 + 32 * j, rows, region);
       }
-      float mx = -__builtin_inff();
+    } else if (m0 < g.V) {
 #pragma unroll
-      for (int i = 0; i < kWM; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, core.acc[i][j][v]);
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      // the reference of the span: this binary32 value itself, so its rounding
-      // costs nothing; 0 where every logit is -inf (all exponentials are 0)
-      const float m2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2e;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWM; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          sum += __builtin_amdgcn_exp2f(__builtin_fmaf(core.acc[i][j][v], kLog2e, -m2));
-      sum += __shfl_xor(sum, 32, 64);
-      const bool live = row < rows;
-      if (live && half == 0 && m0 < g.V) g.stats[row * g.spans + m0 / kSpan] = float2{m2, sum};
-      const int target = live ? row_target(g, g.first + row) : -1;
-      const int at = target - (int)m0;   // words below 2^31: no overflow
-      if (__ballot(target >= 0 && at >= 0 && at < kSpan)) {
-#pragma unroll
-        for (int i = 0; i < kWM; ++i)
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            if (target >= 0 && at == acc_m(i, v, half)) g.tlogit[g.first + row] = core.acc[i][j][v];
-      }
-      if (g.keep) {
-        const float c0 = m2 / kCodeSpan;
-#pragma unroll
-        for (int i = 0; i < kWM; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = __builtin_fmaf(core.acc[i][j][4 * q + e], -kLog2e / kCodeSpan, c0);
-            stage_put(region, i, q,
-                      v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[0], x[1])),
-                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[2], x[3]))});
-          }
-        wave_lds_done();
-        if (m0 < g.ldc) {
-          const int64_t r0 = tn * 64 * WN + wn * 32 * WN + j * 32;
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const int r = 4 * p + (lane >> 4), c = lane & 15;
-            const v4u val = stage_get(region, r, c);
-            if (r0 + r < rows)
-              *reinterpret_cast<v4u*>(g.codes + (r0 + r) * g.ldc + m0 + 8 * c) = val;
-          }
-        }
-        wave_lds_done();
+      for (int j = 0; j < WN; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        logits_block<WN, KEEP, false>(g, core.acc, j, (int)(g.V - m0), m0, row0 + 32 * j, rows,
+                                      region);
       }
     }
     // the next tile's loads write the region: every wave is past it
@@ -259,9 +287,12 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
 
 // codes -> d = g (p - [target]), BF16, in place.  Each thread 8 entries of a
 // row.  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
-// close to 1.  A weight of 0 gives zeros whatever the row holds.
+// close to 1.  A weight of 0 gives zeros whatever the row holds.  Weights are
+// relative to their largest (all 1 for a mean), which multiplies the FP32 results
+// instead: a mean's 1/n, rounded to BF16 in every d alike, would be a common
+// error of up to 2^-8.
 __global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
-  const int64_t vecs = g.ldc / 8, rows = piece_rows(g);
+  const int64_t vecs = g.wide / 8, rows = piece_rows(g);
   const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (v >= vecs) return;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
@@ -293,26 +324,28 @@ __global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
 template <int WN, class RowOf>
 __device__ __forceinline__ void store_tile(v16f (&acc)[kWM][WN], uint8_t* region, uint16_t* out,
                                            int64_t ld, int64_t m0, int64_t m_end, int64_t n0,
-                                           int64_t n_end, RowOf row_of) {
-  const int lane = threadIdx.x & 63;
+                                           int64_t n_end, float scale, RowOf row_of) {
 #pragma unroll
   for (int j = 0; j < WN; ++j) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int lane = fresh_lane();
+    const uint32_t base = stage_base(lane);
 #pragma unroll
     for (int i = 0; i < kWM; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         typedef float f4 __attribute__((ext_vector_type(4)));
         typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-        const f4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                      acc[i][j][4 * q + 3]};
-        stage_put(region, i, q, __builtin_bit_cast(v2u, __builtin_convertvector(v, b4)));
+        const f4 v = f4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                        acc[i][j][4 * q + 3]} * scale;
+        stage_put(region, base, i, q, __builtin_bit_cast(v2u, __builtin_convertvector(v, b4)));
       }
     wave_lds_done();
     const int c = lane & 15;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int r = 4 * p + (lane >> 4);
-      const v4u val = stage_get(region, r, c);
+      const v4u val = stage_get(region, lane, p);
       const int64_t n = n0 + j * 32 + r;
       if (n < n_end && m0 + 8 * c < m_end)
         *reinterpret_cast<v4u*>(out + row_of(n) * ld + m0 + 8 * c) = val;
@@ -361,7 +394,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
   const int64_t rows = piece_rows(g);
   const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
   const int64_t tiles = tm_all * tn_all, split = g.meta->split;
-  const int64_t steps = g.ldc / kBK, per = (steps + split - 1) / split;
+  const int64_t steps = g.wide / kBK, per = (steps + split - 1) / split;
   int64_t item;
   for (int64_t round = 0; next_item(tiles * split, round, item); ++round) {
     const int64_t part = item / tiles;
@@ -381,43 +414,60 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
       put_acc<WN>(core.acc, g.part + (item * 4 + wave) * wave_floats(WN));
     } else {
       store_tile<WN>(core.acc, a0 + wave * 8192, g.dh, g.ld_dh, tm * kTM + wm * 128, g.D,
-                     tn * 64 * WN + wn * 32 * WN, rows,
+                     tn * 64 * WN + wn * 32 * WN, rows, g.meta->scale,
                      [&](int64_t n) { return (int64_t)g.idx[g.first + n]; });
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 }
 
-// The parts of a cut dH product added in order and written out.
+// The parts of a cut dH product added in order and written out: one wave per
+// 32 x 32 block, so that few tiles in many parts still fill the chip.
 template <int WN>
-__global__ __launch_bounds__(kThreads, 1) void k_ce_dh_join(CeArgs g) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[32768];
+__global__ __launch_bounds__(256) void k_ce_dh_join(CeArgs g) {
   const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
   const int64_t rows = piece_rows(g);
   const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
   const int64_t tiles = tm_all * tn_all, split = g.meta->split;
   if (split == 1) return;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  const float scale = g.meta->scale;
+  for (int64_t u = blockIdx.x; u < tiles * kWM * WN; u += gridDim.x) {
+    const int64_t tile = u / (kWM * WN);
+    const int block = (int)(u % (kWM * WN)), i = block / WN, j = block % WN;
+    const v4f* at = reinterpret_cast<const v4f*>(g.part + (tile * 4 + wave) * wave_floats(WN)) +
+                    block * 4 * 64 + lane;
+    const int64_t pitch = tiles * wave_floats(WN);   // in v4f: 4 waves of wave_floats / 4
+    v4f sum[4] = {};
+#pragma unroll 4
+    for (int64_t s = 0; s < split; ++s)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[q] += at[s * pitch + q * 64];
     int64_t tm, tn;
     grouped(tile, tm_all, tn_all, tm, tn);
-    v16f acc[kWM][WN];
-    clear<WN>(acc);
-    for (int64_t s = 0; s < split; ++s)
-      add_acc<WN>(acc, g.part + ((s * tiles + tile) * 4 + wave) * wave_floats(WN));
-    store_tile<WN>(acc, lds + wave * 8192, g.dh, g.ld_dh, tm * kTM + wm * 128, g.D,
-                   tn * 64 * WN + wn * 32 * WN, rows,
-                   [&](int64_t n) { return (int64_t)g.idx[g.first + n]; });
+    const int64_t n = tn * 64 * WN + wn * 32 * WN + 32 * j + (lane & 31);
+    if (n >= rows) continue;
+    uint16_t* out = g.dh + (int64_t)g.idx[g.first + n] * g.ld_dh;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+      const int64_t m = tm * kTM + wm * 128 + 32 * i + 8 * q + 4 * half;
+      if (m < g.D)
+        *reinterpret_cast<v2u*>(out + m) =
+            __builtin_bit_cast(v2u, __builtin_convertvector(sum[q] * scale, b4));
+    }
   }
 }
 
 // dW tile: m over D (H transposed), n over the words (d transposed), k over the
-// piece's rows.
+// piece's rows.  PIECES: the sum goes on over several pieces, held in FP32.
+template <bool PIECES>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
   constexpr int WN = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
   const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
   const int64_t rows = piece_rows(g);
-  if (rows == 0 && g.add && !g.finish) return;   // an empty piece in the middle
+  if (PIECES && rows == 0 && g.add && !g.finish) return;   // an empty piece in the middle
   const int64_t tm_all = (g.D + kTM - 1) / kTM, tn_all = (g.V + 255) / 256;
   int64_t item;
   for (int64_t round = 0; next_item(tm_all * tn_all, round, item); ++round) {
@@ -428,13 +478,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
     Core<true, true, WN> core;
     clear<WN>(core.acc);
     core.a.init(Operand{g.h + g.first * g.ldh, g.ldh, g.D}, tm * kTM, rows, wave, wm * 128);
-    core.b.init(Operand{g.codes, g.ldc, g.ldc}, tn * 256, rows, wave, wn * 128);
+    core.b.init(Operand{g.codes, g.ldc, g.wide}, tn * 256, rows, wave, wn * 128);
     core.run(a0, b0, a1, b1, wave, 0, rows);
     float* acc_at = g.dw_acc + ((tn * tm_all + tm) * 4 + wave) * wave_floats(WN);
-    if (g.add) add_acc<WN>(core.acc, acc_at);
-    if (g.finish)
+    if (PIECES && g.add) add_acc<WN>(core.acc, acc_at);
+    if (!PIECES || g.finish)
       store_tile<WN>(core.acc, a0 + wave * 8192, g.dw, g.ld_dw, tm * kTM + wm * 128, g.D,
-                     tn * 256 + wn * 128, g.V, [](int64_t n) { return n; });
+                     tn * 256 + wn * 128, g.V, g.meta->scale, [](int64_t n) { return n; });
     else
       put_acc<WN>(core.acc, acc_at);
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -465,8 +515,10 @@ constexpr int kPrepThreads = 1024;
 __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
   __shared__ uint32_t wave_sum[kPrepThreads / 64];
   __shared__ unsigned long long best;
+  __shared__ uint32_t top;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t n = 0;
+  uint32_t most = 0;   // bits of the largest |weight|
   for (int64_t t0 = 0; t0 < p.T; t0 += kPrepThreads) {
     const int64_t t = t0 + threadIdx.x;
     int64_t target = -1;
@@ -485,17 +537,26 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
     if (live) {
       p.idx[at] = (int32_t)t;
       p.tgt[at] = (int32_t)target;
-      if (p.row_weight != nullptr) p.weight[at] = p.row_weight[t];
+      if (p.row_weight != nullptr)
+        most = max(most, __float_as_uint(p.row_weight[t]) & 0x7FFFFFFFu);
     } else if (t < p.T) {
       p.loss[t] = 0.0f;
       if (p.lse != nullptr) p.lse[t] = 0.0f;
     }
   }
-  if (p.row_weight == nullptr)
-    for (int64_t i = threadIdx.x; i < n; i += kPrepThreads) p.weight[i] = 1.0f / (float)n;
-
-  if (threadIdx.x == 0) best = ~0ull;
+  if (threadIdx.x == 0) {
+    best = ~0ull;
+    top = 0;
+  }
   __syncthreads();
+  if (most != 0) atomicMax(&top, most);
+  __syncthreads();   // also: idx is written
+  // weights that are all 0, or not all finite, stay as they are
+  float scale = __uint_as_float(top);
+  if (p.row_weight == nullptr) scale = 1.0f / (float)(n > 0 ? n : 1);
+  else if (top == 0 || top >= 0x7F800000u) scale = 1.0f;
+  for (int64_t i = threadIdx.x; i < n; i += kPrepThreads)
+    p.weight[i] = p.row_weight == nullptr ? 1.0f : p.row_weight[p.idx[i]] / scale;
   const int64_t rows = n < p.piece ? n : p.piece;
   const int64_t tiles = p.tiles_m * ((rows + p.rows_per_tile - 1) / p.rows_per_tile);
   const int64_t s = threadIdx.x + 1;
@@ -508,13 +569,14 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
   if (threadIdx.x == 0) {
     p.meta->n = (int)n;
     p.meta->split = (int)(best & 0xFFFFu);
+    p.meta->scale = scale;
   }
 }
 
 // hc[r] = h[idx[r]]; the gradient of a token without a target is zero.
 __global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ h, int64_t ldh,
-                                                   uint16_t* __restrict__ hc, int64_t T, int64_t V,
-                                                   int64_t D, const Meta* meta,
+                                                   uint16_t* __restrict__ hc, int64_t ldhc,
+                                                   int64_t T, int64_t V, int64_t D, const Meta* meta,
                                                    const int32_t* __restrict__ idx,
                                                    const void* targets, int targets_type,
                                                    uint16_t* __restrict__ dh, int64_t ld_dh) {
@@ -524,7 +586,7 @@ __global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ 
   if (r < meta->n) {
     const uint16_t* src = h + (int64_t)idx[r] * ldh;
     for (int64_t c = lane * 8; c < D; c += 512)
-      *reinterpret_cast<v4u*>(hc + r * D + c) = *reinterpret_cast<const v4u*>(src + c);
+      *reinterpret_cast<v4u*>(hc + r * ldhc + c) = *reinterpret_cast<const v4u*>(src + c);
   }
   const int64_t target = target_of(targets, targets_type, r);
   if (target < 0 || target >= V)
@@ -538,7 +600,7 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int tokens_wn(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
 
 struct CePlan {
-  int64_t piece, pieces, spans, ldc, max_items;
+  int64_t piece, pieces, spans, ldc, ldhc, max_items;
   int wn;
   // workspace offsets
   int64_t meta, idx, tgt, weight, tlogit, lse2, rloss, hc, stats, codes, part, dw_acc, total;
@@ -549,7 +611,8 @@ constexpr int64_t kCodeBytes = int64_t(4) << 30;   // default bound of the code 
 CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
   CePlan p{};
   p.spans = (V + kSpan - 1) / kSpan;
-  p.ldc = p.spans * kSpan;
+  p.ldc = p.spans * kSpan + 64;   // an odd number of 128-byte lines
+  p.ldhc = up(D, 64) + (up(D, 64) / 64 % 2 == 0 ? 64 : 0);
   p.piece = T;
   if (grad) {
     if (piece <= 0) {
@@ -575,12 +638,12 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
     p.weight = take(T * 4);
     p.lse2 = take(T * 4);
     p.rloss = take(T * 4);
-    p.hc = take(T * D * 2);
+    p.hc = take(T * p.ldhc * 2);
     p.codes = take(p.piece * p.ldc * 2);
     const int64_t tiles = (D + kTM - 1) / kTM * ((p.piece + 64 * p.wn - 1) / (64 * p.wn));
     // 0: no token, or more tiles than that: never cut
     p.max_items = tiles == 0 ? 0 : kMaxItems / tiles * tiles;
-    const int64_t most = p.ldc / kBK / 8 * tiles;
+    const int64_t most = p.spans * kSpan / kBK / 8 * tiles;
     if (p.max_items > most) p.max_items = most;
     p.part = take(p.max_items * 4 * wave_floats(p.wn) * 4);
     if (p.pieces > 1)
@@ -593,16 +656,19 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
 template <int WN>
 void products(const CeArgs& a, int cus, hipStream_t s) {
   const dim3 grid(cus), block(kThreads);
-  hipLaunchKernelGGL(k_ce_logits<WN>, grid, block, 0, s, a);
+  if (a.keep)
+    hipLaunchKernelGGL((k_ce_logits<WN, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_ce_logits<WN, false>), grid, block, 0, s, a);
   hipLaunchKernelGGL(k_ce_rows, dim3((uint32_t)((a.piece + 3) / 4)), dim3(256), 0, s, a);
   if (!a.keep) return;
-  const int64_t vecs = a.ldc / 8;
+  const int64_t vecs = a.wide / 8;
   hipLaunchKernelGGL(k_ce_dlogits,
                      dim3((uint32_t)((vecs + 255) / 256),
                           (uint32_t)(a.piece < 16384 ? a.piece : 16384)),
                      dim3(256), 0, s, a);
   hipLaunchKernelGGL(k_ce_dh<WN>, grid, block, 0, s, a);
-  hipLaunchKernelGGL(k_ce_dh_join<WN>, grid, block, 0, s, a);
+  hipLaunchKernelGGL(k_ce_dh_join<WN>, dim3(8 * cus), dim3(256), 0, s, a);
 }
 
 void products(const CeArgs& a, int wn, int cus, hipStream_t s) {
@@ -635,6 +701,7 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
   a.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
   a.stats = reinterpret_cast<float2*>(ws + p.stats);
   a.ldc = p.ldc;
+  a.wide = p.spans * kSpan;
   a.spans = p.spans;
   a.loss = c.loss;
   a.lse = c.lse;
@@ -662,19 +729,22 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
   PrepArgs pa{c.targets, c.targets_type, c.T, c.V, c.D, p.piece, c.row_weight, meta,
               reinterpret_cast<int32_t*>(ws + p.idx), reinterpret_cast<int32_t*>(ws + p.tgt),
               reinterpret_cast<float*>(ws + p.weight), c.loss, c.lse, cus, 64 * p.wn,
-              a.tiles_dh_m, p.ldc / kBK, p.max_items};
+              a.tiles_dh_m, a.wide / kBK, p.max_items};
   hipLaunchKernelGGL(k_ce_prep, dim3(1), dim3(kPrepThreads), 0, s, pa);
   if (c.T > 0)
     hipLaunchKernelGGL(k_ce_gather, dim3((uint32_t)((c.T + 3) / 4)), dim3(256), 0, s, a.h, c.ldh,
-                       hc, c.T, c.V, c.D, meta, a.idx, c.targets, c.targets_type, a.dh, c.ld_dh);
+                       hc, p.ldhc, c.T, c.V, c.D, meta, a.idx, c.targets, c.targets_type, a.dh, c.ld_dh);
   a.h = hc;
-  a.ldh = c.D;
+  a.ldh = p.ldhc;
   for (int64_t q = 0; q < p.pieces; ++q) {
     a.first = q * p.piece;
     a.add = q > 0;
     a.finish = q + 1 == p.pieces;
     if (c.T > 0) products(a, p.wn, cus, s);
-    hipLaunchKernelGGL(k_ce_dw, dim3(cus), dim3(kThreads), 0, s, a);
+    if (p.pieces > 1)
+      hipLaunchKernelGGL(k_ce_dw<true>, dim3(cus), dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL(k_ce_dw<false>, dim3(cus), dim3(kThreads), 0, s, a);
   }
   return hipGetLastError();
 }

@@ -16,11 +16,13 @@
 // consecutive k of its row).  Neither product of the backward pass therefore
 // needs a transposed copy of an operand.
 //
-// Pipeline: fragments are read one 16-deep sub-step ahead.  At the last sub-step
-// of a stage all its fragments are in registers: wait for the next stage's
-// loads (issued a whole step, 64 MFMAs, earlier), barrier, refill the freed
-// stage with the step after next between the sub-step's MFMAs, and read the
-// next stage's first fragments.
+// Pipeline: a step is four phases of 16 k.  In the first every wave reads the
+// fragments of the other three, 96 registers; a barrier later the stage is free
+// and its refill with the step after next is issued between the second
+// and third phases' MFMAs, spread out: issued together, the loads stall the waves
+// at issue (all four leave the barrier at once).  Before the fourth phase the next stage must have landed: its loads were
+// issued a step and a half (96 MFMAs, 3072 cycles) earlier, with the refill just
+// issued still in flight.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -62,6 +64,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t by
 // chunk) per cycle over 256 B; swz is a bijection on the even and on the odd
 // rows of any 16, so they touch distinct bank groups.
 __device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ ((r & 1) << 1)) & 7; }
+
+// s_waitcnt immediate: vmcnt <= n, nothing else waited on
+constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
 // ROWS rows of an operand, one stage at a time.
 template <bool TR, int ROWS>
@@ -193,59 +198,67 @@ struct Core {
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
   }
 
-  __device__ __forceinline__ void load_all(uint8_t* sa, uint8_t* sb, int wave, int64_t k0) {
-    a.step(k0);
-    b.step(k0);
+  __device__ __forceinline__ void load_a(uint8_t* sa, int wave, int64_t k0) {
 #pragma unroll
     for (int q = 0; q < LA::kLoads; ++q) a.load(sa, wave, q, k0);
+  }
+  __device__ __forceinline__ void load_b(uint8_t* sb, int wave, int64_t k0) {
 #pragma unroll
     for (int q = 0; q < LB::kLoads; ++q) b.load(sb, wave, q, k0);
   }
+  __device__ __forceinline__ void load_all(uint8_t* sa, uint8_t* sb, int wave, int64_t k0) {
+    a.step(k0);
+    b.step(k0);
+    load_a(sa, wave, k0);
+    load_b(sb, wave, k0);
+  }
 
-  // Spread a sub-step's LDS reads between its MFMAs.
+  // The order of a phase: after each MFMA its share of LDS reads (0x100) and of
+  // loads to LDS (0x010).
+  template <int READS, int LOADS>
   __device__ __forceinline__ void interleave() {
-    constexpr int kMfma = kWM * WN, kRead = kWM * LA::kReads + WN * LB::kReads;
-    constexpr int kPer = (kRead + kMfma - 1) / kMfma;
+    constexpr int kMfma = kWM * WN;
+    constexpr int kPerR = (READS + kMfma - 1) / kMfma, kPerL = (LOADS + kMfma - 1) / kMfma;
+    constexpr int kGap = LOADS > 0 && LOADS < kMfma ? kMfma / LOADS : 1;
 #pragma unroll
     for (int m = 0; m < kMfma; ++m) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (m * kPer < kRead) __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);
+      if (m * kPerR < READS) __builtin_amdgcn_sched_group_barrier(0x100, kPerR, 0);
+      if (m % kGap == 0 && m / kGap * kPerL < LOADS)
+        __builtin_amdgcn_sched_group_barrier(0x010, kPerL, 0);
     }
   }
 
-  // The same with the refill's loads, one after each MFMA.
-  __device__ __forceinline__ void interleave_loads() {
-    constexpr int kMfma = kWM * WN, kRead = kWM * LA::kReads + WN * LB::kReads;
-    constexpr int kLoad = LA::kLoads + LB::kLoads;
-    constexpr int kPerR = (kRead + kMfma - 1) / kMfma, kPerL = (kLoad + kMfma - 1) / kMfma;
-#pragma unroll
-    for (int m = 0; m < kMfma; ++m) {
-      if (m * kPerR < kRead) __builtin_amdgcn_sched_group_barrier(0x100, kPerR, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (m * kPerL < kLoad) __builtin_amdgcn_sched_group_barrier(0x010, kPerL, 0);
-    }
-  }
-
-  // One stage: (ca, cb) holds step s, (na, nb) step s + 1.
-  __device__ __forceinline__ void stage(Frags<WN>& cur, uint8_t* ca, uint8_t* cb, uint8_t* na,
+  // One stage: (ca, cb) holds step s, (na, nb) step s + 1; f[0] is read already.
+  __device__ __forceinline__ void stage(Frags<WN> (&f)[4], uint8_t* ca, uint8_t* cb, uint8_t* na,
                                         uint8_t* nb, int wave, int64_t s) {
-    Frags<WN> nxt;
+    constexpr int kRead = kWM * LA::kReads + WN * LB::kReads;
+    constexpr int kLoad = LA::kLoads + LB::kLoads;
 #pragma unroll
-    for (int ks = 0; ks < 3; ++ks) {
-      read(nxt, ca, cb, ks + 1);
-      mfma(cur);
-      interleave();
-      cur = nxt;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // own loads of the next stage landed, own reads of this one done; then all waves'
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int ks = 1; ks < 4; ++ks) read(f[ks], ca, cb, ks);
+    mfma(f[0]);
+    interleave<3 * kRead, 0>();
     __builtin_amdgcn_sched_barrier(0);
-    read(nxt, na, nb, 0);
-    load_all(ca, cb, wave, (s + 2) * kBK);
-    mfma(cur);
-    interleave_loads();
-    cur = nxt;
+    // this wave holds the whole stage in registers; when all do, it is free
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    a.step((s + 2) * kBK);
+    b.step((s + 2) * kBK);
+    load_a(ca, wave, (s + 2) * kBK);
+    mfma(f[1]);
+    interleave<0, LA::kLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+    load_b(cb, wave, (s + 2) * kBK);
+    mfma(f[2]);
+    interleave<0, LB::kLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+    // the next stage has landed: all but the loads just issued
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoad));
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    read(f[0], na, nb, 0);
+    mfma(f[3]);
+    interleave<kRead, 0>();
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -258,11 +271,11 @@ struct Core {
     load_all(a0, b0, wave, s0 * kBK);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     load_all(a1, b1, wave, (s0 + 1) * kBK);
-    Frags<WN> cur;
-    read(cur, a0, b0, 0);
+    Frags<WN> f[4];
+    read(f[0], a0, b0, 0);
     for (int64_t s = s0; s * kBK < k_end; s += 2) {
-      stage(cur, a0, b0, a1, b1, wave, s);
-      stage(cur, a1, b1, a0, b0, wave, s + 1);
+      stage(f, a0, b0, a1, b1, wave, s);
+      stage(f, a1, b1, a0, b0, wave, s + 1);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }

@@ -596,6 +596,15 @@ __global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ 
 // ---------------------------------------------------------------- the plan
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// Row pitch of an operand laid out here: an odd number of 256-byte pieces, so that
+// a column of 128-byte lines (what a K-contiguous stage reads of 256 rows) spreads
+// over all channels of an L2, and rows start on a piece (what the transposed
+// stages read is two whole pieces of each row).
+int64_t odd_pitch(int64_t cols) {
+  const int64_t pieces = (cols + 127) / 128;
+  return (pieces + (pieces % 2 == 0)) * 128;
+}
+
 // Width of a tile of tokens: the narrowest that holds them all, at most 256.
 int tokens_wn(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
 
@@ -611,8 +620,8 @@ constexpr int64_t kCodeBytes = int64_t(4) << 30;   // default bound of the code 
 CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
   CePlan p{};
   p.spans = (V + kSpan - 1) / kSpan;
-  p.ldc = p.spans * kSpan + 64;   // an odd number of 128-byte lines
-  p.ldhc = up(D, 64) + (up(D, 64) / 64 % 2 == 0 ? 64 : 0);
+  p.ldc = odd_pitch(V);
+  p.ldhc = odd_pitch(D);
   p.piece = T;
   if (grad) {
     if (piece <= 0) {

@@ -54,9 +54,14 @@ struct Operand {
   int64_t rows;   // rows that exist; others read as zero, or only reach results that are not stored
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
-  const int64_t b = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)b, (int)kBufFlags);
+// A descriptor from values that are the same in every lane.  They are moved to
+// scalar registers explicitly: sizes that were loaded from memory are not known
+// to be uniform, and a descriptor in vector registers puts a loop around every
+// load.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint16_t* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>(uniform64((int64_t)(uintptr_t)p)), (short)0, uniform(bytes),
+      (int)kBufFlags);
 }
 
 // Stage position of 16-byte chunk j of row r in the K-contiguous layout:
@@ -80,14 +85,15 @@ struct Loader<false, ROWS> {
   uint32_t voff[kLoads];
   int chunk[2];       // source chunk of this lane, in even and odd loads
   uint32_t frag[4];   // LDS offset of this lane's fragment of block 0, by sub-step
-  int K, k_base;      // k_base: first k of the offsets' origin
+  int K;
 
   __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k_total, int wave,
                                        int frag_row0) {
     const int lane = threadIdx.x & 63;
     const int64_t rem = o.rows - row0;
-    buf = rsrc(o.p + row0 * o.ld, rem > 0 ? ((rem < ROWS ? rem - 1 : ROWS - 1) * o.ld + k_total) * 2 : 0);
-    K = (int)k_total;
+    const int64_t last = rem < ROWS ? rem - 1 : ROWS - 1;   // below 2^31 bytes (pitch < 2^22)
+    buf = rsrc(o.p + row0 * o.ld, rem > 0 ? (int)((last * o.ld + k_total) * 2) : 0);
+    K = uniform((int)k_total);
 #pragma unroll
     for (int par = 0; par < 2; ++par) chunk[par] = (lane & 7) ^ swz(par * 8 + (lane >> 3));
 #pragma unroll
@@ -136,7 +142,7 @@ struct Loader<true, ROWS> {
     ld = o.ld;
     pitch = (int)(o.ld * 2);
     tail = (int)((o.ld - (o.rows - row0)) * 2);
-    K = (int)k_total;
+    K = uniform((int)k_total);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
       const int k = wave * 16 + q * 2 + (lane >> 5);
@@ -155,8 +161,7 @@ struct Loader<true, ROWS> {
   // however long K is; rows at or past K lie past num_records.
   __device__ __forceinline__ void step(int64_t k0) {
     const int left = min(max(K - (int)k0, 0), kBK);
-    buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + k0 * ld), (short)0,
-                                            max(left * pitch - tail, 0), (int)kBufFlags);
+    buf = rsrc(base + k0 * ld, max(left * pitch - tail, 0));
   }
   __device__ __forceinline__ void load(uint8_t* stage, int wave, int q, int64_t) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(stage + (wave * 16 + q * 2) * 512), 16,

@@ -7,8 +7,10 @@
 // Both are bound by HBM: the forward moves T * D elements in and out, the
 // gradient reads T * D and writes all V * D.  The gradient is deterministic:
 // a stable sort of the tokens by id puts the rows of one word side by side in
-// ascending t, and every dW row is one FP32 sum in that order, written once
-// (no atomics, no zeroing pass).
+// ascending t, and every dW row is one FP32 sum in that order (no atomics).
+// The sort needs one or a few workgroups and the zeros of dW need no sort, so
+// the sort's first launch writes them with all its other workgroups; the rows
+// of the words that occur are then written over them, at most T rows.
 #include "lm_device.h"
 #include "lm_kernels.h"
 
@@ -124,13 +126,58 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* scratc
 // returns this thread's bin total (0 past the bins).
 __device__ __forceinline__ uint32_t scan_waves(uint32_t* counts, int bins) {
   uint32_t run = 0;
-  if ((int)threadIdx.x < bins)
+  if ((int)threadIdx.x < bins) {
+    uint32_t c[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = counts[w * kBinsMax + threadIdx.x];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = counts[w * kBinsMax + threadIdx.x];
       counts[w * kBinsMax + threadIdx.x] = run;
-      run += c;
+      run += c[w];
     }
+  }
   return run;
+}
+
+// Zeros of dW, written by the workgroups of a sort launch that do not sort:
+// `rows` rows of `cols` elements (a contiguous dW as one row).
+struct Fill {
+  uint8_t* p;
+  int64_t rows, row_bytes, pitch;   // bytes; rows 0: nothing
+};
+
+// 4 KiB pieces (whole rows where dW has gaps) dealt in turn to kFillBlocks workgroups, 256 threads of each: what
+// is in flight is one narrow window of dW.  1.3 GB take 204 us (6.6 TB/s) so; 1024
+// threads 230 us, 255 workgroups 235 .. 280 us, 64 KiB pieces 218 us and more.
+constexpr int kFillBlocks = 128, kFillThreads = 256;
+
+__device__ __forceinline__ void fill_zero(const Fill& f, int64_t block) {
+  constexpr int64_t kPiece = 16 * kFillThreads;
+  if (threadIdx.x >= kFillThreads) return;
+  if (f.rows == 1) {
+    const int64_t whole = f.row_bytes / 16 * 16;
+#pragma unroll 4
+    for (int64_t o = block * kPiece + 16 * threadIdx.x; o < whole; o += kFillBlocks * kPiece)
+      *reinterpret_cast<v4u_any2*>(f.p + o) = v4u_any2{};
+    if (block == 0)
+      for (int64_t e = whole + 2 * threadIdx.x; e < f.row_bytes; e += 2 * kFillThreads)
+        *reinterpret_cast<uint16_t*>(f.p + e) = 0;
+    return;
+  }
+  for (int64_t r = block; r < f.rows; r += kFillBlocks) {
+    uint8_t* p = f.p + r * f.pitch;
+    for (int64_t o = 16 * threadIdx.x; o < f.row_bytes; o += kPiece) {
+      if (o + 16 <= f.row_bytes) {
+        *reinterpret_cast<v4u_any2*>(p + o) = v4u_any2{};
+      } else {
+        for (int64_t e = o; e < f.row_bytes; e += 2) *reinterpret_cast<uint16_t*>(p + e) = 0;
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(kFillThreads) void k_fill(Fill fill) {
+  fill_zero(fill, blockIdx.x);
 }
 
 // All passes in one workgroup, keys and token numbers in LDS between passes
@@ -139,7 +186,12 @@ __device__ __forceinline__ uint32_t scan_waves(uint32_t* counts, int bins) {
 template <int STEPS>
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(EmbedArgs a, int bits, int passes,
                                                              uint32_t* __restrict__ keys_out,
-                                                             uint32_t* __restrict__ idx_out) {
+                                                             uint32_t* __restrict__ idx_out,
+                                                             Fill fill) {
+  if (blockIdx.x > 0) {
+    fill_zero(fill, blockIdx.x - 1);
+    return;
+  }
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* counts = reinterpret_cast<uint32_t*>(smem);           // [waves][bins]
   uint32_t* bin_base = counts + kSortWaves * kBinsMax;            // [bins]
@@ -202,6 +254,7 @@ struct SortPass {
   uint32_t* hist;   // [bins][tiles]
   int64_t tiles;
   int shift, bits;
+  Fill fill;        // count kernel: workgroups past the tiles
 };
 
 __device__ __forceinline__ uint32_t tile_key(const SortPass& p, int64_t i) {
@@ -212,6 +265,10 @@ __device__ __forceinline__ uint32_t tile_key(const SortPass& p, int64_t i) {
 
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortPass p) {
   __shared__ uint32_t bin[kBinsMax];
+  if (blockIdx.x >= p.tiles) {
+    fill_zero(p.fill, blockIdx.x - p.tiles);
+    return;
+  }
   const int bins = 1 << p.bits;
   for (int i = threadIdx.x; i < bins; i += kSortThreads) bin[i] = 0;
   __syncthreads();
@@ -282,32 +339,44 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(SortPass p) {
 // ----------------------------------------------------------------- gradient
 // A frequent word owns a long run of the sorted tokens.  Aligned windows of
 // 64 sorted tokens that lie wholly inside one run are summed first, each by
-// its own wave into an FP32 partial row; the row kernel then adds at most 63
-// single rows before, the partials, and at most 63 rows after.
+// its own wave into an FP32 partial row; the run kernel then adds at most 63
+// single rows before, the partials, and at most 63 rows after.  Loads go out
+// up to sixteen rows at a time: a chain of single rows is bound by their latency.
 constexpr int kWindow = 64;
 
-// The sum of dY rows idx[0 .. count) at columns c .. c + 7 added to acc, in
-// order.  idx and count are the same for the whole wave (scalar loads).
-template <class Y>
-__device__ __forceinline__ void add_rows(v8f& acc, const Y* __restrict__ dy, int64_t ld, int64_t c,
-                                         int64_t count, const uint32_t* __restrict__ idx) {
-  int64_t j = 0;
-  for (; j + 4 <= count; j += 4) {
-    v8f v[4];
+// acc += at(j) + .. + at(j + N - 1), in this order, with all N loads out first.
+template <int N, class A, class At>
+__device__ __forceinline__ void add_batch(A& acc, int64_t j, At at) {
+  A v[N];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load8(dy + (int64_t)idx[j + u] * ld + c);
+  for (int u = 0; u < N; ++u) v[u] = at(j + u);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc += v[u];
-  }
-  for (; j < count; ++j) acc += load8(dy + (int64_t)idx[j] * ld + c);
+  for (int u = 0; u < N; ++u) acc += v[u];
 }
 
-// The same at one column (the fewer than 8 at the end of a row).
-template <class Y>
-__device__ __forceinline__ void add_rows(float& acc, const Y* __restrict__ dy, int64_t ld,
-                                         int64_t c, int64_t count,
-                                         const uint32_t* __restrict__ idx) {
-  for (int64_t j = 0; j < count; ++j) acc += load1(dy + (int64_t)idx[j] * ld + c);
+// acc += at(0) + .. + at(count - 1), in this order; count is the same for the
+// whole wave.
+template <class A, class At>
+__device__ __forceinline__ void add_all(A& acc, int64_t count, At at) {
+  int64_t j = 0;
+  for (; j + 16 <= count; j += 16) add_batch<16>(acc, j, at);
+  if (count & 8) { add_batch<8>(acc, j, at); j += 8; }
+  if (count & 4) { add_batch<4>(acc, j, at); j += 4; }
+  if (count & 2) { add_batch<2>(acc, j, at); j += 2; }
+  if (count & 1) add_batch<1>(acc, j, at);
+}
+
+__device__ __forceinline__ v8f load_as(const v8f&, const bf16_t* p) { return load8(p); }
+__device__ __forceinline__ v8f load_as(const v8f&, const float* p) { return load8(p); }
+__device__ __forceinline__ float load_as(const float&, const bf16_t* p) { return load1(p); }
+__device__ __forceinline__ float load_as(const float&, const float* p) { return load1(p); }
+
+// The sum of dY rows idx[0 .. count) at columns c .. c + 7 (A = v8f) or at column
+// c (float) added to acc.
+template <class A, class Y>
+__device__ __forceinline__ void add_rows(A& acc, const Y* __restrict__ dy, int64_t ld, int64_t c,
+                                         int64_t count, const uint32_t* __restrict__ idx) {
+  add_all(acc, count, [&](int64_t j) { return load_as(acc, dy + (int64_t)idx[j] * ld + c); });
 }
 
 template <class Y>
@@ -359,13 +428,8 @@ struct RowArgs {
   int64_t n, vocab, dim, ld_dy, ld_dw;
   const float* partial;
   float scale;
-  int rows_per;       // vocabulary rows per wave
-  int64_t cols_per;   // columns per wave (a multiple of kWaveCols)
   bool accumulate;
 };
-
-__device__ __forceinline__ void add_partial(v8f& acc, const float* p) { acc += load8(p); }
-__device__ __forceinline__ void add_partial(float& acc, const float* p) { acc += *p; }
 
 // The whole sum of run [s, e) at columns c .. c + 7 (v8f) or column c (float).
 template <class A, class Y>
@@ -378,55 +442,38 @@ __device__ __forceinline__ A run_sum(const RowArgs& r, const Y* __restrict__ dy,
     return acc;
   }
   add_rows(acc, dy, r.ld_dy, c, w0 * kWindow - s, r.idx + s);
-  for (int64_t w = w0; w < w1; ++w) add_partial(acc, r.partial + w * r.dim + c);
+  add_all(acc, w1 - w0, [&](int64_t w) { return load_as(acc, r.partial + (w0 + w) * r.dim + c); });
   add_rows(acc, dy, r.ld_dy, c, e - w1 * kWindow, r.idx + w1 * kWindow);
   return acc;
 }
 
-// dW rows: a wave owns rows_per consecutive vocabulary rows (and a column
-// range when the vocabulary alone does not fill the chip).  It finds its
-// first sorted position by probing, then walks the runs with a 64-key window
-// held one key per lane.  Rows of absent words are zeros (or stay as they
-// are when accumulating).
+// dW rows of the words that occur: a workgroup for each sorted position and
+// range of columns (8 per thread); those that are not the first of a run leave.
 template <class Y, class G>
-__global__ __launch_bounds__(64) void k_embed_rows(RowArgs r, const Y* __restrict__ dy,
-                                                   G* __restrict__ dw) {
-  const int lane = threadIdx.x;
-  const int64_t v0 = (int64_t)blockIdx.x * r.rows_per;
-  const int64_t v1 = v0 + r.rows_per < r.vocab ? v0 + r.rows_per : r.vocab;
-  const int64_t c0 = blockIdx.y * r.cols_per;
-  const int64_t c1 = c0 + r.cols_per < r.dim ? c0 + r.cols_per : r.dim;
-  int64_t s = uniform64(lower_bound(r.keys, 0, r.n, (uint32_t)v0));
-  int64_t wb = s;
-  uint32_t key = wb + lane < r.n ? r.keys[wb + lane] : kNoKey;
-  for (int64_t v = v0; v < v1; ++v) {
-    int64_t e;
-    if ((uint32_t)__builtin_amdgcn_readlane((int)key, 63) <= (uint32_t)v) {
-      // the run may go past the window
-      e = uniform64(lower_bound(r.keys, s, r.n - s, (uint32_t)v + 1u));
-      wb = e;
-      key = wb + lane < r.n ? r.keys[wb + lane] : kNoKey;
-    } else {
-      e = s + __popcll(__ballot(key == (uint32_t)v));
+__global__ __launch_bounds__(256) void k_embed_runs(RowArgs r, const Y* __restrict__ dy,
+                                                    G* __restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  const int64_t s = blockIdx.x;
+  const uint32_t v = r.keys[s];
+  if (v >= (uint32_t)r.vocab || (s > 0 && r.keys[s - 1] == v)) return;
+  // the run's end: within the next 64 keys, or by search
+  const uint64_t same = __ballot(s + lane < r.n && r.keys[s + lane < r.n ? s + lane : s] == v);
+  int64_t e = s + 64;
+  if (~same != 0) e = s + __popcll(same);
+  else e = lower_bound(r.keys, e, r.n - e, v + 1u);
+  e = uniform64(e);
+  G* dst = dw + (int64_t)v * r.ld_dw;
+  const int64_t c = (int64_t)blockIdx.y * blockDim.x * kVec + threadIdx.x * kVec;
+  if (c + kVec <= r.dim) {
+    v8f sum = run_sum<v8f>(r, dy, s, e, c) * r.scale;
+    if (r.accumulate) sum += load8(dst + c);
+    store8(dst + c, sum);
+  } else {
+    for (int64_t k = c; k < r.dim; ++k) {
+      float sum = run_sum<float>(r, dy, s, e, k) * r.scale;
+      if (r.accumulate) sum += load1(dst + k);
+      store1(dst + k, sum);
     }
-    if (e > s || !r.accumulate) {
-      G* dst = dw + v * r.ld_dw;
-      for (int64_t c = c0 + lane * kVec; c < c1; c += kWaveCols) {
-        if (c + kVec <= c1) {
-          v8f sum = v8f{};
-          if (e > s) sum = run_sum<v8f>(r, dy, s, e, c) * r.scale;
-          if (r.accumulate) sum += load8(dst + c);
-          store8(dst + c, sum);
-        } else {
-          for (int64_t k = c; k < c1; ++k) {
-            float sum = e > s ? run_sum<float>(r, dy, s, e, k) * r.scale : 0.0f;
-            if (r.accumulate) sum += load1(dst + k);
-            store1(dst + k, sum);
-          }
-        }
-      }
-    }
-    s = e;
   }
 }
 
@@ -468,26 +515,28 @@ EmbedWs embed_ws(int64_t n, int64_t vocab, int64_t dim) {
 
 template <int STEPS>
 hipError_t sort_small(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint32_t* idx,
-                      hipStream_t s) {
+                      const Fill& fill, hipStream_t s) {
   const size_t lds = (kSortWaves * kBinsMax + kBinsMax + kSortWaves) * 4 + STEPS * kSortThreads * 6;
   // above the 64 KiB default of dynamic LDS
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_small<STEPS>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_sort_small<STEPS>, dim3(1), dim3(kSortThreads), lds, s, a, p.bits, p.passes,
-                     keys, idx);
+  const int blocks = fill.rows > 0 ? 1 + kFillBlocks : 1;
+  hipLaunchKernelGGL(k_sort_small<STEPS>, dim3(blocks), dim3(kSortThreads), lds, s, a, p.bits,
+                     p.passes, keys, idx, fill);
   return hipGetLastError();
 }
 
-hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, hipStream_t s) {
+hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const Fill& fill,
+                       hipStream_t s) {
   const SortPlan p = sort_plan(a.vocab);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   uint32_t* idx = reinterpret_cast<uint32_t*>(ws + w.idx);
   if (a.n <= kSmallSort) {
-    if (a.n <= 1 * kSortThreads) return sort_small<1>(a, p, keys, idx, s);
-    if (a.n <= 4 * kSortThreads) return sort_small<4>(a, p, keys, idx, s);
-    if (a.n <= 8 * kSortThreads) return sort_small<8>(a, p, keys, idx, s);
-    return sort_small<16>(a, p, keys, idx, s);
+    if (a.n <= 1 * kSortThreads) return sort_small<1>(a, p, keys, idx, fill, s);
+    if (a.n <= 4 * kSortThreads) return sort_small<4>(a, p, keys, idx, fill, s);
+    if (a.n <= 8 * kSortThreads) return sort_small<8>(a, p, keys, idx, fill, s);
+    return sort_small<16>(a, p, keys, idx, fill, s);
   }
   uint32_t* keys2 = reinterpret_cast<uint32_t*>(ws + w.keys2);
   uint32_t* idx2 = reinterpret_cast<uint32_t*>(ws + w.idx2);
@@ -496,8 +545,9 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, hipStr
   for (int q = 0; q < p.passes; ++q) {
     const bool to_first = (p.passes - 1 - q) % 2 == 0;   // the last pass ends in keys / idx
     SortPass sp{a, kin, iin, to_first ? keys : keys2, to_first ? idx : idx2, hist, w.tiles,
-                q * p.bits, p.bits};
-    hipLaunchKernelGGL(k_sort_count, dim3((uint32_t)w.tiles), dim3(kSortThreads), 0, s, sp);
+                q * p.bits, p.bits, fill};
+    const int64_t blocks = w.tiles + (q == 0 && fill.rows > 0 ? kFillBlocks : 0);
+    hipLaunchKernelGGL(k_sort_count, dim3((uint32_t)blocks), dim3(kSortThreads), 0, s, sp);
     hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(kSortThreads), 0, s, hist,
                        ((int64_t)1 << p.bits) * w.tiles);
     hipLaunchKernelGGL(k_sort_move, dim3((uint32_t)w.tiles), dim3(kSortThreads), 0, s, sp);
@@ -507,8 +557,6 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, hipStr
   return hipGetLastError();
 }
 
-constexpr int64_t kFillWaves = 16384;   // two rounds of 32 waves on each of 256 CUs
-
 template <class Y, class G>
 hipError_t embed_grad(const EmbedArgs& a, const Y* dy, int64_t ld_dy, G* dw, int64_t ld_dw,
                       bool accumulate, uint8_t* ws, hipStream_t s) {
@@ -516,24 +564,29 @@ hipError_t embed_grad(const EmbedArgs& a, const Y* dy, int64_t ld_dy, G* dw, int
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + w.keys);
   const uint32_t* idx = reinterpret_cast<const uint32_t*>(ws + w.idx);
   float* partial = reinterpret_cast<float*>(ws + w.partial);
-  const int64_t col_chunks = (a.dim + kWaveCols - 1) / kWaveCols;
-  if (a.n > 0) {
-    hipError_t e = sort_tokens(a, w, ws, s);
-    if (e != hipSuccess) return e;
-    if (a.n >= kWindow)
-      hipLaunchKernelGGL(k_embed_window<Y>, dim3((uint32_t)(a.n / kWindow), (uint32_t)col_chunks),
-                         dim3(64), 0, s, keys, idx, a.vocab, a.dim, dy, ld_dy, partial);
+  Fill fill{};
+  if (!accumulate) {
+    const bool flat = ld_dw == a.dim;
+    fill = Fill{reinterpret_cast<uint8_t*>(dw), flat ? 1 : a.vocab,
+                (flat ? a.vocab * a.dim : a.dim) * (int64_t)sizeof(G), ld_dw * (int64_t)sizeof(G)};
   }
-  RowArgs r{keys, idx, a.n, a.vocab, a.dim, ld_dy, ld_dw, partial, a.scale, 1, 0, accumulate};
-  int64_t per = a.vocab / kFillWaves;
-  r.rows_per = (int)(per < 1 ? 1 : per > 16 ? 16 : per);
-  const int64_t waves = (a.vocab + r.rows_per - 1) / r.rows_per;
-  int64_t cut = (kFillWaves + waves - 1) / waves;
-  if (cut > col_chunks) cut = col_chunks;
-  r.cols_per = (col_chunks + cut - 1) / cut * kWaveCols;
-  cut = (a.dim + r.cols_per - 1) / r.cols_per;
-  hipLaunchKernelGGL((k_embed_rows<Y, G>), dim3((uint32_t)waves, (uint32_t)cut), dim3(64), 0, s, r,
-                     dy, dw);
+  if (a.n == 0) {
+    if (!accumulate)
+      hipLaunchKernelGGL(k_fill, dim3(kFillBlocks), dim3(kFillThreads), 0, s, fill);
+    return hipGetLastError();
+  }
+  const hipError_t e = sort_tokens(a, w, ws, fill, s);
+  if (e != hipSuccess) return e;
+  if (a.n >= kWindow)
+    hipLaunchKernelGGL(k_embed_window<Y>,
+                       dim3((uint32_t)(a.n / kWindow),
+                            (uint32_t)((a.dim + kWaveCols - 1) / kWaveCols)),
+                       dim3(64), 0, s, keys, idx, a.vocab, a.dim, dy, ld_dy, partial);
+  const RowArgs r{keys, idx, a.n, a.vocab, a.dim, ld_dy, ld_dw, partial, a.scale, accumulate};
+  const int waves = a.dim > 3 * kWaveCols ? 4 : (int)((a.dim + kWaveCols - 1) / kWaveCols);
+  const int64_t cols = waves * kWaveCols;
+  hipLaunchKernelGGL((k_embed_runs<Y, G>), dim3((uint32_t)a.n, (uint32_t)((a.dim + cols - 1) / cols)),
+                     dim3(64 * waves), 0, s, r, dy, dw);
   return hipGetLastError();
 }
 

@@ -92,21 +92,75 @@ __device__ __forceinline__ int64_t target_of(const void* t, int type, int64_t i)
                                 : (int64_t) reinterpret_cast<const int32_t*>(t)[i];
 }
 
-// The target of a row (< 0: none).
-__device__ __forceinline__ int row_target(const CeArgs& g, int64_t row) {
-  if (g.tgt != nullptr) return g.tgt[row];
-  const int64_t t = target_of(g.targets, g.targets_type, row);
-  return t >= 0 && t < g.V ? (int)t : -1;
+// A row's target, loaded without waiting for it.
+struct Target {
+  uint32_t lo, hi;
+  __device__ __forceinline__ void load(const CeArgs& g, int64_t row) {
+    hi = 0;
+    if (g.tgt != nullptr) {
+      lo = (uint32_t)g.tgt[row];
+    } else if (g.targets_type == NVFP4_TYPE_I64) {
+      const v2u w = reinterpret_cast<const v2u*>(g.targets)[row];
+      lo = w.x;
+      hi = w.y;
+    } else {
+      lo = reinterpret_cast<const uint32_t*>(g.targets)[row];
+    }
+  }
+  __device__ __forceinline__ bool exists(const CeArgs& g) const {
+    return hi == 0 && lo < (uint32_t)g.V;
+  }
+  // Its place in the span of words from m0 on; outside 0 .. 127 where it has none there.
+  __device__ __forceinline__ int in_span(const CeArgs& g, int64_t m0) const {
+    return exists(g) ? (int)lo - (int)m0 : -1;
+  }
+};
+
+// Of a product's four quarters of loads: those due before block j of N.
+template <int N, class F>
+__device__ __forceinline__ void for_parts(int j, F f) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    if (p * N / 4 == j) f(p);
 }
 
-// Round `round` of workgroup blockIdx.x over `total` items; each XCD (workgroups
-// are dealt to the 8 in turn) owns a contiguous range.  False: no more.
-__device__ __forceinline__ bool next_item(int64_t total, int64_t round, int64_t& item) {
-  const int64_t per = (total + kXcds - 1) / kXcds;
-  const int64_t at = round * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-  item = (int64_t)(blockIdx.x % kXcds) * per + at;
-  return at < per && item < total;
-}
+// The tiles of a product, walked by a fixed grid.  Each XCD (workgroups are
+// dealt to the 8 in turn) owns a contiguous range of items; inside it tiles run
+// in groups of 8 tile columns m, m fastest, so that the 32 workgroups of an XCD
+// share 8 stretches of A and 4 of B in its L2 (81% of its reads hit).  `parts`
+// repeats all tiles, part by part.  Counts fit 32 bits: T * V and T * D are at
+// most 2^40, tiles 256 x 64 or larger.
+struct Walk {
+  uint32_t tm_all, tn_all, total, at, end, stride;
+  uint32_t tm, tn, part, item;
+
+  __device__ __forceinline__ Walk(int64_t tiles_m, int64_t tiles_n, int64_t parts) {
+    tm_all = uniform((int)tiles_m);
+    tn_all = uniform((int)tiles_n);
+    total = uniform((int)(tiles_m * tiles_n * parts));
+    const uint32_t per = (total + kXcds - 1) / kXcds, xcd = blockIdx.x % kXcds;
+    at = xcd * per + blockIdx.x / kXcds;
+    end = (xcd + 1) * per < total ? (xcd + 1) * per : total;
+    stride = gridDim.x / kXcds;
+  }
+  // The next tile; false: no more.
+  __device__ __forceinline__ bool next() {
+    if (at >= end) return false;
+    item = at;
+    at += stride;
+    locate(item);
+    return true;
+  }
+  __device__ __forceinline__ void locate(uint32_t i) {
+    const uint32_t tiles = tm_all * tn_all;
+    part = i / tiles;
+    i -= part * tiles;
+    const uint32_t group = i / (kGroupM * tn_all), first = group * kGroupM;
+    const uint32_t gm = min(tm_all - first, (uint32_t)kGroupM), in = i - first * tn_all;
+    tn = in / gm;
+    tm = first + in % gm;
+  }
+};
 
 template <int WN>
 __device__ __forceinline__ void clear(v16f (&acc)[kWM][WN]) {
@@ -114,15 +168,6 @@ __device__ __forceinline__ void clear(v16f (&acc)[kWM][WN]) {
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
     for (int j = 0; j < WN; ++j) acc[i][j] = v16f{};
-}
-
-// The lane number, opaque: epilogue addresses derived from it are formed where
-// they are used.  The compiler otherwise keeps them all across the tile loop,
-// spilled, since the products need every register.
-__device__ __forceinline__ int fresh_lane() {
-  int lane = threadIdx.x & 63;
-  asm volatile("" : "+v"(lane));
-  return lane;
 }
 
 // A wave's 32 n x 128 m half-words staged in its own 8 KiB of LDS, row n in 256
@@ -150,8 +195,8 @@ __device__ __forceinline__ void wave_lds_done() {
 // from m0 on); `left` words of the span exist (128 or more: WHOLE).
 template <int WN, bool KEEP, bool WHOLE>
 __device__ __forceinline__ void logits_block(const CeArgs& g, const v16f (&acc)[kWM][WN], int j,
-                                             int left, int64_t m0, int64_t row0, int64_t rows,
-                                             uint8_t* region) {
+                                             int left, int at, int64_t m0, int64_t row0,
+                                             int64_t rows, uint8_t* region) {
   const int lane = fresh_lane(), half = lane >> 5;
   const int64_t row = row0 + (lane & 31);
   // words past the vocabulary take no part
@@ -167,23 +212,23 @@ __device__ __forceinline__ void logits_block(const CeArgs& g, const v16f (&acc)[
   // the reference of the span: this binary32 value itself, so its rounding
   // costs nothing; 0 where every logit is -inf (all exponentials are 0)
   const float m2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2e;
-  float sum = 0.0f;
+  float part[4] = {};   // four chains: a single wave per SIMD hides no latency
 #pragma unroll
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v)
-      sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, v), kLog2e, -m2));
+      part[v & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, v), kLog2e, -m2));
+  float sum = (part[0] + part[1]) + (part[2] + part[3]);
   sum += __shfl_xor(sum, 32, 64);
   if (row < rows && half == 0) g.stats[row * g.spans + m0 / kSpan] = float2{m2, sum};
-  const int target = row < rows ? row_target(g, g.first + row) : -1;
-  const int at = target < 0 ? -1 : target - (int)m0;
   if (__ballot(at >= 0 && at < kSpan)) {
     float own = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWM; ++i)
 #pragma unroll
       for (int v = 0; v < 16; ++v) own = at == acc_m(i, v, half) ? acc[i][j][v] : own;
-    if (at >= 0 && at < kSpan && ((at >> 2) & 1) == half) g.tlogit[g.first + row] = own;
+    if (row < rows && at >= 0 && at < kSpan && ((at >> 2) & 1) == half)
+      g.tlogit[g.first + row] = own;
   }
   if (KEEP) {
     const float c0 = m2 / kCodeSpan;
@@ -200,55 +245,67 @@ __device__ __forceinline__ void logits_block(const CeArgs& g, const v16f (&acc)[
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(x[2], x[3]))});
       }
     wave_lds_done();
+    // rows past the end lie past num_records and are dropped
+    const int left_rows = (int)(rows - row0 < 32 ? rows - row0 : 32);
+    const __amdgpu_buffer_rsrc_t out =
+        rsrc(g.codes + row0 * g.ldc + m0, left_rows > 0 ? ((left_rows - 1) * (int)g.ldc + kSpan) * 2 : 0);
+    uint32_t off = (uint32_t)((lane >> 4) * (int)g.ldc * 2 + (lane & 15) * 16);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int r = 4 * p + (lane >> 4), c = lane & 15;
-      const v4u val = stage_get(region, lane, p);
-      if (row0 + r < rows)
-        *reinterpret_cast<v4u*>(g.codes + (row0 + r) * g.ldc + m0 + 8 * c) = val;
-    }
+    for (int p = 0; p < 8; ++p, off += 4 * (uint32_t)g.ldc * 2)
+      __builtin_amdgcn_raw_buffer_store_b128(stage_get(region, lane, p), out, off, 0, 0);
     wave_lds_done();
   }
 }
 
+// Every product kernel loads the next tile's first two stages under the epilogue
+// of this one, which has LDS of its own (all 160 KiB are in use): a quarter of the
+// loads before each block of rows, since issued together they stall the waves.
 template <int WN, bool KEEP>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
+  __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
   const int wave = uniform(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
+  uint8_t* region = epi + wave * 8192;
   const int64_t rows = piece_rows(g);
-  const int64_t tm_all = (g.V + kTM - 1) / kTM, tn_all = (rows + 64 * WN - 1) / (64 * WN);
-  int64_t item;
-  for (int64_t round = 0; next_item(tm_all * tn_all, round, item); ++round) {
-    int64_t tm, tn;
-    grouped(item, tm_all, tn_all, tm, tn);
-    tm = uniform((int)tm);
-    tn = uniform((int)tn);
-    Core<false, false, WN> core;
+  Walk t((g.V + kTM - 1) / kTM, (rows + 64 * WN - 1) / (64 * WN), 1);
+  Core<false, false, WN> core;
+  const auto begin = [&]() {
+    core.a.init(Operand{g.w, g.ldw, g.V}, (int64_t)t.tm * kTM, g.D, wave, wm * 128);
+    core.b.init(Operand{g.h + g.first * g.ldh, g.ldh, rows}, (int64_t)t.tn * 64 * WN, g.D, wave,
+                wn * 32 * WN);
+  };
+  const auto start = [&](int part) { core.start(a0, b0, a1, b1, wave, 0, part); };
+  bool more = t.next();
+  if (more) {
+    begin();
+    for_parts<1>(0, start);
+  }
+  while (more) {
+    const int64_t m0 = (int64_t)t.tm * kTM + wm * 128;   // the wave's span of words
+    const int64_t row0 = (int64_t)t.tn * 64 * WN + wn * 32 * WN;
     clear<WN>(core.acc);
-    core.a.init(Operand{g.w, g.ldw, g.V}, tm * kTM, g.D, wave, wm * 128);
-    core.b.init(Operand{g.h + g.first * g.ldh, g.ldh, rows}, tn * 64 * WN, g.D, wave, wn * 32 * WN);
     core.run(a0, b0, a1, b1, wave, 0, g.D);
-
-    const int64_t m0 = tm * kTM + wm * 128;   // the wave's span of words
-    const int64_t row0 = tn * 64 * WN + wn * 32 * WN;
-    uint8_t* region = a0 + wave * 8192;
-    if (m0 + kSpan <= g.V) {
+    // the rows' targets, on their way during the set-up of the next tile
+    Target target[WN];
 #pragma unroll
-      for (int j = 0; j < WN; ++j) {
-        __builtin_amdgcn_sched_barrier(0);   // one block of rows at a time: registers
-        logits_block<WN, KEEP, true>(g, core.acc, j, kSpan, m0, row0 + 32 * j, rows, region);
-      }
-    } else if (m0 < g.V) {
-#pragma unroll
-      for (int j = 0; j < WN; ++j) {
-        __builtin_amdgcn_sched_barrier(0);
-        logits_block<WN, KEEP, false>(g, core.acc, j, (int)(g.V - m0), m0, row0 + 32 * j, rows,
-                                      region);
-      }
+    for (int j = 0; j < WN; ++j) {
+      const int64_t row = row0 + 32 * j + (fresh_lane() & 31);
+      target[j].load(g, g.first + (row < rows ? row : rows - 1));
     }
-    // the next tile's loads write the region: every wave is past it
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    more = t.next();
+    if (more) begin();
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      __builtin_amdgcn_sched_barrier(0);   // one block of rows at a time: registers
+      if (more) for_parts<WN>(j, start);
+      const int at = target[j].in_span(g, m0);
+      if (m0 + kSpan <= g.V)
+        logits_block<WN, KEEP, true>(g, core.acc, j, kSpan, at, m0, row0 + 32 * j, rows, region);
+      else if (m0 < g.V)
+        logits_block<WN, KEEP, false>(g, core.acc, j, (int)(g.V - m0), at, m0, row0 + 32 * j, rows,
+                                      region);
+    }
   }
 }
 
@@ -274,8 +331,9 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   if (lane != 0) return;
   const int64_t row = g.first + r;
   const double lse = (double)mx * (1.0 / (double)kLog2e) + log((double)sum);
-  const int target = row_target(g, row);
-  const float loss = target >= 0 ? (float)(lse - (double)g.tlogit[row]) : 0.0f;
+  Target target;
+  target.load(g, row);
+  const float loss = target.exists(g) ? (float)(lse - (double)g.tlogit[row]) : 0.0f;
   const int64_t t = g.idx == nullptr ? row : g.idx[row];
   g.loss[t] = loss;
   if (g.lse != nullptr) g.lse[t] = (float)lse;
@@ -319,69 +377,80 @@ __global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
 }
 
 // ---------------------------------------------------------------- gradients
-// A tile of BF16 results, rows n (tile-relative n0 + ..) to out[row_of(n)], m
-// contiguous, through the wave's LDS region.
-template <int WN, class RowOf>
-__device__ __forceinline__ void store_tile(v16f (&acc)[kWM][WN], uint8_t* region, uint16_t* out,
-                                           int64_t ld, int64_t m0, int64_t m_end, int64_t n0,
-                                           int64_t n_end, float scale, RowOf row_of) {
+// Block column j of a wave's BF16 results, rows n0 .. n0 + 31 and columns m0 ..
+// m0 + 127, through the wave's LDS region: put(lane, p, value) takes 16 bytes of row
+// n0 + 4 p + lane / 16 at column m0 + 8 (lane % 16).
+template <int WN, class Put>
+__device__ __forceinline__ void store_block(const v16f (&acc)[kWM][WN], int j, uint8_t* region,
+                                            float scale, Put put) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+  const int lane = fresh_lane();
+  const uint32_t base = stage_base(lane);
 #pragma unroll
-  for (int j = 0; j < WN; ++j) {
-    __builtin_amdgcn_sched_barrier(0);
-    const int lane = fresh_lane();
-    const uint32_t base = stage_base(lane);
+  for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int i = 0; i < kWM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-        const f4 v = f4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                        acc[i][j][4 * q + 3]} * scale;
-        stage_put(region, base, i, q, __builtin_bit_cast(v2u, __builtin_convertvector(v, b4)));
-      }
-    wave_lds_done();
-    const int c = lane & 15;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int r = 4 * p + (lane >> 4);
-      const v4u val = stage_get(region, lane, p);
-      const int64_t n = n0 + j * 32 + r;
-      if (n < n_end && m0 + 8 * c < m_end)
-        *reinterpret_cast<v4u*>(out + row_of(n) * ld + m0 + 8 * c) = val;
+    for (int q = 0; q < 4; ++q) {
+      const f4 v = f4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                      acc[i][j][4 * q + 3]} * scale;
+      stage_put(region, base, i, q, __builtin_bit_cast(v2u, __builtin_convertvector(v, b4)));
     }
-    wave_lds_done();
-  }
+  wave_lds_done();
+#pragma unroll
+  for (int p = 0; p < 8; ++p) put(lane, p, stage_get(region, lane, p));
+  wave_lds_done();
+}
+
+// Rows one after the other in memory: rows past n_end and columns past m_end are
+// dropped by the descriptor and by an offset past it.
+template <int WN>
+__device__ __forceinline__ void store_rows(const v16f (&acc)[kWM][WN], int j, uint8_t* region,
+                                           float scale, uint16_t* out, int64_t ld, int64_t m0,
+                                           int64_t m_end, int64_t n0, int64_t n_end) {
+  const int rows = (int)(n_end - n0 < 32 ? n_end - n0 : 32), cols = (int)(m_end - m0);
+  const __amdgpu_buffer_rsrc_t buf =
+      rsrc(out + n0 * ld + m0, rows > 0 && cols > 0 ? ((rows - 1) * (int)ld + cols) * 2 : 0);
+  store_block<WN>(acc, j, region, scale, [&](int lane, int p, v4u val) {
+    const int c = (lane & 15) * 8;
+    const uint32_t off = (uint32_t)(((lane >> 4) + 4 * p) * (int)ld * 2 + c * 2);
+    __builtin_amdgcn_raw_buffer_store_b128(val, buf, off | (c < cols ? 0u : kDead), 0, 0);
+  });
+}
+
+// Rows in the places idx gives.
+template <int WN>
+__device__ __forceinline__ void store_rows_at(const v16f (&acc)[kWM][WN], int j, uint8_t* region,
+                                              float scale, uint16_t* out, int64_t ld, int64_t m0,
+                                              int64_t m_end, int64_t n0, int64_t n_end,
+                                              const int32_t* idx) {
+  store_block<WN>(acc, j, region, scale, [&](int lane, int p, v4u val) {
+    const int64_t n = n0 + 4 * p + (lane >> 4), m = m0 + 8 * (lane & 15);
+    if (n < n_end && m < m_end) *reinterpret_cast<v4u*>(out + (int64_t)idx[n] * ld + m) = val;
+  });
 }
 
 // A wave's accumulators in accumulator order: 16-byte pieces, 1 KiB per
 // instruction.
 template <int WN>
-__device__ __forceinline__ void put_acc(v16f (&acc)[kWM][WN], float* p) {
-  v4f* at = reinterpret_cast<v4f*>(p) + (threadIdx.x & 63);
+__device__ __forceinline__ void put_acc(const v16f (&acc)[kWM][WN], int j, float* p) {
+  v4f* at = reinterpret_cast<v4f*>(p) + fresh_lane();
 #pragma unroll
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int j = 0; j < WN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        at[((i * WN + j) * 4 + q) * 64] = v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                                              acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    for (int q = 0; q < 4; ++q)
+      at[((i * WN + j) * 4 + q) * 64] = v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                            acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
 }
 template <int WN>
-__device__ __forceinline__ void add_acc(v16f (&acc)[kWM][WN], const float* p) {
-  const v4f* at = reinterpret_cast<const v4f*>(p) + (threadIdx.x & 63);
+__device__ __forceinline__ void add_acc(v16f (&acc)[kWM][WN], int j, const float* p) {
+  const v4f* at = reinterpret_cast<const v4f*>(p) + fresh_lane();
 #pragma unroll
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int j = 0; j < WN; ++j) {
-      __builtin_amdgcn_sched_barrier(0);   // 16 values in flight: registers
+    for (int q = 0; q < 4; ++q) {
+      const v4f v = at[((i * WN + j) * 4 + q) * 64];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f v = at[((i * WN + j) * 4 + q) * 64];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-      }
+      for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
     }
 }
 constexpr int64_t wave_floats(int wn) { return (int64_t)kWM * wn * 16 * 64; }
@@ -390,34 +459,47 @@ constexpr int64_t wave_floats(int wn) { return (int64_t)kWM * wn * 16 * 64; }
 template <int WN>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
+  __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
   const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
   const int64_t rows = piece_rows(g);
-  const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
-  const int64_t tiles = tm_all * tn_all, split = g.meta->split;
+  const int split = uniform(g.meta->split);
+  const float scale = g.meta->scale;
   const int64_t steps = g.wide / kBK, per = (steps + split - 1) / split;
-  int64_t item;
-  for (int64_t round = 0; next_item(tiles * split, round, item); ++round) {
-    const int64_t part = item / tiles;
-    int64_t tm, tn;
-    grouped(item - part * tiles, tm_all, tn_all, tm, tn);
-    tm = uniform((int)tm);
-    tn = uniform((int)tn);
-    const int64_t s0 = part * per, s1 = s0 + per < steps ? s0 + per : steps;
-    // W's rows end at V: words past it are zero codes in d and read zero in W
-    const int64_t k_end = s1 * kBK;
-    Core<true, false, WN> core;
+  Walk t(g.tiles_dh_m, (rows + 64 * WN - 1) / (64 * WN), split);
+  Core<true, false, WN> core;
+  int64_t s0 = 0, k_end = 0;
+  const auto begin = [&]() {
+    s0 = t.part * per;
+    k_end = (s0 + per < steps ? s0 + per : steps) * kBK;
+    // W's rows end at V: words past it are zeros in d and read zero in W
+    core.a.init(Operand{g.w, g.ldw, g.D}, (int64_t)t.tm * kTM, k_end < g.V ? k_end : g.V, wave,
+                wm * 128);
+    core.b.init(Operand{g.codes, g.ldc, rows}, (int64_t)t.tn * 64 * WN, k_end, wave, wn * 32 * WN);
+  };
+  const auto start = [&](int part) { core.start(a0, b0, a1, b1, wave, s0, part); };
+  bool more = t.next();
+  if (more) {
+    begin();
+    for_parts<1>(0, start);
+  }
+  while (more) {
+    const int64_t m0 = (int64_t)t.tm * kTM + wm * 128;
+    const int64_t n0 = (int64_t)t.tn * 64 * WN + wn * 32 * WN;
+    float* part = g.part + ((int64_t)t.item * 4 + wave) * wave_floats(WN);
     clear<WN>(core.acc);
-    core.a.init(Operand{g.w, g.ldw, g.D}, tm * kTM, k_end < g.V ? k_end : g.V, wave, wm * 128);
-    core.b.init(Operand{g.codes, g.ldc, rows}, tn * 64 * WN, k_end, wave, wn * 32 * WN);
     core.run(a0, b0, a1, b1, wave, s0, k_end);
-    if (split > 1) {
-      put_acc<WN>(core.acc, g.part + (item * 4 + wave) * wave_floats(WN));
-    } else {
-      store_tile<WN>(core.acc, a0 + wave * 8192, g.dh, g.ld_dh, tm * kTM + wm * 128, g.D,
-                     tn * 64 * WN + wn * 32 * WN, rows, g.meta->scale,
-                     [&](int64_t n) { return (int64_t)g.idx[g.first + n]; });
+    more = t.next();
+    if (more) begin();
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) for_parts<WN>(j, start);
+      if (split > 1)
+        put_acc<WN>(core.acc, j, part);
+      else
+        store_rows_at<WN>(core.acc, j, epi + wave * 8192, scale, g.dh, g.ld_dh, m0, g.D,
+                          n0 + 32 * j, rows, g.idx + g.first);
     }
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 }
 
@@ -428,10 +510,11 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(CeArgs g) {
   const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int64_t rows = piece_rows(g);
-  const int64_t tm_all = g.tiles_dh_m, tn_all = (rows + 64 * WN - 1) / (64 * WN);
-  const int64_t tiles = tm_all * tn_all, split = g.meta->split;
+  const int64_t split = g.meta->split;
   if (split == 1) return;
   const float scale = g.meta->scale;
+  Walk t(g.tiles_dh_m, (rows + 64 * WN - 1) / (64 * WN), 1);
+  const int64_t tiles = t.total;
   for (int64_t u = blockIdx.x; u < tiles * kWM * WN; u += gridDim.x) {
     const int64_t tile = u / (kWM * WN);
     const int block = (int)(u % (kWM * WN)), i = block / WN, j = block % WN;
@@ -443,15 +526,14 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(CeArgs g) {
     for (int64_t s = 0; s < split; ++s)
 #pragma unroll
       for (int q = 0; q < 4; ++q) sum[q] += at[s * pitch + q * 64];
-    int64_t tm, tn;
-    grouped(tile, tm_all, tn_all, tm, tn);
-    const int64_t n = tn * 64 * WN + wn * 32 * WN + 32 * j + (lane & 31);
+    t.locate((uint32_t)tile);
+    const int64_t n = (int64_t)t.tn * 64 * WN + wn * 32 * WN + 32 * j + (lane & 31);
     if (n >= rows) continue;
     uint16_t* out = g.dh + (int64_t)g.idx[g.first + n] * g.ld_dh;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-      const int64_t m = tm * kTM + wm * 128 + 32 * i + 8 * q + 4 * half;
+      const int64_t m = (int64_t)t.tm * kTM + wm * 128 + 32 * i + 8 * q + 4 * half;
       if (m < g.D)
         *reinterpret_cast<v2u*>(out + m) =
             __builtin_bit_cast(v2u, __builtin_convertvector(sum[q] * scale, b4));
@@ -465,29 +547,42 @@ template <bool PIECES>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
   constexpr int WN = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
+  __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
   const int wave = uniform(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
   const int64_t rows = piece_rows(g);
   if (PIECES && rows == 0 && g.add && !g.finish) return;   // an empty piece in the middle
-  const int64_t tm_all = (g.D + kTM - 1) / kTM, tn_all = (g.V + 255) / 256;
-  int64_t item;
-  for (int64_t round = 0; next_item(tm_all * tn_all, round, item); ++round) {
-    int64_t tm, tn;
-    grouped(item, tm_all, tn_all, tm, tn);
-    tm = uniform((int)tm);
-    tn = uniform((int)tn);
-    Core<true, true, WN> core;
+  const float scale = g.meta->scale;
+  Walk t((g.D + kTM - 1) / kTM, (g.V + 255) / 256, 1);
+  Core<true, true, WN> core;
+  const auto begin = [&]() {
+    core.a.init(Operand{g.h + g.first * g.ldh, g.ldh, g.D}, (int64_t)t.tm * kTM, rows, wave,
+                wm * 128);
+    core.b.init(Operand{g.codes, g.ldc, g.wide}, (int64_t)t.tn * 256, rows, wave, wn * 128);
+  };
+  const auto start = [&](int part) { core.start(a0, b0, a1, b1, wave, 0, part); };
+  bool more = t.next();
+  if (more) {
+    begin();
+    for_parts<1>(0, start);
+  }
+  while (more) {
+    const int64_t m0 = (int64_t)t.tm * kTM + wm * 128, n0 = (int64_t)t.tn * 256 + wn * 128;
+    float* acc_at = g.dw_acc + (((int64_t)t.tn * t.tm_all + t.tm) * 4 + wave) * wave_floats(WN);
     clear<WN>(core.acc);
-    core.a.init(Operand{g.h + g.first * g.ldh, g.ldh, g.D}, tm * kTM, rows, wave, wm * 128);
-    core.b.init(Operand{g.codes, g.ldc, g.wide}, tn * 256, rows, wave, wn * 128);
     core.run(a0, b0, a1, b1, wave, 0, rows);
-    float* acc_at = g.dw_acc + ((tn * tm_all + tm) * 4 + wave) * wave_floats(WN);
-    if (PIECES && g.add) add_acc<WN>(core.acc, acc_at);
-    if (!PIECES || g.finish)
-      store_tile<WN>(core.acc, a0 + wave * 8192, g.dw, g.ld_dw, tm * kTM + wm * 128, g.D,
-                     tn * 256 + wn * 128, g.V, g.meta->scale, [](int64_t n) { return n; });
-    else
-      put_acc<WN>(core.acc, acc_at);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    more = t.next();
+    if (more) begin();
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) for_parts<WN>(j, start);
+      if (PIECES && g.add) add_acc<WN>(core.acc, j, acc_at);
+      if (!PIECES || g.finish)
+        store_rows<WN>(core.acc, j, epi + wave * 8192, scale, g.dw, g.ld_dw, m0, g.D, n0 + 32 * j,
+                       g.V);
+      else
+        put_acc<WN>(core.acc, j, acc_at);
+    }
   }
 }
 
@@ -513,35 +608,49 @@ constexpr int kPrepThreads = 1024;
 // loss is 0.  Then the dH product's cut: the number of equal parts that lets
 // the compute units finish earliest, counting a fixed cost per part.
 __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
-  __shared__ uint32_t wave_sum[kPrepThreads / 64];
+  __shared__ uint32_t wave_count[kPrepThreads / 64];
   __shared__ unsigned long long best;
   __shared__ uint32_t top;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t n = 0;
   uint32_t most = 0;   // bits of the largest |weight|
-  for (int64_t t0 = 0; t0 < p.T; t0 += kPrepThreads) {
-    const int64_t t = t0 + threadIdx.x;
-    int64_t target = -1;
-    if (t < p.T) target = target_of(p.targets, p.targets_type, t);
-    const bool live = target >= 0 && target < p.V;
-    const uint64_t m = __ballot(live);
-    if (lane == 0) wave_sum[wave] = (uint32_t)__popcll(m);
+  for (int64_t t0 = 0; t0 < p.T; t0 += 8 * kPrepThreads) {
+    // this thread's 8 consecutive tokens
+    const int64_t t = t0 + 8 * threadIdx.x;
+    int64_t target[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      target[i] = t + i < p.T ? target_of(p.targets, p.targets_type, t + i) : -1;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += target[i] >= 0 && target[i] < p.V;
+    uint32_t upto = mine;   // with the wave's lanes before
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)upto, off, 64);
+      if (lane >= off) upto += o;
+    }
+    if (lane == 63) wave_count[wave] = upto;
     __syncthreads();
-    int64_t at = n + __popcll(m & ((1ull << lane) - 1ull));
+    int64_t at = n + upto - mine;
 #pragma unroll
     for (int w = 0; w < kPrepThreads / 64; ++w) {
-      at += w < wave ? wave_sum[w] : 0u;
-      n += wave_sum[w];
+      at += w < wave ? wave_count[w] : 0u;
+      n += wave_count[w];
     }
     __syncthreads();
-    if (live) {
-      p.idx[at] = (int32_t)t;
-      p.tgt[at] = (int32_t)target;
-      if (p.row_weight != nullptr)
-        most = max(most, __float_as_uint(p.row_weight[t]) & 0x7FFFFFFFu);
-    } else if (t < p.T) {
-      p.loss[t] = 0.0f;
-      if (p.lse != nullptr) p.lse[t] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (target[i] >= 0 && target[i] < p.V) {
+        p.idx[at] = (int32_t)(t + i);
+        p.tgt[at] = (int32_t)target[i];
+        if (p.row_weight != nullptr)
+          most = max(most, __float_as_uint(p.row_weight[t + i]) & 0x7FFFFFFFu);
+        ++at;
+      } else if (t + i < p.T) {
+        p.loss[t + i] = 0.0f;
+        if (p.lse != nullptr) p.lse[t + i] = 0.0f;
+      }
     }
   }
   if (threadIdx.x == 0) {
@@ -558,12 +667,12 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
   for (int64_t i = threadIdx.x; i < n; i += kPrepThreads)
     p.weight[i] = p.row_weight == nullptr ? 1.0f : p.row_weight[p.idx[i]] / scale;
   const int64_t rows = n < p.piece ? n : p.piece;
-  const int64_t tiles = p.tiles_m * ((rows + p.rows_per_tile - 1) / p.rows_per_tile);
-  const int64_t s = threadIdx.x + 1;
-  if (s == 1 || (s * tiles <= p.max_items && p.steps / s >= 8)) {
-    const int64_t rounds = (s * tiles + p.cus - 1) / p.cus;
-    const int64_t cost = rounds * ((p.steps + s - 1) / s + 8);
-    atomicMin(&best, (unsigned long long)cost << 16 | (unsigned long long)s);
+  const uint32_t tiles = (uint32_t)p.tiles_m * (uint32_t)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
+  const uint32_t s = threadIdx.x + 1, steps = (uint32_t)p.steps, cus = (uint32_t)p.cus;
+  if (s == 1 || ((uint64_t)s * tiles <= (uint64_t)p.max_items && s * 8 <= steps)) {
+    const uint32_t rounds = (s * tiles + cus - 1) / cus;
+    const uint64_t cost = (uint64_t)rounds * ((steps + s - 1) / s + 8);
+    atomicMin(&best, (unsigned long long)(cost << 16 | s));
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -605,8 +714,24 @@ int64_t odd_pitch(int64_t cols) {
   return (pieces + (pieces % 2 == 0)) * 128;
 }
 
-// Width of a tile of tokens: the narrowest that holds them all, at most 256.
-int tokens_wn(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
+// Width of the tiles of tokens, 64, 128 or 256 (WN 1, 2, 4): a narrower tile wastes
+// less of a last one and of a last round of workgroups, but reads the words' side
+// as often.  A round of the logits kernel takes 0.39 : 0.57 : 1 of the wide tile's
+// (D = 2048; 0.36 : 0.58 : 1 at 512, 0.41 : 0.58 : 1 at 5120); the fewest rounds so
+// weighed win.  333 tokens x 50257 words x 2048: 121, 104 and 109 us.
+int tokens_wn(int64_t rows, int64_t tiles_m, int cus) {
+  int best = 4;
+  int64_t least = INT64_MAX;
+  for (const int wn : {4, 2, 1}) {
+    const int64_t tiles = tiles_m * ((rows + 64 * wn - 1) / (64 * wn));
+    const int64_t cost = (tiles + cus - 1) / cus * (wn == 4 ? 100 : wn == 2 ? 57 : 39);
+    if (cost < least) {
+      least = cost;
+      best = wn;
+    }
+  }
+  return best;
+}
 
 struct CePlan {
   int64_t piece, pieces, spans, ldc, ldhc, max_items;
@@ -631,7 +756,7 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
     if (piece < T) p.piece = piece;
   }
   p.pieces = p.piece > 0 ? (T + p.piece - 1) / p.piece : 1;
-  p.wn = tokens_wn(p.piece);
+  p.wn = tokens_wn(p.piece, (V + kTM - 1) / kTM, num_cus());
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t o = at;

@@ -89,7 +89,7 @@ struct Loader<false, ROWS> {
 
   __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k_total, int wave,
                                        int frag_row0) {
-    const int lane = threadIdx.x & 63;
+    const int lane = fresh_lane();
     const int64_t rem = o.rows - row0;
     const int64_t last = rem < ROWS ? rem - 1 : ROWS - 1;   // below 2^31 bytes (pitch < 2^22)
     buf = rsrc(o.p + row0 * o.ld, rem > 0 ? (int)((last * o.ld + k_total) * 2) : 0);
@@ -137,7 +137,7 @@ struct Loader<true, ROWS> {
 
   __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k_total, int wave,
                                        int frag_row0) {
-    const int lane = threadIdx.x & 63;
+    const int lane = fresh_lane();
     base = o.p + row0;
     ld = o.ld;
     pitch = (int)(o.ld * 2);
@@ -211,12 +211,6 @@ struct Core {
 #pragma unroll
     for (int q = 0; q < LB::kLoads; ++q) b.load(sb, wave, q, k0);
   }
-  __device__ __forceinline__ void load_all(uint8_t* sa, uint8_t* sb, int wave, int64_t k0) {
-    a.step(k0);
-    b.step(k0);
-    load_a(sa, wave, k0);
-    load_b(sb, wave, k0);
-  }
 
   // The order of a phase: after each MFMA its share of LDS reads (0x100) and of
   // loads to LDS (0x010).
@@ -267,15 +261,24 @@ struct Core {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // Quarter `part` of the loads of steps s0 and s0 + 1 (all four before run()).
+  // The stages must be free.
+  __device__ __forceinline__ void start(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
+                                        int64_t s0, int part) {
+    const int64_t k0 = s0 * kBK, k1 = k0 + kBK;
+    if (part == 0) a.step(k0), load_a(a0, wave, k0);
+    if (part == 1) b.step(k0), load_b(b0, wave, k0);
+    if (part == 2) a.step(k1), load_a(a1, wave, k1);
+    if (part == 3) b.step(k1), load_b(b1, wave, k1);
+  }
+
   // acc += the products of k in [64 s0, k_end), k_end the end that both
-  // operands were set up with.  Steps past it load nothing and read as zero, so
-  // the loop runs whole pairs without a branch.  Ends with every wave past its
-  // last LDS access.
+  // operands were set up with, after start(s0, 0 .. 3).  Steps past it load nothing and
+  // read as zero, so the loop runs whole pairs without a branch.  Ends with the
+  // stages free.
   __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
                                       int64_t s0, int64_t k_end) {
-    load_all(a0, b0, wave, s0 * kBK);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    load_all(a1, b1, wave, (s0 + 1) * kBK);
     Frags<WN> f[4];
     read(f[0], a0, b0, 0);
     for (int64_t s = s0; s * kBK < k_end; s += 2) {

@@ -43,7 +43,7 @@ EXPORTED = ("nvfp4_amax", "nvfp4_amax_rht", "nvfp4_quantize1d_rtn", "nvfp4_quant
             "nvfp4_quantize_row_rht", "nvfp4_amax_rht1d", "nvfp4_rht_quantize1d",
             "nvfp4_probe_clock", "nvfp4_probe_clock_bytes", "nvfp4_probe_copy",
             "nvfp4_embed", "nvfp4_embed_grad", "nvfp4_embed_grad_workspace_bytes",
-            "nvfp4_grad_sumsq", "nvfp4_grad_clip", "nvfp4_linear_ce", "nvfp4_linear_ce_grad",
+            "nvfp4_grad_sumsq", "nvfp4_grad_clip", "nvfp4_grad_scale", "nvfp4_linear_ce", "nvfp4_linear_ce_grad",
             "nvfp4_linear_ce_workspace_bytes")
 
 
@@ -122,6 +122,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                  vp, i64, vp, i64, vp],
         "nvfp4_grad_sumsq": [vp, i64, vp, vp],
         "nvfp4_grad_clip": [vp, i64, vp, ctypes.c_double, vp, vp],
+        "nvfp4_grad_scale": [vp, i64, vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -722,6 +723,12 @@ def nvfp4_grad_clip(grads, outs, partials, max_norm, norm_out, stream=None):
                                           _stream(stream)))
 
 
+def nvfp4_grad_scale(grads, outs, factor, stream=None):
+    lst, n = _grad_list(grads, outs)
+    _dev_f32(factor, 1, "factor")
+    _check(load_library().nvfp4_grad_scale(lst, n, _p(factor), _stream(stream)))
+
+
 def _dev_partials(partials):
     if (not partials.is_cuda or partials.dtype != torch.float64 or not partials.is_contiguous()
             or partials.numel() != NVFP4_SUMSQ_WORDS):
@@ -760,6 +767,15 @@ def clip_grads(grads, max_norm: float, out=None, partials: Optional[torch.Tensor
     _dev_partials(partials)
     _check(lib.nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm), s))
     return norm
+
+
+def scale_grads(grads, factor: torch.Tensor):
+    """New tensors factor * gradient, factor one float32 value on the GPU; each
+    product is rounded from FP32 once."""
+    grads = list(grads)
+    outs = [_empty(*g.shape, dtype=g.dtype, device=g.device) for g in grads]
+    nvfp4_grad_scale(grads, outs, factor)
+    return outs
 
 
 PROBE_ZEROS, PROBE_NVFP4_LIKE, PROBE_UNIFORM = 0, 1, 2

@@ -272,4 +272,12 @@ int nvfp4_grad_clip(const nvfp4_grad* list, int64_t count, const double* partial
                                           as_stream(stream)));
 }
 
+int nvfp4_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor, void* stream) {
+  int st = check_grads(list, count, true);
+  if (st) return st;
+  if (factor == nullptr) return fail(NVFP4_ERR_NULL, "factor is NULL");
+  if (!aligned(factor, 4)) return fail(NVFP4_ERR_ALIGN, "factor must be 4-byte aligned");
+  return launched(nvfp4::launch_grad_scale(list, count, factor, as_stream(stream)));
+}
+
 }  // extern "C"

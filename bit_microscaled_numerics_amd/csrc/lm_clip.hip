@@ -119,16 +119,8 @@ __device__ __forceinline__ void chunk_scale(const T* x, O* out, int64_t i0, int6
   }
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_clip(Table t, const double* __restrict__ partials,
-                                                        double max_norm, float* norm_out) {
-  __shared__ double scratch[kThreads / 64];
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < kWords / kThreads; ++i) s += partials[i * kThreads + threadIdx.x];
-  const double norm = __builtin_sqrt(block_sum(s, scratch));
-  const double ratio = max_norm / (norm + 1e-6);
-  const float coef = ratio > 1.0 ? 1.0f : (float)ratio;   // a NaN norm stays NaN
-  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+// out = coef * in over the whole table.
+__device__ __forceinline__ void scale_table(const Table& t, float coef) {
   int k = 0;
   for (uint32_t c = blockIdx.x; c < t.first_chunk[t.count]; c += gridDim.x) {
     while (c >= t.first_chunk[k + 1]) ++k;
@@ -147,6 +139,23 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(Table t, const double* _
       default: chunk_scale(xf, of, i0, i1, coef); break;
     }
   }
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_clip(Table t, const double* __restrict__ partials,
+                                                        double max_norm, float* norm_out) {
+  __shared__ double scratch[kThreads / 64];
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kWords / kThreads; ++i) s += partials[i * kThreads + threadIdx.x];
+  const double norm = __builtin_sqrt(block_sum(s, scratch));
+  const double ratio = max_norm / (norm + 1e-6);
+  const float coef = ratio > 1.0 ? 1.0f : (float)ratio;   // a NaN norm stays NaN
+  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  scale_table(t, coef);
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_scale(Table t, const float* __restrict__ factor) {
+  scale_table(t, *factor);
 }
 
 // The next batch of the list from `at` on: at most kBatch tensors and a chunk
@@ -199,6 +208,16 @@ hipError_t launch_grad_clip(const nvfp4_grad* list, int64_t count, const double*
                        norm_out);
     norm_out = nullptr;
   } while (at < count);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor,
+                             hipStream_t s) {
+  Table t;
+  for (int64_t at = 0; at < count;) {
+    at = next_batch(list, count, at, t);
+    hipLaunchKernelGGL(k_grad_scale, dim3(kWords), dim3(kThreads), 0, s, t, factor);
+  }
   return hipGetLastError();
 }
 

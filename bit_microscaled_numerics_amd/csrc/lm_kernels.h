@@ -32,6 +32,9 @@ hipError_t launch_grad_sumsq(const nvfp4_grad* list, int64_t count, double* part
 hipError_t launch_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials,
                             double max_norm, float* norm_out, hipStream_t s);
 
+hipError_t launch_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor,
+                             hipStream_t s);
+
 // Softmax cross entropy of a head: loss (and lse) of every token; grad: dh and
 // dw as well.  piece: tokens per piece of the gradient (0: chosen here).
 struct CeCall {

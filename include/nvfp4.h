@@ -381,7 +381,7 @@ int64_t nvfp4_linear_ce_workspace_bytes(int64_t T, int64_t V, int64_t D, int gra
  * may equal in (in place, same type); other overlaps race. */
 typedef struct {
   const void* in;
-  void* out;           /* nvfp4_grad_clip only */
+  void* out;           /* nvfp4_grad_clip and nvfp4_grad_scale */
   int64_t numel;       /* may be 0 */
   int32_t in_type, out_type;   /* NVFP4_TYPE_BF16 or NVFP4_TYPE_F32 */
 } nvfp4_grad;
@@ -400,6 +400,11 @@ int nvfp4_grad_sumsq(const nvfp4_grad* list, int64_t count, double* partials, vo
  * is written. */
 int nvfp4_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials, double max_norm,
                     float* norm_out, void* stream);
+
+/* out = in * *factor (device memory) for every tensor of the list, the product
+ * rounded to FP32 and to out's type: the chain rule's factor on gradients that
+ * were formed with the loss.  In place with a factor of 1 nothing is written. */
+int nvfp4_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor, void* stream);
 
 /* ------------------------------------------------------------------------
  * Measurement support (not part of the quantize / GEMM path): the sustained

@@ -152,3 +152,23 @@ def test_on_another_stream():
         norm = nv.clip_grads(dev, 1.0)
     side.synchronize()
     _check(norm, dev, grads, 1.0)
+
+
+@pytest.mark.parametrize("dt,ot", [(BF, BF), (F, BF), (BF, F), (F, F)])
+@pytest.mark.parametrize("factor", [1.0, 1.0 / 3, -2.5, 0.0])
+def test_scale(dt, ot, factor):
+    """out = in * factor, the factor in binary32 (not rounded to the gradients' type)."""
+    say("scale", dt, ot, factor)
+    grads = _grads(9, [1003, 0, 7, 40000], (dt,))
+    dev = [g.cuda() for g in grads]
+    outs = [torch.full(g.shape, 9.0, dtype=ot, device="cuda") for g in grads]
+    f = torch.tensor([factor], dtype=torch.float32, device="cuda")
+    nv.nvfp4_grad_scale(dev, outs, f)
+    for o, g in zip(outs, grads):
+        r = g.double() * f.double().item()
+        assert torch.all((o.cpu().double() - r).abs() <= r.abs() * (U32 + HALF[ot] * (1 + U32)))
+    if dt == ot:
+        new = nv.scale_grads(dev, f)
+        assert all(torch.equal(a, b) for a, b in zip(new, outs))
+        nv.nvfp4_grad_scale(dev, dev, f)
+        assert all(torch.equal(a, b) for a, b in zip(dev, outs))

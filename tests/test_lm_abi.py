@@ -99,6 +99,14 @@ def test_clip_argument_validation(lib):
     assert lib.nvfp4_grad_sumsq(None, 1, FAKE, None) == nv.NVFP4_ERR_NULL
 
 
+def test_scale_argument_validation(lib):
+    lst = ctypes.cast(_grads((FAKE, FAKE, 4, F, F)), ctypes.c_void_p)
+    assert lib.nvfp4_grad_scale(lst, 1, None, None) == nv.NVFP4_ERR_NULL
+    assert lib.nvfp4_grad_scale(lst, 1, FAKE + 2, None) == nv.NVFP4_ERR_ALIGN
+    assert lib.nvfp4_grad_scale(lst, -1, FAKE, None) == nv.NVFP4_ERR_SHAPE
+    assert lib.nvfp4_grad_scale(None, 1, FAKE, None) == nv.NVFP4_ERR_NULL
+
+
 def test_binding_refuses():
     ids = torch.zeros(4, dtype=torch.int64)
     w = torch.zeros(8, 16, dtype=torch.bfloat16)

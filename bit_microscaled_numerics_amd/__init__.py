@@ -590,10 +590,16 @@ def embed(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
           dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """scale * w[ids] as [number of ids][columns] of dtype (w's if None).  An
     id outside 0 .. rows-1 gives a row of zeros."""
-    _dev_matrix(w, "w")
-    out = _empty(ids.numel(), w.shape[1], dtype=w.dtype if dtype is None else dtype,
-                 device=w.device)
-    nvfp4_embed(ids, w, scale, out)
+    it, wt = _dev_ids(ids, "ids"), _dev_matrix(w, "w")
+    ot = wt if dtype is None else _FLOATS.get(dtype)
+    if ot is None:
+        raise ValueError("dtype must be bf16 or float32")
+    n, (vocab, dim) = ids.numel(), w.shape
+    out = _empty(n, dim, dtype=w.dtype if dtype is None else dtype, device=w.device)
+    # its own call of the entry point: a single token's lookup is bound by the host
+    _check(load_library().nvfp4_embed(ids.data_ptr(), it, n, w.data_ptr(), wt, vocab, dim,
+                                      _pitch(w, "w"), scale, out.data_ptr(), ot, dim,
+                                      _stream(None)))
     return out
 
 
@@ -698,15 +704,23 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
 
 
 def _grad_list(grads, outs):
-    """The nvfp4_grad array of a list of gradients (and outputs)."""
-    words = []
+    """The nvfp4_grad array of a list of gradients (and outputs), and its length."""
+    words, types = [], _FLOATS
     for g, o in zip(grads, outs):
-        gt, ot = _FLOATS.get(g.dtype), _FLOATS.get(o.dtype)
-        if gt is None or ot is None or not g.is_cuda or not o.is_cuda:
+        gt = types.get(g.dtype)
+        if gt is None or not g.is_cuda:
             raise ValueError("gradients must be bf16 or float32 CUDA tensors")
-        if not g.is_contiguous() or not o.is_contiguous() or o.shape != g.shape:
-            raise ValueError("gradients and outputs must be contiguous and of equal shapes")
-        words += (g.data_ptr(), o.data_ptr(), g.numel(), gt | ot << 32)
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        at = g.data_ptr()
+        if o is g:
+            words += (at, at, g.numel(), gt | gt << 32)
+            continue
+        ot = types.get(o.dtype)
+        if ot is None or not o.is_cuda or not o.is_contiguous() or o.shape != g.shape:
+            raise ValueError("outputs must be contiguous bf16 or float32 CUDA tensors of their "
+                             "gradients' shapes")
+        words += (at, o.data_ptr(), g.numel(), gt | ot << 32)
     return struct.pack(f"{len(words)}q", *words), len(words) // 4
 
 

@@ -21,6 +21,18 @@ namespace nvfp4 {
 
 namespace {
 
+// The results are not read again here: stored without a place in the 256 MB cache,
+// they leave it to the gradients, and their writes do not trail into the next pass.
+__device__ __forceinline__ void store8_once(bf16_t* p, v8f v) {
+  __builtin_nontemporal_store((v4u_any2)pack8(v), reinterpret_cast<v4u_any2*>(p));
+}
+__device__ __forceinline__ void store8_once(float* p, v8f v) {
+  const v4u lo = __builtin_bit_cast(v4u, __builtin_shufflevector(v, v, 0, 1, 2, 3));
+  const v4u hi = __builtin_bit_cast(v4u, __builtin_shufflevector(v, v, 4, 5, 6, 7));
+  __builtin_nontemporal_store((v4u_any4)lo, reinterpret_cast<v4u_any4*>(p));
+  __builtin_nontemporal_store((v4u_any4)hi, reinterpret_cast<v4u_any4*>(p + 4));
+}
+
 constexpr int kThreads = 256;
 constexpr int kWords = NVFP4_SUMSQ_WORDS;     // = workgroups of a launch
 constexpr int kVecs = 8;                      // 16-byte vectors per thread and chunk
@@ -107,7 +119,7 @@ __device__ __forceinline__ void chunk_scale(const T* x, O* out, int64_t i0, int6
 #pragma unroll
     for (int u = 0; u < kPer; ++u) v[u] = load8(x + i0 + 8 * (u * kThreads + threadIdx.x));
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) store8(out + i0 + 8 * (u * kThreads + threadIdx.x), v[u] * c);
+    for (int u = 0; u < kPer; ++u) store8_once(out + i0 + 8 * (u * kThreads + threadIdx.x), v[u] * c);
     return;
   }
   for (int64_t i = i0 + 8 * threadIdx.x; i < i1; i += 8 * kThreads) {
@@ -119,14 +131,18 @@ __device__ __forceinline__ void chunk_scale(const T* x, O* out, int64_t i0, int6
   }
 }
 
-// out = coef * in over the whole table.
+// out = coef * in over the whole table, whose tensors are in reverse order; the
+// chunks of each are taken last first as well: the pass before ended there, and
+// what it read last is still in the 256 MB cache.  100M FP32 values into BF16:
+// 172 us first to last, 160 us so (183 us with ordinary stores too); 629M BF16
+// values 671 and 649 us (685 us).
 __device__ __forceinline__ void scale_table(const Table& t, float coef) {
   int k = 0;
   for (uint32_t c = blockIdx.x; c < t.first_chunk[t.count]; c += gridDim.x) {
     while (c >= t.first_chunk[k + 1]) ++k;
     if (coef == 1.0f && t.in[k] == t.out[k]) continue;   // in place, nothing to change
     const int64_t per = kChunkBytes / ((t.types[k] & 1) ? 4 : 2);
-    const int64_t i0 = (int64_t)(c - t.first_chunk[k]) * per;
+    const int64_t i0 = (int64_t)(t.first_chunk[k + 1] - 1 - c) * per;
     const int64_t i1 = i0 + per < t.numel[k] ? i0 + per : t.numel[k];
     const auto* xb = reinterpret_cast<const bf16_t*>(t.in[k]);
     const auto* xf = reinterpret_cast<const float*>(t.in[k]);
@@ -158,28 +174,36 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(Table t, const float* _
   scale_table(t, *factor);
 }
 
-// The next batch of the list from `at` on: at most kBatch tensors and a chunk
-// count that fits 31 bits (a tensor of more chunks is a batch by itself only
-// beyond 2^40 bytes, which the caller's size bound excludes).
-int64_t next_batch(const nvfp4_grad* list, int64_t count, int64_t at, Table& t) {
+// Put a gradient at the end of the table; false: the table is full, or its chunk
+// count would pass 31 bits (one tensor alone has at most 2^27 chunks).
+bool put(Table& t, const nvfp4_grad& g) {
+  if (g.numel == 0) return true;
+  const int in32 = g.in_type == NVFP4_TYPE_F32, out32 = g.out_type == NVFP4_TYPE_F32;
+  const int64_t per = kChunkBytes / (in32 ? 4 : 2), n = (g.numel + per - 1) / per;
+  const int64_t chunks = t.first_chunk[t.count] + n;
+  if (t.count == kBatch || chunks > (int64_t(1) << 31) - 1) return false;
+  t.in[t.count] = g.in;
+  t.out[t.count] = g.out;
+  t.numel[t.count] = g.numel;
+  t.types[t.count] = (uint8_t)(in32 | out32 << 1);
+  t.first_chunk[++t.count] = (uint32_t)chunks;
+  return true;
+}
+
+// The batch of the list that starts at `at`; returns its end.
+int64_t batch_from(const nvfp4_grad* list, int64_t count, int64_t at, Table& t) {
   t.count = 0;
   t.first_chunk[0] = 0;
-  int64_t chunks = 0;
-  for (; at < count && t.count < kBatch; ++at) {
-    const nvfp4_grad& g = list[at];
-    if (g.numel == 0) continue;
-    const int in32 = g.in_type == NVFP4_TYPE_F32, out32 = g.out_type == NVFP4_TYPE_F32;
-    const int64_t per = kChunkBytes / (in32 ? 4 : 2);
-    const int64_t n = (g.numel + per - 1) / per;
-    if (chunks + n > (int64_t(1) << 31) - 1) break;
-    chunks += n;
-    t.in[t.count] = g.in;
-    t.out[t.count] = g.out;
-    t.numel[t.count] = g.numel;
-    t.types[t.count] = (uint8_t)(in32 | out32 << 1);
-    t.first_chunk[++t.count] = (uint32_t)chunks;
-  }
+  while (at < count && put(t, list[at])) ++at;
   return at;
+}
+
+// The batch that ends before `end`, last gradient first; returns its start.
+int64_t batch_before(const nvfp4_grad* list, int64_t end, Table& t) {
+  t.count = 0;
+  t.first_chunk[0] = 0;
+  while (end > 0 && put(t, list[end - 1])) --end;
+  return end;
 }
 
 }  // namespace
@@ -191,7 +215,7 @@ hipError_t launch_grad_sumsq(const nvfp4_grad* list, int64_t count, double* part
   int64_t at = 0;
   int add = 0;
   do {   // at least once: an empty list leaves zeros
-    at = next_batch(list, count, at, t);
+    at = batch_from(list, count, at, t);
     hipLaunchKernelGGL(k_grad_sumsq, dim3(kWords), dim3(kThreads), 0, s, t, partials, add);
     add = 1;
   } while (at < count);
@@ -201,21 +225,21 @@ hipError_t launch_grad_sumsq(const nvfp4_grad* list, int64_t count, double* part
 hipError_t launch_grad_clip(const nvfp4_grad* list, int64_t count, const double* partials,
                             double max_norm, float* norm_out, hipStream_t s) {
   Table t;
-  int64_t at = 0;
-  do {
-    at = next_batch(list, count, at, t);
+  int64_t end = count;
+  do {   // at least once, for the norm
+    end = batch_before(list, end, t);
     hipLaunchKernelGGL(k_grad_clip, dim3(kWords), dim3(kThreads), 0, s, t, partials, max_norm,
                        norm_out);
     norm_out = nullptr;
-  } while (at < count);
+  } while (end > 0);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor,
                              hipStream_t s) {
   Table t;
-  for (int64_t at = 0; at < count;) {
-    at = next_batch(list, count, at, t);
+  for (int64_t end = count; end > 0;) {
+    end = batch_before(list, end, t);
     hipLaunchKernelGGL(k_grad_scale, dim3(kWords), dim3(kThreads), 0, s, t, factor);
   }
   return hipGetLastError();

@@ -63,6 +63,29 @@ __device__ __forceinline__ void store8(float* p, v8f v) {
       __builtin_bit_cast(v4u, __builtin_shufflevector(v, v, 4, 5, 6, 7));
 }
 
+// Eight columns of a row for the thread whose own begin at c: at the end of a row
+// whose width is no multiple of 8 they are the row's last eight, of which the first
+// `skip` belong to the thread before.  (A loop over the few columns left would put
+// the latency of a whole sum behind each.)  Needs dim >= 8.
+struct Cols {
+  int64_t at;
+  int skip;
+  __device__ __forceinline__ Cols(int64_t c, int64_t dim)
+      : at(c + 8 <= dim ? c : dim - 8), skip((int)(c - (c + 8 <= dim ? c : dim - 8))) {}
+};
+
+// The eight values to the row, without the first `skip`.
+template <class T>
+__device__ __forceinline__ void store8_from(T* row, Cols k, v8f v) {
+  if (k.skip == 0) {
+    store8(row + k.at, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 1; i < 8; ++i)
+    if (i >= k.skip) store1(row + k.at + i, v[i]);
+}
+
 // A wave-uniform value moved to a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {

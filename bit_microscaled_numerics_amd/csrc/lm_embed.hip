@@ -45,21 +45,22 @@ __global__ __launch_bounds__(64 * kEmbedWaves) void k_embed(EmbedArgs a, const W
   O* dst = out + t * ldo;
   const int64_t c0 = blockIdx.y * cols_per;
   const int64_t c1 = c0 + cols_per < a.dim ? c0 + cols_per : a.dim;
+  if (a.dim < kVec) {
+    if (lane < a.dim && c0 == 0) store1(dst + lane, live ? load1(src + lane) * a.scale : 0.0f);
+    return;
+  }
   for (int64_t c = c0 + lane * kVec; c < c1; c += 4 * kWaveCols) {
     v8f v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (c + u * kWaveCols + kVec <= c1) v[u] = live ? load8(src + c + u * kWaveCols) : v8f{};
+    for (int u = 0; u < 4; ++u) {
+      const int64_t cu = c + u * kWaveCols;
+      v[u] = v8f{};
+      if (live && cu < c1) v[u] = load8(src + Cols(cu, a.dim).at) * a.scale;
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int64_t cu = c + u * kWaveCols;
-      if (cu + kVec <= c1) {
-        v[u] *= a.scale;
-        if (!live) v[u] = v8f{};
-        store8(dst + cu, v[u]);
-      } else {
-        for (int64_t e = cu; e < c1; ++e) store1(dst + e, live ? load1(src + e) * a.scale : 0.0f);
-      }
+      if (cu < c1) store8_from(dst, Cols(cu, a.dim), v[u]);
     }
   }
 }
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(64 * kEmbedWaves) void k_embed(EmbedArgs a, const W
 // its digit; the lowest of them adds the count to the wave's LDS counter.
 constexpr int kDigitMax = 9, kBinsMax = 1 << kDigitMax;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSmallSort = 16 * kSortThreads;   // tokens one workgroup sorts in LDS
+constexpr int kSmallSort = 8 * kSortThreads;    // tokens one workgroup sorts
 constexpr int kTileSteps = 4, kTileKeys = kTileSteps * kSortThreads;
 
 __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t, int64_t n,
@@ -180,18 +181,19 @@ __global__ __launch_bounds__(kFillThreads) void k_fill(Fill fill) {
   fill_zero(fill, blockIdx.x);
 }
 
-// All passes in one workgroup, keys and token numbers in LDS between passes
-// (at most 16384 tokens: 128 KiB).  One launch instead of three per pass,
-// which is what a sort of this size costs.
+// All passes over a tile of tokens in one workgroup, keys and token numbers in LDS
+// between passes.  Up to 8192 tokens are one tile and sorted by this launch alone.
 template <int STEPS>
-__global__ __launch_bounds__(kSortThreads) void k_sort_small(EmbedArgs a, int bits, int passes,
-                                                             uint32_t* __restrict__ keys_out,
-                                                             uint32_t* __restrict__ idx_out,
-                                                             Fill fill) {
-  if (blockIdx.x > 0) {
-    fill_zero(fill, blockIdx.x - 1);
+__global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bits, int passes,
+                                                            int tiles,
+                                                            uint32_t* __restrict__ keys_out,
+                                                            uint32_t* __restrict__ idx_out,
+                                                            Fill fill) {
+  if ((int)blockIdx.x >= tiles) {
+    fill_zero(fill, blockIdx.x - tiles);
     return;
   }
+  const int64_t base = (int64_t)blockIdx.x * STEPS * kSortThreads;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* counts = reinterpret_cast<uint32_t*>(smem);           // [waves][bins]
   uint32_t* bin_base = counts + kSortWaves * kBinsMax;            // [bins]
@@ -205,7 +207,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(EmbedArgs a, int bi
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     at[s] = first + 64 * s;
-    key[s] = key_of(a.ids, wide, at[s], a.n, a.vocab);
+    key[s] = key_of(a.ids, wide, base + at[s], a.n, a.vocab);
   }
   const int bins = 1 << bits;
   for (int p = 0; p < passes; ++p) {
@@ -217,8 +219,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(EmbedArgs a, int bi
     __syncthreads();
     uint32_t total;
     const uint32_t mine = scan_waves(counts, bins);
-    const uint32_t base = block_exclusive(mine, scratch, &total);
-    if ((int)threadIdx.x < bins) bin_base[threadIdx.x] = base;
+    const uint32_t start = block_exclusive(mine, scratch, &total);
+    if ((int)threadIdx.x < bins) bin_base[threadIdx.x] = start;
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -237,10 +239,60 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(EmbedArgs a, int bi
   }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s)
-    if (first + 64 * s < a.n) {
-      keys_out[first + 64 * s] = key[s];
-      idx_out[first + 64 * s] = at[s];
+    if (base + first + 64 * s < a.n) {
+      keys_out[base + first + 64 * s] = key[s];
+      idx_out[base + first + 64 * s] = (uint32_t)base + at[s];
     }
+}
+
+// Up to 8 sorted tiles of 4096 merged: a key's place is its place in its tile, the
+// keys not above it in the tiles before, and the keys below it in the tiles after.
+// Every workgroup holds all keys in LDS (128 KiB) and counts by halving, the 8
+// tiles side by side.  30001 tokens: 24 us with the tiles' sort; the six launches of
+// the pass-by-pass sort below take 35 us.
+constexpr int kMergeTiles = 8;
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __restrict__ keys_in,
+                                                             const uint32_t* __restrict__ idx_in,
+                                                             int n, uint32_t* __restrict__ keys_out,
+                                                             uint32_t* __restrict__ idx_out) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+  // 16 bytes at a time, all loads out at once (the list is padded to 256 bytes)
+  v4u v[kMergeTiles];
+#pragma unroll
+  for (int u = 0; u < kMergeTiles; ++u)
+    if (4 * (u * kSortThreads + (int)threadIdx.x) < n)
+      v[u] = reinterpret_cast<const v4u*>(keys_in)[u * kSortThreads + threadIdx.x];
+#pragma unroll
+  for (int u = 0; u < kMergeTiles; ++u)
+    if (4 * (u * kSortThreads + (int)threadIdx.x) < n)
+      reinterpret_cast<v4u*>(keys)[u * kSortThreads + threadIdx.x] = v[u];
+  const int i = blockIdx.x * kSortThreads + threadIdx.x;
+  const uint32_t at = i < n ? idx_in[i] : 0;
+  __syncthreads();
+  if (i >= n) return;
+  const uint32_t key = keys[i];
+  const int tile = i / kTileKeys;
+  int below[kMergeTiles], len[kMergeTiles];
+  uint32_t limit[kMergeTiles];
+#pragma unroll
+  for (int t = 0; t < kMergeTiles; ++t) {
+    below[t] = 0;
+    len[t] = min(max(n - t * kTileKeys, 0), kTileKeys);
+    limit[t] = key + (t < tile ? 1u : 0u);
+  }
+  for (int step = kTileKeys; step > 0; step >>= 1)
+#pragma unroll
+    for (int t = 0; t < kMergeTiles; ++t) {
+      const int to = below[t] + step;
+      if (to <= len[t] && keys[t * kTileKeys + to - 1] < limit[t]) below[t] = to;
+    }
+  int pos = i - tile * kTileKeys;
+#pragma unroll
+  for (int t = 0; t < kMergeTiles; ++t) pos += t == tile ? 0 : below[t];
+  keys_out[pos] = key;
+  idx_out[pos] = at;
 }
 
 // One pass over tiles of 4096 keys: count, scan over [bin][tile], move.  The
@@ -337,21 +389,33 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(SortPass p) {
 }
 
 // ----------------------------------------------------------------- gradient
-// A frequent word owns a long run of the sorted tokens.  Aligned windows of
-// 64 sorted tokens that lie wholly inside one run are summed first, each by
-// its own wave into an FP32 partial row; the run kernel then adds at most 63
-// single rows before, the partials, and at most 63 rows after.  Loads go out
-// up to sixteen rows at a time: a chain of single rows is bound by their latency.
+// The sorted tokens are cut into windows of 64.  A run of one word inside a window
+// is at most 64 rows and is summed where its dW row is written.  A run that
+// crosses windows is summed window by window first, each piece by its own wave
+// into an FP32 partial row: piece 0 of a window is its rows of the run that came
+// in, piece 1 those of the run that goes on from inside it.  Loads go out up to
+// sixteen rows at a time: a chain of single rows is bound by their latency.
 constexpr int kWindow = 64;
+
+// Eight values (for v8f) or one (float) as they lie in memory, and their value.
+__device__ __forceinline__ v4u load_as(const v8f&, const bf16_t* p) {
+  return *reinterpret_cast<const v4u_any2*>(p);
+}
+__device__ __forceinline__ v8f load_as(const v8f&, const float* p) { return load8(p); }
+__device__ __forceinline__ float load_as(const float&, const bf16_t* p) { return load1(p); }
+__device__ __forceinline__ float load_as(const float&, const float* p) { return load1(p); }
+__device__ __forceinline__ v8f value(v4u v) { return unpack8(v); }
+__device__ __forceinline__ v8f value(v8f v) { return v; }
+__device__ __forceinline__ float value(float v) { return v; }
 
 // acc += at(j) + .. + at(j + N - 1), in this order, with all N loads out first.
 template <int N, class A, class At>
 __device__ __forceinline__ void add_batch(A& acc, int64_t j, At at) {
-  A v[N];
+  decltype(at(j)) v[N];   // as loaded: eight BF16 values wait in four registers
 #pragma unroll
   for (int u = 0; u < N; ++u) v[u] = at(j + u);
 #pragma unroll
-  for (int u = 0; u < N; ++u) acc += v[u];
+  for (int u = 0; u < N; ++u) acc += value(v[u]);
 }
 
 // acc += at(0) + .. + at(count - 1), in this order; count is the same for the
@@ -366,39 +430,53 @@ __device__ __forceinline__ void add_all(A& acc, int64_t count, At at) {
   if (count & 1) add_batch<1>(acc, j, at);
 }
 
-__device__ __forceinline__ v8f load_as(const v8f&, const bf16_t* p) { return load8(p); }
-__device__ __forceinline__ v8f load_as(const v8f&, const float* p) { return load8(p); }
-__device__ __forceinline__ float load_as(const float&, const bf16_t* p) { return load1(p); }
-__device__ __forceinline__ float load_as(const float&, const float* p) { return load1(p); }
-
-// The sum of dY rows idx[0 .. count) at columns c .. c + 7 (A = v8f) or at column
-// c (float) added to acc.
+// The sum of dY rows j0 .. j0 + count - 1 of a window at columns c .. c + 7 (A =
+// v8f) or at column c (float) added to acc.  Lane l of the wave holds row l's
+// number, loaded once for all batches.
 template <class A, class Y>
 __device__ __forceinline__ void add_rows(A& acc, const Y* __restrict__ dy, int64_t ld, int64_t c,
-                                         int64_t count, const uint32_t* __restrict__ idx) {
-  add_all(acc, count, [&](int64_t j) { return load_as(acc, dy + (int64_t)idx[j] * ld + c); });
+                                         int j0, int count, uint32_t row_of_lane) {
+  add_all(acc, count, [&](int64_t j) {
+    const uint32_t row =
+        (uint32_t)__builtin_amdgcn_readlane((int)row_of_lane, uniform(j0 + (int)j));
+    return load_as(acc, dy + (int64_t)row * ld + c);
+  });
 }
 
 template <class Y>
 __global__ __launch_bounds__(64) void k_embed_window(const uint32_t* __restrict__ keys,
-                                                     const uint32_t* __restrict__ idx,
+                                                     const uint32_t* __restrict__ idx, int64_t n,
                                                      int64_t vocab, int64_t dim,
                                                      const Y* __restrict__ dy, int64_t ld,
                                                      float* __restrict__ partial) {
   const int64_t win = blockIdx.x, s = win * kWindow;
-  const uint32_t k0 = keys[s], k1 = keys[s + kWindow - 1];
-  if (k0 != k1 || k0 >= (uint32_t)vocab) return;
-  float* dst = partial + win * dim;
+  const int count = uniform((int)(n - s < kWindow ? n - s : kWindow));
+  const int lane = threadIdx.x;
+  const uint32_t key = lane < count ? keys[s + lane] : kNoKey;
+  const uint32_t row = lane < count ? idx[s + lane] : 0;
+  const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)key);
+  const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)key, count - 1);
+  const bool from = s > 0 && keys[s - 1] == first && first < (uint32_t)vocab;
+  const bool on = s + count < n && keys[s + count] == last && last < (uint32_t)vocab;
+  const int head = from ? __popcll(__ballot(key == first)) : 0;              // rows of piece 0
+  const int tail = on && !(from && head == count) ? __popcll(__ballot(key == last)) : 0;
   const int64_t c = (int64_t)blockIdx.y * kWaveCols + threadIdx.x * kVec;
-  if (c + kVec <= dim) {
-    v8f acc = v8f{};
-    add_rows(acc, dy, ld, c, kWindow, idx + s);
-    store8(dst + c, acc);
-  } else {
-    for (int64_t e = c; e < dim; ++e) {
-      float acc = 0.0f;
-      add_rows(acc, dy, ld, e, kWindow, idx + s);
-      dst[e] = acc;
+  for (int piece = 0; piece < 2; ++piece) {
+    const int rows = piece == 0 ? head : tail;
+    if (rows == 0) continue;
+    const int at = piece == 0 ? 0 : count - tail;
+    float* dst = partial + (2 * win + piece) * dim;
+    if (dim < kVec) {
+      if (lane < dim) {
+        float acc = 0.0f;
+        add_rows(acc, dy, ld, lane, at, rows, row);
+        dst[lane] = acc;
+      }
+    } else if (c < dim) {
+      const Cols k(c, dim);
+      v8f acc = v8f{};
+      add_rows(acc, dy, ld, k.at, at, rows, row);
+      store8_from(dst, k, acc);
     }
   }
 }
@@ -431,49 +509,59 @@ struct RowArgs {
   bool accumulate;
 };
 
-// The whole sum of run [s, e) at columns c .. c + 7 (v8f) or column c (float).
+// The whole sum of run [s, e) at columns c .. c + 7 (v8f) or column c (float); lane l
+// holds the row number of sorted position s + l.
 template <class A, class Y>
 __device__ __forceinline__ A run_sum(const RowArgs& r, const Y* __restrict__ dy, int64_t s,
-                                     int64_t e, int64_t c) {
+                                     int64_t e, int64_t c, uint32_t row) {
   A acc = A{};
-  const int64_t w0 = (s + kWindow - 1) / kWindow, w1 = e / kWindow;   // whole windows
-  if (w0 >= w1) {
-    add_rows(acc, dy, r.ld_dy, c, e - s, r.idx + s);
+  const int64_t w0 = s / kWindow, w1 = (e - 1) / kWindow;
+  if (w0 == w1) {
+    add_rows(acc, dy, r.ld_dy, c, 0, (int)(e - s), row);
     return acc;
   }
-  add_rows(acc, dy, r.ld_dy, c, w0 * kWindow - s, r.idx + s);
-  add_all(acc, w1 - w0, [&](int64_t w) { return load_as(acc, r.partial + (w0 + w) * r.dim + c); });
-  add_rows(acc, dy, r.ld_dy, c, e - w1 * kWindow, r.idx + w1 * kWindow);
+  // piece 1 of the window it starts in, piece 0 of the others
+  acc += value(load_as(acc, r.partial + (2 * w0 + 1) * r.dim + c));
+  add_all(acc, w1 - w0, [&](int64_t w) {
+    return load_as(acc, r.partial + 2 * (w0 + 1 + w) * r.dim + c);
+  });
   return acc;
 }
 
-// dW rows of the words that occur: a workgroup for each sorted position and
-// range of columns (8 per thread); those that are not the first of a run leave.
+// dW rows of the words that occur: `waves` waves (1, 2 or 4 of a workgroup, by the
+// width) for each sorted position, 8 columns per thread and trip; those that are
+// not at the first of a run leave.
 template <class Y, class G>
-__global__ __launch_bounds__(256) void k_embed_runs(RowArgs r, const Y* __restrict__ dy,
+__global__ __launch_bounds__(256) void k_embed_runs(RowArgs r, int waves,
+                                                    const Y* __restrict__ dy,
                                                     G* __restrict__ dw) {
-  const int lane = threadIdx.x & 63;
-  const int64_t s = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t s = (int64_t)blockIdx.x * (4 / waves) + wave / waves;
+  if (s >= r.n) return;
   const uint32_t v = r.keys[s];
   if (v >= (uint32_t)r.vocab || (s > 0 && r.keys[s - 1] == v)) return;
   // the run's end: within the next 64 keys, or by search
-  const uint64_t same = __ballot(s + lane < r.n && r.keys[s + lane < r.n ? s + lane : s] == v);
+  const int64_t at = s + lane < r.n ? s + lane : s;
+  const uint32_t row = r.idx[at];
+  const uint64_t same = __ballot(s + lane < r.n && r.keys[at] == v);
   int64_t e = s + 64;
   if (~same != 0) e = s + __popcll(same);
   else e = lower_bound(r.keys, e, r.n - e, v + 1u);
   e = uniform64(e);
   G* dst = dw + (int64_t)v * r.ld_dw;
-  const int64_t c = (int64_t)blockIdx.y * blockDim.x * kVec + threadIdx.x * kVec;
-  if (c + kVec <= r.dim) {
-    v8f sum = run_sum<v8f>(r, dy, s, e, c) * r.scale;
-    if (r.accumulate) sum += load8(dst + c);
-    store8(dst + c, sum);
-  } else {
-    for (int64_t k = c; k < r.dim; ++k) {
-      float sum = run_sum<float>(r, dy, s, e, k) * r.scale;
-      if (r.accumulate) sum += load1(dst + k);
-      store1(dst + k, sum);
+  if (r.dim < kVec) {
+    if (lane < r.dim) {
+      float sum = run_sum<float>(r, dy, s, e, lane, row) * r.scale;
+      if (r.accumulate) sum += load1(dst + lane);
+      store1(dst + lane, sum);
     }
+    return;
+  }
+  for (int64_t c = (wave % waves * 64 + lane) * kVec; c < r.dim; c += waves * kWaveCols) {
+    const Cols k(c, r.dim);
+    v8f sum = run_sum<v8f>(r, dy, s, e, k.at, row) * r.scale;
+    if (r.accumulate) sum += load8(dst + k.at);
+    store8_from(dst, k, sum);
   }
 }
 
@@ -509,21 +597,22 @@ EmbedWs embed_ws(int64_t n, int64_t vocab, int64_t dim) {
     at = w.hist + pad256(((int64_t)1 << p.bits) * w.tiles * 4);
   }
   w.partial = at;
-  w.total = at + pad256(n / kWindow * dim * 4);
+  w.total = at + (n > kWindow ? pad256((n + kWindow - 1) / kWindow * 2 * dim * 4) : 0);
   return w;
 }
 
 template <int STEPS>
-hipError_t sort_small(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint32_t* idx,
-                      const Fill& fill, hipStream_t s) {
+hipError_t sort_tile(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint32_t* idx,
+                     const Fill& fill, hipStream_t s) {
   const size_t lds = (kSortWaves * kBinsMax + kBinsMax + kSortWaves) * 4 + STEPS * kSortThreads * 6;
   // above the 64 KiB default of dynamic LDS
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_small<STEPS>),
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_tile<STEPS>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const int blocks = fill.rows > 0 ? 1 + kFillBlocks : 1;
-  hipLaunchKernelGGL(k_sort_small<STEPS>, dim3(blocks), dim3(kSortThreads), lds, s, a, p.bits,
-                     p.passes, keys, idx, fill);
+  const int tiles = (int)((a.n + STEPS * kSortThreads - 1) / (STEPS * kSortThreads));
+  const int blocks = tiles + (fill.rows > 0 ? kFillBlocks : 0);
+  hipLaunchKernelGGL(k_sort_tile<STEPS>, dim3(blocks), dim3(kSortThreads), lds, s, a, p.bits,
+                     p.passes, tiles, keys, idx, fill);
   return hipGetLastError();
 }
 
@@ -532,14 +621,22 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const 
   const SortPlan p = sort_plan(a.vocab);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   uint32_t* idx = reinterpret_cast<uint32_t*>(ws + w.idx);
-  if (a.n <= kSmallSort) {
-    if (a.n <= 1 * kSortThreads) return sort_small<1>(a, p, keys, idx, fill, s);
-    if (a.n <= 4 * kSortThreads) return sort_small<4>(a, p, keys, idx, fill, s);
-    if (a.n <= 8 * kSortThreads) return sort_small<8>(a, p, keys, idx, fill, s);
-    return sort_small<16>(a, p, keys, idx, fill, s);
-  }
+  if (a.n <= 1 * kSortThreads) return sort_tile<1>(a, p, keys, idx, fill, s);
+  if (a.n <= kTileKeys) return sort_tile<kTileSteps>(a, p, keys, idx, fill, s);
+  if (a.n <= kSmallSort) return sort_tile<8>(a, p, keys, idx, fill, s);
   uint32_t* keys2 = reinterpret_cast<uint32_t*>(ws + w.keys2);
   uint32_t* idx2 = reinterpret_cast<uint32_t*>(ws + w.idx2);
+  if (a.n <= kMergeTiles * kTileKeys) {
+    hipError_t e = sort_tile<kTileSteps>(a, p, keys2, idx2, fill, s);
+    if (e != hipSuccess) return e;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_merge),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, kMergeTiles * kTileKeys * 4);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_sort_merge, dim3((uint32_t)((a.n + kSortThreads - 1) / kSortThreads)),
+                       dim3(kSortThreads), kMergeTiles * kTileKeys * 4, s, keys2, idx2, (int)a.n,
+                       keys, idx);
+    return hipGetLastError();
+  }
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + w.hist);
   const uint32_t *kin = nullptr, *iin = nullptr;
   for (int q = 0; q < p.passes; ++q) {
@@ -577,16 +674,14 @@ hipError_t embed_grad(const EmbedArgs& a, const Y* dy, int64_t ld_dy, G* dw, int
   }
   const hipError_t e = sort_tokens(a, w, ws, fill, s);
   if (e != hipSuccess) return e;
-  if (a.n >= kWindow)
+  if (a.n > kWindow)
     hipLaunchKernelGGL(k_embed_window<Y>,
-                       dim3((uint32_t)(a.n / kWindow),
+                       dim3((uint32_t)((a.n + kWindow - 1) / kWindow),
                             (uint32_t)((a.dim + kWaveCols - 1) / kWaveCols)),
-                       dim3(64), 0, s, keys, idx, a.vocab, a.dim, dy, ld_dy, partial);
+                       dim3(64), 0, s, keys, idx, a.n, a.vocab, a.dim, dy, ld_dy, partial);
   const RowArgs r{keys, idx, a.n, a.vocab, a.dim, ld_dy, ld_dw, partial, a.scale, accumulate};
-  const int waves = a.dim > 3 * kWaveCols ? 4 : (int)((a.dim + kWaveCols - 1) / kWaveCols);
-  const int64_t cols = waves * kWaveCols;
-  hipLaunchKernelGGL((k_embed_runs<Y, G>), dim3((uint32_t)a.n, (uint32_t)((a.dim + cols - 1) / cols)),
-                     dim3(64 * waves), 0, s, r, dy, dw);
+  const int waves = a.dim > 2 * kWaveCols ? 4 : a.dim > kWaveCols ? 2 : 1, per = 4 / waves;
+  hipLaunchKernelGGL((k_embed_runs<Y, G>), dim3((uint32_t)((a.n + per - 1) / per)), dim3(256), 0, s, r, waves, dy, dw);
   return hipGetLastError();
 }
 

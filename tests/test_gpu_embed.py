@@ -119,6 +119,18 @@ def test_gradient(n, kind, V, D):
     _check_grad(got, ids, dy, V, 1.7)
 
 
+@pytest.mark.parametrize("n", [32767, 32768, 32769, 36865, 70000])
+@pytest.mark.parametrize("kind", ["uniform", "same", "zipf", "outside"])
+def test_gradient_of_many_tokens(n, kind):
+    """Both sides of the largest merged sort (8 tiles of 4096)."""
+    say("embed_grad many", n, kind)
+    g = torch.Generator().manual_seed(n)
+    V, D = 997, 24
+    ids = _ids(g, n, V, kind, torch.int32)
+    dy = _rand(g, n, D)
+    _check_grad(nv.embed_grad(ids.cuda(), dy.cuda(), V), ids, dy, V, 1.0)
+
+
 @pytest.mark.parametrize("V", [2, 65537, 262143, 262144, 300000])
 @pytest.mark.parametrize("n", [100, 17000])
 def test_gradient_key_widths(V, n):

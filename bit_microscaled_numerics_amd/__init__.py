@@ -24,6 +24,12 @@ from typing import Optional, Union
 
 import torch
 
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:   # a torch without it: through the public object
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
@@ -157,9 +163,14 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _current_stream() -> int:
+    """The current stream's handle.  torch hands it out without building a Stream
+    object (0.4 instead of 2.7 us, a quarter of a small call)."""
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return _current_stream() if stream is None else stream.cuda_stream
 
 
 def _empty(*shape, dtype, device) -> torch.Tensor:
@@ -531,6 +542,14 @@ _FLOATS = {torch.bfloat16: NVFP4_TYPE_BF16, torch.float32: NVFP4_TYPE_F32}
 _INDEXES = {torch.int32: NVFP4_TYPE_I32, torch.int64: NVFP4_TYPE_I64}
 
 
+def _one_device(*tensors) -> None:
+    """All tensors on the current device, where the work is launched."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
+
+
 def _dev_matrix(x: torch.Tensor, name: str) -> int:
     """The type of a 2-D bf16 or float32 GPU tensor with contiguous rows."""
     if not x.is_cuda or x.dtype not in _FLOATS or x.dim() != 2:
@@ -564,6 +583,7 @@ def nvfp4_embed(ids, w, scale, out, stream=None):
     it, wt, ot = _dev_ids(ids, "ids"), _dev_matrix(w, "w"), _dev_matrix(out, "out")
     if out.shape[0] != ids.numel() or out.shape[1] != w.shape[1]:
         raise ValueError("out must be [number of ids][columns of w]")
+    _one_device(ids, w, out)
     _check(load_library().nvfp4_embed(_p(ids), it, ids.numel(), _p(w), wt, w.shape[0], w.shape[1],
                                       _pitch(w, "w"), scale, _p(out), ot, _pitch(out, "out"),
                                       _stream(stream)))
@@ -580,6 +600,7 @@ def nvfp4_embed_grad(ids, dy, scale, dw, accumulate, workspace, stream=None):
     it, yt, wt = _dev_ids(ids, "ids"), _dev_matrix(dy, "dy"), _dev_matrix(dw, "dw")
     if dy.shape[0] != ids.numel() or dy.shape[1] != dw.shape[1]:
         raise ValueError("dy must be [number of ids][columns of dw]")
+    _one_device(ids, dy, dw, workspace)
     _check(load_library().nvfp4_embed_grad(_p(ids), it, ids.numel(), _p(dy), yt, _pitch(dy, "dy"),
                                            dw.shape[0], dw.shape[1], scale, _p(dw), wt, _pitch(dw, "dw"),
                                            int(accumulate), _p(workspace), _nbytes(workspace),
@@ -594,6 +615,7 @@ def embed(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
     ot = wt if dtype is None else _FLOATS.get(dtype)
     if ot is None:
         raise ValueError("dtype must be bf16 or float32")
+    _one_device(ids, w)
     n, (vocab, dim) = ids.numel(), w.shape
     out = _empty(n, dim, dtype=w.dtype if dtype is None else dtype, device=w.device)
     # its own call of the entry point: a single token's lookup is bound by the host
@@ -641,6 +663,7 @@ def _ce_inputs(h, w, targets):
     tt = _dev_ids(targets, "targets")
     if targets.numel() != h.shape[0]:
         raise ValueError("one target for each row of h")
+    _one_device(h, w, targets)
     return _pitch(h, "h"), _pitch(w, "w"), h.shape[0], w.shape[0], h.shape[1], tt
 
 
@@ -654,6 +677,7 @@ def nvfp4_linear_ce(h, w, targets, loss, lse, workspace, stream=None):
     ldh, ldw, T, V, D, tt = _ce_inputs(h, w, targets)
     _dev_f32(loss, T, "loss")
     _dev_f32(lse, T, "lse")
+    _one_device(loss, lse, workspace)
     _check(load_library().nvfp4_linear_ce(_p(h), ldh, _p(w), ldw, T, V, D, _p(targets), tt,
                                           _p(loss), _p(lse), _p(workspace), _nbytes(workspace),
                                           _stream(stream)))
@@ -667,6 +691,7 @@ def nvfp4_linear_ce_grad(h, w, targets, row_weight, piece_tokens, loss, lse, dh,
     for x, like, name in ((dh, h, "dh"), (dw, w, "dw")):
         if _dev_matrix(x, name) != NVFP4_TYPE_BF16 or x.shape != like.shape:
             raise ValueError(f"{name} must be bf16 of its input's shape")
+    _one_device(row_weight, loss, lse, dh, dw, workspace)
     _check(load_library().nvfp4_linear_ce_grad(
         _p(h), ldh, _p(w), ldw, T, V, D, _p(targets), tt, _p(row_weight), piece_tokens, _p(loss),
         _p(lse), _p(dh), _pitch(dh, "dh"), _p(dw), _pitch(dw, "dw"), _p(workspace),
@@ -677,12 +702,16 @@ def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
     """(loss, lse) of the output head z = h w^T, float32 [rows of h]: lse the
     log of the sum of exponentials of a row's logits, loss lse minus the
     target's logit (0 where the target is outside 0 .. rows of w - 1)."""
-    T, V, D = _ce_inputs(h, w, targets)[2:5]
-    loss = _empty(T, dtype=torch.float32, device=h.device)
-    lse = _empty(T, dtype=torch.float32, device=h.device)
-    ws = torch.empty(nvfp4_linear_ce_workspace_bytes(T, V, D, False), dtype=torch.uint8,
-                     device=h.device)
-    nvfp4_linear_ce(h, w, targets, loss, lse, ws)
+    ldh, ldw, T, V, D, tt = _ce_inputs(h, w, targets)
+    dev, lib = h.device, load_library()
+    loss = _empty(T, dtype=torch.float32, device=dev)
+    lse = _empty(T, dtype=torch.float32, device=dev)
+    n = nvfp4_linear_ce_workspace_bytes(T, V, D, False)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    # its own call of the entry point: scoring a single token is bound by the host
+    _check(lib.nvfp4_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, T, V, D, targets.data_ptr(),
+                               tt, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
+                               _stream(None)))
     return loss, lse
 
 
@@ -692,24 +721,35 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     row_weight * loss (of the mean over the rows that have a target if None).
     piece_tokens bounds the workspace: about 2 bytes for each of its tokens
     and each word (0: 4 GiB at most)."""
-    T, V, D = _ce_inputs(h, w, targets)[2:5]
-    loss = _empty(T, dtype=torch.float32, device=h.device)
-    lse = _empty(T, dtype=torch.float32, device=h.device)
-    dh = _empty(T, D, dtype=torch.bfloat16, device=h.device)
-    dw = _empty(V, D, dtype=torch.bfloat16, device=h.device)
-    ws = torch.empty(nvfp4_linear_ce_workspace_bytes(T, V, D, True, piece_tokens),
-                     dtype=torch.uint8, device=h.device)
-    nvfp4_linear_ce_grad(h, w, targets, row_weight, piece_tokens, loss, lse, dh, dw, ws)
+    ldh, ldw, T, V, D, tt = _ce_inputs(h, w, targets)
+    _dev_f32(row_weight, T, "row_weight")
+    if row_weight is not None:
+        _one_device(row_weight)
+    dev, lib = h.device, load_library()
+    loss = _empty(T, dtype=torch.float32, device=dev)
+    lse = _empty(T, dtype=torch.float32, device=dev)
+    dh = _empty(T, D, dtype=torch.bfloat16, device=dev)
+    dw = _empty(V, D, dtype=torch.bfloat16, device=dev)
+    n = nvfp4_linear_ce_workspace_bytes(T, V, D, True, piece_tokens)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib.nvfp4_linear_ce_grad(h.data_ptr(), ldh, w.data_ptr(), ldw, T, V, D,
+                                    targets.data_ptr(), tt, _p(row_weight), piece_tokens,
+                                    loss.data_ptr(), lse.data_ptr(), dh.data_ptr(), D,
+                                    dw.data_ptr(), D, ws.data_ptr(), n, _stream(None)))
     return loss, lse, dh, dw
 
 
 def _grad_list(grads, outs):
     """The nvfp4_grad array of a list of gradients (and outputs), and its length."""
-    words, types = [], _FLOATS
+    words, types, dev = [], _FLOATS, None
     for g, o in zip(grads, outs):
         gt = types.get(g.dtype)
         if gt is None or not g.is_cuda:
             raise ValueError("gradients must be bf16 or float32 CUDA tensors")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if g.get_device() != dev or o.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
         if not g.is_contiguous():
             raise ValueError("gradients must be contiguous")
         at = g.data_ptr()
@@ -747,6 +787,7 @@ def _dev_partials(partials):
     if (not partials.is_cuda or partials.dtype != torch.float64 or not partials.is_contiguous()
             or partials.numel() != NVFP4_SUMSQ_WORDS):
         raise ValueError(f"partials must be {NVFP4_SUMSQ_WORDS} contiguous float64 CUDA values")
+    _one_device(partials)
 
 
 def grad_sumsq(grads) -> torch.Tensor:

@@ -104,6 +104,15 @@ def test_sizes(T, V, D):
     _check_all(*_inputs(T, V, D, it=torch.int32 if (T + V) % 2 else torch.int64))
 
 
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17])
+@pytest.mark.parametrize("V,D", [(5, 8), (130, 40), (1000, 256), (4100, 264), (700, 2000)])
+@pytest.mark.parametrize("ignored", ["none", "some"])
+def test_few_tokens(T, V, D, ignored):
+    """Single tokens to a decoding batch, D that is no multiple of a stage (64)."""
+    say("ce few", T, V, D, ignored)
+    _check_all(*_inputs(T, V, D, scale=0.1, ignored=ignored))
+
+
 @pytest.mark.parametrize("T,V,D", [(300, 4099, 520), (520, 33000, 136), (40, 9000, 1032)])
 @pytest.mark.parametrize("weighted", [False, True])
 def test_larger(T, V, D, weighted):

@@ -630,7 +630,7 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1
                accumulate_into: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of ``embed`` with respect to w, [vocab][columns of dy] of
     dtype (dy's if None): row v is scale times the sum of dy's rows whose id
-    is v, in ascending order.  accumulate_into: a gradient that is added to in
+    is v, the same bits every time.  accumulate_into: a gradient that is added to in
     place and returned."""
     _dev_matrix(dy, "dy")
     dw = accumulate_into

@@ -7,7 +7,8 @@
 // Both are bound by HBM: the forward moves T * D elements in and out, the
 // gradient reads T * D and writes all V * D.  The gradient is deterministic:
 // a stable sort of the tokens by id puts the rows of one word side by side in
-// ascending t, and every dW row is one FP32 sum in that order (no atomics).
+// ascending t, and every dW row is the FP32 sum, in that order, of pieces of up to
+// 16 rows, each summed in that order (no atomics).
 // The sort needs one or a few workgroups and the zeros of dW need no sort, so
 // the sort's first launch writes them with all its other workgroups; the rows
 // of the words that occur are then written over them, at most T rows.
@@ -73,7 +74,6 @@ __global__ __launch_bounds__(64 * kEmbedWaves) void k_embed(EmbedArgs a, const W
 // its digit; the lowest of them adds the count to the wave's LDS counter.
 constexpr int kDigitMax = 9, kBinsMax = 1 << kDigitMax;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSmallSort = 8 * kSortThreads;    // tokens one workgroup sorts
 constexpr int kTileSteps = 4, kTileKeys = kTileSteps * kSortThreads;
 
 __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t, int64_t n,
@@ -83,20 +83,35 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t
   return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
 }
 
-// Rank of this lane's key among the wave's earlier keys with the same digit.
-// `counts` are this wave's own.
-__device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, uint32_t* counts) {
-  const int lane = threadIdx.x & 63;
-  uint64_t peers = ~0ull;
-  for (int b = 0; b < bits; ++b) {
-    const uint64_t m = __ballot((digit >> b) & 1u);
-    peers &= ((digit >> b) & 1u) ? m : ~m;
+// rank[s]: how many of the wave's keys before this lane's s-th have its digit (bits
+// shift ..).  `counts` are this wave's own.  The steps' ballots side by side: one
+// after the other they are a chain of latencies.
+template <int STEPS>
+__device__ __forceinline__ void wave_ranks(const uint32_t (&key)[STEPS], uint32_t (&rank)[STEPS],
+                                           int shift, int bits, uint32_t* counts) {
+  uint32_t lo[STEPS], hi[STEPS];   // the lanes with the same digit
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) lo[s] = hi[s] = ~0u;
+  for (int b = shift; b < shift + bits; ++b) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int mine = __builtin_amdgcn_sbfe((int)key[s], b, 1);   // the bit in every place
+      const uint64_t m = __ballot(mine);
+      lo[s] &= ~((uint32_t)m ^ (uint32_t)mine);
+      hi[s] &= ~((uint32_t)(m >> 32) ^ (uint32_t)mine);
+    }
   }
-  const uint32_t before = (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
-  const int first = __ffsll((unsigned long long)peers) - 1;
-  uint32_t base = 0;
-  if (lane == first) base = atomicAdd(&counts[digit], (uint32_t)__popcll(peers));
-  return (uint32_t)__shfl((int)base, first, 64) + before;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    uint32_t* count = &counts[(key[s] >> shift) & ((1u << bits) - 1)];
+    const uint32_t before = __builtin_amdgcn_mbcnt_hi(hi[s], __builtin_amdgcn_mbcnt_lo(lo[s], 0));
+    const uint32_t base = *count;
+    rank[s] = base + before;
+    // the lowest lane of a digit adds all of them, in the wave's order: no atomic
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (before == 0) *count = base + (uint32_t)(__popc(lo[s]) + __popc(hi[s]));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
 }
 
 // Exclusive sum over the workgroup of one value per thread; `scratch` holds
@@ -213,9 +228,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bit
   for (int p = 0; p < passes; ++p) {
     for (int i = threadIdx.x; i < kSortWaves * kBinsMax; i += kSortThreads) counts[i] = 0;
     __syncthreads();
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-      rank[s] = wave_rank((key[s] >> (p * bits)) & (bins - 1), bits, counts + wave * kBinsMax);
+    wave_ranks(key, rank, p * bits, bits, counts + wave * kBinsMax);
     __syncthreads();
     uint32_t total;
     const uint32_t mine = scan_waves(counts, bins);
@@ -245,16 +258,17 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bit
     }
 }
 
-// Up to 8 sorted tiles of 4096 merged: a key's place is its place in its tile, the
-// keys not above it in the tiles before, and the keys below it in the tiles after.
-// Every workgroup holds all keys in LDS (128 KiB) and counts by halving, the 8
-// tiles side by side.  30001 tokens: 24 us with the tiles' sort; the six launches of
-// the pass-by-pass sort below take 35 us.
-constexpr int kMergeTiles = 8;
+// Up to 8 sorted tiles merged: a key's place is its place in its tile, the keys not
+// above it in the tiles before, and the keys below it in the tiles after.  Every
+// workgroup holds all keys in LDS (up to 128 KiB) and counts by halving for 256 of
+// them: with 1024 the random reads of LDS take 11.2 us instead of 5.  30001 tokens:
+// 15 us with the tiles' sort; the six launches of the pass-by-pass sort below, 35 us.
+constexpr int kMergeTiles = 8, kMergeKeys = kSortThreads / 4;   // keys: of a workgroup
 
 __global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __restrict__ keys_in,
                                                              const uint32_t* __restrict__ idx_in,
-                                                             int n, uint32_t* __restrict__ keys_out,
+                                                             int n, int tile_keys,
+                                                             uint32_t* __restrict__ keys_out,
                                                              uint32_t* __restrict__ idx_out) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
@@ -268,31 +282,37 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __r
   for (int u = 0; u < kMergeTiles; ++u)
     if (4 * (u * kSortThreads + (int)threadIdx.x) < n)
       reinterpret_cast<v4u*>(keys)[u * kSortThreads + threadIdx.x] = v[u];
-  const int i = blockIdx.x * kSortThreads + threadIdx.x;
+  // four neighbouring lanes share a key, each counts in two of the tiles
+  constexpr int kEach = kMergeTiles / 4;
+  const int i = blockIdx.x * kMergeKeys + threadIdx.x / 4, t0 = threadIdx.x % 4 * kEach;
   const uint32_t at = i < n ? idx_in[i] : 0;
   __syncthreads();
   if (i >= n) return;
   const uint32_t key = keys[i];
-  const int tile = i / kTileKeys;
-  int below[kMergeTiles], len[kMergeTiles];
-  uint32_t limit[kMergeTiles];
+  const int tile = i / tile_keys;
+  int below[kEach], len[kEach];
+  uint32_t limit[kEach];
 #pragma unroll
-  for (int t = 0; t < kMergeTiles; ++t) {
-    below[t] = 0;
-    len[t] = min(max(n - t * kTileKeys, 0), kTileKeys);
-    limit[t] = key + (t < tile ? 1u : 0u);
+  for (int u = 0; u < kEach; ++u) {
+    const int t = t0 + u;
+    below[u] = 0;
+    len[u] = t == tile ? 0 : min(max(n - t * tile_keys, 0), tile_keys);
+    limit[u] = key + (t < tile ? 1u : 0u);
   }
-  for (int step = kTileKeys; step > 0; step >>= 1)
+  for (int step = tile_keys; step > 0; step >>= 1)
 #pragma unroll
-    for (int t = 0; t < kMergeTiles; ++t) {
-      const int to = below[t] + step;
-      if (to <= len[t] && keys[t * kTileKeys + to - 1] < limit[t]) below[t] = to;
+    for (int u = 0; u < kEach; ++u) {
+      const int to = below[u] + step;
+      if (to <= len[u] && keys[(t0 + u) * tile_keys + to - 1] < limit[u]) below[u] = to;
     }
-  int pos = i - tile * kTileKeys;
-#pragma unroll
-  for (int t = 0; t < kMergeTiles; ++t) pos += t == tile ? 0 : below[t];
-  keys_out[pos] = key;
-  idx_out[pos] = at;
+  int pos = below[0] + below[1];
+  pos += __shfl_xor(pos, 1, 64);
+  pos += __shfl_xor(pos, 2, 64);
+  pos += i - tile * tile_keys;
+  if (threadIdx.x % 4 == 0) {
+    keys_out[pos] = key;
+    idx_out[pos] = at;
+  }
 }
 
 // One pass over tiles of 4096 keys: count, scan over [bin][tile], move.  The
@@ -366,10 +386,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(SortPass p) {
   const int64_t first = (int64_t)blockIdx.x * kTileKeys + wave * 64 * kTileSteps + lane;
   uint32_t key[kTileSteps], rank[kTileSteps];
 #pragma unroll
-  for (int s = 0; s < kTileSteps; ++s) {
-    key[s] = tile_key(p, first + 64 * s);
-    rank[s] = wave_rank((key[s] >> p.shift) & (bins - 1), p.bits, counts + wave * kBinsMax);
-  }
+  for (int s = 0; s < kTileSteps; ++s) key[s] = tile_key(p, first + 64 * s);
+  wave_ranks(key, rank, p.shift, p.bits, counts + wave * kBinsMax);
   __syncthreads();
   scan_waves(counts, bins);
   __syncthreads();
@@ -389,13 +407,16 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(SortPass p) {
 }
 
 // ----------------------------------------------------------------- gradient
-// The sorted tokens are cut into windows of 64.  A run of one word inside a window
-// is at most 64 rows and is summed where its dW row is written.  A run that
-// crosses windows is summed window by window first, each piece by its own wave
-// into an FP32 partial row: piece 0 of a window is its rows of the run that came
-// in, piece 1 those of the run that goes on from inside it.  Loads go out up to
-// sixteen rows at a time: a chain of single rows is bound by their latency.
-constexpr int kWindow = 64;
+// The sorted tokens are cut into windows of 64, a workgroup each and 16 rows a wave,
+// which has all its rows on the way at once (a chain of single rows is bound by
+// their latency); every row of dY is read once.  A run of one word inside the rows
+// of a wave goes straight to dW; the piece of a run that came in (`head`) or goes on
+// (`tail`) goes to LDS, and the wave where the run starts joins the pieces in order.
+// A run that crosses windows leaves one FP32 partial row per window, joined in order
+// by a second kernel.  Windows of 128 are as fast with many tokens and 1 us slower
+// with few.  8192 x 5120 BF16 with words as in text: 43 + 5 us, much of it while the
+// zeros drain; 30001 x 771, few words: 14 + 4 us.
+constexpr int kWaveRows = 16, kSumWaves = 4, kWindow = kWaveRows * kSumWaves;
 
 // Eight values (for v8f) or one (float) as they lie in memory, and their value.
 __device__ __forceinline__ v4u load_as(const v8f&, const bf16_t* p) {
@@ -407,6 +428,142 @@ __device__ __forceinline__ float load_as(const float&, const float* p) { return 
 __device__ __forceinline__ v8f value(v4u v) { return unpack8(v); }
 __device__ __forceinline__ v8f value(v8f v) { return v; }
 __device__ __forceinline__ float value(float v) { return v; }
+
+struct RowArgs {
+  const uint32_t* keys;
+  const uint32_t* idx;
+  int64_t n, vocab, dim, ld_dy, ld_dw;
+  float* partial;
+  float scale;
+};
+
+// Columns c .. c + 7 of a row (v8f), or column c.  At the end of a row a thread's
+// eight overlap those of the thread before, and both hold the same bits there; only
+// a sum that is added to what the row holds has to be written once.
+template <bool ONCE, class G>
+__device__ __forceinline__ void write_row(G* row, const Cols& k, v8f v) {
+  if (ONCE) store8_from(row, k, v);
+  else store8(row + k.at, v);
+}
+template <bool ONCE, class G>
+__device__ __forceinline__ void write_row(G* row, int c, float v) { store1(row + c, v); }
+__device__ __forceinline__ int64_t col(const Cols& k) { return k.at; }
+__device__ __forceinline__ int64_t col(int c) { return c; }
+
+template <bool ADD, class A, class G, class K>
+__device__ __forceinline__ void finish_row(const RowArgs& r, G* __restrict__ dw, uint32_t word, K k,
+                                           A sum) {
+  G* row = dw + (int64_t)word * r.ld_dw;
+  sum *= r.scale;
+  if (ADD) sum += value(load_as(A{}, row + col(k)));
+  write_row<ADD>(row, k, sum);
+}
+
+// What a wave leaves in LDS for the run that came in or goes on: values by lane.
+template <class A>
+struct Pieces {
+  A head[kSumWaves][64], tail[kSumWaves][64];
+  bool through[kSumWaves];   // head holds all rows of the wave and its run goes on
+};
+
+// The rows of a window at this lane's columns; `on`: the lane has columns.  ADD: the
+// sums are added to dW, whose rows are then on the way with dY's.
+template <bool ADD, class A, class Y, class G, class K>
+__device__ __forceinline__ void sum_window(const RowArgs& r, const Y* __restrict__ dy,
+                                           G* __restrict__ dw, Pieces<A>& lds, K k, bool on) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t win = blockIdx.x, p0 = win * kWindow + wave * kWaveRows;
+  const int count = uniform((int)(r.n - p0 < 0 ? 0 : r.n - p0 < kWaveRows ? r.n - p0 : kWaveRows));
+  // lane l: the key of position p0 + l - 1 (no key outside the list), and its row
+  const int64_t at = p0 + lane - 1;
+  const bool real = lane <= kWaveRows + 1 && at >= 0 && at < r.n;
+  const uint32_t key = real ? r.keys[at] : kNoKey;
+  const uint32_t row = real ? r.idx[at] : 0;
+  // bit j: the words of rows j - 1 and j differ, so a run starts at row j
+  const uint64_t starts = __ballot(key != (uint32_t)__shfl_down((int)key, 1, 64));
+  const auto word = [&](int j) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)key, j + 1);
+  };
+  // row j ends a run that starts in these rows, of a word of the vocabulary
+  const auto whole = [&](int j) {
+    return j < count && (starts >> (j + 1) & 1) && (starts & ((2ull << j) - 1)) != 0 &&
+           word(j) < (uint32_t)r.vocab;
+  };
+  constexpr int kBatch = ADD ? kWaveRows / 2 : kWaveRows;   // rows in registers at once
+  A acc = A{};
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += kBatch) {
+    if (!on) break;
+    decltype(load_as(A{}, dy)) v[kBatch];
+    decltype(load_as(A{}, dw)) old[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {   // past the end the last row again, not used
+      const int j = j0 + u < count ? j0 + u : count - 1;
+      const uint32_t from = (uint32_t)__builtin_amdgcn_readlane((int)row, j + 1);
+      v[u] = load_as(A{}, dy + (int64_t)from * r.ld_dy + col(k));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (ADD && whole(j0 + u))
+        old[u] = load_as(A{}, dw + (int64_t)word(j0 + u) * r.ld_dw + col(k));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + u;
+      if (j < count) {
+        acc += value(v[u]);
+        if (starts >> (j + 1) & 1) {
+          if ((starts & ((2ull << j) - 1)) == 0) {
+            lds.head[wave][lane] = acc;
+          } else if (whole(j)) {
+            acc *= r.scale;
+            if (ADD) acc += value(old[u]);
+            write_row<ADD>(dw + (int64_t)word(j) * r.ld_dw, k, acc);
+          }
+          acc = A{};
+        }
+      }
+    }
+  }
+  // the last run goes on past these rows
+  const bool onward = count > 0 && !(starts >> count & 1);
+  const bool fresh = (starts & ((1ull << count) - 1)) != 0;   // and starts in them
+  if (onward) (fresh ? lds.tail : lds.head)[wave][lane] = acc;
+  if (lane == 0) lds.through[wave] = onward && !fresh;
+  __syncthreads();
+  if (!on || count == 0) return;
+  // the pieces of the run that waves w .. go on with, until it ends
+  const auto join = [&](A& sum, int w, bool going) {
+    for (; going && w < kSumWaves; ++w) {
+      sum += lds.head[w][lane];
+      going = uniform((int)lds.through[w]) != 0;
+    }
+    return going;
+  };
+  if (wave == 0 && !(starts & 1) && word(0) < (uint32_t)r.vocab) {
+    A sum = A{};
+    join(sum, 0, true);
+    write_row<false>(r.partial + 2 * win * r.dim, k, sum);
+  }
+  if (onward && fresh && word(count - 1) < (uint32_t)r.vocab) {
+    A sum = lds.tail[wave][lane];
+    if (join(sum, wave + 1, true)) write_row<false>(r.partial + (2 * win + 1) * r.dim, k, sum);
+    else finish_row<ADD>(r, dw, word(count - 1), k, sum);
+  }
+}
+
+template <bool ADD, class Y, class G>
+__global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(RowArgs r, const Y* __restrict__ dy,
+                                                              G* __restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  if (r.dim < kVec) {
+    __shared__ Pieces<float> lds;
+    sum_window<ADD>(r, dy, dw, lds, lane, lane < r.dim);
+  } else {
+    __shared__ Pieces<v8f> lds;
+    const int64_t c = (int64_t)blockIdx.y * kWaveCols + lane * kVec;
+    sum_window<ADD>(r, dy, dw, lds, Cols(c < r.dim ? c : 0, r.dim), c < r.dim);
+  }
+}
 
 // acc += at(j) + .. + at(j + N - 1), in this order, with all N loads out first.
 template <int N, class A, class At>
@@ -430,57 +587,6 @@ __device__ __forceinline__ void add_all(A& acc, int64_t count, At at) {
   if (count & 1) add_batch<1>(acc, j, at);
 }
 
-// The sum of dY rows j0 .. j0 + count - 1 of a window at columns c .. c + 7 (A =
-// v8f) or at column c (float) added to acc.  Lane l of the wave holds row l's
-// number, loaded once for all batches.
-template <class A, class Y>
-__device__ __forceinline__ void add_rows(A& acc, const Y* __restrict__ dy, int64_t ld, int64_t c,
-                                         int j0, int count, uint32_t row_of_lane) {
-  add_all(acc, count, [&](int64_t j) {
-    const uint32_t row =
-        (uint32_t)__builtin_amdgcn_readlane((int)row_of_lane, uniform(j0 + (int)j));
-    return load_as(acc, dy + (int64_t)row * ld + c);
-  });
-}
-
-template <class Y>
-__global__ __launch_bounds__(64) void k_embed_window(const uint32_t* __restrict__ keys,
-                                                     const uint32_t* __restrict__ idx, int64_t n,
-                                                     int64_t vocab, int64_t dim,
-                                                     const Y* __restrict__ dy, int64_t ld,
-                                                     float* __restrict__ partial) {
-  const int64_t win = blockIdx.x, s = win * kWindow;
-  const int count = uniform((int)(n - s < kWindow ? n - s : kWindow));
-  const int lane = threadIdx.x;
-  const uint32_t key = lane < count ? keys[s + lane] : kNoKey;
-  const uint32_t row = lane < count ? idx[s + lane] : 0;
-  const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)key);
-  const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)key, count - 1);
-  const bool from = s > 0 && keys[s - 1] == first && first < (uint32_t)vocab;
-  const bool on = s + count < n && keys[s + count] == last && last < (uint32_t)vocab;
-  const int head = from ? __popcll(__ballot(key == first)) : 0;              // rows of piece 0
-  const int tail = on && !(from && head == count) ? __popcll(__ballot(key == last)) : 0;
-  const int64_t c = (int64_t)blockIdx.y * kWaveCols + threadIdx.x * kVec;
-  for (int piece = 0; piece < 2; ++piece) {
-    const int rows = piece == 0 ? head : tail;
-    if (rows == 0) continue;
-    const int at = piece == 0 ? 0 : count - tail;
-    float* dst = partial + (2 * win + piece) * dim;
-    if (dim < kVec) {
-      if (lane < dim) {
-        float acc = 0.0f;
-        add_rows(acc, dy, ld, lane, at, rows, row);
-        dst[lane] = acc;
-      }
-    } else if (c < dim) {
-      const Cols k(c, dim);
-      v8f acc = v8f{};
-      add_rows(acc, dy, ld, k.at, at, rows, row);
-      store8_from(dst, k, acc);
-    }
-  }
-}
-
 // First sorted position whose key is not below `key`, within [lo, lo + len]:
 // the wave probes 64 places at a time.
 __device__ __forceinline__ int64_t lower_bound(const uint32_t* __restrict__ keys, int64_t lo,
@@ -500,69 +606,33 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* __restrict__ keys
   return lo;
 }
 
-struct RowArgs {
-  const uint32_t* keys;
-  const uint32_t* idx;
-  int64_t n, vocab, dim, ld_dy, ld_dw;
-  const float* partial;
-  float scale;
-  bool accumulate;
-};
-
-// The whole sum of run [s, e) at columns c .. c + 7 (v8f) or column c (float); lane l
-// holds the row number of sorted position s + l.
-template <class A, class Y>
-__device__ __forceinline__ A run_sum(const RowArgs& r, const Y* __restrict__ dy, int64_t s,
-                                     int64_t e, int64_t c, uint32_t row) {
-  A acc = A{};
-  const int64_t w0 = s / kWindow, w1 = (e - 1) / kWindow;
-  if (w0 == w1) {
-    add_rows(acc, dy, r.ld_dy, c, 0, (int)(e - s), row);
-    return acc;
-  }
-  // piece 1 of the window it starts in, piece 0 of the others
-  acc += value(load_as(acc, r.partial + (2 * w0 + 1) * r.dim + c));
-  add_all(acc, w1 - w0, [&](int64_t w) {
-    return load_as(acc, r.partial + 2 * (w0 + 1 + w) * r.dim + c);
-  });
-  return acc;
-}
-
-// dW rows of the words that occur: `waves` waves (1, 2 or 4 of a workgroup, by the
-// width) for each sorted position, 8 columns per thread and trip; those that are
-// not at the first of a run leave.
-template <class Y, class G>
-__global__ __launch_bounds__(256) void k_embed_runs(RowArgs r, int waves,
-                                                    const Y* __restrict__ dy,
-                                                    G* __restrict__ dw) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t s = (int64_t)blockIdx.x * (4 / waves) + wave / waves;
-  if (s >= r.n) return;
-  const uint32_t v = r.keys[s];
-  if (v >= (uint32_t)r.vocab || (s > 0 && r.keys[s - 1] == v)) return;
-  // the run's end: within the next 64 keys, or by search
-  const int64_t at = s + lane < r.n ? s + lane : s;
-  const uint32_t row = r.idx[at];
-  const uint64_t same = __ballot(s + lane < r.n && r.keys[at] == v);
-  int64_t e = s + 64;
-  if (~same != 0) e = s + __popcll(same);
-  else e = lower_bound(r.keys, e, r.n - e, v + 1u);
-  e = uniform64(e);
-  G* dst = dw + (int64_t)v * r.ld_dw;
+// The dW rows of the runs that cross windows, by the window each starts in: piece 1
+// of that window, then piece 0 of those after it.
+template <bool ADD, class G>
+__global__ __launch_bounds__(64) void k_embed_join(RowArgs r, G* __restrict__ dw) {
+  const int64_t win = blockIdx.x, s = win * kWindow, e = s + kWindow;
+  if (e >= r.n) return;
+  const uint32_t word = r.keys[e];
+  if (word >= (uint32_t)r.vocab || r.keys[e - 1] != word) return;
+  if (s > 0 && r.keys[s - 1] == word) return;   // it starts in a window before
+  const int64_t end = uniform64(lower_bound(r.keys, e, r.n - e, word + 1u));
+  const int64_t after = (end - 1) / kWindow - win;
+  const float* first = r.partial + (2 * win + 1) * r.dim;
+  const float* next = r.partial + 2 * (win + 1) * r.dim;
   if (r.dim < kVec) {
-    if (lane < r.dim) {
-      float sum = run_sum<float>(r, dy, s, e, lane, row) * r.scale;
-      if (r.accumulate) sum += load1(dst + lane);
-      store1(dst + lane, sum);
-    }
+    const int c = threadIdx.x;
+    if (c >= r.dim) return;
+    float sum = first[c];
+    add_all(sum, after, [&](int64_t w) { return next[2 * w * r.dim + c]; });
+    finish_row<ADD>(r, dw, word, c, sum);
     return;
   }
-  for (int64_t c = (wave % waves * 64 + lane) * kVec; c < r.dim; c += waves * kWaveCols) {
-    const Cols k(c, r.dim);
-    v8f sum = run_sum<v8f>(r, dy, s, e, k.at, row) * r.scale;
-    if (r.accumulate) sum += load8(dst + k.at);
-    store8_from(dst, k, sum);
-  }
+  const int64_t c = (int64_t)blockIdx.y * kWaveCols + threadIdx.x * kVec;
+  if (c >= r.dim) return;
+  const Cols k(c, r.dim);
+  v8f sum = load8(first + k.at);
+  add_all(sum, after, [&](int64_t w) { return load8(next + 2 * w * r.dim + k.at); });
+  finish_row<ADD>(r, dw, word, k, sum);
 }
 
 struct SortPlan { int bits, passes; };
@@ -590,11 +660,11 @@ EmbedWs embed_ws(int64_t n, int64_t vocab, int64_t dim) {
   w.keys = 0;
   w.idx = list;
   int64_t at = 2 * list;
-  if (n > kSmallSort) {
+  if (n > kTileKeys) {
     w.keys2 = at;
     w.idx2 = at + list;
     w.hist = at + 2 * list;
-    at = w.hist + pad256(((int64_t)1 << p.bits) * w.tiles * 4);
+    at = w.hist + (n > kMergeTiles * kTileKeys ? pad256(((int64_t)1 << p.bits) * w.tiles * 4) : 0);
   }
   w.partial = at;
   w.total = at + (n > kWindow ? pad256((n + kWindow - 1) / kWindow * 2 * dim * 4) : 0);
@@ -616,27 +686,43 @@ hipError_t sort_tile(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint
   return hipGetLastError();
 }
 
+template <int STEPS>
+hipError_t sort_merge(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint32_t* idx,
+                      uint32_t* keys2, uint32_t* idx2, const Fill& fill, hipStream_t s) {
+  hipError_t e = sort_tile<STEPS>(a, p, keys2, idx2, fill, s);
+  if (e != hipSuccess) return e;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_merge),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kMergeTiles * kTileKeys * 4);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_sort_merge, dim3((uint32_t)((a.n + kMergeKeys - 1) / kMergeKeys)),
+                     dim3(kSortThreads), (size_t)pad256(a.n * 4), s, keys2, idx2, (int)a.n,
+                     STEPS * kSortThreads, keys, idx);
+  return hipGetLastError();
+}
+
+// The fewer keys a workgroup sorts the sooner it is done (5, 9 and 16 .. 19 us for
+// 1024, 4096 and 8192), and a merge takes 4 us more; a sort that is done before the
+// zeros are written needs no second launch.
+constexpr int64_t kLongFill = int64_t(96) << 20;   // bytes, 15 us
+
 hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const Fill& fill,
                        hipStream_t s) {
   const SortPlan p = sort_plan(a.vocab);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + w.keys);
   uint32_t* idx = reinterpret_cast<uint32_t*>(ws + w.idx);
   if (a.n <= 1 * kSortThreads) return sort_tile<1>(a, p, keys, idx, fill, s);
+  if (a.n <= 2 * kSortThreads) return sort_tile<2>(a, p, keys, idx, fill, s);
   if (a.n <= kTileKeys) return sort_tile<kTileSteps>(a, p, keys, idx, fill, s);
-  if (a.n <= kSmallSort) return sort_tile<8>(a, p, keys, idx, fill, s);
+  if (a.n <= 8 * kSortThreads && fill.rows * fill.row_bytes >= kLongFill)
+    return sort_tile<8>(a, p, keys, idx, fill, s);
   uint32_t* keys2 = reinterpret_cast<uint32_t*>(ws + w.keys2);
   uint32_t* idx2 = reinterpret_cast<uint32_t*>(ws + w.idx2);
-  if (a.n <= kMergeTiles * kTileKeys) {
-    hipError_t e = sort_tile<kTileSteps>(a, p, keys2, idx2, fill, s);
-    if (e != hipSuccess) return e;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_merge),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, kMergeTiles * kTileKeys * 4);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_sort_merge, dim3((uint32_t)((a.n + kSortThreads - 1) / kSortThreads)),
-                       dim3(kSortThreads), kMergeTiles * kTileKeys * 4, s, keys2, idx2, (int)a.n,
-                       keys, idx);
-    return hipGetLastError();
-  }
+  if (a.n <= kMergeTiles * 1 * kSortThreads)
+    return sort_merge<1>(a, p, keys, idx, keys2, idx2, fill, s);
+  if (a.n <= kMergeTiles * 2 * kSortThreads)
+    return sort_merge<2>(a, p, keys, idx, keys2, idx2, fill, s);
+  if (a.n <= kMergeTiles * kTileKeys)
+    return sort_merge<kTileSteps>(a, p, keys, idx, keys2, idx2, fill, s);
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + w.hist);
   const uint32_t *kin = nullptr, *iin = nullptr;
   for (int q = 0; q < p.passes; ++q) {
@@ -652,6 +738,14 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const 
     iin = sp.idx_out;
   }
   return hipGetLastError();
+}
+
+template <bool ADD, class Y, class G>
+void sum_rows(const RowArgs& r, const Y* dy, G* dw, hipStream_t s) {
+  const dim3 grid((uint32_t)((r.n + kWindow - 1) / kWindow),
+                  (uint32_t)((r.dim + kWaveCols - 1) / kWaveCols));
+  hipLaunchKernelGGL((k_embed_sum<ADD, Y, G>), grid, dim3(64 * kSumWaves), 0, s, r, dy, dw);
+  if (r.n > kWindow) hipLaunchKernelGGL((k_embed_join<ADD, G>), grid, dim3(64), 0, s, r, dw);
 }
 
 template <class Y, class G>
@@ -674,14 +768,9 @@ hipError_t embed_grad(const EmbedArgs& a, const Y* dy, int64_t ld_dy, G* dw, int
   }
   const hipError_t e = sort_tokens(a, w, ws, fill, s);
   if (e != hipSuccess) return e;
-  if (a.n > kWindow)
-    hipLaunchKernelGGL(k_embed_window<Y>,
-                       dim3((uint32_t)((a.n + kWindow - 1) / kWindow),
-                            (uint32_t)((a.dim + kWaveCols - 1) / kWaveCols)),
-                       dim3(64), 0, s, keys, idx, a.n, a.vocab, a.dim, dy, ld_dy, partial);
-  const RowArgs r{keys, idx, a.n, a.vocab, a.dim, ld_dy, ld_dw, partial, a.scale, accumulate};
-  const int waves = a.dim > 2 * kWaveCols ? 4 : a.dim > kWaveCols ? 2 : 1, per = 4 / waves;
-  hipLaunchKernelGGL((k_embed_runs<Y, G>), dim3((uint32_t)((a.n + per - 1) / per)), dim3(256), 0, s, r, waves, dy, dw);
+  const RowArgs r{keys, idx, a.n, a.vocab, a.dim, ld_dy, ld_dw, partial, a.scale};
+  if (accumulate) sum_rows<true>(r, dy, dw, s);
+  else sum_rows<false>(r, dy, dw, s);
   return hipGetLastError();
 }
 

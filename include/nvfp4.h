@@ -327,8 +327,8 @@ int nvfp4_embed(const void* ids, int ids_type, int64_t n, const void* w, int w_t
                 void* stream);
 
 /* The gradient of nvfp4_embed: dw[v] = scale * sum of dy[t] over the tokens t
- * with ids[t] == v, an FP32 sum in ascending t (the same bits every time),
- * rounded once.  Rows of absent words are zeros.  accumulate = 1: added to
+ * with ids[t] == v, an FP32 sum of pieces in ascending t (the same bits every
+ * time), rounded once.  Rows of absent words are zeros.  accumulate = 1: added to
  * dw's own rows instead (rows of absent words are not touched).  Ids outside
  * 0 .. vocab-1 take no gradient.  workspace: 256-byte aligned, of at least
  * nvfp4_embed_grad_workspace_bytes(n, vocab, dim). */

@@ -215,3 +215,36 @@ def test_gradient_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         _check_grad(dw, ids.cpu(), dy.cpu(), V, 1.0)
         assert torch.equal(out, nv.embed(ids, dw, 2.0))
+
+
+@pytest.mark.parametrize("runs", [[16], [17], [15, 1], [1, 15, 16], [16, 48], [16, 49], [64, 64, 1],
+                                  [10, 44, 10, 3], [3, 200, 5, 64, 1], [8, 16, 16, 24, 128, 64]])
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("D", [5, 8, 515, 1030])
+def test_gradient_run_ends(runs, add, D):
+    """Runs of one word that end at, before and after the ends of a wave's 16
+    rows and of a window of 64, the words absent from the vocabulary among them."""
+    say("embed_grad runs", runs, add, D)
+    g = torch.Generator().manual_seed(sum(runs) + D)
+    V = len(runs) + 2
+    for outside in (False, True):
+        ids = torch.cat([torch.full((r,), i + 1) for i, r in enumerate(runs)])
+        if outside:   # the last run's tokens carry no word
+            ids[ids == len(runs)] = V
+        order = torch.randperm(len(ids), generator=g)
+        ids = ids[order]
+        for yt, wt in [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)]:
+            dy, base = _rand(g, len(ids), D, dtype=yt), _rand(g, V, D, dtype=wt)
+            got = base.cuda() if add else None
+            got = nv.embed_grad(ids.cuda(), dy.cuda(), V, 0.7, dtype=wt, accumulate_into=got)
+            _check_grad(got, ids, dy, V, 0.7, base if add else None)
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 4096, 8191, 8192])
+@pytest.mark.parametrize("V,D", [(53, 24), (60001, 420)])
+def test_gradient_with_short_and_long_zeros(n, V, D):
+    """The two sorts of as many tokens: beside a short and beside a long fill."""
+    say("embed_grad fill", n, V, D)
+    g = torch.Generator().manual_seed(n + V)
+    ids, dy = _ids(g, n, V, "outside", torch.int64), _rand(g, n, D)
+    _check_grad(nv.embed_grad(ids.cuda(), dy.cuda(), V), ids, dy, V, 1.0)

@@ -343,36 +343,51 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   }
 }
 
-// codes -> d = g (p - [target]), BF16, in place.  Each thread 8 entries of a
-// row.  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
+// codes -> d = g (p - [target]), BF16, in place; bound by HBM (8192 x 131072: 0.75 ms,
+// 5.7 TB/s).  Each thread four pieces of 8 entries of a row (1000 x 65536: 44 us,
+// with one piece 62).  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
 // close to 1.  A weight of 0 gives zeros whatever the row holds.  Weights are
 // relative to their largest (all 1 for a mean), which multiplies the FP32 results
 // instead: a mean's 1/n, rounded to BF16 in every d alike, would be a common
 // error of up to 2^-8.
+constexpr int kDlogitsVecs = 1024;   // pieces of a workgroup and row
+
 __global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
   const int64_t vecs = g.wide / 8, rows = piece_rows(g);
-  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (v >= vecs) return;
+  const int64_t v0 = (int64_t)blockIdx.x * kDlogitsVecs + threadIdx.x;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    uint16_t* p = g.codes + r * g.ldc + v * 8;
-    const float weight = g.weight[g.first + r];
-    const v4u code = *reinterpret_cast<const v4u*>(p);
-    const int64_t span = v * 8 / kSpan;
-    const float base = (span < g.spans ? g.stats[r * g.spans + span].x : 0.0f) - g.lse2[g.first + r];
-    v8f d;
+    uint16_t* row = g.codes + r * g.ldc;
+    const float weight = g.weight[g.first + r], lse2 = g.lse2[g.first + r];
+    v4u code[kDlogitsVecs / 256];
+    float top[kDlogitsVecs / 256];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = i & 1 ? code[i >> 1] >> 16 : code[i >> 1] & 0xFFFFu;
-      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf((float)c, -kCodeStep, base));
-      d[i] = c == 0xFFFFu && base == base ? 0.0f : e * weight;
+    for (int u = 0; u < kDlogitsVecs / 256; ++u) {
+      const int64_t v = v0 + 256 * u < vecs ? v0 + 256 * u : vecs - 1;
+      code[u] = *reinterpret_cast<const v4u*>(row + v * 8);
+      const int64_t span = v * 8 / kSpan;
+      top[u] = span < g.spans ? g.stats[r * g.spans + span].x : 0.0f;
     }
-    const int64_t at = (int64_t)g.tgt[g.first + r] - v * 8;
-    if (at >= 0 && at < 8) {
-      const float own = expm1f(-g.rloss[g.first + r]) * weight;
+    const int64_t target = (int64_t)g.tgt[g.first + r];
+    const float own = expm1f(-g.rloss[g.first + r]) * weight;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = i == at ? own : d[i];
+    for (int u = 0; u < kDlogitsVecs / 256; ++u) {
+      const int64_t v = v0 + 256 * u;
+      if (v >= vecs) continue;
+      const float base = top[u] - lse2;
+      v8f d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = i & 1 ? code[u][i >> 1] >> 16 : code[u][i >> 1] & 0xFFFFu;
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf((float)c, -kCodeStep, base));
+        d[i] = c == 0xFFFFu && base == base ? 0.0f : e * weight;
+      }
+      const int64_t at = target - v * 8;
+      if (at >= 0 && at < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = i == at ? own : d[i];
+      }
+      *reinterpret_cast<v4u*>(row + v * 8) = weight == 0.0f ? v4u{} : pack8(d);
     }
-    *reinterpret_cast<v4u*>(p) = weight == 0.0f ? v4u{} : pack8(d);
   }
 }
 
@@ -595,7 +610,6 @@ struct PrepArgs {
   Meta* meta;
   int32_t* idx;
   int32_t* tgt;
-  float* weight;
   float* loss;
   float* lse;
   int cus, rows_per_tile;    // of the dH product
@@ -609,8 +623,8 @@ constexpr int kPrepThreads = 1024;
 // the compute units finish earliest, counting a fixed cost per part.
 __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
   __shared__ uint32_t wave_count[kPrepThreads / 64];
-  __shared__ unsigned long long best;
-  __shared__ uint32_t top;
+  __shared__ uint64_t wave_least[kPrepThreads / 64];
+  __shared__ uint32_t wave_most[kPrepThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t n = 0;
   uint32_t most = 0;   // bits of the largest |weight|
@@ -621,6 +635,11 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       target[i] = t + i < p.T ? target_of(p.targets, p.targets_type, t + i) : -1;
+    uint32_t weight[8];   // bits of |weight|, on their way with the targets
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      weight[i] = p.row_weight != nullptr && t + i < p.T
+                      ? __float_as_uint(p.row_weight[t + i]) & 0x7FFFFFFFu : 0u;
     uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) mine += target[i] >= 0 && target[i] < p.V;
@@ -644,8 +663,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
       if (target[i] >= 0 && target[i] < p.V) {
         p.idx[at] = (int32_t)(t + i);
         p.tgt[at] = (int32_t)target[i];
-        if (p.row_weight != nullptr)
-          most = max(most, __float_as_uint(p.row_weight[t + i]) & 0x7FFFFFFFu);
+        most = max(most, weight[i]);
         ++at;
       } else if (t + i < p.T) {
         p.loss[t + i] = 0.0f;
@@ -653,47 +671,57 @@ __global__ __launch_bounds__(kPrepThreads) void k_ce_prep(PrepArgs p) {
       }
     }
   }
-  if (threadIdx.x == 0) {
-    best = ~0ull;
-    top = 0;
-  }
-  __syncthreads();
-  if (most != 0) atomicMax(&top, most);
-  __syncthreads();   // also: idx is written
-  // weights that are all 0, or not all finite, stay as they are
-  float scale = __uint_as_float(top);
-  if (p.row_weight == nullptr) scale = 1.0f / (float)(n > 0 ? n : 1);
-  else if (top == 0 || top >= 0x7F800000u) scale = 1.0f;
-  for (int64_t i = threadIdx.x; i < n; i += kPrepThreads)
-    p.weight[i] = p.row_weight == nullptr ? 1.0f : p.row_weight[p.idx[i]] / scale;
   const int64_t rows = n < p.piece ? n : p.piece;
   const uint32_t tiles = (uint32_t)p.tiles_m * (uint32_t)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
   const uint32_t s = threadIdx.x + 1, steps = (uint32_t)p.steps, cus = (uint32_t)p.cus;
+  uint64_t least = ~0ull;   // (cost, parts)
   if (s == 1 || ((uint64_t)s * tiles <= (uint64_t)p.max_items && s * 8 <= steps)) {
     const uint32_t rounds = (s * tiles + cus - 1) / cus;
-    const uint64_t cost = (uint64_t)rounds * ((steps + s - 1) / s + 8);
-    atomicMin(&best, (unsigned long long)(cost << 16 | s));
+    least = ((uint64_t)rounds * ((steps + s - 1) / s + 8)) << 16 | s;
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    least = min(least, (uint64_t)__shfl_xor((unsigned long long)least, off, 64));
+    most = max(most, (uint32_t)__shfl_xor((int)most, off, 64));
+  }
+  if (lane == 0) {
+    wave_least[wave] = least;
+    wave_most[wave] = most;
   }
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kPrepThreads / 64; ++w) {
+    least = min(least, wave_least[w]);
+    most = max(most, wave_most[w]);
+  }
+  // weights that are all 0, or not all finite, stay as they are
+  float scale = __uint_as_float(most);
+  if (p.row_weight == nullptr) scale = 1.0f / (float)(n > 0 ? n : 1);
+  else if (most == 0 || most >= 0x7F800000u) scale = 1.0f;
   if (threadIdx.x == 0) {
     p.meta->n = (int)n;
-    p.meta->split = (int)(best & 0xFFFFu);
+    p.meta->split = (int)(least & 0xFFFFu);
     p.meta->scale = scale;
   }
 }
 
-// hc[r] = h[idx[r]]; the gradient of a token without a target is zero.
+// hc[r] = h[idx[r]] and the row's weight; the gradient of a token without a target
+// is zero.
 __global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ h, int64_t ldh,
                                                    uint16_t* __restrict__ hc, int64_t ldhc,
                                                    int64_t T, int64_t V, int64_t D, const Meta* meta,
                                                    const int32_t* __restrict__ idx,
+                                                   const float* __restrict__ row_weight,
+                                                   float* __restrict__ weight,
                                                    const void* targets, int targets_type,
                                                    uint16_t* __restrict__ dh, int64_t ld_dh) {
   const int lane = threadIdx.x & 63;
   const int64_t r = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
   if (r >= T) return;
   if (r < meta->n) {
-    const uint16_t* src = h + (int64_t)idx[r] * ldh;
+    const int32_t t = idx[r];
+    const uint16_t* src = h + (int64_t)t * ldh;
+    if (lane == 0) weight[r] = row_weight == nullptr ? 1.0f : row_weight[t] / meta->scale;
     for (int64_t c = lane * 8; c < D; c += 512)
       *reinterpret_cast<v4u*>(hc + r * ldhc + c) = *reinterpret_cast<const v4u*>(src + c);
   }
@@ -798,7 +826,7 @@ void products(const CeArgs& a, int cus, hipStream_t s) {
   if (!a.keep) return;
   const int64_t vecs = a.wide / 8;
   hipLaunchKernelGGL(k_ce_dlogits,
-                     dim3((uint32_t)((vecs + 255) / 256),
+                     dim3((uint32_t)((vecs + kDlogitsVecs - 1) / kDlogitsVecs),
                           (uint32_t)(a.piece < 16384 ? a.piece : 16384)),
                      dim3(256), 0, s, a);
   hipLaunchKernelGGL(k_ce_dh<WN>, grid, block, 0, s, a);
@@ -862,12 +890,13 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
   uint16_t* hc = reinterpret_cast<uint16_t*>(ws + p.hc);
   PrepArgs pa{c.targets, c.targets_type, c.T, c.V, c.D, p.piece, c.row_weight, meta,
               reinterpret_cast<int32_t*>(ws + p.idx), reinterpret_cast<int32_t*>(ws + p.tgt),
-              reinterpret_cast<float*>(ws + p.weight), c.loss, c.lse, cus, 64 * p.wn,
+              c.loss, c.lse, cus, 64 * p.wn,
               a.tiles_dh_m, a.wide / kBK, p.max_items};
   hipLaunchKernelGGL(k_ce_prep, dim3(1), dim3(kPrepThreads), 0, s, pa);
   if (c.T > 0)
     hipLaunchKernelGGL(k_ce_gather, dim3((uint32_t)((c.T + 3) / 4)), dim3(256), 0, s, a.h, c.ldh,
-                       hc, p.ldhc, c.T, c.V, c.D, meta, a.idx, c.targets, c.targets_type, a.dh, c.ld_dh);
+                       hc, p.ldhc, c.T, c.V, c.D, meta, a.idx, c.row_weight,
+                       reinterpret_cast<float*>(ws + p.weight), c.targets, c.targets_type, a.dh, c.ld_dh);
   a.h = hc;
   a.ldh = p.ldhc;
   for (int64_t q = 0; q < p.pieces; ++q) {

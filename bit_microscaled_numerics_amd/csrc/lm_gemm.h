@@ -276,16 +276,22 @@ struct Core {
   // operands were set up with, after start(s0, 0 .. 3).  Steps past it load nothing and
   // read as zero, so the loop runs whole pairs without a branch.  Ends with the
   // stages free.
+  template <class Pace>
   __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
-                                      int64_t s0, int64_t k_end) {
+                                      int64_t s0, int64_t k_end, Pace pace) {
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     Frags<WN> f[4];
     read(f[0], a0, b0, 0);
     for (int64_t s = s0; s * kBK < k_end; s += 2) {
       stage(f, a0, b0, a1, b1, wave, s);
       stage(f, a1, b1, a0, b0, wave, s + 1);
+      pace((int)(s - s0));
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+  __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
+                                      int64_t s0, int64_t k_end) {
+    run(a0, b0, a1, b1, wave, s0, k_end, [](int) {});
   }
 };
 

@@ -297,3 +297,59 @@ def test_offsets_past_32_bits():
     assert (dh.double() - d_dh).norm() <= (2 * HALF + 0.052) * d_dh.norm()
     last = p[:, V - 300:].t() @ h.double()
     assert (dw[V - 300:].double() - last).norm() <= (2 * HALF + 0.052) * last.norm()
+
+
+@pytest.mark.parametrize("V,D", [(100003, 2568), (131072, 2056)])
+def test_long_products(V, D):
+    """8192 tokens and enough words that each workgroup takes thousands of steps, of
+    which the parts of a product differ in length.  64 distinct tokens, repeated with
+    weights of their own, keep the reference small."""
+    say("ce long", V, D)
+    U64, T = 64, 8192
+    hu, w, tu = _inputs(U64, V, D, ignored="none", scale=0.05)
+    rep = torch.arange(T, device="cuda") % U64
+    g = torch.Generator().manual_seed(V)
+    weight = torch.rand(T, generator=g).cuda()
+    weight[weight < 0.05] = 0.0
+    h, t = hu[rep].contiguous(), tu[rep].contiguous()
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t, row_weight=weight)
+    again = nv.linear_ce_grad(h, w, t, row_weight=weight)
+    assert torch.equal(dh, again[2]) and torch.equal(dw, again[3])
+
+    h64, w64 = hu.double(), w.double()
+    z = torch.empty(U64, V, dtype=torch.float64, device="cuda")
+    mag_z = 0.0
+    for v in range(0, V, 8192):
+        part = w64[v:v + 8192].t().contiguous()
+        z[:, v:v + 8192] = h64 @ part
+        mag_z = max(mag_z, float((h64.abs() @ part.abs()).max()))
+    ref_lse = torch.logsumexp(z, 1)
+    at = tu.long().unsqueeze(1)
+    ref_loss = ref_lse - z.gather(1, at).squeeze(1)
+    dz, rel = D * U * mag_z, (80 + V / 128 / 64 + 8) * U + 8 * U
+    assert ((lse.double() - ref_lse[rep]).abs() <= dz + rel + U * ref_lse[rep].abs()).all()
+    assert ((loss.double() - ref_loss[rep]).abs() <= 2 * dz + rel + U * ref_loss[rep].abs()).all()
+    p = torch.exp(z - ref_lse.unsqueeze(1))
+    onehot = torch.zeros_like(p).scatter_(1, at, 1.0)
+    d = p - onehot
+    err = p * (CODE * (1 - onehot) + 2 * (2 * dz + rel) + 8 * U) + 1e-18
+    # weights are held relative to their largest: one more rounding of u each way
+    err = err * (1 + HALF) + (HALF + 3 * U) * d.abs()
+    each = weight.double().unsqueeze(1)
+    total = torch.zeros(U64, 1, dtype=torch.float64, device="cuda").index_add_(0, rep, each)
+    dh_u = tol_dh_u = 0.0
+    h_abs = h64.abs()
+    for v in range(0, V, 8192):
+        part, s = w64[v:v + 8192], slice(v, v + 8192)
+        dh_u = dh_u + d[:, s] @ part
+        e, m = err[:, s].contiguous(), (d[:, s].abs() + err[:, s])
+        tol_dh_u = tol_dh_u + e @ part.abs() + (V + 130) * U * (m @ part.abs())
+        ref = (total * d[:, s]).t().contiguous() @ h64
+        tol = (total * e).t().contiguous() @ h_abs + (T + 130) * U * ((total * m).t().contiguous() @ h_abs)
+        tol = tol + HALF * (ref.abs() + tol)
+        off = (dw[s].double() - ref).abs()
+        assert (off <= tol).all(), ("dw", v, (off - tol).max().item())
+    for i in range(0, T, U64):
+        ref, tol = each[i:i + U64] * dh_u, each[i:i + U64] * tol_dh_u
+        off = (dh[i:i + U64].double() - ref).abs()
+        assert (off <= tol + HALF * (ref.abs() + tol)).all(), ("dh", i)

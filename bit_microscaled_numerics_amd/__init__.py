@@ -743,12 +743,12 @@ def _grad_list(grads, outs):
     """The nvfp4_grad array of a list of gradients (and outputs), and its length."""
     words, types, dev = [], _FLOATS, None
     for g, o in zip(grads, outs):
-        gt = types.get(g.dtype)
-        if gt is None or not g.is_cuda:
+        gt, at_dev = types.get(g.dtype), g.get_device()   # -1: not on a GPU
+        if gt is None or at_dev < 0:
             raise ValueError("gradients must be bf16 or float32 CUDA tensors")
         if dev is None:
             dev = torch.cuda.current_device()
-        if g.get_device() != dev or o.get_device() != dev:
+        if at_dev != dev or (o is not g and o.get_device() != dev):
             raise ValueError("all tensors must be on the current CUDA device")
         if not g.is_contiguous():
             raise ValueError("gradients must be contiguous")
@@ -757,7 +757,7 @@ def _grad_list(grads, outs):
             words += (at, at, g.numel(), gt | gt << 32)
             continue
         ot = types.get(o.dtype)
-        if ot is None or not o.is_cuda or not o.is_contiguous() or o.shape != g.shape:
+        if ot is None or not o.is_contiguous() or o.shape != g.shape:
             raise ValueError("outputs must be contiguous bf16 or float32 CUDA tensors of their "
                              "gradients' shapes")
         words += (at, o.data_ptr(), g.numel(), gt | ot << 32)
@@ -818,9 +818,10 @@ def clip_grads(grads, max_norm: float, out=None, partials: Optional[torch.Tensor
     lib, s = load_library(), _stream(None)
     if partials is None:
         partials = torch.empty(NVFP4_SUMSQ_WORDS, dtype=torch.float64, device=dev)
-        _check(lib.nvfp4_grad_sumsq(lst, n, _p(partials), s))
-    _dev_partials(partials)
-    _check(lib.nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm), s))
+        _check(lib.nvfp4_grad_sumsq(lst, n, partials.data_ptr(), s))
+    else:
+        _dev_partials(partials)
+    _check(lib.nvfp4_grad_clip(lst, n, partials.data_ptr(), max_norm, norm.data_ptr(), s))
     return norm
 
 

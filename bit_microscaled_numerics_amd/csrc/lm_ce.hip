@@ -218,14 +218,6 @@ struct Pace {
   }
 };
 
-template <int WN>
-__device__ __forceinline__ void clear(v16f (&acc)[kWM][WN]) {
-#pragma unroll
-  for (int i = 0; i < kWM; ++i)
-#pragma unroll
-    for (int j = 0; j < WN; ++j) acc[i][j] = v16f{};
-}
-
 // A wave's 32 n x 128 m half-words staged in its own 8 KiB of LDS, row n in 256
 // bytes, chunk c at c ^ (n & 15): 8-byte writes of 4 consecutive m, 16-byte
 // reads of whole rows.
@@ -268,12 +260,23 @@ __device__ __forceinline__ void logits_block(const CeArgs& g, const v16f (&acc)[
   // the reference of the span: this binary32 value itself, so its rounding
   // costs nothing; 0 where every logit is -inf (all exponentials are 0)
   const float m2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2e;
-  float part[4] = {};   // four chains: a single wave per SIMD hides no latency
+  // Eight at a time and four chains of sums: a single wave per SIMD hides no latency,
+  // and left alone the compiler takes them one by one.
+  float part[4] = {};
 #pragma unroll
   for (int i = 0; i < kWM; ++i)
 #pragma unroll
-    for (int v = 0; v < 16; ++v)
-      part[v & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(z(i, v), kLog2e, -m2));
+    for (int v0 = 0; v0 < 16; v0 += 8) {
+      float e[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) e[v] = __builtin_fmaf(z(i, v0 + v), kLog2e, -m2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) e[v] = __builtin_amdgcn_exp2f(e[v]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) part[v & 3] += e[v];
+    }
   float sum = (part[0] + part[1]) + (part[2] + part[3]);
   sum += __shfl_xor(sum, 32, 64);
   if (row < rows && half == 0) g.stats[row * g.spans + m0 / kSpan] = float2{m2, sum};
@@ -340,7 +343,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
   while (more) {
     const int64_t m0 = (int64_t)t.tm * kTM + wm * 128;   // the wave's span of words
     const int64_t row0 = (int64_t)t.tn * 64 * WN + wn * 32 * WN;
-    clear<WN>(core.acc);
     core.run(a0, b0, a1, b1, wave, 0, g.D);
     // the rows' targets, on their way during the set-up of the next tile
     Target target[WN];
@@ -560,7 +562,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
     const int64_t m0 = (int64_t)t.tm * kTM + wm * 128;
     const int64_t n0 = (int64_t)t.tn * 64 * WN + wn * 32 * WN;
     float* part = g.part + ((int64_t)t.item * 4 + wave) * wave_floats(WN);
-    clear<WN>(core.acc);
     pace.item(t, wave, k_end / kBK - s0, per);
     core.run(a0, b0, a1, b1, wave, s0, k_end, [&](int step) { pace(step, wave); });
     more = t.next();
@@ -644,7 +645,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
   while (more) {
     const int64_t m0 = (int64_t)t.tm * kTM + wm * 128, n0 = (int64_t)t.tn * 256 + wn * 128;
     float* acc_at = g.dw_acc + (((int64_t)t.tn * t.tm_all + t.tm) * 4 + wave) * wave_floats(WN);
-    clear<WN>(core.acc);
     pace.item(t, wave, 0, 0);
     core.run(a0, b0, a1, b1, wave, 0, rows, [&](int step) { pace(step, wave); });
     more = t.next();

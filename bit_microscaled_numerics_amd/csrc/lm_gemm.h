@@ -196,12 +196,15 @@ struct Core {
     for (int j = 0; j < WN; ++j) f.b[j] = b.read(sb, ks, j);
   }
 
+  // FIRST: the sums begin here, from the constant zero.
+  template <bool FIRST = false>
   __device__ __forceinline__ void mfma(const Frags<WN>& f) {
 #pragma unroll
     for (int i = 0; i < kWM; ++i)
 #pragma unroll
       for (int j = 0; j < WN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j],
+                                                            FIRST ? v16f{} : acc[i][j], 0, 0, 0);
   }
 
   __device__ __forceinline__ void load_a(uint8_t* sa, int wave, int64_t k0) {
@@ -230,13 +233,14 @@ struct Core {
   }
 
   // One stage: (ca, cb) holds step s, (na, nb) step s + 1; f[0] is read already.
+  template <bool FIRST = false>
   __device__ __forceinline__ void stage(Frags<WN> (&f)[4], uint8_t* ca, uint8_t* cb, uint8_t* na,
                                         uint8_t* nb, int wave, int64_t s) {
     constexpr int kRead = kWM * LA::kReads + WN * LB::kReads;
     constexpr int kLoad = LA::kLoads + LB::kLoads;
 #pragma unroll
     for (int ks = 1; ks < 4; ++ks) read(f[ks], ca, cb, ks);
-    mfma(f[0]);
+    mfma<FIRST>(f[0]);
     interleave<3 * kRead, 0>();
     __builtin_amdgcn_sched_barrier(0);
     // this wave holds the whole stage in registers; when all do, it is free
@@ -273,17 +277,33 @@ struct Core {
     if (part == 3) b.step(k1), load_b(b1, wave, k1);
   }
 
-  // acc += the products of k in [64 s0, k_end), k_end the end that both
+  // acc = the products of k in [64 s0, k_end), k_end the end that both
   // operands were set up with, after start(s0, 0 .. 3).  Steps past it load nothing and
   // read as zero, so the loop runs whole pairs without a branch.  Ends with the
   // stages free.
   template <class Pace>
   __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
                                       int64_t s0, int64_t k_end, Pace pace) {
+    // Narrow tiles start their sums from the constant zero in a first pair of its own
+    // (1 to 2% of 333 x 50257 x 2048); with wide ones that costs spills.
+    constexpr bool kPeel = WN < 4;
+    if (!kPeel) {
+#pragma unroll
+      for (int i = 0; i < kWM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j) acc[i][j] = v16f{};
+    }
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     Frags<WN> f[4];
     read(f[0], a0, b0, 0);
-    for (int64_t s = s0; s * kBK < k_end; s += 2) {
+    int64_t s = s0;
+    if (kPeel) {
+      stage<true>(f, a0, b0, a1, b1, wave, s);
+      stage(f, a1, b1, a0, b0, wave, s + 1);
+      pace(0);
+      s += 2;
+    }
+    for (; s * kBK < k_end; s += 2) {
       stage(f, a0, b0, a1, b1, wave, s);
       stage(f, a1, b1, a0, b0, wave, s + 1);
       pace((int)(s - s0));

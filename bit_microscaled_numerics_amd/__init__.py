@@ -632,16 +632,30 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1
     dtype (dy's if None): row v is scale times the sum of dy's rows whose id
     is v, the same bits every time.  accumulate_into: a gradient that is added to in
     place and returned."""
-    _dev_matrix(dy, "dy")
+    it, yt = _dev_ids(ids, "ids"), _dev_matrix(dy, "dy")
+    n, dim = dy.shape
+    if n != ids.numel():
+        raise ValueError("dy must be [number of ids][columns of dw]")
     dw = accumulate_into
     if dw is None:
-        dw = _empty(vocab, dy.shape[1], dtype=dy.dtype if dtype is None else dtype,
-                    device=dy.device)
-    elif dw.shape[0] != vocab or (dtype is not None and dw.dtype != dtype):
-        raise ValueError("accumulate_into must be [vocab][columns of dy] of the given dtype")
-    n = nvfp4_embed_grad_workspace_bytes(ids.numel(), vocab, dy.shape[1])
-    ws = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
-    nvfp4_embed_grad(ids, dy, scale, dw, accumulate_into is not None, ws)
+        wt = yt if dtype is None else _FLOATS.get(dtype)
+        if wt is None:
+            raise ValueError("dtype must be bf16 or float32")
+        _one_device(ids, dy)
+        dw, pitch = _empty(vocab, dim, dtype=dtype or dy.dtype, device=dy.device), dim
+    else:
+        wt = _dev_matrix(dw, "accumulate_into")
+        if dw.shape != (vocab, dim) or (dtype is not None and dw.dtype != dtype):
+            raise ValueError("accumulate_into must be [vocab][columns of dy] of the given dtype")
+        _one_device(ids, dy, dw)
+        pitch = _pitch(dw, "accumulate_into")
+    size = nvfp4_embed_grad_workspace_bytes(n, vocab, dim)
+    ws = torch.empty(size, dtype=torch.uint8, device=dy.device) if size else None
+    # its own call of the entry point: a few tokens' gradient is bound by the host
+    _check(load_library().nvfp4_embed_grad(ids.data_ptr(), it, n, dy.data_ptr(), yt,
+                                           _pitch(dy, "dy"), vocab, dim, scale, dw.data_ptr(), wt,
+                                           pitch, int(accumulate_into is not None), _p(ws), size,
+                                           _stream(None)))
     return dw
 
 

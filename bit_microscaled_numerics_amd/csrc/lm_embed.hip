@@ -677,10 +677,11 @@ template <int STEPS>
 hipError_t sort_tile(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uint32_t* idx,
                      const Fill& fill, hipStream_t s) {
   const size_t lds = (kSortWaves * kBinsMax + kBinsMax + kSortWaves) * 4 + STEPS * kSortThreads * 6;
-  // above the 64 KiB default of dynamic LDS
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_tile<STEPS>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return e;
+  if (lds > 64 * 1024) {   // above the default of dynamic LDS
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_tile<STEPS>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   const int tiles = (int)((a.n + STEPS * kSortThreads - 1) / (STEPS * kSortThreads));
   const int blocks = tiles + (fill.rows > 0 ? kFillBlocks : 0);
   hipLaunchKernelGGL(k_sort_tile<STEPS>, dim3(blocks), dim3(kSortThreads), lds, s, a, p.bits,

@@ -260,12 +260,14 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bit
     }
 }
 
-// Up to 8 sorted tiles merged: a key's place is its place in its tile, the keys not
+// Up to 16 sorted tiles merged: a key's place is its place in its tile, the keys not
 // above it in the tiles before, and the keys below it in the tiles after.  Every
-// workgroup holds all keys in LDS (up to 128 KiB) and counts by halving for 256 of
-// them: with 1024 the random reads of LDS take 11.2 us instead of 5.  30001 tokens:
-// 16 us with the tiles' sort; the six launches of the pass-by-pass sort below, 31 us.
-constexpr int kMergeTiles = 8, kMergeKeys = kSortThreads / 4;   // keys: of a workgroup
+// workgroup holds all keys in LDS (up to 128 KiB) and counts by halving for 128 of
+// them, 8 lanes a key: with one lane a key the random reads of LDS take twice as long
+// as all else.  30001 tokens: 14 us with the tiles' sort (16 with tiles of 4096); the six
+// launches of the pass-by-pass sort below, 31 us.
+constexpr int kMergeTiles = 16, kMergeMax = 32768, kMergeLanes = 8;
+constexpr int kMergeKeys = kSortThreads / kMergeLanes;   // of a workgroup
 
 __global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __restrict__ keys_in,
                                                              const uint32_t* __restrict__ idx_in,
@@ -275,18 +277,20 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __r
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
   // 16 bytes at a time, all loads out at once (the list is padded to 256 bytes)
-  v4u v[kMergeTiles];
+  constexpr int kLoads = kMergeMax / 4 / kSortThreads;
+  v4u v[kLoads];
 #pragma unroll
-  for (int u = 0; u < kMergeTiles; ++u)
+  for (int u = 0; u < kLoads; ++u)
     if (4 * (u * kSortThreads + (int)threadIdx.x) < n)
       v[u] = reinterpret_cast<const v4u*>(keys_in)[u * kSortThreads + threadIdx.x];
 #pragma unroll
-  for (int u = 0; u < kMergeTiles; ++u)
+  for (int u = 0; u < kLoads; ++u)
     if (4 * (u * kSortThreads + (int)threadIdx.x) < n)
       reinterpret_cast<v4u*>(keys)[u * kSortThreads + threadIdx.x] = v[u];
-  // four neighbouring lanes share a key, each counts in two of the tiles
-  constexpr int kEach = kMergeTiles / 4;
-  const int i = blockIdx.x * kMergeKeys + threadIdx.x / 4, t0 = threadIdx.x % 4 * kEach;
+  // neighbouring lanes share a key, each counts in two of the tiles
+  constexpr int kEach = kMergeTiles / kMergeLanes;
+  const int i = blockIdx.x * kMergeKeys + threadIdx.x / kMergeLanes;
+  const int t0 = threadIdx.x % kMergeLanes * kEach;
   const uint32_t at = i < n ? idx_in[i] : 0;
   __syncthreads();
   if (i >= n) return;
@@ -308,10 +312,10 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_merge(const uint32_t* __r
       if (to <= len[u] && keys[(t0 + u) * tile_keys + to - 1] < limit[u]) below[u] = to;
     }
   int pos = below[0] + below[1];
-  pos += __shfl_xor(pos, 1, 64);
-  pos += __shfl_xor(pos, 2, 64);
+#pragma unroll
+  for (int off = 1; off < kMergeLanes; off <<= 1) pos += __shfl_xor(pos, off, 64);
   pos += i - tile * tile_keys;
-  if (threadIdx.x % 4 == 0) {
+  if (threadIdx.x % kMergeLanes == 0) {
     keys_out[pos] = key;
     idx_out[pos] = at;
   }
@@ -666,7 +670,7 @@ EmbedWs embed_ws(int64_t n, int64_t vocab, int64_t dim) {
     w.keys2 = at;
     w.idx2 = at + list;
     w.hist = at + 2 * list;
-    at = w.hist + (n > kMergeTiles * kTileKeys ? pad256(((int64_t)1 << p.bits) * w.tiles * 4) : 0);
+    at = w.hist + (n > kMergeMax ? pad256(((int64_t)1 << p.bits) * w.tiles * 4) : 0);
   }
   w.partial = at;
   w.total = at + (n > kWindow ? pad256((n + kWindow - 1) / kWindow * 2 * dim * 4) : 0);
@@ -695,7 +699,7 @@ hipError_t sort_merge(const EmbedArgs& a, const SortPlan& p, uint32_t* keys, uin
   hipError_t e = sort_tile<STEPS>(a, p, keys2, idx2, fill, s);
   if (e != hipSuccess) return e;
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_sort_merge),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kMergeTiles * kTileKeys * 4);
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kMergeMax * 4);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_sort_merge, dim3((uint32_t)((a.n + kMergeKeys - 1) / kMergeKeys)),
                      dim3(kSortThreads), (size_t)pad256(a.n * 4), s, keys2, idx2, (int)a.n,
@@ -722,10 +726,8 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const 
   uint32_t* idx2 = reinterpret_cast<uint32_t*>(ws + w.idx2);
   if (a.n <= kMergeTiles * 1 * kSortThreads)
     return sort_merge<1>(a, p, keys, idx, keys2, idx2, fill, s);
-  if (a.n <= kMergeTiles * 2 * kSortThreads)
+  if (a.n <= kMergeMax)
     return sort_merge<2>(a, p, keys, idx, keys2, idx2, fill, s);
-  if (a.n <= kMergeTiles * kTileKeys)
-    return sort_merge<kTileSteps>(a, p, keys, idx, keys2, idx2, fill, s);
   uint32_t* hist = reinterpret_cast<uint32_t*>(ws + w.hist);
   const uint32_t *kin = nullptr, *iin = nullptr;
   for (int q = 0; q < p.passes; ++q) {

@@ -664,6 +664,48 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
 }
 
 // -------------------------------------------------------------- preparation
+// dW of at most 32 tokens: K is at most one pair of MFMA steps, so nothing is staged
+// and the kernel is bound by writing dW.  A wave keeps its 128 columns of h in
+// registers and goes over the words 32 at a time.  (In tiles of 256 x 256 most of the
+// time is their epilogue, all compute units in step: 1 x 65536 x 5120 @A@ us, so @B@.)
+constexpr int kFewTokens = 32;
+
+__global__ __launch_bounds__(256) void k_ce_dw_few(CeArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), half = lane >> 5;
+  const int n = (int)piece_rows(g);
+  const float scale = g.meta->scale;
+  const int64_t m0 = (int64_t)blockIdx.x * 128;
+  const auto eight = [&](const uint16_t* p, int64_t ld, int t0, bool on) {
+    v8u16 x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = on && t0 + e < n ? p[(int64_t)(t0 + e) * ld] : (uint16_t)0;
+    return __builtin_bit_cast(v8bf, x);
+  };
+  v8bf a[2][kWM];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int i = 0; i < kWM; ++i) {
+      const int64_t m = m0 + 32 * i + (lane & 31);
+      a[ks][i] = eight(g.h + m, g.ldh, 16 * ks + 8 * half, m < g.D);
+    }
+  const int64_t groups = (g.V + 31) / 32;
+  for (int64_t q = (int64_t)blockIdx.y * 4 + wave; q < groups; q += (int64_t)gridDim.y * 4) {
+    const int64_t v = q * 32 + (lane & 31);
+    v16f acc[kWM][1];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const v8bf b = eight(g.codes + v, g.ldc, 16 * ks + 8 * half, v < g.V);
+#pragma unroll
+      for (int i = 0; i < kWM; ++i)
+        acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[ks][i], b,
+                                                            ks == 0 ? v16f{} : acc[i][0], 0, 0, 0);
+    }
+    store_rows<1>(acc, 0, epi + wave * 8192, scale, g.dw, g.ld_dw, m0, g.D, q * 32, g.V);
+  }
+}
+
 struct PrepArgs {
   const void* targets;
   int targets_type;
@@ -902,6 +944,12 @@ void products(const CeArgs& a, int wn, int cus, hipStream_t s) {
   else products<4>(a, cus, s);
 }
 
+void dw_few(const CeArgs& a, int cus, hipStream_t s) {
+  const int64_t x = (a.D + 127) / 128, most = (a.V + 127) / 128, fill = (8 * cus + x - 1) / x;
+  hipLaunchKernelGGL(k_ce_dw_few, dim3((uint32_t)x, (uint32_t)(most < fill ? most : fill)),
+                     dim3(256), 0, s, a);
+}
+
 }  // namespace
 
 int64_t ce_workspace_bytes(int64_t T, int64_t V, int64_t D, bool grad, int64_t piece) {
@@ -969,6 +1017,8 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
     if (c.T > 0) products(a, p.wn, cus, s);
     if (p.pieces > 1)
       hipLaunchKernelGGL(k_ce_dw<true>, dim3(cus), dim3(kThreads), 0, s, a);
+    else if (c.T <= kFewTokens)
+      dw_few(a, cus, s);
     else
       hipLaunchKernelGGL(k_ce_dw<false>, dim3(cus), dim3(kThreads), 0, s, a);
   }

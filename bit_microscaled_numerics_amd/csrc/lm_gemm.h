@@ -37,6 +37,7 @@ namespace lm {
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
+typedef uint16_t v8u16 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_void;
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
 

@@ -666,43 +666,60 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
 // -------------------------------------------------------------- preparation
 // dW of at most 32 tokens: K is at most one pair of MFMA steps, so nothing is staged
 // and the kernel is bound by writing dW.  A wave keeps its 128 columns of h in
-// registers and goes over the words 32 at a time.  (In tiles of 256 x 256 most of the
-// time is their epilogue, all compute units in step: 1 x 65536 x 5120 @A@ us, so @B@.)
+// registers and goes over the words 64 at a time: a lane reads two neighbouring
+// words of d at once, and the even and the odd ones are a block of rows each.  (In
+// tiles of 256 x 256 most of the time is their epilogue, all compute units in step:
+// 1 x 65536 x 5120 187 us, so 107, 6.3 TB/s; with 32 tokens 200 and 130.)
 constexpr int kFewTokens = 32;
 
 __global__ __launch_bounds__(256) void k_ce_dw_few(CeArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), half = lane >> 5;
-  const int n = (int)piece_rows(g);
+  const int n = uniform((int)piece_rows(g));
   const float scale = g.meta->scale;
   const int64_t m0 = (int64_t)blockIdx.x * 128;
-  const auto eight = [&](const uint16_t* p, int64_t ld, int t0, bool on) {
-    v8u16 x;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = on && t0 + e < n ? p[(int64_t)(t0 + e) * ld] : (uint16_t)0;
-    return __builtin_bit_cast(v8bf, x);
-  };
-  v8bf a[2][kWM];
+  v8u16 a[2][kWM];
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
     for (int i = 0; i < kWM; ++i) {
       const int64_t m = m0 + 32 * i + (lane & 31);
-      a[ks][i] = eight(g.h + m, g.ldh, 16 * ks + 8 * half, m < g.D);
-    }
-  const int64_t groups = (g.V + 31) / 32;
-  for (int64_t q = (int64_t)blockIdx.y * 4 + wave; q < groups; q += (int64_t)gridDim.y * 4) {
-    const int64_t v = q * 32 + (lane & 31);
-    v16f acc[kWM][1];
+      const int t = 16 * ks + 8 * half;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const v8bf b = eight(g.codes + v, g.ldc, 16 * ks + 8 * half, v < g.V);
+      for (int e = 0; e < 8; ++e)
+        a[ks][i][e] = m < g.D && t + e < n ? g.h[(t + e) * g.ldh + m] : (uint16_t)0;
+    }
+  for (int64_t v0 = ((int64_t)blockIdx.y * 4 + wave) * 64; v0 < g.V; v0 += (int64_t)gridDim.y * 256) {
+    const int64_t v = v0 + 2 * (lane & 31);   // the row of codes goes on past an odd V
+    v8u16 d[2][2];   // [even, odd words][step]
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = 16 * ks + 8 * half + e;
+        const uint32_t two =
+            v < g.V && t < n ? *reinterpret_cast<const uint32_t*>(g.codes + t * g.ldc + v) : 0u;
+        d[0][ks][e] = (uint16_t)two;
+        d[1][ks][e] = (uint16_t)(two >> 16);
+      }
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      v16f acc[kWM][1];
 #pragma unroll
       for (int i = 0; i < kWM; ++i)
-        acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[ks][i], b,
-                                                            ks == 0 ? v16f{} : acc[i][0], 0, 0, 0);
+        acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a[0][i]),
+                                                            __builtin_bit_cast(v8bf, d[odd][0]),
+                                                            v16f{}, 0, 0, 0);
+      if (n > 16) {
+#pragma unroll
+        for (int i = 0; i < kWM; ++i)
+          acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a[1][i]),
+                                                              __builtin_bit_cast(v8bf, d[odd][1]),
+                                                              acc[i][0], 0, 0, 0);
+      }
+      store_rows<1>(acc, 0, epi + wave * 8192, scale, g.dw + (v0 + odd) * g.ld_dw, 2 * g.ld_dw, m0,
+                    g.D, 0, (g.V - v0 - odd + 1) / 2);
     }
-    store_rows<1>(acc, 0, epi + wave * 8192, scale, g.dw, g.ld_dw, m0, g.D, q * 32, g.V);
   }
 }
 
@@ -945,7 +962,7 @@ void products(const CeArgs& a, int wn, int cus, hipStream_t s) {
 }
 
 void dw_few(const CeArgs& a, int cus, hipStream_t s) {
-  const int64_t x = (a.D + 127) / 128, most = (a.V + 127) / 128, fill = (8 * cus + x - 1) / x;
+  const int64_t x = (a.D + 127) / 128, most = (a.V + 255) / 256, fill = (8 * cus + x - 1) / x;
   hipLaunchKernelGGL(k_ce_dw_few, dim3((uint32_t)x, (uint32_t)(most < fill ? most : fill)),
                      dim3(256), 0, s, a);
 }

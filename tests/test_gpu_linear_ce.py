@@ -353,3 +353,25 @@ def test_long_products(V, D):
         ref, tol = each[i:i + U64] * dh_u, each[i:i + U64] * tol_dh_u
         off = (dh[i:i + U64].double() - ref).abs()
         assert (off <= tol + HALF * (ref.abs() + tol)).all(), ("dh", i)
+
+
+@pytest.mark.parametrize("T", [1, 16, 31, 32, 33])
+@pytest.mark.parametrize("V,D", [(1, 8), (63, 136), (1025, 72), (2111, 1000)])
+@pytest.mark.parametrize("ignored", ["none", "some", "all"])
+def test_few_tokens_and_their_words(T, V, D, ignored):
+    """Both sides of the kernel for few tokens; odd vocabularies and widths."""
+    say("ce few", T, V, D, ignored)
+    h, w, t = _inputs(T, V, D, seed=3, ignored=ignored)
+    g = torch.Generator().manual_seed(T)
+    weight = torch.rand(T, generator=g) * torch.randint(0, 2, (T,), generator=g)
+    _, _, dh, dw = _check_all(h, w, t)
+    if ignored == "all":
+        assert not dh.any() and not dw.any()
+    # results inside a wider matrix: nothing is written beside them
+    wide = torch.full((V, D + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    ws = torch.empty(nv.nvfp4_linear_ce_workspace_bytes(T, V, D, True), dtype=torch.uint8, device="cuda")
+    nv.nvfp4_linear_ce_grad(h, w, t, weight.cuda(), 0, loss, lse, dh, wide[:, :D], ws)
+    ref = Ref(h, w, t, weight)
+    _close(wide[:, :D], ref.dw, ref.tol_dw + 3 * U * ref.dw.abs(), "dw")
+    assert torch.all(wide[:, D:] == 3.0)

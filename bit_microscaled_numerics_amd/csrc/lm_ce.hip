@@ -179,6 +179,11 @@ struct Walk {
 // 27.1 -> 26.7 ms on two cards).  At 1300 steps a workgroup it gains nothing.  The
 // wait is a hint only: it is bounded, and a workgroup that waits in vain (mates not
 // running yet) stops taking part.
+// Kernels for shorter products are built without it (ON false): the test in the loop
+// alone costs dW 5% where it has 16 steps a tile.
+constexpr int64_t kPaceSteps = 2048;   // from so many steps a workgroup on
+
+template <bool ON>
 struct Pace {
   uint32_t* count;
   uint32_t due, mates;   // count when all have arrived; workgroups of the XCD
@@ -187,7 +192,7 @@ struct Pace {
 
   __device__ __forceinline__ Pace(Meta* meta, int which, int64_t steps)
       : count(meta->pace[which][blockIdx.x % kXcds]), due(0), mates(gridDim.x / kXcds),
-        short_by(0), on(steps >= 2048) {}
+        short_by(0), on(ON && steps >= kPaceSteps) {}
   __device__ __forceinline__ void arrive(uint32_t n) {
     if ((threadIdx.x & 63) == 0)
       __hip_atomic_fetch_add(count, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -195,6 +200,7 @@ struct Pace {
   // Before an item of `steps` steps; the longest of its round has `most`.  The last
   // round of the XCD may be short of some mates.
   __device__ __forceinline__ void item(const Walk& t, int wave, int64_t steps, int64_t most) {
+    if (!ON) return;
     if (t.item - blockIdx.x / kXcds + mates > t.end) on = false;
     if (!on || wave != 0) return;
     due += short_by * mates;
@@ -202,7 +208,7 @@ struct Pace {
     if (short_by != 0) arrive(short_by);
   }
   __device__ __forceinline__ void operator()(int step, int wave) {
-    if (!on || wave != 0) return;
+    if (!ON || !on || wave != 0) return;
     if (step % 32 == 0) {
       due += mates;
       arrive(1);
@@ -539,7 +545,7 @@ __device__ __forceinline__ void add_acc(v16f (&acc)[kWM][WN], int j, const float
 constexpr int64_t wave_floats(int wn) { return (int64_t)kWM * wn * 16 * 64; }
 
 // dH tile: m over D (W transposed), n over the piece's rows, k over the words.
-template <int WN>
+template <int WN, bool PACED>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[8192 * WN], b1[8192 * WN];
   __shared__ __attribute__((aligned(1024))) uint8_t epi[32768];
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dh(CeArgs g) {
   const int64_t steps = g.wide / kBK, per = (steps + split - 1) / split;
   Walk t(g.tiles_dh_m, (rows + 64 * WN - 1) / (64 * WN), split);
   Core<true, false, WN> core;
-  Pace pace(g.meta, 0, (int64_t)t.total * per / gridDim.x);
+  Pace<PACED> pace(g.meta, 0, (int64_t)t.total * per / gridDim.x);
   int64_t s0 = 0, k_end = 0;
   const auto begin = [&]() {
     s0 = t.part * per;
@@ -641,7 +647,7 @@ __global__ __launch_bounds__(256) void k_ce_dh_join(CeArgs g) {
 
 // dW tile: m over D (H transposed), n over the words (d transposed), k over the
 // piece's rows.  PIECES: the sum goes on over several pieces, held in FP32.
-template <bool PIECES>
+template <bool PIECES, bool PACED>
 __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
   constexpr int WN = 4;
   __shared__ __attribute__((aligned(1024))) uint8_t a0[32768], a1[32768], b0[32768], b1[32768];
@@ -652,7 +658,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
   const float scale = g.meta->scale;
   Walk t((g.D + kTM - 1) / kTM, (g.V + 255) / 256, 1);
   Core<true, true, WN> core;
-  Pace pace(g.meta, 1, (int64_t)t.total * (rows / kBK) / gridDim.x);
+  Pace<PACED> pace(g.meta, 1, (int64_t)t.total * (rows / kBK) / gridDim.x);
   const auto begin = [&]() {
     core.a.init(Operand{g.h + g.first * g.ldh, g.ldh, g.D}, (int64_t)t.tm * kTM, rows, wave,
                 wm * 128);
@@ -973,7 +979,12 @@ void products(const CeArgs& a, int cus, hipStream_t s) {
                      dim3((uint32_t)((vecs + kDlogitsVecs - 1) / kDlogitsVecs),
                           (uint32_t)(a.piece < 16384 ? a.piece : 16384)),
                      dim3(256), 0, s, a);
-  hipLaunchKernelGGL(k_ce_dh<WN>, grid, block, 0, s, a);
+  // wide tiles are what long products have
+  const int64_t steps = a.tiles_dh_m * ((a.piece + 255) / 256) * (a.wide / kBK);
+  if (WN == 4 && steps / cus >= kPaceSteps)
+    hipLaunchKernelGGL((k_ce_dh<WN, WN == 4>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_ce_dh<WN, false>), grid, block, 0, s, a);
   hipLaunchKernelGGL(k_ce_dh_join<WN>, dim3(8 * cus), dim3(256), 0, s, a);
 }
 
@@ -983,10 +994,25 @@ void products(const CeArgs& a, int wn, int cus, hipStream_t s) {
   else products<4>(a, cus, s);
 }
 
-void dw_few(const CeArgs& a, int cus, hipStream_t s) {
+void word_grad_few(const CeArgs& a, int cus, hipStream_t s) {
   const int64_t x = (a.D + 127) / 128, most = (a.V + 255) / 256, fill = (8 * cus + x - 1) / x;
   hipLaunchKernelGGL(k_ce_dw_few, dim3((uint32_t)x, (uint32_t)(most < fill ? most : fill)),
                      dim3(256), 0, s, a);
+}
+
+template <bool PIECES>
+void word_grad(const CeArgs& a, int cus, hipStream_t s) {
+  const int64_t steps = a.tiles_dh_m * ((a.V + 255) / 256) * ((a.piece + kBK - 1) / kBK);
+  if (steps / cus >= kPaceSteps)
+    hipLaunchKernelGGL((k_ce_dw<PIECES, true>), dim3(cus), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_ce_dw<PIECES, false>), dim3(cus), dim3(kThreads), 0, s, a);
+}
+
+void word_grad(const CeArgs& a, bool pieces, int cus, hipStream_t s) {
+  if (pieces) word_grad<true>(a, cus, s);
+  else if (a.T <= kFewTokens) word_grad_few(a, cus, s);
+  else word_grad<false>(a, cus, s);
 }
 
 }  // namespace
@@ -1054,12 +1080,7 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
     a.add = q > 0;
     a.finish = q + 1 == p.pieces;
     if (c.T > 0) products(a, p.wn, cus, s);
-    if (p.pieces > 1)
-      hipLaunchKernelGGL(k_ce_dw<true>, dim3(cus), dim3(kThreads), 0, s, a);
-    else if (c.T <= kFewTokens)
-      dw_few(a, cus, s);
-    else
-      hipLaunchKernelGGL(k_ce_dw<false>, dim3(cus), dim3(kThreads), 0, s, a);
+    word_grad(a, p.pieces > 1, cus, s);
   }
   return hipGetLastError();
 }

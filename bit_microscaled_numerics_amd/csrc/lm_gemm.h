@@ -285,6 +285,7 @@ struct Core {
   template <class Pace>
   __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
                                       int64_t s0, int64_t k_end, Pace pace) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass rejects a second use of what this instantiates
     // Narrow tiles start their sums from the constant zero in a first pair of its own
     // (1 to 2% of 333 x 50257 x 2048); with wide ones that costs spills.
     constexpr bool kPeel = WN < 4;
@@ -310,6 +311,7 @@ struct Core {
       pace((int)(s - s0));
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#endif
   }
   __device__ __forceinline__ void run(uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1, int wave,
                                       int64_t s0, int64_t k_end) {

@@ -86,6 +86,17 @@ __device__ __forceinline__ void store8_from(T* row, Cols k, v8f v) {
     if (i >= k.skip) store1(row + k.at + i, v[i]);
 }
 
+// One dimension of a launch holds fewer than 2^32 threads; a grid past that is taken
+// modulo 2^32 without an error.  Workgroups that are counted by tokens therefore lie
+// along x up to kGridX and go on along z.
+constexpr int64_t kGridX = int64_t(1) << 21;
+
+inline dim3 grid_xz(int64_t blocks, int64_t y = 1) {
+  return dim3((uint32_t)(blocks < kGridX ? blocks : kGridX), (uint32_t)y,
+              (uint32_t)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_xz() { return (int64_t)blockIdx.z * kGridX + blockIdx.x; }
+
 // A wave-uniform value moved to a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(64 * kEmbedWaves) void k_embed(EmbedArgs a, const W
                                                             int64_t ldw, O* __restrict__ out,
                                                             int64_t ldo, int64_t cols_per) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kEmbedWaves + uniform(threadIdx.x >> 6);
+  const int64_t t = block_xz() * kEmbedWaves + uniform(threadIdx.x >> 6);
   if (t >= a.n) return;
   const int64_t id = uniform64(load_id(a.ids, a.ids_type == NVFP4_TYPE_I64, t));
   const bool live = id >= 0 && id < a.vocab;
@@ -786,8 +786,7 @@ hipError_t embed(const EmbedArgs& a, const W* w, int64_t ldw, O* out, int64_t ld
   const int64_t chunks = (a.dim + kWaveCols - 1) / kWaveCols;
   const int64_t cols_per = many ? chunks * kWaveCols : kWaveCols;
   hipLaunchKernelGGL((k_embed<W, O>),
-                     dim3((uint32_t)((a.n + kEmbedWaves - 1) / kEmbedWaves),
-                          (uint32_t)(many ? 1 : chunks)),
+                     grid_xz((a.n + kEmbedWaves - 1) / kEmbedWaves, many ? 1 : chunks),
                      dim3(64 * kEmbedWaves), 0, s, a, w, ldw, out, ldo, cols_per);
   return hipGetLastError();
 }

@@ -248,3 +248,17 @@ def test_gradient_with_short_and_long_zeros(n, V, D):
     g = torch.Generator().manual_seed(n + V)
     ids, dy = _ids(g, n, V, "outside", torch.int64), _rand(g, n, D)
     _check_grad(nv.embed_grad(ids.cuda(), dy.cuda(), V), ids, dy, V, 1.0)
+
+
+def test_lookup_of_more_tokens_than_a_launch_has_threads():
+    """2^26 tokens and some: one wave each is 2^32 threads, more than one dimension of
+    a launch holds."""
+    n, V, D = (1 << 26) + 77, 1000, 8
+    say("embed 2^26", n)
+    g = torch.Generator().manual_seed(1)
+    w = _rand(g, V + 1, D, dtype=torch.bfloat16).cuda()
+    w[V] = 0   # what an id outside gives
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % (V + 1)
+    out = nv.embed(ids, w[:V])
+    for at in range(0, n, 1 << 24):
+        assert torch.equal(out[at:at + (1 << 24)], w[ids[at:at + (1 << 24)].long()])

@@ -478,7 +478,7 @@ template <bool ADD, class A, class Y, class G, class K>
 __device__ __forceinline__ void sum_window(const RowArgs& r, const Y* __restrict__ dy,
                                            G* __restrict__ dw, Pieces<A>& lds, K k, bool on) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t win = blockIdx.x, p0 = win * kWindow + wave * kWaveRows;
+  const int64_t win = block_xz(), p0 = win * kWindow + wave * kWaveRows;
   const int count = uniform((int)(r.n - p0 < 0 ? 0 : r.n - p0 < kWaveRows ? r.n - p0 : kWaveRows));
   // lane l: the key of position p0 + l - 1 (no key outside the list), and its row
   const int64_t at = p0 + lane - 1;
@@ -616,7 +616,7 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* __restrict__ keys
 // of that window, then piece 0 of those after it.
 template <bool ADD, class G>
 __global__ __launch_bounds__(64) void k_embed_join(RowArgs r, G* __restrict__ dw) {
-  const int64_t win = blockIdx.x, s = win * kWindow, e = s + kWindow;
+  const int64_t win = block_xz(), s = win * kWindow, e = s + kWindow;
   if (e >= r.n) return;
   const uint32_t word = r.keys[e];
   if (word >= (uint32_t)r.vocab || r.keys[e - 1] != word) return;
@@ -747,8 +747,7 @@ hipError_t sort_tokens(const EmbedArgs& a, const EmbedWs& w, uint8_t* ws, const 
 
 template <bool ADD, class Y, class G>
 void sum_rows(const RowArgs& r, const Y* dy, G* dw, hipStream_t s) {
-  const dim3 grid((uint32_t)((r.n + kWindow - 1) / kWindow),
-                  (uint32_t)((r.dim + kWaveCols - 1) / kWaveCols));
+  const dim3 grid = grid_xz((r.n + kWindow - 1) / kWindow, (r.dim + kWaveCols - 1) / kWaveCols);
   hipLaunchKernelGGL((k_embed_sum<ADD, Y, G>), grid, dim3(64 * kSumWaves), 0, s, r, dy, dw);
   if (r.n > kWindow) hipLaunchKernelGGL((k_embed_join<ADD, G>), grid, dim3(64), 0, s, r, dw);
 }

@@ -262,3 +262,16 @@ def test_lookup_of_more_tokens_than_a_launch_has_threads():
     out = nv.embed(ids, w[:V])
     for at in range(0, n, 1 << 24):
         assert torch.equal(out[at:at + (1 << 24)], w[ids[at:at + (1 << 24)].long()])
+
+
+def test_gradient_of_more_tokens_than_a_launch_has_threads():
+    """2^30 tokens and some.  Every gradient is 1, so a piece of a sum is a whole number;
+    sums of whole windows are multiples of 64 below 2^30, exact in binary32, and only the
+    few other pieces round."""
+    n, V = (1 << 30) + 130, 3
+    say("embed_grad 2^30", n)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % 4   # a quarter carries no word
+    dy = torch.ones(n, 1, dtype=torch.bfloat16, device="cuda")
+    got = nv.embed_grad(ids, dy, V, dtype=torch.float32).cpu().double()
+    want = torch.tensor([(n - v + 3) // 4 for v in range(V)], dtype=torch.float64).unsqueeze(1)
+    assert torch.all((got - want).abs() <= want * 8 * U32), (got, want)

@@ -378,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
 // there, so that lse - z loses nothing to the size of lse.
 __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  const int64_t r = block_xz() * 4 + uniform(threadIdx.x >> 6);
   if (r >= piece_rows(g)) return;
   const float2* st = g.stats + r * g.spans;
   // four spans a lane on their way at once (1 x 131072: 10.3 -> 7.2 us,
@@ -865,7 +865,7 @@ __global__ __launch_bounds__(256) void k_ce_gather(const uint16_t* __restrict__ 
                                                    const void* targets, int targets_type,
                                                    uint16_t* __restrict__ dh, int64_t ld_dh) {
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  const int64_t r = block_xz() * 4 + uniform(threadIdx.x >> 6);
   if (r >= T) return;
   if (r < meta->n) {
     const int32_t t = idx[r];
@@ -972,7 +972,7 @@ void products(const CeArgs& a, int cus, hipStream_t s) {
     hipLaunchKernelGGL((k_ce_logits<WN, true>), grid, block, 0, s, a);
   else
     hipLaunchKernelGGL((k_ce_logits<WN, false>), grid, block, 0, s, a);
-  hipLaunchKernelGGL(k_ce_rows, dim3((uint32_t)((a.piece + 3) / 4)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_ce_rows, grid_xz((a.piece + 3) / 4), dim3(256), 0, s, a);
   if (!a.keep) return;
   const int64_t vecs = a.wide / 8;
   hipLaunchKernelGGL(k_ce_dlogits,
@@ -1070,8 +1070,8 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
               a.tiles_dh_m, a.wide / kBK, p.max_items};
   hipLaunchKernelGGL(k_ce_prep, dim3(1), dim3(kPrepThreads), 0, s, pa);
   if (c.T > 0)
-    hipLaunchKernelGGL(k_ce_gather, dim3((uint32_t)((c.T + 3) / 4)), dim3(256), 0, s, a.h, c.ldh,
-                       hc, p.ldhc, c.T, c.V, c.D, meta, a.idx, c.row_weight,
+    hipLaunchKernelGGL(k_ce_gather, grid_xz((c.T + 3) / 4), dim3(256), 0, s, a.h, c.ldh, hc,
+                       p.ldhc, c.T, c.V, c.D, meta, a.idx, c.row_weight,
                        reinterpret_cast<float*>(ws + p.weight), c.targets, c.targets_type, a.dh, c.ld_dh);
   a.h = hc;
   a.ldh = p.ldhc;

@@ -375,3 +375,28 @@ def test_few_tokens_and_their_words(T, V, D, ignored):
     ref = Ref(h, w, t, weight)
     _close(wide[:, :D], ref.dw, ref.tol_dw + 3 * U * ref.dw.abs(), "dw")
     assert torch.all(wide[:, D:] == 3.0)
+
+
+def test_more_tokens_than_a_launch_has_threads():
+    """2^26 tokens and some: one wave each is 2^32 threads, more than one dimension of
+    a launch holds.  The first and the last tokens have targets."""
+    T, V, D, U64 = (1 << 26) + 71, 5, 8, 64
+    say("ce 2^26", T)
+    hu, w, tu = _inputs(U64, V, D, ignored="none")
+    rep = torch.arange(T, device="cuda", dtype=torch.int32) % U64
+    h, t = hu.repeat(T // U64 + 1, 1)[:T], tu.repeat(T // U64 + 1)[:T]   # row i is hu[rep[i]]
+    ref = Ref(hu, w, tu)
+    loss, lse = nv.linear_ce(h, w, t)
+    for s in (slice(0, 1 << 20), slice(T - (1 << 20), T), slice((1 << 26) - 512, T)):
+        r = rep[s].cpu().long()
+        _close(loss[s], ref.loss[r], ref.tol_loss[r], "loss")
+        _close(lse[s], ref.lse[r], ref.tol_lse[r], "lse")
+    cut = 500   # live tokens at either end
+    t[cut:T - cut] = -100
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t)
+    ends = torch.cat([torch.arange(cut), torch.arange(T - cut, T)]).cuda()
+    ref = Ref(h[ends], w, t[ends])
+    _close(loss[ends], ref.loss, ref.tol_loss, "loss with gradient")
+    _close(dh[ends], ref.dh, ref.tol_dh, "dh")
+    _close(dw, ref.dw, ref.tol_dw, "dw")
+    assert not loss[cut:T - cut].any() and not dh[cut:T - cut].any()

@@ -52,13 +52,24 @@ class EmbeddingFunction(torch.autograd.Function):
         return None, embed_grad(flat, dy, ctx.vocab, ctx.scale, ctx.dtype), None, None
 
 
+def _total(x: torch.Tensor) -> torch.Tensor:
+    """The sum of a vector.  A torch sum over more than about 10^5 values is joined by
+    several workgroups through a counter that a memset clears; a captured graph does not
+    repeat that reliably (the mean of 300007 losses was 0 from the second replay on), so a
+    long vector is summed in rows first."""
+    while x.numel() > 32768:
+        whole = x.numel() // 512 * 512
+        x = torch.cat((x[:whole].view(-1, 512).sum(1), x[whole:]))
+    return x.sum()
+
+
 def _reduce(loss: torch.Tensor, targets: torch.Tensor, vocab: int,
             row_weight: Optional[torch.Tensor]) -> torch.Tensor:
     """The weighted sum, or the mean over the tokens that have a target."""
     live = (targets >= 0) & (targets < vocab)
     if row_weight is None:
-        return loss.sum() / live.sum().clamp(min=1)
-    return torch.where(live, loss * row_weight, torch.zeros_like(loss)).sum()
+        return _total(loss) / _total(live).clamp(min=1)
+    return _total(torch.where(live, loss * row_weight, torch.zeros_like(loss)))
 
 
 class LinearCrossEntropyFunction(torch.autograd.Function):

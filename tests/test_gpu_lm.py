@@ -227,3 +227,33 @@ def test_example_learns_and_repeats(tied):
         assert abs(first[0][0] - math.log(500)) < 1.0
     assert first[-1][0] < first[0][0] - 0.1
     assert ex.train(12, 500, 64, 2048, tied) == first
+
+
+@pytest.mark.parametrize("train", [False, True])
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_loss_of_many_tokens_in_a_graph(train, reduction):
+    """The captured loss, replayed on fresh inputs with eager work between, is the eager one."""
+    say("lm graph", train, reduction)
+    T, V, D = 300007, 40, 8
+    x = torch.randn(T, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    w = torch.randn(V, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    t = torch.randint(-1, V, (T,), generator=torch.Generator().manual_seed(3)).cuda()
+    x.requires_grad_(train)
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        lm.linear_cross_entropy(x, w, t, reduction=reduction)
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = lm.linear_cross_entropy(x, w, t, reduction=reduction)
+    for seed in range(4):
+        g = torch.Generator().manual_seed(10 + seed)
+        with torch.no_grad():
+            x.copy_(torch.randn(T, D, generator=g))
+            t.copy_(torch.randint(-1 - seed, V, (T,), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = loss.item()
+        eager = lm.linear_cross_entropy(x, w, t, reduction=reduction).item()
+        assert got == eager, seed

@@ -75,21 +75,24 @@ def _reduce(loss: torch.Tensor, targets: torch.Tensor, vocab: int,
 class LinearCrossEntropyFunction(torch.autograd.Function):
     """The loss of the head z = x weight^T, FP32: the sum over tokens of
     row_weight * loss, or the mean over the tokens that have a target (row_weight
-    None; 0 if none has).  x [T][dim], weight [vocab][dim], both bf16."""
+    None; 0 if none has).  x [T][dim], weight [vocab][dim], both bf16.  Differentiable
+    by x, weight and row_weight."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                 row_weight: Optional[torch.Tensor], piece_tokens: int):
         loss, _, dx, dw = linear_ce_grad(x, weight, targets, row_weight, piece_tokens)
-        ctx.save_for_backward(dx, dw)
+        # a token's loss (0 without a target) is the derivative by its weight
+        ctx.save_for_backward(dx, dw, loss if ctx.needs_input_grad[3] else None)
         return _reduce(loss, targets, weight.shape[0], row_weight)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dloss: torch.Tensor):
-        dx, dw = ctx.saved_tensors
-        dx, dw = scale_grads((dx, dw), dloss.float().reshape(1).contiguous())
-        return dx, dw, None, None, None
+        dx, dw, loss = ctx.saved_tensors
+        dloss = dloss.float().reshape(1).contiguous()
+        dx, dw = scale_grads((dx, dw), dloss)
+        return dx, dw, None, None if loss is None else loss * dloss, None
 
 
 class TokenLossFunction(torch.autograd.Function):

@@ -257,3 +257,19 @@ def test_loss_of_many_tokens_in_a_graph(train, reduction):
         got = loss.item()
         eager = lm.linear_cross_entropy(x, w, t, reduction=reduction).item()
         assert got == eager, seed
+
+
+@pytest.mark.parametrize("frozen", [False, True])
+def test_row_weights_take_a_gradient(frozen):
+    """d(sum of weight * loss)/d weight_t is token t's loss, 0 without a target, whether
+    x and weight are trained or not."""
+    say("lm row weight", frozen)
+    x, w, t = _data()
+    ref, _, _ = _reference(x, w, t)
+    x.requires_grad_(not frozen)
+    w.requires_grad_(not frozen)
+    rw = torch.rand(96, generator=torch.Generator().manual_seed(6)).cuda().requires_grad_()
+    (lm.linear_cross_entropy(x, w, t, rw, reduction="sum") * 2.0).backward()
+    assert rw.grad is not None and rw.grad.dtype == torch.float32
+    assert torch.all((rw.grad.double().cpu() - 2 * ref).abs() <= 2e-4)
+    assert torch.all(rw.grad[t < 0] == 0)

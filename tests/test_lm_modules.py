@@ -1,0 +1,82 @@
+"""The torch layer of the head and its loss on the CPU, with the library's calls replaced
+by their definitions: what is differentiable, what is handed on, what is refused."""
+import pytest
+import torch
+
+from bit_microscaled_numerics_amd import lm
+
+
+def _ce(h, w, t):
+    """nv.linear_ce's contract in binary32: (loss, lse)."""
+    z = h.float() @ w.float().t()
+    live = (t >= 0) & (t < w.shape[0])
+    at = t.clamp(0, w.shape[0] - 1).long().unsqueeze(1)
+    lse = torch.logsumexp(z, 1)
+    return torch.where(live, lse - z.gather(1, at).squeeze(1), torch.zeros_like(lse)), lse
+
+
+def _ce_grad(h, w, t, row_weight=None, piece_tokens=0):
+    """nv.linear_ce_grad's contract: (loss, lse, dh, dw)."""
+    live = (t >= 0) & (t < w.shape[0])
+    if row_weight is None:
+        row_weight = torch.full((h.shape[0],), 1.0 / max(1, int(live.sum())))
+    with torch.enable_grad():
+        hr, wr = h.detach().float().requires_grad_(), w.detach().float().requires_grad_()
+        loss, lse = _ce(hr, wr, t)
+        dh, dw = torch.autograd.grad((loss * row_weight.detach()).sum(), (hr, wr))
+    return loss.detach(), lse.detach(), dh.to(h.dtype), dw.to(w.dtype)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The definitions in place of the library; collects what they are given."""
+    log = {"operands": [], "scaled": []}
+
+    def ce(h, w, t):
+        log["operands"].append((h, w))
+        return _ce(h, w, t)
+
+    def ce_grad(h, w, t, row_weight=None, piece_tokens=0):
+        log["operands"].append((h, w))
+        return _ce_grad(h, w, t, row_weight, piece_tokens)
+
+    def scale(grads, factor):
+        log["scaled"].append(len(grads))
+        return [(g.float() * factor).to(g.dtype) for g in grads]
+
+    monkeypatch.setattr(lm, "linear_ce", ce)
+    monkeypatch.setattr(lm, "linear_ce_grad", ce_grad)
+    monkeypatch.setattr(lm, "scale_grads", scale)
+    return log
+
+
+def _data(T=24, V=30, D=16):
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(T, D, generator=g).to(torch.bfloat16)
+    w = (torch.randn(V, D, generator=g) * 0.2).to(torch.bfloat16)
+    t = torch.randint(0, V, (T,), generator=g)
+    t[::5] = -100
+    return x, w, t
+
+
+@pytest.mark.parametrize("shape", [(24,), (4, 6)])
+@pytest.mark.parametrize("train_x,train_w", [(True, True), (True, False), (False, True),
+                                             (False, False)])
+def test_row_weights_take_a_gradient(calls, shape, train_x, train_w):
+    """d(sum of weight * loss)/d weight_t = loss_t whichever of x and weight is trained."""
+    x, w, t = _data()
+    loss, _ = _ce(x, w, t)
+    x.requires_grad_(train_x)
+    w.requires_grad_(train_w)
+    rw = torch.rand(24, generator=torch.Generator().manual_seed(1)).view(shape).requires_grad_()
+    out = lm.linear_cross_entropy(x.view(*shape, 16), w, t.view(shape), rw, reduction="sum")
+    (out * 3.0).backward()
+    assert rw.grad.shape == shape
+    assert torch.allclose(rw.grad.reshape(-1), 3 * loss, rtol=1e-6, atol=0)
+    assert torch.all(rw.grad.reshape(-1)[t < 0] == 0)
+    # a weight formed from parameters trains them
+    a = torch.tensor(0.5, requires_grad=True)
+    lm.linear_cross_entropy(x.view(*shape, 16), w, t.view(shape), torch.exp(a).expand(shape),
+                            reduction="sum").backward()
+    want = loss.sum().item() * torch.exp(torch.tensor(0.5)).item()
+    assert abs(a.grad.item() - want) <= 1e-5 * want

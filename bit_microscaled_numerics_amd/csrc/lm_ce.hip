@@ -62,6 +62,7 @@ struct Meta {
 struct CeArgs {
   const uint16_t* h;       // [.][ldh]: the tokens themselves, or the gathered ones
   const uint16_t* w;
+  uint16_t* hc;            // h where it is the gathered ones, else null
   int64_t ldh, ldw, T, V, D;
   Meta* meta;              // null: all T tokens
   int64_t first, piece;    // this piece's first row and most rows
@@ -418,7 +419,8 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
 // codes -> d = g (p - [target]), BF16, in place; bound by HBM (8192 x 131072: 0.75 ms,
 // 5.7 TB/s).  Each thread four pieces of 8 entries of a row (1000 x 65536: 44 us,
 // with one piece 62).  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
-// close to 1.  A weight of 0 gives zeros whatever the row holds.  Weights are
+// close to 1.  A weight of 0 masks a row: zeros whatever it holds, and its gathered h is
+// cleared too, since 0 times an infinity or NaN there would reach all of dW.  Weights are
 // relative to their largest (all 1 for a mean), which multiplies the FP32 results
 // instead: a mean's 1/n, rounded to BF16 in every d alike, would be a common
 // error of up to 2^-8.
@@ -432,6 +434,9 @@ __global__ __launch_bounds__(256) void k_ce_dlogits(CeArgs g) {
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     uint16_t* row = g.codes + r * g.ldc;
     const float weight = g.weight[g.first + r], lse2 = g.lse2[g.first + r];
+    if (weight == 0.0f && blockIdx.x == 0)
+      for (int64_t c = threadIdx.x * 8; c < g.D; c += 2048)
+        *reinterpret_cast<v4u*>(g.hc + (g.first + r) * g.ldh + c) = v4u{};
     v4u code[kDlogitsVecs / 256];
     float top[kDlogitsVecs / 256];
 #pragma unroll
@@ -1073,7 +1078,7 @@ hipError_t launch_ce(const CeCall& c, hipStream_t s) {
     hipLaunchKernelGGL(k_ce_gather, grid_xz((c.T + 3) / 4), dim3(256), 0, s, a.h, c.ldh, hc,
                        p.ldhc, c.T, c.V, c.D, meta, a.idx, c.row_weight,
                        reinterpret_cast<float*>(ws + p.weight), c.targets, c.targets_type, a.dh, c.ld_dh);
-  a.h = hc;
+  a.h = a.hc = hc;
   a.ldh = p.ldhc;
   for (int64_t q = 0; q < p.pieces; ++q) {
     a.first = q * p.piece;

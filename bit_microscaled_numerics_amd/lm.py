@@ -69,7 +69,10 @@ def _reduce(loss: torch.Tensor, targets: torch.Tensor, vocab: int,
     live = (targets >= 0) & (targets < vocab)
     if row_weight is None:
         return _total(loss) / _total(live).clamp(min=1)
-    return _total(torch.where(live, loss * row_weight, torch.zeros_like(loss)))
+    # a weight of 0 masks a token also where its loss is not finite
+    term = loss * row_weight
+    return _total(torch.where(live & ((row_weight != 0) | (term == 0)), term,
+                              torch.zeros_like(loss)))
 
 
 class LinearCrossEntropyFunction(torch.autograd.Function):

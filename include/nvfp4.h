@@ -360,7 +360,9 @@ int nvfp4_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, int6
  * BF16, accumulated in FP32 (d enters the products rounded to BF16).  dh, dw:
  * row pitches multiples of 8, 16-byte aligned.  A token without a target costs
  * no arithmetic, has a zero row in dh and an lse of 0, and nothing in its row
- * of h (infinities, NaN) reaches another result.
+ * of h (infinities, NaN) reaches another result.  A row_weight of 0 masks a token
+ * for the gradients: whatever its row of h holds, its row of dh is zero and dw
+ * takes nothing from it (its loss is still written).
  * Tokens are taken piece_tokens at a time (0: as many as a buffer of 4 GiB
  * allows at 2 bytes per token and word); the workspace is
  * nvfp4_linear_ce_workspace_bytes(T, V, D, 1, piece_tokens) bytes.  The result

@@ -400,3 +400,26 @@ def test_more_tokens_than_a_launch_has_threads():
     _close(dh[ends], ref.dh, ref.tol_dh, "dh")
     _close(dw, ref.dw, ref.tol_dw, "dw")
     assert not loss[cut:T - cut].any() and not dh[cut:T - cut].any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [20, 100])
+def test_nonfinite_rows_of_weight_zero_reach_no_gradient(T, bad):
+    """A weight of 0 masks a token: what its row holds stays out of dh and dw."""
+    say("ce weight 0", T, bad)
+    h, w, t = _inputs(T, 300, 64, ignored="none")
+    weight = torch.rand(T, generator=torch.Generator().manual_seed(4)).cuda()
+    weight[5:9] = 0.0
+    weight[11] = -0.0
+    want = nv.linear_ce_grad(h, w, t, row_weight=weight)
+    h[5:9], h[11] = bad, bad
+    for piece in (0, 16):
+        loss, lse, dh, dw = nv.linear_ce_grad(h, w, t, row_weight=weight, piece_tokens=piece)
+        keep = weight != 0
+        assert torch.equal(loss[keep], want[0][keep]) and not torch.isfinite(loss[~keep]).any()
+        assert torch.equal(dh, want[2]) and torch.all(dh[~keep] == 0)
+        if piece == 0:
+            assert torch.equal(dw, want[3])
+        else:
+            ref = Ref(torch.where(keep.unsqueeze(1), h, torch.zeros_like(h)), w, t, weight)
+            _close(dw, ref.dw, ref.tol_dw, "dw in pieces")

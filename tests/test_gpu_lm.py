@@ -273,3 +273,30 @@ def test_row_weights_take_a_gradient(frozen):
     assert rw.grad is not None and rw.grad.dtype == torch.float32
     assert torch.all((rw.grad.double().cpu() - 2 * ref).abs() <= 2e-4)
     assert torch.all(rw.grad[t < 0] == 0)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_masked_tokens_may_hold_anything(bad):
+    """Tokens masked by a weight of 0, or by a choice among the tokens' losses: the loss and
+    the gradients are those of the other tokens."""
+    say("lm masked", bad)
+    x, w, t = _data()
+    mask = torch.arange(96, device="cuda") % 5 == 2
+    weight = torch.where(mask, 0.0, 0.5)
+    zeros = torch.where(mask.unsqueeze(1), torch.zeros_like(x), x)
+    ref, dx, dw = _reference(zeros, w, t, weight)
+    total = (ref * weight.double().cpu()).sum().item()
+    x = torch.where(mask.unsqueeze(1), torch.full_like(x, bad), x)
+    for mode in ("weights", "tokens"):
+        xg, wg = x.clone().requires_grad_(), w.clone().requires_grad_()
+        if mode == "weights":
+            loss = lm.linear_cross_entropy(xg, wg, t, weight, reduction="sum")
+        else:
+            tokens = lm.linear_cross_entropy(xg, wg, t, reduction="none")
+            loss = torch.where(mask, torch.zeros_like(tokens), tokens * 0.5).sum()
+        assert abs(loss.item() - total) <= 1e-3
+        loss.backward()
+        _near(xg.grad, dx, 2.5 * HALF)
+        _near(wg.grad, dw, 2.5 * HALF)
+        with torch.no_grad():
+            assert abs(lm.linear_cross_entropy(x, w, t, weight, reduction="sum").item() - total) <= 1e-3

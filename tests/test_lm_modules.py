@@ -80,3 +80,23 @@ def test_row_weights_take_a_gradient(calls, shape, train_x, train_w):
                             reduction="sum").backward()
     want = loss.sum().item() * torch.exp(torch.tensor(0.5)).item()
     assert abs(a.grad.item() - want) <= 1e-5 * want
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("train", [False, True])
+def test_losses_of_weight_zero_do_not_count(calls, bad, train):
+    """A masked token's loss that is not finite stays out of the sum; a finite one still
+    has its derivative by the weight."""
+    x, w, t = _data()
+    loss, _ = _ce(x, w, t)
+    weight = torch.full((24,), 0.5)
+    weight[7] = weight[8] = 0.0
+    want = (loss * weight).sum().item()
+    x[7] = bad
+    x.requires_grad_(train)
+    weight.requires_grad_()
+    out = lm.linear_cross_entropy(x, w, t, weight, reduction="sum")
+    assert abs(out.item() - want) <= 1e-5 * want
+    out.backward()
+    keep = torch.arange(24) != 7
+    assert torch.allclose(weight.grad[keep], loss[keep], rtol=1e-6, atol=0)

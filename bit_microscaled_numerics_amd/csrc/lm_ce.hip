@@ -376,7 +376,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_logits(CeArgs g) {
 
 // ----------------------------------------------------------------- row sums
 // One wave per row: the spans' (maximum, sum) joined; loss in binary64 from
-// there, so that lse - z loses nothing to the size of lse.
+// there, so that lse - z loses nothing to the size of lse.  The sums are FP32: relative to
+// a sum near 1 they are off by some 2^-24, and so is a small loss in absolute terms.  It is
+// held at 0 or more (lse >= z; NaN stays).
 __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   const int lane = threadIdx.x & 63;
   const int64_t r = block_xz() * 4 + uniform(threadIdx.x >> 6);
@@ -406,7 +408,8 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   const double lse = (double)mx * (1.0 / (double)kLog2e) + log((double)sum);
   Target target;
   target.load(g, row);
-  const float loss = target.exists(g) ? (float)(lse - (double)g.tlogit[row]) : 0.0f;
+  float loss = target.exists(g) ? (float)(lse - (double)g.tlogit[row]) : 0.0f;
+  loss = loss < 0.0f ? 0.0f : loss;
   const int64_t t = g.idx == nullptr ? row : g.idx[row];
   g.loss[t] = loss;
   if (g.lse != nullptr) g.lse[t] = (float)lse;
@@ -418,10 +421,11 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
 
 // codes -> d = g (p - [target]), BF16, in place; bound by HBM (8192 x 131072: 0.75 ms,
 // 5.7 TB/s).  Each thread four pieces of 8 entries of a row (1000 x 65536: 44 us,
-// with one piece 62).  At the target p - 1 = exp(-loss) - 1 directly, exact also where p is
-// close to 1.  A weight of 0 masks a row: zeros whatever it holds, and its gathered h is
-// cleared too, since 0 times an infinity or NaN there would reach all of dW.  Weights are
-// relative to their largest (all 1 for a mean), which multiplies the FP32 results
+// with one piece 62).  At the target p - 1 = exp(-loss) - 1, which loses nothing to a p
+// close to 1 beyond the loss's own error: some 2^-24, more than the BF16 rounding of d once
+// 1 - p is below about 1e-5.  A weight of 0 masks a row: zeros whatever it holds, and its
+// gathered h is cleared too, since 0 times an infinity or NaN there would reach all of dW.
+// Weights are relative to their largest (all 1 for a mean), which multiplies the FP32 results
 // instead: a mean's 1/n, rounded to BF16 in every d alike, would be a common
 // error of up to 2^-8.
 constexpr int kDlogitsVecs = 1024;   // pieces of a workgroup and row

@@ -343,7 +343,8 @@ int nvfp4_embed_grad(const void* ids, int ids_type, int64_t n, const void* dy, i
  *   lse[t]  = log sum_v exp(z_tv),   loss[t] = lse[t] - z_t,targets[t].
  * h [T][D] and w [V][D] are BF16 with D and both row pitches multiples of 8
  * and 16-byte aligned bases; loss and lse (nullable) FP32 [T]; targets I32 or
- * I64.  A target outside 0 .. V-1 (an ignore mark such as -100) is none: its
+ * I64.  loss is never negative; its error is that of FP32 sums, absolute where it
+ * is small.  A target outside 0 .. V-1 (an ignore mark such as -100) is none: its
  * loss is 0.  The logits are never stored.  T may be 0.  Rows whose logits are
  * not all finite give a loss and gradient that are not finite; other rows are
  * not affected.  workspace: 256-byte aligned, of at least

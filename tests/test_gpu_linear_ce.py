@@ -423,3 +423,29 @@ def test_nonfinite_rows_of_weight_zero_reach_no_gradient(T, bad):
         else:
             ref = Ref(torch.where(keep.unsqueeze(1), h, torch.zeros_like(h)), w, t, weight)
             _close(dw, ref.dw, ref.tol_dw, "dw in pieces")
+
+
+@pytest.mark.parametrize("V", [300, 4099])
+def test_confident_tokens(V):
+    """Targets that lead by 1 .. 60 in the logit: the losses of the surest are below what
+    binary32 sums near 1 can show, and still not negative, nor does the gradient push a
+    target away; within the bounds above."""
+    T, D = 60, 64
+    say("ce confident", V)
+    g = torch.Generator().manual_seed(V)
+    w = (torch.randn(V, D, generator=g) * 0.01).to(torch.bfloat16)
+    t = torch.randperm(V, generator=g)[:T]
+    h = torch.randn(T, D, generator=g).to(torch.bfloat16)
+    for i in range(T):   # the words of the targets point along their rows
+        hi = h[i].float()
+        w[t[i]] = (hi * ((i + 1.0) / (hi @ hi))).to(torch.bfloat16)
+    h, w, t = h.cuda(), w.cuda(), t.cuda()
+    assert Ref(h, w, t).loss.min() < 1e-9
+    loss, _, _, _ = _check_all(h, w, t)
+    assert torch.all(loss >= 0) and torch.all(nv.linear_ce(h, w, t)[0] >= 0)
+    one = torch.ones(T, device="cuda")
+    for i in range(T - 8, T):   # one live row at a time: its target's row of dw is d h, d <= 0
+        alone = torch.full_like(t, -100)
+        alone[i] = t[i]
+        _, _, _, dw = nv.linear_ce_grad(h, w, alone, row_weight=one)
+        assert torch.all(dw[t[i]].float() * h[i].float() <= 0)

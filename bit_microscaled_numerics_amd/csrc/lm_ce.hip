@@ -894,10 +894,11 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // Row pitch of an operand laid out here: an odd number of 256-byte pieces, so that
 // a column of 128-byte lines (what a K-contiguous stage reads of 256 rows) spreads
 // over all channels of an L2, and rows start on a piece (what the transposed
-// stages read is two whole pieces of each row).
+// stages read is two whole pieces of each row).  At most 2^22 elements: 256 rows then
+// span less than 2^31 bytes, what a descriptor and its offsets past the end hold.
 int64_t odd_pitch(int64_t cols) {
   const int64_t pieces = (cols + 127) / 128;
-  return (pieces + (pieces % 2 == 0)) * 128;
+  return (pieces + (pieces % 2 == 0 && pieces < (1 << 22) / 128)) * 128;
 }
 
 // Width of the tiles of tokens, 64, 128 or 256 (WN 1, 2, 4): a narrower tile wastes

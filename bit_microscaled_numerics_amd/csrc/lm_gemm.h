@@ -93,7 +93,7 @@ struct Loader<false, ROWS> {
                                        int frag_row0) {
     const int lane = fresh_lane();
     const int64_t rem = o.rows - row0;
-    const int64_t last = rem < ROWS ? rem - 1 : ROWS - 1;   // below 2^31 bytes (pitch < 2^22)
+    const int64_t last = rem < ROWS ? rem - 1 : ROWS - 1;   // below 2^31 bytes (pitch <= 2^22)
     buf = rsrc(o.p + row0 * o.ld, rem > 0 ? (int)((last * o.ld + k_total) * 2) : 0);
     K = uniform((int)k_total);
 #pragma unroll

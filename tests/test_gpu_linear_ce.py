@@ -449,3 +449,35 @@ def test_confident_tokens(V):
         alone[i] = t[i]
         _, _, _, dw = nv.linear_ce_grad(h, w, alone, row_weight=one)
         assert torch.all(dw[t[i]].float() * h[i].float() <= 0)
+
+
+def test_widest_rows():
+    """D just below 2^22 with a whole tile of tokens: the gathered rows' byte offsets
+    stay below 2^31.  Everything else in the workspace starts as NaN."""
+    T, V, D = 257, 3, (1 << 22) - 8
+    say("ce wide", T, V, D)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    h = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda").normal_(0, 0.0005, generator=g)
+    t = torch.arange(T, device="cuda") % V
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    ws = torch.full((nv.nvfp4_linear_ce_workspace_bytes(T, V, D, True),), 255, dtype=torch.uint8,
+                    device="cuda")
+    nv.nvfp4_linear_ce_grad(h, w, t, None, 0, loss, lse, dh, dw, ws)
+    z = torch.zeros(T, V, dtype=torch.float64, device="cuda")
+    for c in range(0, D, 1 << 18):
+        z += h[:, c:c + (1 << 18)].double() @ w[:, c:c + (1 << 18)].double().t().contiguous()
+    p = torch.softmax(z, 1)
+    p[torch.arange(T), t] -= 1
+    ref = torch.logsumexp(z, 1) - z.gather(1, t.unsqueeze(1)).squeeze(1)
+    # partial sums are of the order 0.0005 sqrt(D) = 1: D / 16 roundings of u each are at
+    # most 0.016 in z, relative in p
+    assert torch.all((loss.double() - ref).abs() <= 0.032)
+    p /= T
+    for c in (0, 1 << 21, D - 4096):
+        s = slice(c, c + 4096)
+        rdh = p @ w[:, s].double()
+        rdw = p.t().contiguous() @ h[:, s].double()
+        assert (dh[:, s].double() - rdh).norm() <= (2 * HALF + 0.032) * rdh.norm()
+        assert (dw[:, s].double() - rdw).norm() <= (2 * HALF + 0.032) * rdw.norm()

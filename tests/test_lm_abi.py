@@ -183,3 +183,13 @@ def test_ce_binding_refuses():
     for f in (nv.linear_ce, nv.linear_ce_grad):
         with pytest.raises(ValueError, match="CUDA"):
             f(h, h, t)
+
+
+def test_ce_gathered_rows_stay_below_2_31_bytes(lib):
+    """256 gathered rows are one operand with 32-bit byte offsets: their pitch, seen in the
+    workspace of one more row, is at most 2^22 elements for every D that is accepted."""
+    q = lib.nvfp4_linear_ce_workspace_bytes
+    base, at = (1 << 22) - 136, (1 << 22) - 128    # the pitch of rows of `base` elements
+    for D in ((1 << 22) - 128, (1 << 22) - 64, (1 << 22) - 8):
+        more = q(256, 8, D, 1, 0) - q(256, 8, base, 1, 0)
+        assert at + more / 512 <= 1 << 22, D

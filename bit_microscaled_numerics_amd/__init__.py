@@ -755,6 +755,8 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
 
 def _grad_list(grads, outs):
     """The nvfp4_grad array of a list of gradients (and outputs), and its length."""
+    if len(grads) != len(outs):
+        raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
     words, types, dev = [], _FLOATS, None
     for g, o in zip(grads, outs):
         gt, at_dev = types.get(g.dtype), g.get_device()   # -1: not on a GPU
@@ -779,20 +781,21 @@ def _grad_list(grads, outs):
 
 
 def nvfp4_grad_sumsq(grads, partials, stream=None):
+    grads = list(grads)
     lst, n = _grad_list(grads, grads)
     _dev_partials(partials)
     _check(load_library().nvfp4_grad_sumsq(lst, n, _p(partials), _stream(stream)))
 
 
 def nvfp4_grad_clip(grads, outs, partials, max_norm, norm_out, stream=None):
-    lst, n = _grad_list(grads, outs)
+    lst, n = _grad_list(list(grads), list(outs))
     _dev_partials(partials)
     _check(load_library().nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm_out),
                                           _stream(stream)))
 
 
 def nvfp4_grad_scale(grads, outs, factor, stream=None):
-    lst, n = _grad_list(grads, outs)
+    lst, n = _grad_list(list(grads), list(outs))
     _dev_f32(factor, 1, "factor")
     _check(load_library().nvfp4_grad_scale(lst, n, _p(factor), _stream(stream)))
 

@@ -172,3 +172,15 @@ def test_scale(dt, ot, factor):
         assert all(torch.equal(a, b) for a, b in zip(new, outs))
         nv.nvfp4_grad_scale(dev, dev, f)
         assert all(torch.equal(a, b) for a, b in zip(dev, outs))
+
+
+def test_lists_that_are_read_once():
+    """Generators: every gradient counts."""
+    grads = _grads(11, [1000, 7, 31, 4], (F, BF))
+    dev = [g.cuda() for g in grads]
+    outs = [torch.empty_like(g) for g in dev]
+    partials = torch.empty(nv.NVFP4_SUMSQ_WORDS, dtype=torch.float64, device="cuda")
+    norm = torch.empty(1, device="cuda")
+    nv.nvfp4_grad_sumsq((g for g in dev), partials)
+    nv.nvfp4_grad_clip((g for g in dev), (o for o in outs), partials, 1.0, norm)
+    _check(norm, outs, grads, 1.0)

@@ -193,3 +193,14 @@ def test_ce_gathered_rows_stay_below_2_31_bytes(lib):
     for D in ((1 << 22) - 128, (1 << 22) - 64, (1 << 22) - 8):
         more = q(256, 8, D, 1, 0) - q(256, 8, base, 1, 0)
         assert at + more / 512 <= 1 << 22, D
+
+
+def test_lists_of_different_lengths_are_refused():
+    """Before anything of either list is looked at, from sequences and generators."""
+    x, partials, one = torch.zeros(4), torch.zeros(nv.NVFP4_SUMSQ_WORDS), torch.zeros(1)
+    for n, m in ((2, 1), (1, 2), (1, 0), (0, 1)):
+        for kind in (list, iter):
+            with pytest.raises(ValueError, match=f"{m} outputs for {n} gradients"):
+                nv.nvfp4_grad_clip(kind([x] * n), kind([x] * m), partials, 1.0, one)
+            with pytest.raises(ValueError, match=f"{m} outputs for {n} gradients"):
+                nv.nvfp4_grad_scale(kind([x] * n), kind([x] * m), one)

@@ -789,6 +789,8 @@ def nvfp4_grad_sumsq(grads, partials, stream=None):
 
 def nvfp4_grad_clip(grads, outs, partials, max_norm, norm_out, stream=None):
     lst, n = _grad_list(list(grads), list(outs))
+    _dev_f32(norm_out, 1, "norm_out")
+    _one_device(norm_out)
     _dev_partials(partials)
     _check(load_library().nvfp4_grad_clip(lst, n, _p(partials), max_norm, _p(norm_out),
                                           _stream(stream)))
@@ -797,6 +799,7 @@ def nvfp4_grad_clip(grads, outs, partials, max_norm, norm_out, stream=None):
 def nvfp4_grad_scale(grads, outs, factor, stream=None):
     lst, n = _grad_list(list(grads), list(outs))
     _dev_f32(factor, 1, "factor")
+    _one_device(factor)
     _check(load_library().nvfp4_grad_scale(lst, n, _p(factor), _stream(stream)))
 
 

@@ -184,3 +184,15 @@ def test_lists_that_are_read_once():
     nv.nvfp4_grad_sumsq((g for g in dev), partials)
     nv.nvfp4_grad_clip((g for g in dev), (o for o in outs), partials, 1.0, norm)
     _check(norm, outs, grads, 1.0)
+
+
+def test_norm_and_factor_have_to_be_on_the_gpu():
+    dev = [torch.ones(5, device="cuda")]
+    partials = nv.grad_sumsq(dev)
+    for bad in (torch.zeros(1), torch.zeros(1, dtype=BF, device="cuda"), torch.zeros(2, device="cuda")):
+        with pytest.raises(ValueError, match="norm_out"):
+            nv.nvfp4_grad_clip(dev, dev, partials, 1.0, bad)
+        with pytest.raises(ValueError, match="factor"):
+            nv.nvfp4_grad_scale(dev, dev, bad)
+    nv.nvfp4_grad_clip(dev, dev, partials, 100.0, None)   # the norm is not wanted
+    assert torch.all(dev[0] == 1)

@@ -204,3 +204,35 @@ def test_lists_of_different_lengths_are_refused():
                 nv.nvfp4_grad_clip(kind([x] * n), kind([x] * m), partials, 1.0, one)
             with pytest.raises(ValueError, match=f"{m} outputs for {n} gradients"):
                 nv.nvfp4_grad_scale(kind([x] * n), kind([x] * m), one)
+
+
+class _Elsewhere:
+    """What the checks see of a float32 value (or float64 partial sums) on GPU `device`."""
+    is_cuda = True
+
+    def __init__(self, device, n=1, dtype=torch.float32):
+        self.device_index, self.n, self.dtype = device, n, dtype
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.n
+
+    def get_device(self):
+        return self.device_index
+
+
+def test_norm_and_factor_are_one_float32_on_the_current_device(monkeypatch):
+    partials = torch.zeros(nv.NVFP4_SUMSQ_WORDS, dtype=torch.float64)
+    for bad in (torch.zeros(1), torch.zeros(1, dtype=torch.bfloat16), torch.zeros(2),
+                _Elsewhere(0, n=2), _Elsewhere(0, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="norm_out"):
+            nv.nvfp4_grad_clip([], [], partials, 1.0, bad)
+        with pytest.raises(ValueError, match="factor"):
+            nv.nvfp4_grad_scale([], [], bad)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        nv.nvfp4_grad_clip([], [], partials, 1.0, _Elsewhere(1))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        nv.nvfp4_grad_scale([], [], _Elsewhere(1))

@@ -569,8 +569,12 @@ def _pitch(x: torch.Tensor, name: str) -> int:
     return x.stride(0)
 
 
-def _nbytes(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _nbytes(workspace: Optional[torch.Tensor]) -> int:
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _dev_ids(ids: torch.Tensor, name: str) -> int:

@@ -236,3 +236,12 @@ def test_norm_and_factor_are_one_float32_on_the_current_device(monkeypatch):
         nv.nvfp4_grad_clip([], [], partials, 1.0, _Elsewhere(1))
     with pytest.raises(ValueError, match="current CUDA device"):
         nv.nvfp4_grad_scale([], [], _Elsewhere(1))
+
+
+def test_workspace_is_one_piece():
+    """Its size counts from its first byte on: gaps in it belong to somebody else."""
+    assert nv._nbytes(None) == 0 and nv._nbytes(torch.zeros(6, dtype=torch.int32)) == 24
+    for ws in (torch.zeros(64, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(512),
+               torch.zeros(8, 16, dtype=torch.uint8)[:, :8]):
+        with pytest.raises(ValueError, match="contiguous"):
+            nv._nbytes(ws)

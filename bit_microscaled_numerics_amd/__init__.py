@@ -853,7 +853,8 @@ def scale_grads(grads, factor: torch.Tensor):
     """New tensors factor * gradient, factor one float32 value on the GPU; each
     product is rounded from FP32 once."""
     grads = list(grads)
-    outs = [_empty(*g.shape, dtype=g.dtype, device=g.device) for g in grads]
+    # flat first: a 0-dimensional gradient has no sizes to allocate by
+    outs = [_empty(g.numel(), dtype=g.dtype, device=g.device).view(g.shape) for g in grads]
     nvfp4_grad_scale(grads, outs, factor)
     return outs
 

@@ -196,3 +196,14 @@ def test_norm_and_factor_have_to_be_on_the_gpu():
             nv.nvfp4_grad_scale(dev, dev, bad)
     nv.nvfp4_grad_clip(dev, dev, partials, 100.0, None)   # the norm is not wanted
     assert torch.all(dev[0] == 1)
+
+
+def test_gradients_without_a_dimension():
+    """0-dimensional gradients (a scalar parameter's) scale, clip and count like others."""
+    grads = [torch.tensor(3.0), torch.tensor([4.0, 0.0])]
+    dev = [g.cuda() for g in grads]
+    new = nv.scale_grads(dev, torch.tensor([0.5], device="cuda"))
+    assert [g.shape for g in new] == [(), (2,)]
+    assert new[0].item() == 1.5 and new[1].tolist() == [2.0, 0.0]
+    norm = nv.clip_grads(dev, 1.0)
+    _check(norm, dev, grads, 1.0)

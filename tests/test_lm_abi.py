@@ -245,3 +245,8 @@ def test_workspace_is_one_piece():
                torch.zeros(8, 16, dtype=torch.uint8)[:, :8]):
         with pytest.raises(ValueError, match="contiguous"):
             nv._nbytes(ws)
+
+
+def test_scale_of_a_gradient_without_a_dimension_reaches_its_checks():
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.scale_grads([torch.tensor(3.0)], torch.ones(1))

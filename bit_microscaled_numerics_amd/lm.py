@@ -118,6 +118,15 @@ class TokenLossFunction(torch.autograd.Function):
         return dx, dw, None, None
 
 
+def _operand(x: torch.Tensor) -> torch.Tensor:
+    """A bf16 matrix as the products take it: rows that start on 16 bytes.  A piece of a flat
+    buffer may start anywhere; it is copied then."""
+    if x.dim() == 2 and x.shape[1] % 8 == 0 and (
+            x.data_ptr() % 16 or (x.shape[0] > 1 and x.stride(0) % 8)):
+        return x.clone(memory_format=torch.contiguous_format)
+    return x
+
+
 def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                          row_weight: Optional[torch.Tensor] = None, reduction: str = "mean",
                          piece_tokens: int = 0) -> torch.Tensor:
@@ -126,7 +135,8 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     outside 0 .. vocab - 1 do not count.  reduction "mean" (over the targets),
     "sum" (of row_weight * loss, row_weight [..] float32 or all 1) or "none" (each
     token's loss, shaped like targets).  piece_tokens bounds the workspace (0: 2
-    bytes for each token and word, 4 GiB at most)."""
+    bytes for each token and word, 4 GiB at most).  x and weight are copied in a call
+    where their rows do not start on 16 bytes (a piece of a flat buffer)."""
     if reduction not in ("mean", "sum", "none"):
         raise ValueError(f"reduction {reduction!r} is none of mean, sum, none")
     if row_weight is not None and reduction != "sum":
@@ -134,7 +144,8 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     if x.shape[:-1] != targets.shape:
         raise ValueError(f"x {tuple(x.shape)} and targets {tuple(targets.shape)} do not match")
     flat = targets.reshape(-1).contiguous()
-    rows = x.reshape(-1, x.shape[-1]).contiguous()
+    rows = _operand(x.reshape(-1, x.shape[-1]).contiguous())
+    weight = _operand(weight)
     train = torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad)
     if reduction == "none":
         if not train:

@@ -300,3 +300,25 @@ def test_masked_tokens_may_hold_anything(bad):
         _near(wg.grad, dw, 2.5 * HALF)
         with torch.no_grad():
             assert abs(lm.linear_cross_entropy(x, w, t, weight, reduction="sum").item() - total) <= 1e-3
+
+
+@pytest.mark.parametrize("lead", [1, 4])
+def test_operands_at_any_place_of_a_flat_buffer(lead):
+    """A weight (and rows) that start off 16 bytes give what aligned ones give."""
+    say("lm flat", lead)
+    x, w, t = _data()
+    want = lm.linear_cross_entropy(x, w, t)
+    wa, xa = w.clone().requires_grad_(), x.clone().requires_grad_()
+    lm.linear_cross_entropy(xa, wa, t).backward()
+    flat = torch.zeros(w.numel() + x.numel() + 2 * lead, dtype=torch.bfloat16, device="cuda")
+    flat[lead:lead + w.numel()].copy_(w.view(-1))
+    flat[2 * lead + w.numel():].copy_(x.view(-1))
+    wv = flat[lead:lead + w.numel()].view_as(w)
+    xv = flat[2 * lead + w.numel():].view_as(x)
+    assert torch.equal(lm.linear_cross_entropy(xv, wv, t), want)
+    tokens = lm.linear_cross_entropy(xv, wv, t, reduction="none")
+    assert torch.equal(tokens, lm.linear_cross_entropy(x, w, t, reduction="none"))
+    wp, xp = wv.detach().requires_grad_(), xv.detach().requires_grad_()
+    assert wp.data_ptr() % 16 != 0
+    lm.linear_cross_entropy(xp, wp, t).backward()
+    assert torch.equal(wp.grad, wa.grad) and torch.equal(xp.grad, xa.grad)

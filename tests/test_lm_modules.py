@@ -100,3 +100,35 @@ def test_losses_of_weight_zero_do_not_count(calls, bad, train):
     out.backward()
     keep = torch.arange(24) != 7
     assert torch.allclose(weight.grad[keep], loss[keep], rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("lead", [0, 1, 4, 8])
+@pytest.mark.parametrize("mode", ["train", "none", "score"])
+def test_operands_at_any_place_of_a_flat_buffer(calls, lead, mode):
+    """What the products are given starts on 16 bytes; gradients reach the pieces."""
+    x, w, t = _data()
+    flat = torch.zeros(2 * lead + w.numel() + x.numel(), dtype=torch.bfloat16)
+    wv = flat[lead:lead + w.numel()].view_as(w).copy_(w)
+    xv = flat[2 * lead + w.numel():].view_as(x).copy_(x)
+    if mode == "score":
+        assert lm.linear_cross_entropy(xv, wv, t) == lm.linear_cross_entropy(x, w, t)
+    else:
+        wv, xv = wv.detach().requires_grad_(), xv.detach().requires_grad_()
+        w.requires_grad_()
+        x.requires_grad_()
+        kw = dict(reduction="none") if mode == "none" else {}
+        lm.linear_cross_entropy(xv, wv, t, **kw).sum().backward()
+        lm.linear_cross_entropy(x, w, t, **kw).sum().backward()
+        assert torch.equal(xv.grad, x.grad) and torch.equal(wv.grad, w.grad)
+    assert all(o.data_ptr() % 16 == 0 for pair in calls["operands"] for o in pair)
+    # aligned operands are handed on as they are
+    if mode == "score" and lead in (0, 8):
+        assert calls["operands"][0][1].data_ptr() == wv.data_ptr()
+
+
+def test_rows_off_their_pitch_are_copied(calls):
+    x, w, t = _data()
+    wide = torch.zeros(30, 19, dtype=torch.bfloat16)
+    wide[:, :16] = w
+    assert lm.linear_cross_entropy(x, wide[:, :16], t) == lm.linear_cross_entropy(x, w, t)
+    assert calls["operands"][0][1].stride(0) == 16

@@ -178,7 +178,7 @@ class ScaledEmbedding(torch.nn.Module):
 
 
 class CrossEntropyHead(torch.nn.Module):
-    """Output head and loss.  weight: a parameter to share (a tied embedding)."""
+    """Output head and loss.  weight: a bf16 parameter to share (a tied embedding)."""
 
     def __init__(self, dim: int, vocab: int, device=None,
                  weight: Optional[torch.nn.Parameter] = None):
@@ -189,6 +189,8 @@ class CrossEntropyHead(torch.nn.Module):
             torch.nn.init.normal_(weight, std=1.0 / math.sqrt(dim))
         elif weight.shape != (vocab, dim):
             raise ValueError(f"weight must be [{vocab}][{dim}]")
+        elif weight.dtype != torch.bfloat16:
+            raise ValueError(f"weight must be bf16 to be shared with a head, not {weight.dtype}")
         self.weight = weight
 
     def forward(self, x: torch.Tensor, targets: torch.Tensor, **kw) -> torch.Tensor:

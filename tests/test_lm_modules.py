@@ -132,3 +132,12 @@ def test_rows_off_their_pitch_are_copied(calls):
     wide[:, :16] = w
     assert lm.linear_cross_entropy(x, wide[:, :16], t) == lm.linear_cross_entropy(x, w, t)
     assert calls["operands"][0][1].stride(0) == 16
+
+
+def test_float32_table_cannot_be_shared_with_a_head():
+    """Refused where the model is put together, not by its first loss."""
+    table = lm.ScaledEmbedding(30, 16, dtype=torch.float32)
+    with pytest.raises(ValueError, match="bf16"):
+        lm.CrossEntropyHead(16, 30, weight=table.weight)
+    tied = lm.ScaledEmbedding(30, 16)
+    assert lm.CrossEntropyHead(16, 30, weight=tied.weight).weight is tied.weight

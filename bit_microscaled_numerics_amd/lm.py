@@ -85,8 +85,11 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     def forward(ctx, x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                 row_weight: Optional[torch.Tensor], piece_tokens: int):
         loss, _, dx, dw = linear_ce_grad(x, weight, targets, row_weight, piece_tokens)
-        # a token's loss (0 without a target) is the derivative by its weight
-        ctx.save_for_backward(dx, dw, loss if ctx.needs_input_grad[3] else None)
+        # a token's loss (0 without a target) is the derivative by its weight; what is not
+        # asked for is not kept until the backward pass (dw is as large as the weight)
+        need = ctx.needs_input_grad
+        ctx.save_for_backward(dx if need[0] else None, dw if need[1] else None,
+                              loss if need[3] else None)
         return _reduce(loss, targets, weight.shape[0], row_weight)
 
     @staticmethod
@@ -94,8 +97,9 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     def backward(ctx, dloss: torch.Tensor):
         dx, dw, loss = ctx.saved_tensors
         dloss = dloss.float().reshape(1).contiguous()
-        dx, dw = scale_grads((dx, dw), dloss)
-        return dx, dw, None, None if loss is None else loss * dloss, None
+        scaled = iter(scale_grads([g for g in (dx, dw) if g is not None], dloss))
+        return (None if dx is None else next(scaled), None if dw is None else next(scaled), None,
+                None if loss is None else loss * dloss, None)
 
 
 class TokenLossFunction(torch.autograd.Function):

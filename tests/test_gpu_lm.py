@@ -322,3 +322,14 @@ def test_operands_at_any_place_of_a_flat_buffer(lead):
     assert wp.data_ptr() % 16 != 0
     lm.linear_cross_entropy(xp, wp, t).backward()
     assert torch.equal(wp.grad, wa.grad) and torch.equal(xp.grad, xa.grad)
+
+
+@pytest.mark.parametrize("train_x,train_w", [(True, False), (False, True)])
+def test_one_side_frozen(train_x, train_w):
+    x, w, t = _data()
+    _, _, dx, dw = nv.linear_ce_grad(x, w, t)
+    x.requires_grad_(train_x)
+    w.requires_grad_(train_w)
+    lm.linear_cross_entropy(x, w, t).backward()
+    assert torch.equal(x.grad, dx) if train_x else x.grad is None
+    assert torch.equal(w.grad, dw) if train_w else w.grad is None

@@ -141,3 +141,18 @@ def test_float32_table_cannot_be_shared_with_a_head():
         lm.CrossEntropyHead(16, 30, weight=table.weight)
     tied = lm.ScaledEmbedding(30, 16)
     assert lm.CrossEntropyHead(16, 30, weight=tied.weight).weight is tied.weight
+
+
+@pytest.mark.parametrize("train_x,train_w", [(True, True), (True, False), (False, True)])
+def test_gradients_nobody_asks_for_are_not_kept(calls, train_x, train_w):
+    x, w, t = _data()
+    _, _, dx, dw = _ce_grad(x, w, t)
+    x.requires_grad_(train_x)
+    w.requires_grad_(train_w)
+    loss = lm.linear_cross_entropy(x, w, t)
+    kept = [s for s in loss.grad_fn.saved_tensors if s is not None]
+    assert [tuple(s.shape) for s in kept] == [(24, 16)] * train_x + [(30, 16)] * train_w
+    loss.backward()
+    assert calls["scaled"] == [train_x + train_w]
+    assert torch.equal(x.grad, dx) if train_x else x.grad is None
+    assert torch.equal(w.grad, dw) if train_w else w.grad is None

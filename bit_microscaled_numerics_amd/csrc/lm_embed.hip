@@ -199,7 +199,8 @@ __global__ __launch_bounds__(kFillThreads) void k_fill(Fill fill) {
 }
 
 // All passes over a tile of tokens in one workgroup, keys and token numbers in LDS
-// between passes.  Up to 8192 tokens are one tile and sorted by this launch alone.
+// between passes.  Up to 4096 tokens (8192 beside a long fill) are one tile and sorted by
+// this launch alone.
 template <int STEPS>
 __global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bits, int passes,
                                                             int tiles,

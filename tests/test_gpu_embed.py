@@ -275,3 +275,34 @@ def test_gradient_of_more_tokens_than_a_launch_has_threads():
     got = nv.embed_grad(ids, dy, V, dtype=torch.float32).cpu().double()
     want = torch.tensor([(n - v + 3) // 4 for v in range(V)], dtype=torch.float64).unsqueeze(1)
     assert torch.all((got - want).abs() <= want * 8 * U32), (got, want)
+
+
+# More than 32768 tokens: the sort in passes over tiles of 4096, with 1 (V <= 511), 2
+# and 3 (V >= 2^18) passes, and with histograms of more than the 4096 words that the scan
+# takes at a time.
+@pytest.mark.parametrize("n", [32769, 40000, 70000])
+@pytest.mark.parametrize("V", [300, 511, 131072, 300000])
+@pytest.mark.parametrize("kind", ["zipf", "outside"])
+def test_gradient_of_many_tokens_and_words(n, V, kind):
+    say("embed_grad many words", n, V, kind)
+    g = torch.Generator().manual_seed(n + V)
+    ids = _ids(g, n, V, kind, torch.int64 if n % 2 else torch.int32)
+    ids[0], ids[n // 2], ids[-1] = V - 1, 0, V
+    dy = _rand(g, n, 9)
+    first = nv.embed_grad(ids.cuda(), dy.cuda(), V, 0.7)
+    _check_grad(first, ids, dy, V, 0.7)
+    assert torch.equal(nv.embed_grad(ids.cuda(), dy.cuda(), V, 0.7), first)
+
+
+@pytest.mark.parametrize("V", [300, 131072, 300000])
+def test_gradient_of_many_tokens_accumulates(V):
+    """More than 32768 tokens added to what dW holds; absent words' rows are not touched."""
+    say("embed_grad many, added", V)
+    g = torch.Generator().manual_seed(V + 1)
+    n = 40001
+    ids, dy = _ids(g, n, V, "zipf", torch.int64), _rand(g, n, 9)
+    base = _rand(g, V, 9)
+    got = nv.embed_grad(ids.cuda(), dy.cuda(), V, 0.9, accumulate_into=base.cuda())
+    _check_grad(got, ids, dy, V, 0.9, base)
+    absent = torch.bincount(ids, minlength=V) == 0
+    assert torch.equal(got.cpu()[absent], base[absent])

@@ -481,3 +481,84 @@ def test_widest_rows():
         rdw = p.t().contiguous() @ h[:, s].double()
         assert (dh[:, s].double() - rdh).norm() <= (2 * HALF + 0.032) * rdh.norm()
         assert (dw[:, s].double() - rdw).norm() <= (2 * HALF + 0.032) * rdw.norm()
+
+
+def _check_repeated(hu, w, tu, rep, weight, piece):
+    """Token i is row rep[i] of the distinct ones (hu, tu), with a weight of its own: the
+    reference needs only the distinct rows' logits.  Bounds as above; weights are held
+    relative to their largest, one more rounding of u each way.  In blocks of words, so that
+    w may pass 2^32 bytes."""
+    distinct, (V, D), T = hu.shape[0], w.shape, rep.numel()
+    h, t = hu[rep].contiguous(), tu[rep].contiguous()
+    loss, lse, dh, dw = nv.linear_ce_grad(h, w, t, row_weight=weight, piece_tokens=piece)
+    again = nv.linear_ce_grad(h, w, t, row_weight=weight, piece_tokens=piece)
+    assert torch.equal(dh, again[2]) and torch.equal(dw, again[3])
+    del again
+    live = (tu >= 0) & (tu < V)
+    h64 = hu.double()
+    z = torch.empty(distinct, V, dtype=torch.float64, device="cuda")
+    dz = torch.zeros(distinct, dtype=torch.float64, device="cuda")
+    for v in range(0, V, 8192):
+        part = w[v:v + 8192].double().t().contiguous()
+        z[:, v:v + 8192] = h64 @ part
+        dz = torch.maximum(dz, (h64.abs() @ part.abs()).amax(1))
+    dz, rel = D * U * dz, (80 + V / 128 / 64 + 8) * U + 8 * U
+    ref_lse = torch.logsumexp(z, 1)
+    at = tu.long().clamp(0, V - 1).unsqueeze(1)
+    ref_loss = (ref_lse - z.gather(1, at).squeeze(1)) * live
+    ok = (loss.double() - ref_loss[rep]).abs() <= (2 * dz + rel + U * ref_loss)[rep] * live[rep]
+    assert ok.all(), "loss"
+    ok = (lse.double() - (ref_lse * live)[rep]).abs() <= (dz + rel + U * ref_lse.abs())[rep] * live[rep]
+    assert ok.all(), "lse"
+    p = torch.exp(z - ref_lse.unsqueeze(1)) * live.unsqueeze(1)
+    onehot = torch.zeros_like(p).scatter_(1, at, 1.0) * live.unsqueeze(1)
+    d = p - onehot
+    err = p * (CODE * (1 - onehot) + 2 * (2 * dz + rel).unsqueeze(1) + 8 * U) + 1e-18 * live.unsqueeze(1)
+    err = err * (1 + HALF) + (HALF + 3 * U) * d.abs()
+    each = weight.double().unsqueeze(1)
+    total = torch.zeros(distinct, 1, dtype=torch.float64, device="cuda").index_add_(0, rep, each)
+    dh_u = tol_u = 0.0
+    for v in range(0, V, 8192):
+        part, s = w[v:v + 8192].double(), slice(v, v + 8192)
+        e, m = err[:, s].contiguous(), d[:, s].abs() + err[:, s]
+        dh_u = dh_u + d[:, s].contiguous() @ part
+        tol_u = tol_u + e @ part.abs() + (V + 130) * U * (m @ part.abs())
+        ref = (total * d[:, s]).t().contiguous() @ h64
+        tol = (total * e).t().contiguous() @ h64.abs()
+        tol = tol + (T + 130) * U * ((total * m).t().contiguous() @ h64.abs())
+        off = (dw[s].double() - ref).abs()
+        assert (off <= tol + HALF * (ref.abs() + tol)).all(), ("dw", v)
+    for i in range(0, T, 4096):
+        r = rep[i:i + 4096]
+        ref, tol = each[i:i + 4096] * dh_u[r], each[i:i + 4096] * tol_u[r]
+        off = (dh[i:i + 4096].double() - ref).abs()
+        assert (off <= tol + HALF * (ref.abs() + tol)).all(), ("dh", i)
+
+
+@pytest.mark.parametrize("T,D,piece", [(16484, 2056, 8192), (16484, 2056, 0), (16484, 1032, 5000)])
+def test_long_pieces(T, D, piece):
+    """Long products in pieces: dW's sums go on in FP32 from piece to piece, the workgroups
+    kept together (2048 steps and more) in the whole pieces and not in the short last one.
+    piece 0: the 4 GiB of codes for 131072 words hold 16128 tokens, so the default has two
+    pieces too.  Tokens without a target and of weight 0 among them."""
+    V, distinct = 131072, 64
+    say("ce long pieces", T, D, piece)
+    hu, w, tu = _inputs(distinct, V, D, ignored="none", scale=0.05)
+    tu[5::16] = -100
+    rep = torch.arange(T, device="cuda") * 7 % distinct
+    weight = torch.rand(T, generator=torch.Generator().manual_seed(D + piece)).cuda()
+    weight[weight < 0.05] = 0.0
+    _check_repeated(hu, w, tu, rep, weight, piece)
+
+
+@pytest.mark.parametrize("T", [33, 130])
+def test_words_gradient_past_32_bits(T):
+    """dW of 5.2 GB from the general kernel (more than 32 tokens)."""
+    V, D = 320000, 8192
+    say("ce dw 5.2 GB", T)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda").normal_(0, 0.01, generator=g)
+    h = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    t = V - 1 - torch.arange(T, device="cuda") * 2400
+    weight = torch.rand(T, generator=g, device="cuda")
+    _check_repeated(h, w, t, torch.arange(T, device="cuda"), weight, 0)

@@ -18,7 +18,7 @@ left out.
 from __future__ import annotations
 
 import math
-from typing import Iterable, Optional
+from typing import Iterable, Optional, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -201,12 +201,14 @@ class CrossEntropyHead(torch.nn.Module):
         return linear_cross_entropy(x, self.weight, targets, **kw)
 
 
-def clip_grad_norm(parameters: Iterable[torch.nn.Parameter], max_norm: float, group=None
-                   ) -> torch.Tensor:
-    """Clip the gradients of parameters in place to a global 2-norm of max_norm;
+def clip_grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
+                   group=None) -> torch.Tensor:
+    """Clip the gradients of parameters (or of one) in place to a global 2-norm of max_norm;
     returns the norm (float32 [1], on the GPU, not waited for; 0 without gradients).  group: a process
     group over which the parameters are sharded; the squares of all its ranks
     count (one all-reduce of 4 KiB)."""
+    if isinstance(parameters, torch.Tensor):   # iterating over it would give its rows
+        parameters = (parameters,)
     grads = [p.grad for p in parameters if p.grad is not None]
     partials = None
     if group is not None:

@@ -156,3 +156,22 @@ def test_gradients_nobody_asks_for_are_not_kept(calls, train_x, train_w):
     assert calls["scaled"] == [train_x + train_w]
     assert torch.equal(x.grad, dx) if train_x else x.grad is None
     assert torch.equal(w.grad, dw) if train_w else w.grad is None
+
+
+def _clip(grads, max_norm, partials=None):
+    """nv.clip_grads's contract in place: what is not contiguous is refused."""
+    if not all(g.is_contiguous() for g in grads):
+        raise ValueError("gradients must be contiguous")
+    norm = sum(g.double().square().sum() for g in grads).sqrt()
+    for g in grads:
+        g.mul_(min(1.0, max_norm / (norm.item() + 1e-6)))
+    return norm.float().reshape(1)
+
+
+def test_one_parameter_is_clipped(monkeypatch):
+    """A parameter by itself, not an iterable of its rows (which have no gradients)."""
+    monkeypatch.setattr(lm, "clip_grads", _clip)
+    p = torch.nn.Parameter(torch.zeros(4, 4))
+    p.grad = torch.ones(4, 4)
+    assert lm.clip_grad_norm(p, 1.0).item() == 4.0
+    assert torch.allclose(p.grad, torch.full((4, 4), 0.25))

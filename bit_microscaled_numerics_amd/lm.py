@@ -201,6 +201,14 @@ class CrossEntropyHead(torch.nn.Module):
         return linear_cross_entropy(x, self.weight, targets, **kw)
 
 
+def _in_memory_order(g: torch.Tensor) -> torch.Tensor:
+    """The gradient with its dimensions in the order of memory: a transposed parameter's is
+    contiguous so, and neither a norm nor a factor minds the order."""
+    if g.is_contiguous():
+        return g
+    return g.permute(sorted(range(g.dim()), key=g.stride, reverse=True))
+
+
 def clip_grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
                    group=None) -> torch.Tensor:
     """Clip the gradients of parameters (or of one) in place to a global 2-norm of max_norm;
@@ -209,7 +217,7 @@ def clip_grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_
     count (one all-reduce of 4 KiB)."""
     if isinstance(parameters, torch.Tensor):   # iterating over it would give its rows
         parameters = (parameters,)
-    grads = [p.grad for p in parameters if p.grad is not None]
+    grads = [_in_memory_order(p.grad) for p in parameters if p.grad is not None]
     partials = None
     if group is not None:
         # a rank without gradients takes part in the sum all the same

@@ -333,3 +333,13 @@ def test_one_side_frozen(train_x, train_w):
     lm.linear_cross_entropy(x, w, t).backward()
     assert torch.equal(x.grad, dx) if train_x else x.grad is None
     assert torch.equal(w.grad, dw) if train_w else w.grad is None
+
+
+def test_clip_of_one_parameter_and_of_a_transposed_one():
+    p = torch.nn.Parameter(torch.zeros(6, 40, device="cuda").t())
+    g = torch.Generator().manual_seed(8)
+    (p * torch.randn(40, 6, generator=g).cuda()).sum().backward()
+    assert not p.grad.is_contiguous()
+    before = p.grad.double().cpu()
+    assert abs(lm.clip_grad_norm(p, 1.0).item() - before.norm().item()) <= 1e-6 * before.norm()
+    _near(p.grad, before / (before.norm() + 1e-6), 4 * U)

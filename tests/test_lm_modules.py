@@ -175,3 +175,26 @@ def test_one_parameter_is_clipped(monkeypatch):
     p.grad = torch.ones(4, 4)
     assert lm.clip_grad_norm(p, 1.0).item() == 4.0
     assert torch.allclose(p.grad, torch.full((4, 4), 0.25))
+
+
+def test_gradients_in_another_order_of_memory_are_clipped(monkeypatch):
+    """A transposed (or channels-last) parameter's gradient has its strides; gaps are refused."""
+    monkeypatch.setattr(lm, "clip_grads", _clip)
+    ps = [torch.nn.Parameter(torch.zeros(4, 6).t()),
+          torch.nn.Parameter(torch.zeros(2, 3, 5, 4).to(memory_format=torch.channels_last)),
+          torch.nn.Parameter(torch.zeros(3, 1, 2).transpose(0, 2)), torch.nn.Parameter(torch.zeros(5))]
+    g = torch.Generator().manual_seed(0)
+    for p in ps:
+        p.grad = torch.empty_like(p).copy_(torch.randn(p.shape, generator=g))
+    before = [p.grad.clone() for p in ps]
+    assert not ps[0].grad.is_contiguous() and not ps[1].grad.is_contiguous()
+    norm = lm.clip_grad_norm(ps, 1.0).item()
+    want = sum(b.double().square().sum() for b in before).sqrt().item()
+    assert abs(norm - want) <= 1e-6 * want
+    for p, b in zip(ps, before):
+        assert p.grad.stride() == b.stride()
+        assert torch.allclose(p.grad, b / want, rtol=1e-5, atol=1e-7)
+    p = torch.nn.Parameter(torch.zeros(4, 6))
+    p.grad = torch.ones(4, 12)[:, ::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        lm.clip_grad_norm([p], 1.0)

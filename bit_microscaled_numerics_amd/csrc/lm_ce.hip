@@ -1,5 +1,5 @@
 // lm_ce.hip -- softmax cross entropy of an output head z = h w^T over a large
-// vocabulary, with its gradient, without the logits:
+// vocabulary, with its gradient, without logits in FP32:
 //
 //   lse_t  = log sum_v exp(z_tv),   loss_t = lse_t - z_t,target
 //   d_tv   = g_t (exp(z_tv - lse_t) - [v = target_t])
@@ -24,9 +24,9 @@
 //                equal parts when the tiles do not fill the compute units.
 //  k_ce_dw       dW = d^T H.
 //
-// 8192 tokens x 131072 words x 5120: logits 8.5 .. 9.0 ms, dH 8.3 .. 8.7, dW 8.0 .. 8.3
-// (1.2 .. 1.38 PFLOP/s), codes to d 0.8, the rest 0.2.  The products are bound by
-// power there: 73 .. 78% of the matrix cores' cycles at a clock of 1.7 GHz.  With few
+// 8192 tokens x 131072 words x 5120: logits 8.6 .. 9.2 ms, dH 8.3 .. 8.6, dW 7.9 .. 8.2
+// (1.2 .. 1.39 PFLOP/s), codes to d 0.8, the rest 0.2.  The products are bound by
+// power there: 71 .. 78% of the matrix cores' cycles at a clock of 1.7 GHz.  With few
 // tokens or a short K it is the epilogues: 1003 x 32003 x 512 takes 52 us for the
 // logits, half of it their epilogue.
 //
@@ -419,8 +419,8 @@ __global__ __launch_bounds__(256) void k_ce_rows(CeArgs g) {
   }
 }
 
-// codes -> d = g (p - [target]), BF16, in place; bound by HBM (8192 x 131072: 0.75 ms,
-// 5.7 TB/s).  Each thread four pieces of 8 entries of a row (1000 x 65536: 44 us,
+// codes -> d = g (p - [target]), BF16, in place; bound by HBM (8192 x 131072: 0.78 ms,
+// 5.5 TB/s).  Each thread four pieces of 8 entries of a row (1000 x 65536: 45 us,
 // with one piece 62).  At the target p - 1 = exp(-loss) - 1, which loses nothing to a p
 // close to 1 beyond the loss's own error: some 2^-24, more than the BF16 rounding of d once
 // 1 - p is below about 1e-5.  A weight of 0 masks a row: zeros whatever it holds, and its
@@ -704,9 +704,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_ce_dw(CeArgs g) {
 // dW of at most 32 tokens: K is at most one pair of MFMA steps, so nothing is staged
 // and the kernel is bound by writing dW.  A wave keeps its 128 columns of h in
 // registers and goes over the words 64 at a time: a lane reads two neighbouring
-// words of d at once, and the even and the odd ones are a block of rows each.  (In
-// tiles of 256 x 256 most of the time is their epilogue, all compute units in step:
-// 1 x 65536 x 5120 187 us, so 107, 6.3 TB/s; with 32 tokens 200 and 130.)
+// words of d at once, and the even and the odd ones are a block of rows each.  1 x 65536
+// x 5120: 110 us (6.1 TB/s), 32 tokens 139 (4.8).  In tiles of 256 x 256, where most of
+// the time is their epilogue, all compute units in step, 33 tokens take 205.
 constexpr int kFewTokens = 32;
 
 __global__ __launch_bounds__(256) void k_ce_dw_few(CeArgs g) {

@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_tile(EmbedArgs a, int bit
 // above it in the tiles before, and the keys below it in the tiles after.  Every
 // workgroup holds all keys in LDS (up to 128 KiB) and counts by halving for 128 of
 // them, 8 lanes a key: with one lane a key the random reads of LDS take twice as long
-// as all else.  30001 tokens: 14 us with the tiles' sort (16 with tiles of 4096); the six
+// as all else.  30001 tokens: 16 us with the tiles' sort (2 more with tiles of 4096); the six
 // launches of the pass-by-pass sort below, 31 us.
 constexpr int kMergeTiles = 16, kMergeMax = 32768, kMergeLanes = 8;
 constexpr int kMergeKeys = kSortThreads / kMergeLanes;   // of a workgroup
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(SortPass p) {
 // A run that crosses windows leaves one FP32 partial row per window, joined in order
 // by a second kernel.  Windows of 128 are as fast with many tokens and 1 us slower
 // with few.  8192 x 5120 BF16 with words as in text: 43 + 5 us, much of it while the
-// zeros drain; 30001 x 771, few words: 14 + 4 us.
+// zeros drain; 30001 x 771, few words: 15 + 6 us.
 constexpr int kWaveRows = 16, kSumWaves = 4, kWindow = kWaveRows * kSumWaves;
 
 // Eight values (for v8f) or one (float) as they lie in memory, and their value.

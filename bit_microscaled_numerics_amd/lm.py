@@ -10,9 +10,10 @@ kernels, on the current stream.  There is no CPU path.
   loss.backward()
   norm = clip_grad_norm(model.parameters(), 1.0)
 
-The head's loss and its gradients come from one call in the forward pass, so the
-logits are never stored and never computed twice; backward multiplies the stored
-gradients by the incoming one.  Targets outside 0 .. vocab - 1 (padding, -100) are
+The head's loss and its gradients come from one call in the forward pass: the logits
+are never stored in FP32 (16-bit values in a bounded workspace, during the call) and
+never computed twice; backward multiplies the stored gradients by the incoming one,
+which rounds them to BF16 once more unless it is a power of two.  Targets outside 0 .. vocab - 1 (padding, -100) are
 left out.
 """
 from __future__ import annotations

@@ -345,7 +345,7 @@ int nvfp4_embed_grad(const void* ids, int ids_type, int64_t n, const void* dy, i
  * and 16-byte aligned bases; loss and lse (nullable) FP32 [T]; targets I32 or
  * I64.  loss is never negative; its error is that of FP32 sums, absolute where it
  * is small.  A target outside 0 .. V-1 (an ignore mark such as -100) is none: its
- * loss is 0.  The logits are never stored.  T may be 0.  Rows whose logits are
+ * loss is 0.  Nothing of the size of the logits is stored.  T may be 0.  Rows whose logits are
  * not all finite give a loss and gradient that are not finite; other rows are
  * not affected.  workspace: 256-byte aligned, of at least
  * nvfp4_linear_ce_workspace_bytes(T, V, D, 0, 0). */
@@ -364,8 +364,9 @@ int nvfp4_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, int6
  * of h (infinities, NaN) reaches another result.  A row_weight of 0 masks a token
  * for the gradients: whatever its row of h holds, its row of dh is zero and dw
  * takes nothing from it (its loss is still written).
- * Tokens are taken piece_tokens at a time (0: as many as a buffer of 4 GiB
- * allows at 2 bytes per token and word); the workspace is
+ * Between the products the workspace holds a 16-bit value per token and word.
+ * Tokens are taken piece_tokens at a time to bound it (0: as many as 4 GiB
+ * allow); the workspace is
  * nvfp4_linear_ce_workspace_bytes(T, V, D, 1, piece_tokens) bytes.  The result
  * is the same bits every time. */
 int nvfp4_linear_ce_grad(const void* h, int64_t ldh, const void* w, int64_t ldw, int64_t T,

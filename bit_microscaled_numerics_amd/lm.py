@@ -70,10 +70,11 @@ def _reduce(loss: torch.Tensor, targets: torch.Tensor, vocab: int,
     live = (targets >= 0) & (targets < vocab)
     if row_weight is None:
         return _total(loss) / _total(live).clamp(min=1)
-    # a weight of 0 masks a token also where its loss is not finite
     term = loss * row_weight
-    return _total(torch.where(live & ((row_weight != 0) | (term == 0)), term,
-                              torch.zeros_like(loss)))
+    counts = live & (row_weight != 0)   # a weight of 0 masks a loss that is not finite too
+    if row_weight.requires_grad and torch.is_grad_enabled():
+        counts = counts | (live & (term == 0))   # a finite one is the derivative by its weight
+    return _total(torch.where(counts, term, torch.zeros_like(term)))
 
 
 class LinearCrossEntropyFunction(torch.autograd.Function):

@@ -12,7 +12,9 @@ Two layers:
     ``gemm``, which allocate outputs with ``torch.empty`` and return
     :class:`NVFP4Tensor` operands, and the operators at the ends of a training
     step beside them: ``embed`` / ``embed_grad``, ``linear_ce`` /
-    ``linear_ce_grad`` and ``clip_grads``.
+    ``linear_ce_grad`` and ``clip_grads``, and those of self-attention between
+    linear layers: ``qk_norm_rope`` / ``qk_norm_rope_grad`` and ``attention`` /
+    ``attention_grad``.
 """
 from __future__ import annotations
 
@@ -50,7 +52,9 @@ EXPORTED = ("nvfp4_amax", "nvfp4_amax_rht", "nvfp4_quantize1d_rtn", "nvfp4_quant
             "nvfp4_probe_clock", "nvfp4_probe_clock_bytes", "nvfp4_probe_copy",
             "nvfp4_embed", "nvfp4_embed_grad", "nvfp4_embed_grad_workspace_bytes",
             "nvfp4_grad_sumsq", "nvfp4_grad_clip", "nvfp4_grad_scale", "nvfp4_linear_ce", "nvfp4_linear_ce_grad",
-            "nvfp4_linear_ce_workspace_bytes")
+            "nvfp4_linear_ce_workspace_bytes", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_grad",
+            "nvfp4_qk_norm_rope_grad_workspace_bytes", "nvfp4_attention", "nvfp4_attention_grad",
+            "nvfp4_attention_workspace_bytes")
 
 
 class NVFP4Error(RuntimeError):
@@ -129,6 +133,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "nvfp4_grad_sumsq": [vp, i64, vp, vp],
         "nvfp4_grad_clip": [vp, i64, vp, ctypes.c_double, vp, vp],
         "nvfp4_grad_scale": [vp, i64, vp, vp],
+        "nvfp4_qk_norm_rope": [vp, vp, vp, vp, vp, vp],
+        "nvfp4_qk_norm_rope_grad": [vp] * 9 + [vp, i64, vp],
+        "nvfp4_attention": [vp] * 6 + [vp, i64, vp],
+        "nvfp4_attention_grad": [vp] * 10 + [vp, i64, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -148,6 +156,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.nvfp4_embed_grad_workspace_bytes.restype = ctypes.c_int64
     lib.nvfp4_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, i32, i64]
     lib.nvfp4_linear_ce_workspace_bytes.restype = ctypes.c_int64
+    lib.nvfp4_qk_norm_rope_grad_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.nvfp4_qk_norm_rope_grad_workspace_bytes.restype = ctypes.c_int64
+    lib.nvfp4_attention_workspace_bytes.argtypes = [vp, i32]
+    lib.nvfp4_attention_workspace_bytes.restype = ctypes.c_int64
     _lib = lib
     return lib
 
@@ -857,6 +869,244 @@ def scale_grads(grads, factor: torch.Tensor):
     outs = [_empty(g.numel(), dtype=g.dtype, device=g.device).view(g.shape) for g in grads]
     nvfp4_grad_scale(grads, outs, factor)
     return outs
+
+
+# ------------------------------------------------------- attention, and what feeds it
+def _heads(x: torch.Tensor, dims: int, dtype, name: str) -> bytes:
+    """The nvfp4_heads of a GPU tensor [tokens][heads][D], or [sequences] of them."""
+    if not x.is_cuda or x.dtype != dtype or x.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
+    st = x.stride()
+    if st[-1] != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return struct.pack("4q", x.data_ptr(), st[0] if dims == 4 else 0, st[-3], st[-2])
+
+
+def _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm) -> bytes:
+    """The nvfp4_rope of a call whose q and k are checked by ``_heads``."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q and k must be [tokens][heads][D] of the same tokens and D")
+    T, D = q.shape[0], q.shape[2]
+    kind = _FLOATS.get(q.dtype)
+    if kind is None:
+        raise ValueError("q and k must be bf16 or float32")
+    wt, ids, rot = NVFP4_TYPE_F32, NVFP4_TYPE_I32, 0
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        if not w.is_cuda or w.dtype not in _FLOATS or w.numel() != D or not w.is_contiguous():
+            raise ValueError(f"{name} must be {D} contiguous bf16 or float32 CUDA values")
+        wt = _FLOATS[w.dtype]
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    if inv_freq is not None:
+        ids, rot = _dev_ids(positions, "positions"), 2 * inv_freq.numel()
+        if positions.numel() != T:
+            raise ValueError("one position for each token")
+        _dev_f32(inv_freq, inv_freq.numel(), "inv_freq")
+    elif positions is not None:
+        raise ValueError("positions go with inv_freq")
+    _one_device(q, k, q_weight, k_weight, positions, inv_freq)
+    return struct.pack("5q5if4q", T, q.shape[1], k.shape[1], D, rot, kind, wt, ids, int(interleaved),
+                       int(norm), eps, _p(q_weight) or 0, _p(k_weight) or 0, _p(positions) or 0,
+                       _p(inv_freq) or 0)
+
+
+def _like(x, shape, name):
+    if x.shape != shape:
+        raise ValueError(f"{name} must be of shape {tuple(shape)}")
+
+
+def nvfp4_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm, q_out,
+                       k_out, stream=None):
+    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    _like(q_out, q.shape, "q_out")
+    _like(k_out, k.shape, "k_out")
+    _one_device(q_out, k_out)
+    dt = q.dtype
+    _check(load_library().nvfp4_qk_norm_rope(
+        r, _heads(q, 3, dt, "q"), _heads(k, 3, dt, "k"), _heads(q_out, 3, dt, "q_out"),
+        _heads(k_out, 3, dt, "k_out"), _stream(stream)))
+
+
+def nvfp4_qk_norm_rope_grad_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
+    n = int(load_library().nvfp4_qk_norm_rope_grad_workspace_bytes(T, Hq, Hkv, D))
+    if n < 0:
+        _check(n)
+    return n
+
+
+def nvfp4_qk_norm_rope_grad(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
+                            norm, dq_in, dk_in, dq_weight, dk_weight, workspace, stream=None):
+    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    for x, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dq_in, q, "dq_in"), (dk_in, k, "dk_in")):
+        _like(x, like.shape, name)
+    for x, w, name in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
+        if x is not None and (w is None or x.dtype != w.dtype or x.numel() != w.numel()
+                              or not x.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous, of its weight's size and type")
+    _one_device(dq, dk, dq_in, dk_in, dq_weight, dk_weight, workspace)
+    dt = q.dtype
+    _check(load_library().nvfp4_qk_norm_rope_grad(
+        r, _heads(dq, 3, dt, "dq"), _heads(dk, 3, dt, "dk"), _heads(q, 3, dt, "q"),
+        _heads(k, 3, dt, "k"), _heads(dq_in, 3, dt, "dq_in"), _heads(dk_in, 3, dt, "dk_in"),
+        _p(dq_weight), _p(dk_weight), _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, norm: bool = True):
+    """(q, k) with each head's row of D values divided by its root mean square, times
+    its side's weight [D], and rotated by the token's position: pairs (j, j + rot/2), or
+    (2j, 2j + 1) if interleaved, by positions[t] * inv_freq[j], rot = 2 * the number
+    of inv_freq (float32).  q [tokens][heads][D] and k [tokens][key heads][D], both bf16
+    or float32, with strides (pieces of a projection's rows); the results are contiguous.
+    Without inv_freq nothing is rotated; norm=False leaves the norm out."""
+    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    dt, dev = q.dtype, q.device
+    qo, ko = _empty(*q.shape, dtype=dt, device=dev), _empty(*k.shape, dtype=dt, device=dev)
+    # its own call of the entry point: a single token's rows are bound by the host
+    _check(load_library().nvfp4_qk_norm_rope(
+        r, _heads(q, 3, dt, "q"), _heads(k, 3, dt, "k"), _heads(qo, 3, dt, "q"),
+        _heads(ko, 3, dt, "k"), _stream(None)))
+    return qo, ko
+
+
+def qk_norm_rope_grad(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                      q_weight: Optional[torch.Tensor] = None,
+                      k_weight: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None,
+                      inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      interleaved: bool = False, norm: bool = True,
+                      out: Optional[tuple] = None):
+    """(dq, dk, dq_weight, dk_weight): the gradient of ``qk_norm_rope`` from the gradients
+    of its results and its own inputs; None for a weight that is not there.  out: the
+    tensors that take the first two, such as pieces of a projection's gradient."""
+    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    dt, dev = q.dtype, q.device
+    _like(dq, q.shape, "dq")
+    _like(dk, k.shape, "dk")
+    if out is None:
+        qi, ki = _empty(*q.shape, dtype=dt, device=dev), _empty(*k.shape, dtype=dt, device=dev)
+    else:
+        qi, ki = out
+        _like(qi, q.shape, "out[0]")
+        _like(ki, k.shape, "out[1]")
+    dwq, dwk = (None if w is None else _empty(w.numel(), dtype=w.dtype, device=dev).view(w.shape)
+                for w in (q_weight, k_weight))
+    _one_device(dq, dk, qi, ki)
+    n = nvfp4_qk_norm_rope_grad_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2])
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _check(load_library().nvfp4_qk_norm_rope_grad(
+        r, _heads(dq, 3, dt, "dq"), _heads(dk, 3, dt, "dk"), _heads(q, 3, dt, "q"),
+        _heads(k, 3, dt, "k"), _heads(qi, 3, dt, "out[0]"), _heads(ki, 3, dt, "out[1]"), _p(dwq),
+        _p(dwk), _p(ws), n, _stream(None)))
+    return qi, ki, dwq, dwk
+
+
+def _attn(q, k, v, scale, causal, window, cu_q, cu_k):
+    """(the nvfp4_attn of a call, the operands' number of dimensions)."""
+    dims = 3 if cu_q is not None else q.dim()
+    if dims not in (3, 4) or q.dim() != dims or k.dim() != dims or v.shape != k.shape:
+        raise ValueError("q, k and v must be [tokens][heads][D], or without cu_q also "
+                         "[sequences][tokens][heads][D], k and v of one shape")
+    if q.shape[-1] != k.shape[-1] or (dims == 4 and q.shape[0] != k.shape[0]):
+        raise ValueError("q and k must have the same D and number of sequences")
+    batch, at, kind = (q.shape[0] if dims == 4 else 1), (0, 0), 0
+    if cu_q is not None:
+        cu_k = cu_q if cu_k is None else cu_k
+        kind = _dev_ids(cu_q, "cu_q")
+        if _dev_ids(cu_k, "cu_k") != kind or cu_k.numel() != cu_q.numel() or cu_q.numel() < 1:
+            raise ValueError("cu_q and cu_k must be of one type and of one length, sequences + 1")
+        batch, at = cu_q.numel() - 1, (cu_q.data_ptr(), cu_k.data_ptr())
+    elif cu_k is not None:
+        raise ValueError("cu_k goes with cu_q")
+    _one_device(q, k, v, cu_q, cu_k)
+    D = q.shape[-1]
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return struct.pack("8qiiqf4x", batch, q.shape[-3], k.shape[-3], q.shape[-2], k.shape[-2], D, *at,
+                       kind, int(causal), window, scale), dims
+
+
+def nvfp4_attention_workspace_bytes(a: bytes, grad: bool) -> int:
+    n = int(load_library().nvfp4_attention_workspace_bytes(a, int(grad)))
+    if n < 0:
+        _check(n)
+    return n
+
+
+def nvfp4_attention(q, k, v, scale, causal, window, cu_q, cu_k, out, lse, workspace, stream=None):
+    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    _like(out, q.shape, "out")
+    _dev_f32(lse, q.shape[:-1].numel(), "lse")
+    _one_device(out, lse, workspace)
+    bf = torch.bfloat16
+    _check(load_library().nvfp4_attention(
+        a, _heads(q, dims, bf, "q"), _heads(k, dims, bf, "k"), _heads(v, dims, bf, "v"),
+        _heads(out, dims, bf, "out"), _p(lse), _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def nvfp4_attention_grad(dout, q, k, v, out, lse, scale, causal, window, cu_q, cu_k, dq, dk, dv,
+                         workspace, stream=None):
+    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    for x, like, name in ((dout, q, "dout"), (out, q, "out"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _like(x, like.shape, name)
+    _dev_f32(lse, q.shape[:-1].numel(), "lse")
+    _one_device(dout, out, lse, dq, dk, dv, workspace)
+    h = [_heads(x, dims, torch.bfloat16, name) for x, name in
+         ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    _check(load_library().nvfp4_attention_grad(a, *h[:5], _p(lse), *h[5:], _p(workspace),
+                                               _nbytes(workspace), _stream(stream)))
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
+              causal: bool = False, window: int = 0, cu_q: Optional[torch.Tensor] = None,
+              cu_k: Optional[torch.Tensor] = None):
+    """(out, lse) of softmax attention: out like q, contiguous, lse float32 [.., heads],
+    the log of the sum of a row's exponentials.  q [tokens][heads][D], k and v [keys][key heads][D]
+    bf16, of one sequence, or with cu_q (int32 or int64, on the GPU) of several one after
+    the other: sequence s is rows cu_q[s] .. cu_q[s+1]-1 of q and cu_k[s] .. of k
+    (cu_k None: cu_q); or [sequences][tokens][heads][D].  heads is a multiple of key heads; strides
+    are multiples of 8, D one up to 128.  scale: of the products (1/sqrt(D) if None).  causal: query
+    i of nq sees keys up to i + nk - nq; window > 0: only the last `window` of those.  A
+    query that sees no key has a row of zeros and an lse of -inf."""
+    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    bf, dev = torch.bfloat16, q.device
+    out = _empty(*q.shape, dtype=bf, device=dev)
+    lse = _empty(*q.shape[:-1], dtype=torch.float32, device=dev)
+    n = nvfp4_attention_workspace_bytes(a, False)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    # its own call of the entry point: a single token's attention is bound by the host
+    _check(load_library().nvfp4_attention(
+        a, _heads(q, dims, bf, "q"), _heads(k, dims, bf, "k"), _heads(v, dims, bf, "v"),
+        _heads(out, dims, bf, "out"), lse.data_ptr(), _p(ws), n, _stream(None)))
+    return out, lse
+
+
+def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   out: torch.Tensor, lse: torch.Tensor, scale: Optional[float] = None,
+                   causal: bool = False, window: int = 0, cu_q: Optional[torch.Tensor] = None,
+                   cu_k: Optional[torch.Tensor] = None, grads: Optional[tuple] = None):
+    """(dq, dk, dv): the gradient of ``attention`` from the gradient of its out, with the
+    out and lse that it returned for the same arguments.  grads: the tensors that take them."""
+    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    bf, dev = torch.bfloat16, q.device
+    if grads is None:
+        grads = tuple(_empty(*x.shape, dtype=bf, device=dev) for x in (q, k, v))
+    dq, dk, dv = grads
+    for x, like, name in ((dout, q, "dout"), (out, q, "out"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _like(x, like.shape, name)
+    _dev_f32(lse, q.shape[:-1].numel(), "lse")
+    _one_device(dout, out, lse, dq, dk, dv)
+    h = [_heads(x, dims, bf, name) for x, name in
+         ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    n = nvfp4_attention_workspace_bytes(a, True)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _check(load_library().nvfp4_attention_grad(a, *h[:5], lse.data_ptr(), *h[5:], _p(ws), n,
+                                               _stream(None)))
+    return dq, dk, dv
 
 
 PROBE_ZEROS, PROBE_NVFP4_LIKE, PROBE_UNIFORM = 0, 1, 2

@@ -1,0 +1,212 @@
+// lm_attn.h -- what the attention kernels share: operands, which keys a query sees, and
+// the arithmetic of single rows (internal to libnvfp4.so).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lm_attn_kernels.h"
+#include "lm_device.h"
+
+namespace nvfp4 {
+namespace attn {
+
+struct Rows {   // strides in elements
+  const uint16_t* p;
+  int64_t batch, token, head;
+};
+
+struct Args {
+  Rows q, k, v, out, dout, dq, dk, dv;
+  float* lse;      // [sequence][Tq][Hq], or [Tq][Hq]
+  float* delta;    // likewise (gradient)
+  const void* cu_q;
+  const void* cu_k;
+  int wide_cu, causal;
+  int batch;       // sequences behind one another (cu), or the operands' first dimension
+  int Tq, Tk, Hq, Hkv, G, D;
+  int64_t window;
+  float scale, scale2;   // scale2 = scale * log2(e)
+};
+
+struct Range {   // of keys, or of query tokens
+  int lo, hi;
+};
+
+__device__ __forceinline__ int cu_at(const void* cu, int wide, int i, int most) {
+  const int64_t x = wide ? static_cast<const int64_t*>(cu)[i] : (int64_t) static_cast<const int32_t*>(cu)[i];
+  return (int)(x < 0 ? 0 : x > most ? most : x);
+}
+
+// The sequence of row t: the last one that begins at or before t (empty ones before it
+// begin there too); -1 if none does.
+__device__ __forceinline__ int sequence_of(const void* cu, int wide, int n, int t, int most) {
+  int lo = 0, hi = n + 1;   // cu[lo - 1] <= t < cu[hi], as far as looked
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu_at(cu, wide, mid, most) <= t)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo - 1;
+}
+
+__device__ __forceinline__ int clamp64(int64_t x, int lo, int hi) {
+  return (int)(x < lo ? lo : x > hi ? hi : x);
+}
+
+struct Span {   // a sequence's queries and keys
+  int q0, q1, k0, k1;
+};
+__device__ __forceinline__ Span span_of(const Args& a, int s) {
+  if (s < 0 || s >= a.batch) return Span{0, 0, 0, 0};
+  return Span{cu_at(a.cu_q, a.wide_cu, s, a.Tq), cu_at(a.cu_q, a.wide_cu, s + 1, a.Tq),
+              cu_at(a.cu_k, a.wide_cu, s, a.Tk), cu_at(a.cu_k, a.wide_cu, s + 1, a.Tk)};
+}
+
+// The keys that query token t sees; empty for a t past the end.
+__device__ __forceinline__ Range keys_of(const Args& a, int t) {
+  if (t >= a.Tq) return Range{0, 0};
+  Span s{0, a.Tq, 0, a.Tk};
+  if (a.cu_q != nullptr) s = span_of(a, sequence_of(a.cu_q, a.wide_cu, a.batch, t, a.Tq));
+  if (t < s.q0 || t >= s.q1 || s.k1 <= s.k0) return Range{0, 0};
+  if (!a.causal) return Range{s.k0, s.k1};
+  const int64_t end = (int64_t)(t - s.q0) + 1 + (s.k1 - s.k0) - (s.q1 - s.q0);
+  const int hi = s.k0 + clamp64(end, 0, s.k1 - s.k0);
+  const int lo = a.window > 0 ? s.k0 + clamp64(end - a.window, 0, s.k1 - s.k0) : s.k0;
+  return Range{lo, hi};
+}
+
+// The query tokens that see key j.
+__device__ __forceinline__ Range queries_of(const Args& a, int j) {
+  if (j >= a.Tk) return Range{0, 0};
+  Span s{0, a.Tq, 0, a.Tk};
+  if (a.cu_q != nullptr) s = span_of(a, sequence_of(a.cu_k, a.wide_cu, a.batch, j, a.Tk));
+  if (j < s.k0 || j >= s.k1 || s.q1 <= s.q0) return Range{0, 0};
+  if (!a.causal) return Range{s.q0, s.q1};
+  const int64_t first = (int64_t)(j - s.k0) - ((s.k1 - s.k0) - (s.q1 - s.q0));
+  const int lo = s.q0 + clamp64(first, 0, s.q1 - s.q0);
+  const int hi = a.window > 0 ? s.q0 + clamp64(first + a.window, 0, s.q1 - s.q0) : s.q1;
+  return Range{lo, hi};
+}
+
+__device__ __forceinline__ int64_t stat_at(const Args& a, int b, int t, int h) {
+  return ((int64_t)b * a.Tq + t) * a.Hq + h;
+}
+__device__ __forceinline__ const bf16_t* row_of(const Rows& r, int b, int t, int h) {
+  return reinterpret_cast<const bf16_t*>(r.p) + b * r.batch + t * r.token + h * r.head;
+}
+__device__ __forceinline__ bf16_t* row_of_out(const Rows& r, int b, int t, int h) {
+  return const_cast<bf16_t*>(row_of(r, b, t, h));
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+  return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+__device__ __forceinline__ float dot(const bf16_t* x, const bf16_t* y, int D) {
+  float s = 0.0f;
+  for (int d = 0; d < D; d += 8) {
+    const v8f a = load8(x + d), b = load8(y + d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+  }
+  return s;
+}
+
+// --------------------------------------------------------------- single rows
+// One wave, one row at a time; only keys (or queries) that count are looked at, so
+// nothing that a mask hides can reach a result.  A lane forms the score of one key of
+// 64, then owns two columns.
+
+struct RowSum {   // columns lane and lane + 64
+  float x0 = 0.0f, x1 = 0.0f;
+  // += w * row
+  __device__ __forceinline__ void add(const bf16_t* row, int D, float w) {
+    const int lane = threadIdx.x & 63;
+    if (lane < D) x0 = fmaf(w, load1(row + lane), x0);
+    if (lane + 64 < D) x1 = fmaf(w, load1(row + lane + 64), x1);
+  }
+  __device__ __forceinline__ void store(bf16_t* row, int D, float f) const {
+    const int lane = threadIdx.x & 63;
+    if (lane < D) store1(row + lane, x0 * f);
+    if (lane + 64 < D) store1(row + lane + 64, x1 * f);
+  }
+};
+
+struct Soft {   // scores in log2: the running maximum, the sum relative to it
+  float m, l;
+  RowSum o;
+};
+
+// The query's softmax over keys lo .. hi - 1.
+__device__ inline Soft row_forward(const Args& a, int b, int t, int h, int lo, int hi) {
+  const int lane = threadIdx.x & 63, hk = h / a.G;
+  const bf16_t* q = row_of(a.q, b, t, h);
+  Soft r{-INFINITY, 0.0f, {}};
+  for (int j0 = lo; j0 < hi; j0 += 64) {
+    const int j = j0 + lane, n = min(64, hi - j0);
+    const float s = j < hi ? dot(q, row_of(a.k, b, j, hk), a.D) * a.scale2 : -INFINITY;
+    // a NaN score must not be dropped by the maximum
+    const float m = fmaxf(r.m, wave_max(s)), at = m == -INFINITY ? 0.0f : m;
+    const float p = j < hi ? exp2f(s - at) : 0.0f, f = r.m == -INFINITY ? 0.0f : exp2f(r.m - at);
+    r.l = r.l * f + wave_sum(p);
+    r.o.x0 *= f;
+    r.o.x1 *= f;
+    r.m = m;
+    for (int i = 0; i < n; ++i) r.o.add(row_of(a.v, b, j0 + i, hk), a.D, __shfl(p, i));
+  }
+  return r;
+}
+
+// p and ds of one query and key.
+__device__ __forceinline__ void pair_grad(const Args& a, int b, int t, int h, int j, float& p, float& ds) {
+  const int hk = h / a.G;
+  const float lse = a.lse[stat_at(a, b, t, h)], delta = a.delta[stat_at(a, b, t, h)];
+  const float s = dot(row_of(a.q, b, t, h), row_of(a.k, b, j, hk), a.D) * a.scale;
+  p = expf(s - lse);
+  ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) - delta);
+}
+
+__device__ inline void row_dq(const Args& a, int b, int t, int h) {
+  const int lane = threadIdx.x & 63, hk = h / a.G;
+  const Range r = keys_of(a, t);
+  RowSum dq;
+  for (int j0 = r.lo; j0 < r.hi; j0 += 64) {
+    const int j = j0 + lane, n = min(64, r.hi - j0);
+    float p = 0.0f, ds = 0.0f;
+    if (j < r.hi) pair_grad(a, b, t, h, j, p, ds);
+    for (int i = 0; i < n; ++i) dq.add(row_of(a.k, b, j0 + i, hk), a.D, __shfl(ds, i));
+  }
+  dq.store(row_of_out(a.dq, b, t, h), a.D, a.scale);
+}
+
+// Query rows lo .. hi - 1 (token * G + head of the group), added to dk and dv.
+__device__ inline void row_dkv(const Args& a, int b, int j, int hk, int64_t lo, int64_t hi, RowSum& dk,
+                               RowSum& dv) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r0 = lo; r0 < hi; r0 += 64) {
+    const int64_t r = r0 + lane;
+    const int n = (int)min((int64_t)64, hi - r0);
+    float p = 0.0f, ds = 0.0f;
+    if (r < hi) pair_grad(a, b, (int)(r / a.G), hk * a.G + (int)(r % a.G), j, p, ds);
+    for (int i = 0; i < n; ++i) {
+      const int t = (int)((r0 + i) / a.G), h = hk * a.G + (int)((r0 + i) % a.G);
+      dv.add(row_of(a.dout, b, t, h), a.D, __shfl(p, i));
+      dk.add(row_of(a.q, b, t, h), a.D, __shfl(ds, i));
+    }
+  }
+}
+
+Args make_args(const AttnCall& c);
+
+}  // namespace attn
+}  // namespace nvfp4

@@ -411,6 +411,107 @@ int nvfp4_grad_clip(const nvfp4_grad* list, int64_t count, const double* partial
 int nvfp4_grad_scale(const nvfp4_grad* list, int64_t count, const float* factor, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Self-attention between a model's NVFP4 linear layers: norms and position
+ * rotation of queries and keys, and softmax attention, each with its gradient.
+ * The recipe keeps attention in BF16 (the same paragraph); sums, statistics and
+ * angles are FP32 or wider.  All results are the same bits every time.
+ * ------------------------------------------------------------------------ */
+
+/* Heads of tokens: element (b, t, h, d) at p[b*batch + t*token + h*head + d], strides in
+ * elements.  batch is read only by the attention calls without cu_q.  Head and
+ * token rows must not overlap (one of the two strides steps over all rows of the
+ * other).  A projection's fused rows are three of these. */
+typedef struct {
+  const void* p;       /* written through where the call says so */
+  int64_t batch, token, head;
+} nvfp4_heads;
+
+/* What nvfp4_qk_norm_rope does to a head's row x of D values:
+ *   z = x * r * w,   r = norm ? 1 / sqrt(mean(x^2) + eps) : 1   (w NULL: all 1)
+ *   (a, b) = (a cos u - b sin u, b cos u + a sin u),   u = positions[t] * inv_freq[j]
+ * for the pairs j < rot/2 of z: (z[j], z[j + rot/2]), or (z[2j], z[2j+1]) if
+ * interleaved; z[rot ..] stays.  Angles are formed in FP64 from any position
+ * (|position| up to 2^31 is exact to FP32), all else in FP32; one rounding at the end. */
+typedef struct {
+  int64_t T, Hq, Hkv, D;     /* tokens and heads 0 or more; D even, 2 .. 512 */
+  int64_t rot;               /* even, 0 .. D */
+  int32_t type;              /* of q, k and the results: BF16 or F32 */
+  int32_t weight_type;       /* of q_weight, k_weight and their gradients: BF16 or F32 */
+  int32_t positions_type;    /* I32 or I64 */
+  int32_t interleaved, norm; /* 0 or 1; without norm the weights must be NULL */
+  float eps;                 /* 0 or more */
+  const void* q_weight;      /* [D] or NULL */
+  const void* k_weight;
+  const void* positions;     /* [T] */
+  const float* inv_freq;     /* [rot/2] */
+} nvfp4_rope;
+
+/* q_out and k_out may be q and k (in place, the same strides); other overlaps race. */
+int nvfp4_qk_norm_rope(const nvfp4_rope* r, const nvfp4_heads* q, const nvfp4_heads* k,
+                       const nvfp4_heads* q_out, const nvfp4_heads* k_out, void* stream);
+
+/* Its gradient: dq, dk (the incoming ones) to dq_in, dk_in, which may be dq and dk (in place, the
+ * same strides), and dq_weight, dk_weight [D] of weight_type (nullable: not formed; must
+ * be NULL without their weight), FP32 sums over tokens and heads in an order fixed by the sizes,
+ * joined in FP64.  q and k are the unchanged inputs.  workspace: 256-byte aligned, of at least
+ * nvfp4_qk_norm_rope_grad_workspace_bytes(T, Hq, Hkv, D). */
+int64_t nvfp4_qk_norm_rope_grad_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
+int nvfp4_qk_norm_rope_grad(const nvfp4_rope* r, const nvfp4_heads* dq, const nvfp4_heads* dk,
+                            const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* dq_in,
+                            const nvfp4_heads* dk_in, void* dq_weight, void* dk_weight,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Softmax attention.  Query head h reads key head h / (Hq / Hkv).
+ *   s_ij = scale * sum_d q[i][d] k[j][d] over the keys j that query i sees,
+ *   lse[i] = log sum_j exp(s_ij),   out[i] = sum_j exp(s_ij - lse[i]) v[j]
+ * Query i of a sequence with nq queries and nk keys sees all of its keys; with
+ * causal those up to j = i + nk - nq (the last query sees the last key); with
+ * a window > 0 (causal only) the last `window` of those.  A query that sees no key
+ * has a row of zeros and an lse of -infinity.
+ * Sequences: without cu_q, `batch` of them with Tq queries and Tk keys each.  With
+ * cu_q (and cu_k, which may be the same), Tq and Tk count the rows of all sequences together,
+ * and sequence s is queries cu_q[s] .. cu_q[s+1]-1 and keys cu_k[s] .. cu_k[s+1]-1:
+ * batch + 1 ascending device values each, from 0 on.  Rows behind the last sequence (or
+ * before the first) belong to none: they see nothing and nothing sees them; their
+ * results are zeros.  Values of cu that do not ascend or exceed Tq, Tk give unspecified
+ * results, without an access outside the operands.
+ * What a query does not see (infinities, NaN) does not reach its results, nor its
+ * gradients those of the keys that it does not see.
+ * q, k, v, out and gradients BF16, 16-byte aligned with strides that are multiples of 8;
+ * lse FP32 [batch][Tq][Hq] ([Tq][Hq] with cu_q).  Accumulation is FP32; the
+ * probabilities (and in the gradient the scores' gradients) enter their products rounded to BF16. */
+typedef struct {
+  int64_t batch, Tq, Tk;     /* 0 or more */
+  int64_t Hq, Hkv;           /* Hq a multiple of Hkv */
+  int64_t D;                 /* a multiple of 8, 8 .. 128 */
+  const void* cu_q;          /* NULL: sequences of one length */
+  const void* cu_k;
+  int32_t cu_type;           /* I32 or I64 */
+  int32_t causal;            /* 0 or 1 */
+  int64_t window;            /* 0: none */
+  float scale;
+} nvfp4_attn;
+
+/* workspace (also of the gradient): 256-byte aligned, of at least
+ * nvfp4_attention_workspace_bytes(a, grad) bytes, which depends on the sizes alone; NULL
+ * where that is 0. */
+int64_t nvfp4_attention_workspace_bytes(const nvfp4_attn* a, int grad);
+int nvfp4_attention(const nvfp4_attn* a, const nvfp4_heads* q, const nvfp4_heads* k,
+                    const nvfp4_heads* v, const nvfp4_heads* out, float* lse, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Its gradient, from out and lse of the forward call (the probabilities are formed
+ * again from lse): with p_ij = exp(s_ij - lse[i]) and delta_i = sum_d dout[i][d] out[i][d],
+ *   dv[j] = sum_i p_ij dout[i],   ds_ij = p_ij (sum_d dout[i][d] v[j][d] - delta_i)
+ *   dq[i] = scale sum_j ds_ij k[j],   dk[j] = scale sum_i ds_ij q[i]
+ * with the sums over i running over the query heads of a key head too. */
+int nvfp4_attention_grad(const nvfp4_attn* a, const nvfp4_heads* dout, const nvfp4_heads* q,
+                         const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                         const float* lse, const nvfp4_heads* dq, const nvfp4_heads* dk,
+                         const nvfp4_heads* dv, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
  * Measurement support (not part of the quantize / GEMM path): the sustained
  * throughput and shader clock of the FP16 matrix cores running the GEMM fast
  * path's MFMA pattern (v_mfma_f32_32x32x16_f16, 8 x 2 independent

@@ -206,6 +206,131 @@ __device__ inline void row_dkv(const Args& a, int b, int j, int hk, int64_t lo, 
   }
 }
 
+// ------------------------------------------------------------------- tiles
+// Products run on v_mfma_f32_32x32x16_bf16.  Rows of q (and dout) are counted over the
+// heads of a group: row r is token r / G of head r % G, so that all heads of a group share the
+// tiles of their keys.
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_void;
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+constexpr uint32_t kDead = 0x80000000u;   // a byte offset past every descriptor: reads zero
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint16_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>(uniform64((int64_t)(uintptr_t)p)), (short)0, 0x7fffffff, 0x00020000);
+}
+
+__device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// A tile in LDS: rows of DP values (64 or 128), 16-byte chunk c of row r at c ^ swz(r).
+// swz makes both reads free of bank conflicts: 16 lanes that take the same chunk of 16
+// consecutive rows (fragments along d), and the transposing read, where 32 lanes take
+// 64 bytes of 4 consecutive rows.
+template <int DP>
+struct Tile {
+  static constexpr int kRow = DP * 2, kChunks = DP / 8, kSteps = DP / 16, kBlocks = DP / 32;
+  static __device__ __forceinline__ int swz(int r) {
+    return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 2) & 3);
+  }
+  // Lane's place in a fragment along d of rows 0 .. 31: row lane & 31, chunk 2 ks + half.
+  static __device__ __forceinline__ int frag(int lane, int ks) {
+    const int r = lane & 31;
+    return r * kRow + (((2 * ks + (lane >> 5)) ^ swz(r)) << 4);
+  }
+  // Lane's place in the transposing read of block db of 32 columns: rows 4 half + (0 .. 3)
+  // of a step of 16, and 8 on (hi).
+  static __device__ __forceinline__ int frag_t(int lane, int db, int hi) {
+    const int g = lane >> 4, j = lane & 15, r = 4 * (g >> 1) + (j >> 2) + 8 * hi;
+    return r * kRow + (((db * 4 + 2 * (g & 1) + ((j & 3) >> 1)) ^ swz(r)) << 4) + (j & 1) * 8;
+  }
+  static __device__ __forceinline__ v8bf read(const uint8_t* at) {
+    return *reinterpret_cast<const v8bf*>(at);
+  }
+  // 8 values of the lane's column: rows of lo, then of hi.
+  static __device__ __forceinline__ v8bf read_t(const uint8_t* lo, const uint8_t* hi) {
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)lo);
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)hi);
+    return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+// Loads ROWS consecutive key rows into LDS, 4 waves together; rows past the end and
+// columns past D read zero.
+template <int DP, int ROWS>
+struct KeyLoader {
+  using T = Tile<DP>;
+  static constexpr int kLoads = ROWS * T::kRow / 4096;   // per wave, 1 KiB each
+  const uint16_t* base;
+  int64_t ld;
+  int end;
+  uint32_t voff[kLoads];
+  int row[kLoads];
+
+  __device__ __forceinline__ void init(const Rows& x, int b, int hk, int rows, int D, int wave) {
+    const int lane = threadIdx.x & 63;
+    base = x.p + b * x.batch + hk * x.head;
+    ld = x.token;
+    end = rows;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int at = (wave * kLoads + q) * 1024 + lane * 16;
+      row[q] = at / T::kRow;
+      const int chunk = (at % T::kRow / 16) ^ T::swz(row[q]);
+      voff[q] = (uint32_t)row[q] * (uint32_t)ld * 2 + chunk * 16;
+      if (chunk * 8 >= D) row[q] = 0x7fffffff;   // always past the end
+    }
+  }
+  __device__ __forceinline__ void load(uint8_t* lds, int wave, int j0) const {
+    const __amdgpu_buffer_rsrc_t buf = descriptor(base + (int64_t)j0 * ld);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(lds + (wave * kLoads + q) * 1024), 16,
+                                               voff[q] | (row[q] < end - j0 ? 0u : kDead), 0, 0, 0);
+  }
+};
+
+// max and sum over a lane and the one 32 away
+__device__ __forceinline__ float pair_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Eight scores or probabilities as the second operand of a product.
+__device__ __forceinline__ v8bf pack_half(const v16f& x, int half) {
+  v8f y;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[8 * half + i];
+  return __builtin_convertvector(y, v8bf);
+}
+
+// Word v of an accumulator: row (v & 3) + 8 (v >> 2) + 4 half, column lane & 31.
+__device__ __forceinline__ constexpr int acc_row(int v) { return (v & 3) + 8 * (v >> 2); }
+
+// Eight workgroups in a row run on the eight XCDs.  Sequences and key heads go round
+// the XCDs, so that an XCD's L2 holds the keys of its own; what 8 does not divide comes last.
+struct Job {
+  int pair, tile;
+};
+__device__ __forceinline__ Job job_of(int64_t id, int pairs, int tiles) {
+  const int64_t whole = (int64_t)(pairs & ~7) * tiles;
+  if (id < whole) {
+    const int64_t i = id >> 3;
+    return Job{(int)((id & 7) + 8 * (i / tiles)), (int)(i % tiles)};
+  }
+  const int64_t i = id - whole;
+  return Job{(pairs & ~7) + (int)(i / tiles), (int)(i % tiles)};
+}
+
 Args make_args(const AttnCall& c);
 
 }  // namespace attn

@@ -46,17 +46,225 @@ Args make_args(const AttnCall& c) {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kRowsWG = 128, kKeys = 64;   // query rows of a workgroup, keys of a tile
+constexpr int kPartTiles = 512, kPartKeys = 128;   // see parts_of
 
-__global__ __launch_bounds__(kWaves * 64) void k_attn_rows(Args a, int64_t rows) {
+struct Part {   // of a row's softmax, where several workgroups share its keys
+  float* o;     // [part][row][D], not normalized
+  float* ml;    // [part][row][2]: maximum (log2), sum
+  int n;
+};
+
+// Forward.  4 waves of 32 query rows each; the keys pass in tiles of 64 through two LDS
+// stages filled by loads that write LDS directly.  Scores are formed transposed (S^T = K
+// Q^T): a lane then holds one query's scores of 32 keys, so the softmax needs one
+// exchange (with the lane 32 away), and the probabilities are, as they stand, the second operand of
+// O^T = V^T P^T; V is read transposed from LDS.  The sums are rescaled only when
+// a maximum grows by more than 2^8: until then the probabilities are at most 2^8 and lose nothing.
+template <int DP, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, Part part) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass drops the stubs of kernels with these builtins
+  using T = Tile<DP>;
+  constexpr int kStage = 2 * kKeys * T::kRow;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  int(*ends)[4] = reinterpret_cast<int(*)[4]>(lds);
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int64_t id = SPLIT ? block_xz() / part.n : block_xz();
+  const int sp = SPLIT ? (int)(block_xz() % part.n) : 0;
+  if (id >= (int64_t)pairs * tiles) return;
+  const Job job = job_of(id, pairs, tiles);
+  const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
+  const int64_t rows = (int64_t)a.Tq * a.G;
+  // long rows of a causal sequence first
+  const int64_t r = (int64_t)(tiles - 1 - job.tile) * kRowsWG + wave * 32 + (lane & 31);
+  const bool live = r < rows;
+  const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
+  const Range mine = keys_of(a, t);
+
+  // the keys that any row sees, of the wave and of the workgroup; those that all see
+  const bool some = mine.lo < mine.hi;
+  int lo = some ? mine.lo : 0x7fffffff, hi = some ? mine.hi : 0;
+  int all_lo = live ? mine.lo : 0, all_hi = live ? mine.hi : 0x7fffffff;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    lo = min(lo, __shfl_xor(lo, m));
+    hi = max(hi, __shfl_xor(hi, m));
+    all_lo = max(all_lo, __shfl_xor(all_lo, m));
+    all_hi = min(all_hi, __shfl_xor(all_hi, m));
+  }
+  lo = uniform(lo), hi = uniform(hi), all_lo = uniform(all_lo), all_hi = uniform(all_hi);
+  if (lane == 0) ends[0][wave] = lo, ends[1][wave] = hi;
+  __syncthreads();
+  int j0 = min(min(ends[0][0], ends[0][1]), min(ends[0][2], ends[0][3]));
+  int j1 = max(max(ends[1][0], ends[1][1]), max(ends[1][2], ends[1][3]));
+  j0 = uniform(j0), j1 = uniform(j1);
+  __syncthreads();
+  if (SPLIT && j0 < j1) {
+    const int per = ((j1 - j0 + kKeys - 1) / kKeys + part.n - 1) / part.n;
+    const int64_t from = j0 + (int64_t)sp * per * kKeys, to = from + per * kKeys;
+    j0 = (int)min(from, (int64_t)j1);
+    j1 = (int)min(to, (int64_t)j1);
+  }
+
+  v8bf q[T::kSteps];
+  {
+    const bf16_t* row = row_of(a.q, b, live ? t : 0, h);
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks) {
+      const int d = 16 * ks + 8 * half;
+      v4u x{};
+      if (live && d < a.D) x = *reinterpret_cast<const v4u*>(row + d);
+      q[ks] = __builtin_bit_cast(v8bf, x);
+    }
+  }
+  KeyLoader<DP, kKeys> lk, lv;
+  lk.init(a.k, b, hk, a.Tk, a.D, wave);
+  lv.init(a.v, b, hk, a.Tk, a.D, wave);
+  int fk[T::kSteps], fv[T::kBlocks][2];
+#pragma unroll
+  for (int ks = 0; ks < T::kSteps; ++ks) fk[ks] = T::frag(lane, ks);
+#pragma unroll
+  for (int db = 0; db < T::kBlocks; ++db) fv[db][0] = T::frag_t(lane, db, 0), fv[db][1] = T::frag_t(lane, db, 1);
+
+  v16f o[T::kBlocks] = {};
+  float m = -INFINITY, l = 0.0f;   // m: of the products, before scale
+  if (j0 < j1) {
+    lk.load(lds, wave, j0);
+    lv.load(lds + kStage / 2, wave, j0);
+  }
+  for (int j = j0, stage = 0; j < j1; j += kKeys, stage ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint8_t* at = lds + stage * kStage;
+    if (j + kKeys < j1) {
+      uint8_t* next = lds + (stage ^ 1) * kStage;
+      lk.load(next, wave, j + kKeys);
+      lv.load(next + kStage / 2, wave, j + kKeys);
+    }
+    const int last = SPLIT ? min(hi, j1) : hi;
+    if (j >= last || j + kKeys <= lo) continue;
+    v16f s[2] = {};
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) s[kb] = mfma(T::read(at + fk[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
+    if (j < all_lo || j + kKeys > (SPLIT ? min(all_hi, j1) : all_hi)) {
+      const uint32_t n = (uint32_t)max((SPLIT ? min(mine.hi, j1) : mine.hi) - mine.lo, 0);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if ((uint32_t)(j + kb * 32 + 4 * half - mine.lo + acc_row(v)) >= n) s[kb][v] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) top = fmaxf(top, s[kb][v]);
+    top = fmaxf(m, pair_max(top));
+    if (__any((top - m) * a.scale2 > 8.0f)) {
+      const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.scale2);
+      l *= f;
+#pragma unroll
+      for (int db = 0; db < T::kBlocks; ++db) o[db] *= f;
+      m = top;
+    }
+    const float shift = m == -INFINITY ? 0.0f : m * a.scale2;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[kb][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][v], a.scale2, -shift));
+        l += s[kb][v];
+      }
+    const uint8_t* vt = at + kStage / 2;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const v8bf p = pack_half(s[ks >> 1], ks & 1);
+#pragma unroll
+      for (int db = 0; db < T::kBlocks; ++db)
+        o[db] = mfma(T::read_t(vt + fv[db][0] + ks * 16 * T::kRow, vt + fv[db][1] + ks * 16 * T::kRow), p, o[db]);
+    }
+  }
+  l = pair_sum(l);
+
+  // A value that is not finite may come from a key that a row does not see, multiplied by 0:
+  // such rows are formed again, one by one.
+  float odd = 0.0f;
+#pragma unroll
+  for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) odd = __builtin_fmaf(o[db][v], 0.0f, odd);
+  uint64_t again = __ballot(live && odd != 0.0f);
+  const float f = SPLIT ? 1.0f : some ? 1.0f / l : 0.0f;
+  const int64_t at = SPLIT ? (int64_t)sp * pairs * rows + job.pair * rows + r : 0;
+  if (live) {
+#pragma unroll
+    for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = db * 32 + 8 * i + 4 * half;
+        if (d >= a.D) continue;
+        typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+        v4f x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = o[db][4 * i + e] * f;
+        if (SPLIT)
+          *reinterpret_cast<v4f*>(part.o + at * a.D + d) = x;
+        else
+          *reinterpret_cast<v4bf*>(row_of_out(a.out, b, t, h) + d) = __builtin_convertvector(x, v4bf);
+      }
+    if (half == 0) {
+      if (SPLIT) {
+        part.ml[2 * at] = m * a.scale2;
+        part.ml[2 * at + 1] = l;
+      } else {
+        a.lse[stat_at(a, b, t, h)] = some ? (m * a.scale2 + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+  for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
+    const int from = __builtin_ctzll(again);
+    const int tt = __shfl(t, from), hh = __shfl(h, from), lo1 = __shfl(mine.lo, from), hi1 = __shfl(mine.hi, from);
+    const int64_t at1 = at - (lane & 31) + from;
+    const Soft x = row_forward(a, b, tt, hh, SPLIT ? max(lo1, j0) : lo1, SPLIT ? min(hi1, j1) : hi1);
+    if (SPLIT) {
+      if (lane < a.D) part.o[at1 * a.D + lane] = x.o.x0;
+      if (lane + 64 < a.D) part.o[at1 * a.D + lane + 64] = x.o.x1;
+      if (lane == 0) part.ml[2 * at1] = x.m, part.ml[2 * at1 + 1] = x.l;
+    } else {
+      x.o.store(row_of_out(a.out, b, tt, hh), a.D, lo1 < hi1 ? 1.0f / x.l : 0.0f);
+      if (lane == 0)
+        a.lse[stat_at(a, b, tt, hh)] = lo1 < hi1 ? (x.m + __builtin_amdgcn_logf(x.l)) * kLn2 : -INFINITY;
+    }
+  }
+#endif
+}
+
+// The parts of each row joined, in order: one wave a row.
+__global__ __launch_bounds__(kWaves * 64) void k_attn_join(Args a, int64_t rows, Part part) {
   const int64_t r = block_xz() * kWaves + (threadIdx.x >> 6);
   if (r >= rows) return;
-  const int h = (int)(r % a.Hq), t = (int)(r / a.Hq % a.Tq), b = (int)(r / a.Hq / a.Tq);
+  const int lane = threadIdx.x & 63;
+  const int64_t in_pair = (int64_t)a.Tq * a.G;
+  const int pair = (int)(r / in_pair), rr = (int)(r % in_pair);
+  const int b = pair / a.Hkv, t = rr / a.G, h = pair % a.Hkv * a.G + rr % a.G;
+  float m = -INFINITY;
+  for (int i = 0; i < part.n; ++i) m = fmaxf(m, part.ml[2 * (i * rows + r)]);
+  float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
+  for (int i = 0; i < part.n; ++i) {
+    const int64_t at = i * rows + r;
+    const float mi = part.ml[2 * at];
+    const float f = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
+    const float li = part.ml[2 * at + 1];
+    l += li * f;
+    if (lane < a.D) x0 += part.o[at * a.D + lane] * f;
+    if (lane + 64 < a.D) x1 += part.o[at * a.D + lane + 64] * f;
+  }
   const Range k = keys_of(a, t);
-  const Soft s = row_forward(a, b, t, h, k.lo, k.hi);
-  const bool any = k.lo < k.hi;
-  s.o.store(row_of_out(a.out, b, t, h), a.D, any ? 1.0f / s.l : 0.0f);
-  if ((threadIdx.x & 63) == 0)
-    a.lse[stat_at(a, b, t, h)] = any ? (s.m + log2f(s.l)) * 0.6931471805599453f : -INFINITY;
+  const bool some = k.lo < k.hi;
+  const RowSum o{x0, x1};
+  o.store(row_of_out(a.out, b, t, h), a.D, some ? 1.0f / l : 0.0f);
+  if (lane == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 __global__ __launch_bounds__(kWaves * 64) void k_attn_delta(Args a, int64_t rows) {
@@ -96,14 +304,51 @@ int64_t blocks(int64_t rows) { return (rows + kWaves - 1) / kWaves; }
 
 using namespace attn;
 
+namespace {
+
+// Workgroups that share a row's keys: while the tiles of queries leave most of the
+// chip idle, parts of at least 128 keys.
+int parts_of(const nvfp4_attn& a) {
+  const int64_t G = a.Hq / a.Hkv, tiles = (a.Tq * G + kRowsWG - 1) / kRowsWG * sequences(a) * a.Hkv;
+  if (tiles == 0 || tiles >= kPartTiles) return 1;
+  const int64_t keys = a.Tk / kPartKeys, want = kPartTiles / tiles;
+  const int64_t n = keys < want ? keys : want;
+  return n < 1 ? 1 : (int)n;
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
 int64_t attn_workspace_bytes(const nvfp4_attn& a, bool grad) {
-  return grad ? sequences(a) * a.Tq * a.Hq * 4 : 0;
+  const int64_t rows = sequences(a) * a.Tq * a.Hq;
+  if (grad) return rows * 4;
+  const int n = parts_of(a);
+  return n > 1 ? up256(rows * n * a.D * 4) + rows * n * 8 : 0;
 }
 
 hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
   const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq;
   if (rows == 0) return hipSuccess;
-  k_attn_rows<<<grid_xz(blocks(rows)), kWaves * 64, 0, s>>>(make_args(c), rows);
+  const Args a = make_args(c);
+  const int pairs = (int)(sequences(c.a) * a.Hkv);
+  const int tiles = (int)(((int64_t)a.Tq * a.G + kRowsWG - 1) / kRowsWG);
+  Part part{nullptr, nullptr, parts_of(c.a)};
+  const int64_t n = (int64_t)pairs * tiles;
+  if (part.n == 1) {
+    if (a.D <= 64)
+      k_attn<64, false><<<grid_xz(n), 256, 0, s>>>(a, pairs, tiles, part);
+    else
+      k_attn<128, false><<<grid_xz(n), 256, 0, s>>>(a, pairs, tiles, part);
+    return hipGetLastError();
+  }
+  part.o = static_cast<float*>(c.ws);
+  part.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * part.n * a.D * 4));
+  if (a.D <= 64)
+    k_attn<64, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
+  else
+    k_attn<128, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
+  k_attn_join<<<grid_xz(blocks(rows)), kWaves * 64, 0, s>>>(a, rows, part);
   return hipGetLastError();
 }
 

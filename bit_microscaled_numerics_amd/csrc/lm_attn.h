@@ -19,7 +19,7 @@ struct Rows {   // strides in elements
 struct Args {
   Rows q, k, v, out, dout, dq, dk, dv;
   float* lse;      // [sequence][Tq][Hq], or [Tq][Hq]
-  float* delta;    // likewise (gradient)
+  float2* stats;   // gradient: {lse in log2, delta} of [sequence * key head][row]
   const void* cu_q;
   const void* cu_k;
   int wide_cu, causal;
@@ -170,10 +170,9 @@ __device__ inline Soft row_forward(const Args& a, int b, int t, int h, int lo, i
 // p and ds of one query and key.
 __device__ __forceinline__ void pair_grad(const Args& a, int b, int t, int h, int j, float& p, float& ds) {
   const int hk = h / a.G;
-  const float lse = a.lse[stat_at(a, b, t, h)], delta = a.delta[stat_at(a, b, t, h)];
-  const float s = dot(row_of(a.q, b, t, h), row_of(a.k, b, j, hk), a.D) * a.scale;
-  p = expf(s - lse);
-  ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) - delta);
+  const float2 st = a.stats[((int64_t)b * a.Hkv + hk) * a.Tq * a.G + (int64_t)t * a.G + (h - hk * a.G)];
+  p = exp2f(fmaf(dot(row_of(a.q, b, t, h), row_of(a.k, b, j, hk), a.D), a.scale2, -st.x));
+  ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) - st.y);
 }
 
 __device__ inline void row_dq(const Args& a, int b, int t, int h) {
@@ -294,6 +293,132 @@ struct KeyLoader {
                                                voff[q] | (row[q] < end - j0 ? 0u : kDead), 0, 0, 0);
   }
 };
+
+// Loads 32 consecutive rows of q and of dout into LDS, 4 waves together: the rows of a
+// group of heads are tokens and heads in turn.  Call with ascending r0, a step of 32 at a
+// time.
+template <int DP>
+struct RowLoader {
+  using T = Tile<DP>;
+  static constexpr int kLoads = 32 * T::kRow / 4096;   // per wave and operand
+  const uint16_t* base[2];
+  int64_t ld[2];
+  int step_t, step_g, G, end, t0, g0;   // t0, g0: token and head of the tile's first row
+  int t[kLoads], g[kLoads], row[kLoads], chunk[kLoads];
+  uint32_t head[2];
+
+  __device__ __forceinline__ void init(const Args& a, int b, int hk, int r0, int wave) {
+    const int lane = threadIdx.x & 63;
+    G = a.G;
+    base[0] = a.q.p + b * a.q.batch + (int64_t)hk * G * a.q.head;
+    base[1] = a.dout.p + b * a.dout.batch + (int64_t)hk * G * a.dout.head;
+    ld[0] = a.q.token, ld[1] = a.dout.token;
+    head[0] = (uint32_t)a.q.head * 2, head[1] = (uint32_t)a.dout.head * 2;
+    step_t = 32 / G, step_g = 32 - step_t * G;
+    end = a.Tq * G;
+    t0 = r0 / G, g0 = r0 - t0 * G;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int at = (wave * kLoads + q) * 1024 + lane * 16;
+      row[q] = r0 + at / T::kRow;
+      chunk[q] = ((at % T::kRow / 16) ^ T::swz(at / T::kRow)) * 16;
+      t[q] = row[q] / G;
+      g[q] = row[q] - t[q] * G;
+      if (chunk[q] >= a.D * 2) chunk[q] = -1;
+    }
+  }
+  // The rows at hand to LDS, q's first; then on to the next 32.
+  __device__ __forceinline__ void load(uint8_t* lds, int wave) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const __amdgpu_buffer_rsrc_t buf = descriptor(base[x] + (int64_t)t0 * ld[x]);
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const uint32_t off = (uint32_t)(t[q] - t0) * (uint32_t)ld[x] * 2 + (uint32_t)g[q] * head[x] + chunk[q];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            buf, (lds_void)(lds + x * 32 * T::kRow + (wave * kLoads + q) * 1024), 16,
+            row[q] < end && chunk[q] >= 0 ? off : kDead, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      row[q] += 32;
+      t[q] += step_t;
+      g[q] += step_g;
+      if (g[q] >= G) g[q] -= G, ++t[q];
+    }
+    t0 += step_t;
+    g0 += step_g;
+    if (g0 >= G) g0 -= G, ++t0;
+  }
+};
+
+// The range that any of the rows (or keys) of a wave reaches, and the one that all
+// reach; rows that do not exist reach all.
+struct Reach {
+  int lo, hi, all_lo, all_hi;
+};
+__device__ __forceinline__ Reach reach_of(bool live, int lo, int hi) {
+  Reach r{lo < hi ? lo : 0x7fffffff, lo < hi ? hi : 0, live ? lo : 0, live ? hi : 0x7fffffff};
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    r.lo = min(r.lo, __shfl_xor(r.lo, m));
+    r.hi = max(r.hi, __shfl_xor(r.hi, m));
+    r.all_lo = max(r.all_lo, __shfl_xor(r.all_lo, m));
+    r.all_hi = min(r.all_hi, __shfl_xor(r.all_hi, m));
+  }
+  return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi)};
+}
+// The reach of 4 waves; lds is free before and after.
+__device__ __forceinline__ Range reach_of_all(uint8_t* lds, const Reach& r, int wave) {
+  int(*ends)[4] = reinterpret_cast<int(*)[4]>(lds);
+  if ((threadIdx.x & 63) == 0) ends[0][wave] = r.lo, ends[1][wave] = r.hi;
+  __syncthreads();
+  const int lo = min(min(ends[0][0], ends[0][1]), min(ends[0][2], ends[0][3]));
+  const int hi = max(max(ends[1][0], ends[1][1]), max(ends[1][2], ends[1][3]));
+  __syncthreads();
+  return Range{uniform(lo), uniform(hi)};
+}
+
+// Lane's fragments along d of one row of global memory.
+template <int DP>
+__device__ __forceinline__ void row_frags(v8bf (&f)[DP / 16], const bf16_t* row, bool live, int D, int half) {
+#pragma unroll
+  for (int ks = 0; ks < DP / 16; ++ks) {
+    const int d = 16 * ks + 8 * half;
+    v4u x{};
+    if (live && d < D) x = *reinterpret_cast<const v4u*>(row + d);
+    f[ks] = __builtin_bit_cast(v8bf, x);
+  }
+}
+
+// An accumulator of columns lane & 31 as rows of global memory, times f.
+template <int BLOCKS>
+__device__ __forceinline__ void store_columns(bf16_t* row, const v16f (&o)[BLOCKS], float f, int D, int half) {
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int db = 0; db < BLOCKS; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = db * 32 + 8 * i + 4 * half;
+      if (d >= D) continue;
+      v4f x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = o[db][4 * i + e] * f;
+      *reinterpret_cast<v4bf*>(row + d) = __builtin_convertvector(x, v4bf);
+    }
+}
+
+// 0, or NaN if a sum is not finite.
+template <int BLOCKS>
+__device__ __forceinline__ float odd_of(const v16f (&o)[BLOCKS]) {
+  float odd = 0.0f;
+#pragma unroll
+  for (int db = 0; db < BLOCKS; ++db)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) odd = __builtin_fmaf(o[db][v], 0.0f, odd);
+  return odd;
+}
 
 // max and sum over a lane and the one 32 away
 __device__ __forceinline__ float pair_max(float x) {

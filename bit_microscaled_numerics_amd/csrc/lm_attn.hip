@@ -25,7 +25,7 @@ Args make_args(const AttnCall& c) {
   a.dk = rows(c.dk);
   a.dv = rows(c.dv);
   a.lse = c.lse;
-  a.delta = static_cast<float*>(c.ws);
+  a.stats = static_cast<float2*>(c.ws);
   a.cu_q = n.cu_q;
   a.cu_k = n.cu_k;
   a.wide_cu = n.cu_type == NVFP4_TYPE_I64;
@@ -67,7 +67,6 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   using T = Tile<DP>;
   constexpr int kStage = 2 * kKeys * T::kRow;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
-  int(*ends)[4] = reinterpret_cast<int(*)[4]>(lds);
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
   const int64_t id = SPLIT ? block_xz() / part.n : block_xz();
   const int sp = SPLIT ? (int)(block_xz() % part.n) : 0;
@@ -81,24 +80,11 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
   const Range mine = keys_of(a, t);
 
-  // the keys that any row sees, of the wave and of the workgroup; those that all see
   const bool some = mine.lo < mine.hi;
-  int lo = some ? mine.lo : 0x7fffffff, hi = some ? mine.hi : 0;
-  int all_lo = live ? mine.lo : 0, all_hi = live ? mine.hi : 0x7fffffff;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    lo = min(lo, __shfl_xor(lo, m));
-    hi = max(hi, __shfl_xor(hi, m));
-    all_lo = max(all_lo, __shfl_xor(all_lo, m));
-    all_hi = min(all_hi, __shfl_xor(all_hi, m));
-  }
-  lo = uniform(lo), hi = uniform(hi), all_lo = uniform(all_lo), all_hi = uniform(all_hi);
-  if (lane == 0) ends[0][wave] = lo, ends[1][wave] = hi;
-  __syncthreads();
-  int j0 = min(min(ends[0][0], ends[0][1]), min(ends[0][2], ends[0][3]));
-  int j1 = max(max(ends[1][0], ends[1][1]), max(ends[1][2], ends[1][3]));
-  j0 = uniform(j0), j1 = uniform(j1);
-  __syncthreads();
+  const Reach reach = reach_of(live, mine.lo, mine.hi);
+  const int lo = reach.lo, hi = reach.hi, all_lo = reach.all_lo, all_hi = reach.all_hi;
+  const Range all = reach_of_all(lds, reach, wave);
+  int j0 = all.lo, j1 = all.hi;
   if (SPLIT && j0 < j1) {
     const int per = ((j1 - j0 + kKeys - 1) / kKeys + part.n - 1) / part.n;
     const int64_t from = j0 + (int64_t)sp * per * kKeys, to = from + per * kKeys;
@@ -107,16 +93,7 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   }
 
   v8bf q[T::kSteps];
-  {
-    const bf16_t* row = row_of(a.q, b, live ? t : 0, h);
-#pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks) {
-      const int d = 16 * ks + 8 * half;
-      v4u x{};
-      if (live && d < a.D) x = *reinterpret_cast<const v4u*>(row + d);
-      q[ks] = __builtin_bit_cast(v8bf, x);
-    }
-  }
+  row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
   KeyLoader<DP, kKeys> lk, lv;
   lk.init(a.k, b, hk, a.Tk, a.D, wave);
   lv.init(a.v, b, hk, a.Tk, a.D, wave);
@@ -189,30 +166,23 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 
   // A value that is not finite may come from a key that a row does not see, multiplied by 0:
   // such rows are formed again, one by one.
-  float odd = 0.0f;
-#pragma unroll
-  for (int db = 0; db < T::kBlocks; ++db)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) odd = __builtin_fmaf(o[db][v], 0.0f, odd);
+  const float odd = odd_of(o);
   uint64_t again = __ballot(live && odd != 0.0f);
-  const float f = SPLIT ? 1.0f : some ? 1.0f / l : 0.0f;
   const int64_t at = SPLIT ? (int64_t)sp * pairs * rows + job.pair * rows + r : 0;
   if (live) {
+    if (SPLIT) {
 #pragma unroll
-    for (int db = 0; db < T::kBlocks; ++db)
+      for (int db = 0; db < T::kBlocks; ++db)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = db * 32 + 8 * i + 4 * half;
-        if (d >= a.D) continue;
-        typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-        v4f x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = o[db][4 * i + e] * f;
-        if (SPLIT)
-          *reinterpret_cast<v4f*>(part.o + at * a.D + d) = x;
-        else
-          *reinterpret_cast<v4bf*>(row_of_out(a.out, b, t, h) + d) = __builtin_convertvector(x, v4bf);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const int d = db * 32 + 8 * i + 4 * half;
+          if (d < a.D)
+            *reinterpret_cast<v4f*>(part.o + at * a.D + d) =
+                v4f{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+        }
+    } else {
+      store_columns(row_of_out(a.out, b, t, h), o, some ? 1.0f / l : 0.0f, a.D, half);
+    }
     if (half == 0) {
       if (SPLIT) {
         part.ml[2 * at] = m * a.scale2;
@@ -267,33 +237,234 @@ __global__ __launch_bounds__(kWaves * 64) void k_attn_join(Args a, int64_t rows,
   if (lane == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-__global__ __launch_bounds__(kWaves * 64) void k_attn_delta(Args a, int64_t rows) {
-  const int64_t r = block_xz() * kWaves + (threadIdx.x >> 6);
+// lse in log2 and delta of every row, in the order of the rows of a key head: 8 lanes a row.
+__global__ __launch_bounds__(256) void k_attn_stats(Args a, int64_t rows) {
+  const int64_t r = block_xz() * 32 + (threadIdx.x >> 3);
+  const int in_row = threadIdx.x & 7;
   if (r >= rows) return;
-  const int h = (int)(r % a.Hq), t = (int)(r / a.Hq % a.Tq), b = (int)(r / a.Hq / a.Tq);
+  const int64_t in_pair = (int64_t)a.Tq * a.G;
+  const int pair = (int)(r / in_pair), rr = (int)(r % in_pair);
+  const int b = pair / a.Hkv, t = rr / a.G, h = pair % a.Hkv * a.G + rr % a.G;
   const bf16_t* o = row_of(a.out, b, t, h);
   const bf16_t* d = row_of(a.dout, b, t, h);
   float s = 0.0f;
-  for (int i = threadIdx.x & 63; i < a.D; i += 64) s += load1(o + i) * load1(d + i);
-  s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) a.delta[r] = s;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = in_row * 8 + 64 * i;
+    if (at >= a.D) continue;
+    const v8f x = load8(o + at), y = load8(d + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], y[e], s);
+  }
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) s += __shfl_xor(s, m);
+  if (in_row == 0) a.stats[r] = float2{a.lse[stat_at(a, b, t, h)] * kLog2e, s};
 }
 
-__global__ __launch_bounds__(kWaves * 64) void k_attn_dq_rows(Args a, int64_t rows) {
-  const int64_t r = block_xz() * kWaves + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  row_dq(a, (int)(r / a.Hq / a.Tq), (int)(r / a.Hq % a.Tq), (int)(r % a.Hq));
+#ifdef __HIP_DEVICE_COMPILE__
+// dk and dv of 128 keys: 4 waves of 32, which hold K and the sums of both results in
+// registers (V in LDS), while the query rows that see them pass in tiles of 32 through two
+// LDS stages.  S = Q K^T and dP = dO V^T leave a lane one key and 16 rows; p and ds are, as they
+// stand, the second operands of dV^T = dO^T P and dK^T = Q^T dS.
+template <int DP>
+__device__ __forceinline__ void grad_keys(const Args& a, uint8_t* lds, Job job, int tiles) {
+  using T = Tile<DP>;
+  constexpr int kStage = 2 * 32 * T::kRow, kV = 2 * kStage, kStats = kV + 128 * T::kRow;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
+  const int64_t key = (int64_t)job.tile * 128 + wave * 32 + (lane & 31);
+  const bool live = key < a.Tk;
+  const int j = live ? (int)key : a.Tk;
+  const Range seen = queries_of(a, j);
+  const int rlo = seen.lo * a.G, rhi = seen.hi * a.G;
+  const Reach reach = reach_of(live, rlo, rhi);
+  const Range all = reach_of_all(lds, reach, wave);
+
+  v8bf k[T::kSteps];
+  row_frags<DP>(k, row_of(a.k, b, live ? j : 0, hk), live, a.D, half);
+  {
+    v8bf v[T::kSteps];
+    row_frags<DP>(v, row_of(a.v, b, live ? j : 0, hk), live, a.D, half);
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks)   // read back by the same lane
+      *reinterpret_cast<v8bf*>(lds + kV + ((wave * T::kSteps + ks) * 64 + lane) * 16) = v[ks];
+  }
+  const uint8_t* mine_v = lds + kV + (wave * T::kSteps * 64 + lane) * 16;
+  int fr[T::kSteps], ft[T::kBlocks][2];
+#pragma unroll
+  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = T::frag(lane, ks);
+#pragma unroll
+  for (int db = 0; db < T::kBlocks; ++db) ft[db][0] = T::frag_t(lane, db, 0), ft[db][1] = T::frag_t(lane, db, 1);
+
+  v16f dk[T::kBlocks] = {}, dv[T::kBlocks] = {};
+  RowLoader<DP> rows;
+  const int64_t all_rows = (int64_t)a.Tq * a.G;
+  const float2* stats = a.stats + job.pair * all_rows;
+  auto load_stats = [&](int stage, int r0) {   // 64 words
+    const __amdgpu_buffer_rsrc_t buf = descriptor(reinterpret_cast<const uint16_t*>(stats + r0));
+    if (wave == 0)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(lds + kStats + stage * 256), 4,
+                                               r0 + (lane >> 1) < all_rows ? (uint32_t)lane * 4 : kDead, 0, 0, 0);
+  };
+  if (all.lo < all.hi) {
+    rows.init(a, b, hk, all.lo, wave);
+    rows.load(lds, wave);
+    load_stats(0, all.lo);
+  }
+  for (int r = all.lo, stage = 0; r < all.hi; r += 32, stage ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint8_t* tq = lds + stage * kStage;
+    const uint8_t* td = tq + kStage / 2;
+    if (r + 32 < all.hi) {
+      rows.load(lds + (stage ^ 1) * kStage, wave);
+      load_stats(stage ^ 1, r + 32);
+    }
+    if (r >= reach.hi || r + 32 <= reach.lo) continue;
+    v16f s{}, dp{};
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks) s = mfma(T::read(tq + fr[ks]), k[ks], s);
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks) dp = mfma(T::read(td + fr[ks]), T::read(mine_v + ks * 1024), dp);
+    const bool cut = r < reach.all_lo || r + 32 > reach.all_hi;
+    const uint32_t first = (uint32_t)(r + 4 * half - rlo), n = (uint32_t)max(rhi - rlo, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f st[2] = {*reinterpret_cast<const v4f*>(lds + kStats + stage * 256 + (8 * i + 4 * half) * 8),
+                         *reinterpret_cast<const v4f*>(lds + kStats + stage * 256 + (8 * i + 4 * half) * 8 + 16)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int v = 4 * i + e;
+        s[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], a.scale2, -st[e >> 1][2 * (e & 1)]));
+        dp[v] = s[v] * (dp[v] - st[e >> 1][2 * (e & 1) + 1]);
+      }
+    }
+    if (cut) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (first + acc_row(v) >= n) s[v] = dp[v] = 0.0f;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const v8bf p = pack_half(s, ks), ds = pack_half(dp, ks);
+#pragma unroll
+      for (int db = 0; db < T::kBlocks; ++db) {
+        const int lo = ft[db][0] + ks * 16 * T::kRow, hi = ft[db][1] + ks * 16 * T::kRow;
+        dv[db] = mfma(T::read_t(td + lo, td + hi), p, dv[db]);
+        dk[db] = mfma(T::read_t(tq + lo, tq + hi), ds, dk[db]);
+      }
+    }
+  }
+  const float odd = odd_of(dk) + odd_of(dv);
+  uint64_t again = __ballot(live && odd != 0.0f);
+  if (live) {
+    store_columns(row_of_out(a.dk, b, j, hk), dk, a.scale, a.D, half);
+    store_columns(row_of_out(a.dv, b, j, hk), dv, 1.0f, a.D, half);
+  }
+  for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
+    const int from = __builtin_ctzll(again), jj = __shfl(j, from);
+    RowSum xk, xv;
+    row_dkv(a, b, jj, hk, __shfl(rlo, from), __shfl(rhi, from), xk, xv);
+    xk.store(row_of_out(a.dk, b, jj, hk), a.D, a.scale);
+    xv.store(row_of_out(a.dv, b, jj, hk), a.D, 1.0f);
+  }
 }
 
-__global__ __launch_bounds__(kWaves * 64) void k_attn_dkv_rows(Args a, int64_t rows) {
-  const int64_t r = block_xz() * kWaves + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  const int h = (int)(r % a.Hkv), j = (int)(r / a.Hkv % a.Tk), b = (int)(r / a.Hkv / a.Tk);
-  const Range t = queries_of(a, j);
-  RowSum dk, dv;
-  row_dkv(a, b, j, h, (int64_t)t.lo * a.G, (int64_t)t.hi * a.G, dk, dv);
-  dk.store(row_of_out(a.dk, b, j, h), a.D, a.scale);
-  dv.store(row_of_out(a.dv, b, j, h), a.D, 1.0f);
+// dq of 128 query rows, laid out as the forward kernel: S^T = K Q^T, dP^T = V dO^T, and
+// dS^T as it stands is the second operand of dQ^T = K^T dS^T.
+template <int DP>
+__device__ __forceinline__ void grad_queries(const Args& a, uint8_t* lds, Job job, int tiles) {
+  using T = Tile<DP>;
+  constexpr int kStage = 2 * kKeys * T::kRow;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
+  const int64_t rows = (int64_t)a.Tq * a.G;
+  const int64_t r = (int64_t)(tiles - 1 - job.tile) * kRowsWG + wave * 32 + (lane & 31);
+  const bool live = r < rows;
+  const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
+  const Range mine = keys_of(a, t);
+  const Reach reach = reach_of(live, mine.lo, mine.hi);
+  const Range all = reach_of_all(lds, reach, wave);
+  const float2 st = live ? a.stats[job.pair * rows + r] : float2{0.0f, 0.0f};
+
+  v8bf q[T::kSteps], g[T::kSteps];
+  row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
+  row_frags<DP>(g, row_of(a.dout, b, live ? t : 0, h), live, a.D, half);
+  KeyLoader<DP, kKeys> lk, lv;
+  lk.init(a.k, b, hk, a.Tk, a.D, wave);
+  lv.init(a.v, b, hk, a.Tk, a.D, wave);
+  int fr[T::kSteps], ft[T::kBlocks][2];
+#pragma unroll
+  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = T::frag(lane, ks);
+#pragma unroll
+  for (int db = 0; db < T::kBlocks; ++db) ft[db][0] = T::frag_t(lane, db, 0), ft[db][1] = T::frag_t(lane, db, 1);
+
+  v16f dq[T::kBlocks] = {};
+  if (all.lo < all.hi) {
+    lk.load(lds, wave, all.lo);
+    lv.load(lds + kStage / 2, wave, all.lo);
+  }
+  for (int j = all.lo, stage = 0; j < all.hi; j += kKeys, stage ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint8_t* tk = lds + stage * kStage;
+    const uint8_t* tv = tk + kStage / 2;
+    if (j + kKeys < all.hi) {
+      uint8_t* next = lds + (stage ^ 1) * kStage;
+      lk.load(next, wave, j + kKeys);
+      lv.load(next + kStage / 2, wave, j + kKeys);
+    }
+    if (j >= reach.hi || j + kKeys <= reach.lo) continue;
+    v16f s[2] = {}, dp[2] = {};
+#pragma unroll
+    for (int ks = 0; ks < T::kSteps; ++ks)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        s[kb] = mfma(T::read(tk + fr[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
+        dp[kb] = mfma(T::read(tv + fr[ks] + kb * 32 * T::kRow), g[ks], dp[kb]);
+      }
+    const bool cut = j < reach.all_lo || j + kKeys > reach.all_hi;
+    const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(mine.hi - mine.lo, 0);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        dp[kb][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][v], a.scale2, -st.x)) * (dp[kb][v] - st.y);
+    if (cut) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (first + kb * 32 + acc_row(v) >= n) dp[kb][v] = 0.0f;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const v8bf ds = pack_half(dp[ks >> 1], ks & 1);
+#pragma unroll
+      for (int db = 0; db < T::kBlocks; ++db)
+        dq[db] = mfma(T::read_t(tk + ft[db][0] + ks * 16 * T::kRow, tk + ft[db][1] + ks * 16 * T::kRow), ds, dq[db]);
+    }
+  }
+  const float odd = odd_of(dq);
+  uint64_t again = __ballot(live && odd != 0.0f);
+  if (live) store_columns(row_of_out(a.dq, b, t, h), dq, a.scale, a.D, half);
+  for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
+    const int from = __builtin_ctzll(again);
+    row_dq(a, b, __shfl(t, from), __shfl(h, from));
+  }
+}
+#endif
+
+// One launch for both halves of the gradient: the keys' workgroups, which are few and
+// long, come first, the queries' fill what they leave.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[256 * Tile<DP>::kRow + 512];
+  const int64_t id = block_xz(), keys = (int64_t)pairs * key_tiles;
+  if (id < keys)
+    grad_keys<DP>(a, lds, job_of(id, pairs, key_tiles), key_tiles);
+  else if (id - keys < (int64_t)pairs * row_tiles)
+    grad_queries<DP>(a, lds, job_of(id - keys, pairs, row_tiles), row_tiles);
+#endif
 }
 
 int64_t sequences(const nvfp4_attn& a) { return a.cu_q == nullptr ? a.batch : 1; }
@@ -322,7 +493,7 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 int64_t attn_workspace_bytes(const nvfp4_attn& a, bool grad) {
   const int64_t rows = sequences(a) * a.Tq * a.Hq;
-  if (grad) return rows * 4;
+  if (grad) return rows * 8;
   const int n = parts_of(a);
   return n > 1 ? up256(rows * n * a.D * 4) + rows * n * 8 : 0;
 }
@@ -353,13 +524,18 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
 }
 
 hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
-  const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq, keys = sequences(c.a) * c.a.Tk * c.a.Hkv;
+  const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq;
   const Args a = make_args(c);
-  if (rows > 0) {
-    k_attn_delta<<<grid_xz(blocks(rows)), kWaves * 64, 0, s>>>(a, rows);
-    k_attn_dq_rows<<<grid_xz(blocks(rows)), kWaves * 64, 0, s>>>(a, rows);
-  }
-  if (keys > 0) k_attn_dkv_rows<<<grid_xz(blocks(keys)), kWaves * 64, 0, s>>>(a, keys);
+  const int pairs = (int)(sequences(c.a) * a.Hkv);
+  const int row_tiles = (int)(((int64_t)a.Tq * a.G + kRowsWG - 1) / kRowsWG);
+  const int key_tiles = (int)(((int64_t)a.Tk + 127) / 128);
+  const int64_t n = (int64_t)pairs * row_tiles + (int64_t)pairs * key_tiles;
+  if (n == 0) return hipSuccess;
+  if (rows > 0) k_attn_stats<<<grid_xz((rows + 31) / 32), 256, 0, s>>>(a, rows);
+  if (a.D <= 64)
+    k_attn_grad<64><<<grid_xz(n), 256, 0, s>>>(a, pairs, key_tiles, row_tiles);
+  else
+    k_attn_grad<128><<<grid_xz(n), 256, 0, s>>>(a, pairs, key_tiles, row_tiles);
   return hipGetLastError();
 }
 

@@ -223,6 +223,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint16_t* p) 
       reinterpret_cast<void*>(uniform64((int64_t)(uintptr_t)p)), (short)0, 0x7fffffff, 0x00020000);
 }
 
+// The order of a phase of MFMAS products that need PER reads of LDS each: the reads of AHEAD
+// products first, then one product's reads after each product.  (Left alone, the compiler
+// reads a product's operands right before it and waits out the LDS each time.)
+template <int MFMAS, int PER, int AHEAD>
+__device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * PER, 0);
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (AHEAD + i < MFMAS) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+  }
+}
+
 __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -259,12 +272,19 @@ struct Tile {
   }
 };
 
-// Loads ROWS consecutive key rows into LDS, 4 waves together; rows past the end and
+// All loads to LDS have landed, in every wave; what a wave read is free.  The wait is a
+// builtin: the compiler then knows that reads need no wait of their own.
+__device__ __forceinline__ void tile_landed() {
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), and lgkmcnt(0): its reads have ended
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// Loads ROWS consecutive key rows into LDS, WAVES waves together; rows past the end and
 // columns past D read zero.
-template <int DP, int ROWS>
+template <int DP, int ROWS, int WAVES>
 struct KeyLoader {
   using T = Tile<DP>;
-  static constexpr int kLoads = ROWS * T::kRow / 4096;   // per wave, 1 KiB each
+  static constexpr int kLoads = ROWS * T::kRow / 1024 / WAVES;   // per wave, 1 KiB each
   const uint16_t* base;
   int64_t ld;
   int end;
@@ -294,13 +314,13 @@ struct KeyLoader {
   }
 };
 
-// Loads 32 consecutive rows of q and of dout into LDS, 4 waves together: the rows of a
-// group of heads are tokens and heads in turn.  Call with ascending r0, a step of 32 at a
-// time.
-template <int DP>
+// Loads ROWS consecutive rows of q and of dout into LDS, WAVES waves together: the rows
+// of a group of heads are tokens and heads in turn.  Each call takes the rows before the last
+// call's.
+template <int DP, int ROWS, int WAVES>
 struct RowLoader {
   using T = Tile<DP>;
-  static constexpr int kLoads = 32 * T::kRow / 4096;   // per wave and operand
+  static constexpr int kLoads = ROWS * T::kRow / 1024 / WAVES;   // per wave and operand
   const uint16_t* base[2];
   int64_t ld[2];
   int step_t, step_g, G, end, t0, g0;   // t0, g0: token and head of the tile's first row
@@ -314,7 +334,7 @@ struct RowLoader {
     base[1] = a.dout.p + b * a.dout.batch + (int64_t)hk * G * a.dout.head;
     ld[0] = a.q.token, ld[1] = a.dout.token;
     head[0] = (uint32_t)a.q.head * 2, head[1] = (uint32_t)a.dout.head * 2;
-    step_t = 32 / G, step_g = 32 - step_t * G;
+    step_t = ROWS / G, step_g = ROWS - step_t * G;
     end = a.Tq * G;
     t0 = r0 / G, g0 = r0 - t0 * G;
 #pragma unroll
@@ -327,7 +347,7 @@ struct RowLoader {
       if (chunk[q] >= a.D * 2) chunk[q] = -1;
     }
   }
-  // The rows at hand to LDS, q's first; then on to the next 32.
+  // The rows at hand to LDS, q's first; then back by ROWS.
   __device__ __forceinline__ void load(uint8_t* lds, int wave) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -336,20 +356,20 @@ struct RowLoader {
       for (int q = 0; q < kLoads; ++q) {
         const uint32_t off = (uint32_t)(t[q] - t0) * (uint32_t)ld[x] * 2 + (uint32_t)g[q] * head[x] + chunk[q];
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            buf, (lds_void)(lds + x * 32 * T::kRow + (wave * kLoads + q) * 1024), 16,
+            buf, (lds_void)(lds + x * ROWS * T::kRow + (wave * kLoads + q) * 1024), 16,
             row[q] < end && chunk[q] >= 0 ? off : kDead, 0, 0, 0);
       }
     }
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      row[q] += 32;
-      t[q] += step_t;
-      g[q] += step_g;
-      if (g[q] >= G) g[q] -= G, ++t[q];
+      row[q] -= ROWS;
+      t[q] -= step_t;
+      g[q] -= step_g;
+      if (g[q] < 0) g[q] += G, --t[q];
     }
-    t0 += step_t;
-    g0 += step_g;
-    if (g0 >= G) g0 -= G, ++t0;
+    t0 -= step_t;
+    g0 -= step_g;
+    if (g0 < 0) g0 += G, --t0;
   }
 };
 
@@ -369,13 +389,15 @@ __device__ __forceinline__ Reach reach_of(bool live, int lo, int hi) {
   }
   return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi)};
 }
-// The reach of 4 waves; lds is free before and after.
+// The reach of WAVES waves; lds is free before and after.
+template <int WAVES>
 __device__ __forceinline__ Range reach_of_all(uint8_t* lds, const Reach& r, int wave) {
-  int(*ends)[4] = reinterpret_cast<int(*)[4]>(lds);
-  if ((threadIdx.x & 63) == 0) ends[0][wave] = r.lo, ends[1][wave] = r.hi;
+  int* ends = reinterpret_cast<int*>(lds);
+  if ((threadIdx.x & 63) == 0) ends[2 * wave] = r.lo, ends[2 * wave + 1] = r.hi;
   __syncthreads();
-  const int lo = min(min(ends[0][0], ends[0][1]), min(ends[0][2], ends[0][3]));
-  const int hi = max(max(ends[1][0], ends[1][1]), max(ends[1][2], ends[1][3]));
+  int lo = ends[0], hi = ends[1];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) lo = min(lo, ends[2 * w]), hi = max(hi, ends[2 * w + 1]);
   __syncthreads();
   return Range{uniform(lo), uniform(hi)};
 }
@@ -446,14 +468,14 @@ __device__ __forceinline__ constexpr int acc_row(int v) { return (v & 3) + 8 * (
 struct Job {
   int pair, tile;
 };
-__device__ __forceinline__ Job job_of(int64_t id, int pairs, int tiles) {
-  const int64_t whole = (int64_t)(pairs & ~7) * tiles;
-  if (id < whole) {
-    const int64_t i = id >> 3;
-    return Job{(int)((id & 7) + 8 * (i / tiles)), (int)(i % tiles)};
+__device__ __forceinline__ Job job_of(uint32_t id, int pairs, int tiles) {
+  const uint32_t even = (uint32_t)pairs & ~7u, n = (uint32_t)tiles;
+  if (id < even * n) {
+    const uint32_t i = id >> 3, p = i / n;
+    return Job{(int)((id & 7) + 8 * p), (int)(i - p * n)};
   }
-  const int64_t i = id - whole;
-  return Job{(pairs & ~7) + (int)(i / tiles), (int)(i % tiles)};
+  const uint32_t i = id - even * n, p = i / n;
+  return Job{(int)(even + p), (int)(i - p * n)};
 }
 
 Args make_args(const AttnCall& c);

@@ -44,9 +44,26 @@ Args make_args(const AttnCall& c) {
 }
 
 namespace {
+#ifdef VPRIO
+#define PRIO(x) __builtin_amdgcn_s_setprio(x)
+#else
+#define PRIO(x)
+#endif
+#ifndef AH1
+#define AH1 3
+#define AH2 2
+#define AH3 3
+#define AH4 4
+#endif
+#ifdef VSB
+#define SB __builtin_amdgcn_sched_barrier(0)
+#else
+#define SB
+#endif
 
 constexpr int kWaves = 4;
 constexpr int kRowsWG = 128, kKeys = 64;   // query rows of a workgroup, keys of a tile
+constexpr int kGradRows = 256;   // query rows of a workgroup of the gradient
 constexpr int kPartTiles = 512, kPartKeys = 128;   // see parts_of
 
 struct Part {   // of a row's softmax, where several workgroups share its keys
@@ -66,11 +83,12 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass drops the stubs of kernels with these builtins
   using T = Tile<DP>;
   constexpr int kStage = 2 * kKeys * T::kRow;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  // one array per stage: loads into the next one are not waited for by reads of this one
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStage], lds1[kStage];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
-  const int64_t id = SPLIT ? block_xz() / part.n : block_xz();
-  const int sp = SPLIT ? (int)(block_xz() % part.n) : 0;
-  if (id >= (int64_t)pairs * tiles) return;
+  const uint32_t block = (uint32_t)block_xz(), id = SPLIT ? block / (uint32_t)part.n : block;
+  const int sp = SPLIT ? (int)(block - id * (uint32_t)part.n) : 0;
+  if (id >= (uint32_t)pairs * (uint32_t)tiles) return;
   const Job job = job_of(id, pairs, tiles);
   const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
   const int64_t rows = (int64_t)a.Tq * a.G;
@@ -83,7 +101,7 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   const bool some = mine.lo < mine.hi;
   const Reach reach = reach_of(live, mine.lo, mine.hi);
   const int lo = reach.lo, hi = reach.hi, all_lo = reach.all_lo, all_hi = reach.all_hi;
-  const Range all = reach_of_all(lds, reach, wave);
+  const Range all = reach_of_all<4>(lds, reach, wave);
   int j0 = all.lo, j1 = all.hi;
   if (SPLIT && j0 < j1) {
     const int per = ((j1 - j0 + kKeys - 1) / kKeys + part.n - 1) / part.n;
@@ -94,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 
   v8bf q[T::kSteps];
   row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
-  KeyLoader<DP, kKeys> lk, lv;
+  KeyLoader<DP, kKeys, 4> lk, lv;
   lk.init(a.k, b, hk, a.Tk, a.D, wave);
   lv.init(a.v, b, hk, a.Tk, a.D, wave);
   int fk[T::kSteps], fv[T::kBlocks][2];
@@ -109,21 +127,23 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
     lk.load(lds, wave, j0);
     lv.load(lds + kStage / 2, wave, j0);
   }
-  for (int j = j0, stage = 0; j < j1; j += kKeys, stage ^= 1) {
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    const uint8_t* at = lds + stage * kStage;
+  auto tile = [&](int j, const uint8_t* at, uint8_t* next) __attribute__((always_inline)) {
+    tile_landed();
     if (j + kKeys < j1) {
-      uint8_t* next = lds + (stage ^ 1) * kStage;
       lk.load(next, wave, j + kKeys);
       lv.load(next + kStage / 2, wave, j + kKeys);
     }
     const int last = SPLIT ? min(hi, j1) : hi;
-    if (j >= last || j + kKeys <= lo) continue;
+    if (j >= last || j + kKeys <= lo) return;
     v16f s[2] = {};
+    PRIO(1);
 #pragma unroll
     for (int ks = 0; ks < T::kSteps; ++ks)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) s[kb] = mfma(T::read(at + fk[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
+    interleave<2 * T::kSteps, 1, 6>();
+    __builtin_amdgcn_sched_barrier(0);
+    PRIO(0);
     if (j < all_lo || j + kKeys > (SPLIT ? min(all_hi, j1) : all_hi)) {
       const uint32_t n = (uint32_t)max((SPLIT ? min(mine.hi, j1) : mine.hi) - mine.lo, 0);
 #pragma unroll
@@ -154,6 +174,8 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
         l += s[kb][v];
       }
     const uint8_t* vt = at + kStage / 2;
+    SB;
+    PRIO(1);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const v8bf p = pack_half(s[ks >> 1], ks & 1);
@@ -161,6 +183,11 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
       for (int db = 0; db < T::kBlocks; ++db)
         o[db] = mfma(T::read_t(vt + fv[db][0] + ks * 16 * T::kRow, vt + fv[db][1] + ks * 16 * T::kRow), p, o[db]);
     }
+    PRIO(0);
+  };
+  for (int j = j0; j < j1; j += 2 * kKeys) {
+    tile(j, lds, lds1);
+    if (j + kKeys < j1) tile(j + kKeys, lds1, lds);
   }
   l = pair_sum(l);
 
@@ -262,87 +289,96 @@ __global__ __launch_bounds__(256) void k_attn_stats(Args a, int64_t rows) {
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
-// dk and dv of 128 keys: 4 waves of 32, which hold K and the sums of both results in
-// registers (V in LDS), while the query rows that see them pass in tiles of 32 through two
-// LDS stages.  S = Q K^T and dP = dO V^T leave a lane one key and 16 rows; p and ds are, as they
-// stand, the second operands of dV^T = dO^T P and dK^T = Q^T dS.
 template <int DP>
-__device__ __forceinline__ void grad_keys(const Args& a, uint8_t* lds, Job job, int tiles) {
+struct GradLds {   // one array per stage: loads into the next are not waited for by reads of this
+  uint8_t *s0, *s1, *v, *stats;
+};
+
+// dk and dv of 128 keys: 8 waves, as 4 groups of 32 keys by 2 halves of the query rows.  A
+// wave holds K and its sums of both results in registers (V in LDS), while the rows that see
+// the keys pass in tiles of 64 through two LDS stages.  S = Q K^T and dP = dO V^T
+// leave a lane one key and 16 rows; p and ds are, as they stand, the second operands of
+// dV^T = dO^T P and dK^T = Q^T dS.  The rows pass from the last one down: the last
+// rows of a causal sequence see all keys, so the workgroups of a key head start on the same
+// rows and find them in their XCD's L2.
+template <int DP>
+__device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds, Job job) {
   using T = Tile<DP>;
-  constexpr int kStage = 2 * 32 * T::kRow, kV = 2 * kStage, kStats = kV + 128 * T::kRow;
+  constexpr int kHalf = 64 * T::kRow;   // of a stage: q, then dout
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  const int kg = wave & 3, rg = wave >> 2;
   const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
-  const int64_t key = (int64_t)job.tile * 128 + wave * 32 + (lane & 31);
+  const int64_t key = (int64_t)job.tile * 128 + kg * 32 + (lane & 31);
   const bool live = key < a.Tk;
   const int j = live ? (int)key : a.Tk;
   const Range seen = queries_of(a, j);
   const int rlo = seen.lo * a.G, rhi = seen.hi * a.G;
   const Reach reach = reach_of(live, rlo, rhi);
-  const Range all = reach_of_all(lds, reach, wave);
+  const Range all = reach_of_all<8>(lds.s0, reach, wave);
 
   v8bf k[T::kSteps];
   row_frags<DP>(k, row_of(a.k, b, live ? j : 0, hk), live, a.D, half);
-  {
+  if (rg == 0) {
     v8bf v[T::kSteps];
     row_frags<DP>(v, row_of(a.v, b, live ? j : 0, hk), live, a.D, half);
 #pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks)   // read back by the same lane
-      *reinterpret_cast<v8bf*>(lds + kV + ((wave * T::kSteps + ks) * 64 + lane) * 16) = v[ks];
+    for (int ks = 0; ks < T::kSteps; ++ks)
+      *reinterpret_cast<v8bf*>(lds.v + ((kg * T::kSteps + ks) * 64 + lane) * 16) = v[ks];
   }
-  const uint8_t* mine_v = lds + kV + (wave * T::kSteps * 64 + lane) * 16;
+  const uint8_t* mine_v = lds.v + (kg * T::kSteps * 64 + lane) * 16;
   int fr[T::kSteps], ft[T::kBlocks][2];
 #pragma unroll
-  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = T::frag(lane, ks);
+  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = rg * 32 * T::kRow + T::frag(lane, ks);
 #pragma unroll
-  for (int db = 0; db < T::kBlocks; ++db) ft[db][0] = T::frag_t(lane, db, 0), ft[db][1] = T::frag_t(lane, db, 1);
+  for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ft[db][x] = rg * 32 * T::kRow + T::frag_t(lane, db, x);
 
   v16f dk[T::kBlocks] = {}, dv[T::kBlocks] = {};
-  RowLoader<DP> rows;
   const int64_t all_rows = (int64_t)a.Tq * a.G;
   const float2* stats = a.stats + job.pair * all_rows;
-  auto load_stats = [&](int stage, int r0) {   // 64 words
-    const __amdgpu_buffer_rsrc_t buf = descriptor(reinterpret_cast<const uint16_t*>(stats + r0));
-    if (wave == 0)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(lds + kStats + stage * 256), 4,
-                                               r0 + (lane >> 1) < all_rows ? (uint32_t)lane * 4 : kDead, 0, 0, 0);
-  };
-  if (all.lo < all.hi) {
-    rows.init(a, b, hk, all.lo, wave);
-    rows.load(lds, wave);
-    load_stats(0, all.lo);
-  }
-  for (int r = all.lo, stage = 0; r < all.hi; r += 32, stage ^= 1) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const uint8_t* tq = lds + stage * kStage;
-    const uint8_t* td = tq + kStage / 2;
-    if (r + 32 < all.hi) {
-      rows.load(lds + (stage ^ 1) * kStage, wave);
-      load_stats(stage ^ 1, r + 32);
+  RowLoader<DP, 64, 8> rows;
+  auto load = [&](uint8_t* stage, int st, int r) __attribute__((always_inline)) {
+    rows.load(stage, wave);
+    if (wave < 2) {   // the statistics of 32 rows
+      const int r0 = r + wave * 32;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          descriptor(reinterpret_cast<const uint16_t*>(stats + r0)), (lds_void)(lds.stats + st * 512 + wave * 256),
+          4, r0 + (lane >> 1) < all_rows ? (uint32_t)lane * 4 : kDead, 0, 0, 0);
     }
-    if (r >= reach.hi || r + 32 <= reach.lo) continue;
+  };
+  auto tile = [&](int r, uint8_t* now, uint8_t* next, int st) __attribute__((always_inline)) {
+    tile_landed();
+    if (r > all.lo) load(next, st ^ 1, r - 64);
+    const int r0 = r + rg * 32;
+    if (r0 >= reach.hi || r0 + 32 <= reach.lo) return;
+    const uint8_t* td = now + kHalf;
     v16f s{}, dp{};
 #pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks) s = mfma(T::read(tq + fr[ks]), k[ks], s);
+    for (int ks = 0; ks < T::kSteps; ++ks) s = mfma(T::read(now + fr[ks]), k[ks], s);
+    interleave<T::kSteps, 1, AH1>();
 #pragma unroll
     for (int ks = 0; ks < T::kSteps; ++ks) dp = mfma(T::read(td + fr[ks]), T::read(mine_v + ks * 1024), dp);
-    const bool cut = r < reach.all_lo || r + 32 > reach.all_hi;
-    const uint32_t first = (uint32_t)(r + 4 * half - rlo), n = (uint32_t)max(rhi - rlo, 0);
+    interleave<T::kSteps, 2, AH2>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* st_at = lds.stats + st * 512 + rg * 256 + half * 32;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const v4f st[2] = {*reinterpret_cast<const v4f*>(lds + kStats + stage * 256 + (8 * i + 4 * half) * 8),
-                         *reinterpret_cast<const v4f*>(lds + kStats + stage * 256 + (8 * i + 4 * half) * 8 + 16)};
+      const v4f x[2] = {*reinterpret_cast<const v4f*>(st_at + i * 64), *reinterpret_cast<const v4f*>(st_at + i * 64 + 16)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int v = 4 * i + e;
-        s[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], a.scale2, -st[e >> 1][2 * (e & 1)]));
-        dp[v] = s[v] * (dp[v] - st[e >> 1][2 * (e & 1) + 1]);
+        s[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], a.scale2, -x[e >> 1][2 * (e & 1)]));
+        dp[v] = s[v] * (dp[v] - x[e >> 1][2 * (e & 1) + 1]);
       }
     }
-    if (cut) {
+    if (r0 < reach.all_lo || r0 + 32 > reach.all_hi) {
+      const uint32_t first = (uint32_t)(r0 + 4 * half - rlo), n = (uint32_t)max(rhi - rlo, 0);
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         if (first + acc_row(v) >= n) s[v] = dp[v] = 0.0f;
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const v8bf p = pack_half(s, ks), ds = pack_half(dp, ks);
@@ -350,10 +386,45 @@ __device__ __forceinline__ void grad_keys(const Args& a, uint8_t* lds, Job job, 
       for (int db = 0; db < T::kBlocks; ++db) {
         const int lo = ft[db][0] + ks * 16 * T::kRow, hi = ft[db][1] + ks * 16 * T::kRow;
         dv[db] = mfma(T::read_t(td + lo, td + hi), p, dv[db]);
-        dk[db] = mfma(T::read_t(tq + lo, tq + hi), ds, dk[db]);
+        dk[db] = mfma(T::read_t(now + lo, now + hi), ds, dk[db]);
       }
     }
+    interleave<4 * T::kBlocks, 2, AH3>();
+  };
+  if (all.lo < all.hi) {
+    const int last = all.lo + (all.hi - 1 - all.lo) / 64 * 64;
+    rows.init(a, b, hk, last, wave);
+    load(lds.s0, 0, last);
+    for (int r = last; r >= all.lo; r -= 128) {
+      tile(r, lds.s0, lds.s1, 0);
+      if (r - 64 >= all.lo) tile(r - 64, lds.s1, lds.s0, 1);
+    }
   }
+  // the halves' sums
+  uint8_t* part = (kg < 2 ? lds.s0 : lds.s1) + (kg & 1) * 64 * T::kRow + lane * 16;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    v16f(&sum)[T::kBlocks] = x ? dv : dk;
+    __syncthreads();
+#pragma unroll
+    for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (rg == 1)
+          *reinterpret_cast<v4f*>(part + (db * 4 + i) * 1024) =
+              v4f{sum[db][4 * i], sum[db][4 * i + 1], sum[db][4 * i + 2], sum[db][4 * i + 3]};
+    __syncthreads();
+    if (rg == 1) continue;
+#pragma unroll
+    for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const v4f y = *reinterpret_cast<const v4f*>(part + (db * 4 + i) * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[db][4 * i + e] += y[e];
+      }
+  }
+  if (rg == 1) return;
   const float odd = odd_of(dk) + odd_of(dv);
   uint64_t again = __ballot(live && odd != 0.0f);
   if (live) {
@@ -369,27 +440,27 @@ __device__ __forceinline__ void grad_keys(const Args& a, uint8_t* lds, Job job, 
   }
 }
 
-// dq of 128 query rows, laid out as the forward kernel: S^T = K Q^T, dP^T = V dO^T, and
+// dq of 256 query rows, laid out as the forward kernel: S^T = K Q^T, dP^T = V dO^T, and
 // dS^T as it stands is the second operand of dQ^T = K^T dS^T.
 template <int DP>
-__device__ __forceinline__ void grad_queries(const Args& a, uint8_t* lds, Job job, int tiles) {
+__device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& lds, Job job, int tiles) {
   using T = Tile<DP>;
-  constexpr int kStage = 2 * kKeys * T::kRow;
+  constexpr int kHalf = kKeys * T::kRow;   // of a stage: K, then V
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
   const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
   const int64_t rows = (int64_t)a.Tq * a.G;
-  const int64_t r = (int64_t)(tiles - 1 - job.tile) * kRowsWG + wave * 32 + (lane & 31);
+  const int64_t r = (int64_t)(tiles - 1 - job.tile) * kGradRows + wave * 32 + (lane & 31);
   const bool live = r < rows;
   const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
   const Range mine = keys_of(a, t);
   const Reach reach = reach_of(live, mine.lo, mine.hi);
-  const Range all = reach_of_all(lds, reach, wave);
+  const Range all = reach_of_all<8>(lds.s0, reach, wave);
   const float2 st = live ? a.stats[job.pair * rows + r] : float2{0.0f, 0.0f};
 
   v8bf q[T::kSteps], g[T::kSteps];
   row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
   row_frags<DP>(g, row_of(a.dout, b, live ? t : 0, h), live, a.D, half);
-  KeyLoader<DP, kKeys> lk, lv;
+  KeyLoader<DP, kKeys, 8> lk, lv;
   lk.init(a.k, b, hk, a.Tk, a.D, wave);
   lv.init(a.v, b, hk, a.Tk, a.D, wave);
   int fr[T::kSteps], ft[T::kBlocks][2];
@@ -399,49 +470,54 @@ __device__ __forceinline__ void grad_queries(const Args& a, uint8_t* lds, Job jo
   for (int db = 0; db < T::kBlocks; ++db) ft[db][0] = T::frag_t(lane, db, 0), ft[db][1] = T::frag_t(lane, db, 1);
 
   v16f dq[T::kBlocks] = {};
-  if (all.lo < all.hi) {
-    lk.load(lds, wave, all.lo);
-    lv.load(lds + kStage / 2, wave, all.lo);
-  }
-  for (int j = all.lo, stage = 0; j < all.hi; j += kKeys, stage ^= 1) {
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    const uint8_t* tk = lds + stage * kStage;
-    const uint8_t* tv = tk + kStage / 2;
+  auto tile = [&](int j, uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
+    tile_landed();
     if (j + kKeys < all.hi) {
-      uint8_t* next = lds + (stage ^ 1) * kStage;
       lk.load(next, wave, j + kKeys);
-      lv.load(next + kStage / 2, wave, j + kKeys);
+      lv.load(next + kHalf, wave, j + kKeys);
     }
-    if (j >= reach.hi || j + kKeys <= reach.lo) continue;
+    if (j >= reach.hi || j + kKeys <= reach.lo) return;
+    const uint8_t* tv = now + kHalf;
     v16f s[2] = {}, dp[2] = {};
 #pragma unroll
     for (int ks = 0; ks < T::kSteps; ++ks)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        s[kb] = mfma(T::read(tk + fr[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
+        s[kb] = mfma(T::read(now + fr[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
         dp[kb] = mfma(T::read(tv + fr[ks] + kb * 32 * T::kRow), g[ks], dp[kb]);
       }
-    const bool cut = j < reach.all_lo || j + kKeys > reach.all_hi;
-    const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(mine.hi - mine.lo, 0);
+    interleave<4 * T::kSteps, 1, AH4>();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         dp[kb][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][v], a.scale2, -st.x)) * (dp[kb][v] - st.y);
-    if (cut) {
+    if (j < reach.all_lo || j + kKeys > reach.all_hi) {
+      const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(mine.hi - mine.lo, 0);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           if (first + kb * 32 + acc_row(v) >= n) dp[kb][v] = 0.0f;
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const v8bf ds = pack_half(dp[ks >> 1], ks & 1);
 #pragma unroll
       for (int db = 0; db < T::kBlocks; ++db)
-        dq[db] = mfma(T::read_t(tk + ft[db][0] + ks * 16 * T::kRow, tk + ft[db][1] + ks * 16 * T::kRow), ds, dq[db]);
+        dq[db] = mfma(T::read_t(now + ft[db][0] + ks * 16 * T::kRow, now + ft[db][1] + ks * 16 * T::kRow), ds, dq[db]);
     }
+    interleave<4 * T::kBlocks, 2, AH4>();
+  };
+  if (all.lo < all.hi) {
+    lk.load(lds.s0, wave, all.lo);
+    lv.load(lds.s0 + kHalf, wave, all.lo);
+  }
+  for (int j = all.lo; j < all.hi; j += 2 * kKeys) {
+    tile(j, lds.s0, lds.s1);
+    if (j + kKeys < all.hi) tile(j + kKeys, lds.s1, lds.s0);
   }
   const float odd = odd_of(dq);
   uint64_t again = __ballot(live && odd != 0.0f);
@@ -456,13 +532,15 @@ __device__ __forceinline__ void grad_queries(const Args& a, uint8_t* lds, Job jo
 // One launch for both halves of the gradient: the keys' workgroups, which are few and
 // long, come first, the queries' fill what they leave.
 template <int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles) {
+__global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[256 * Tile<DP>::kRow + 512];
-  const int64_t id = block_xz(), keys = (int64_t)pairs * key_tiles;
+  constexpr int kRow = Tile<DP>::kRow;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[128 * kRow], s1[128 * kRow], v[128 * kRow], stats[1024];
+  const GradLds<DP> lds{s0, s1, v, stats};
+  const uint32_t id = (uint32_t)block_xz(), keys = (uint32_t)pairs * (uint32_t)key_tiles;
   if (id < keys)
-    grad_keys<DP>(a, lds, job_of(id, pairs, key_tiles), key_tiles);
-  else if (id - keys < (int64_t)pairs * row_tiles)
+    grad_keys<DP>(a, lds, job_of(id, pairs, key_tiles));
+  else if (id - keys < (uint32_t)pairs * (uint32_t)row_tiles)
     grad_queries<DP>(a, lds, job_of(id - keys, pairs, row_tiles), row_tiles);
 #endif
 }
@@ -527,15 +605,15 @@ hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
   const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq;
   const Args a = make_args(c);
   const int pairs = (int)(sequences(c.a) * a.Hkv);
-  const int row_tiles = (int)(((int64_t)a.Tq * a.G + kRowsWG - 1) / kRowsWG);
+  const int row_tiles = (int)(((int64_t)a.Tq * a.G + kGradRows - 1) / kGradRows);
   const int key_tiles = (int)(((int64_t)a.Tk + 127) / 128);
   const int64_t n = (int64_t)pairs * row_tiles + (int64_t)pairs * key_tiles;
   if (n == 0) return hipSuccess;
   if (rows > 0) k_attn_stats<<<grid_xz((rows + 31) / 32), 256, 0, s>>>(a, rows);
   if (a.D <= 64)
-    k_attn_grad<64><<<grid_xz(n), 256, 0, s>>>(a, pairs, key_tiles, row_tiles);
+    k_attn_grad<64><<<grid_xz(n), 512, 0, s>>>(a, pairs, key_tiles, row_tiles);
   else
-    k_attn_grad<128><<<grid_xz(n), 256, 0, s>>>(a, pairs, key_tiles, row_tiles);
+    k_attn_grad<128><<<grid_xz(n), 512, 0, s>>>(a, pairs, key_tiles, row_tiles);
   return hipGetLastError();
 }
 

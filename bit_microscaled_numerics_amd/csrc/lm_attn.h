@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "lm_attn_kernels.h"
 #include "lm_device.h"
 
@@ -223,16 +225,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint16_t* p) 
       reinterpret_cast<void*>(uniform64((int64_t)(uintptr_t)p)), (short)0, 0x7fffffff, 0x00020000);
 }
 
-// The order of a phase of MFMAS products that need PER reads of LDS each: the reads of AHEAD
-// products first, then one product's reads after each product.  (Left alone, the compiler
-// reads a product's operands right before it and waits out the LDS each time.)
-template <int MFMAS, int PER, int AHEAD>
-__device__ __forceinline__ void interleave() {
-  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * PER, 0);
+// N products whose operands come from LDS: each is read AHEAD products before its own.
+// (Left alone, the compiler reads a product's operands right before it, to spare
+// registers, and waits out the LDS each time.)  Arithmetic may move across.
+template <int N, int AHEAD, class Read, class Use>
+__device__ __forceinline__ void pipeline(Read read, Use use) {
+  constexpr int kArithmetic = 0x2 | 0x4 | 0x400;
+  decltype(read(0)) f[AHEAD];
 #pragma unroll
-  for (int i = 0; i < MFMAS; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (AHEAD + i < MFMAS) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+  for (int i = 0; i < AHEAD; ++i) f[i] = read(i);
+  __builtin_amdgcn_sched_barrier(kArithmetic);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, f[i % AHEAD]);
+    if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
+    __builtin_amdgcn_sched_barrier(kArithmetic);
   }
 }
 
@@ -240,34 +247,35 @@ __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A tile in LDS: rows of DP values (64 or 128), 16-byte chunk c of row r at c ^ swz(r).
-// swz makes both reads free of bank conflicts: 16 lanes that take the same chunk of 16
-// consecutive rows (fragments along d), and the transposing read, where 32 lanes take
-// 64 bytes of 4 consecutive rows.
-template <int DP>
+// A tile of ROWS rows of DP values (64 or 128) in LDS: blocks of 32 columns, in each 64
+// bytes a row, whose 16-byte chunk c lies at c ^ ((row >> 2) & 3).  Both reads are free of bank
+// conflicts: the same chunk of 16 rows (fragments along d) and the transposing read, where 32
+// lanes take 64 bytes of 4 rows, cover 256 bytes each.  Two lane addresses serve all reads of a kind;
+// blocks and steps are immediate offsets.
+template <int DP, int ROWS>
 struct Tile {
-  static constexpr int kRow = DP * 2, kChunks = DP / 8, kSteps = DP / 16, kBlocks = DP / 32;
-  static __device__ __forceinline__ int swz(int r) {
-    return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 2) & 3);
+  static constexpr int kSteps = DP / 16, kBlocks = DP / 32;   // of 16 and of 32 columns
+  static constexpr int kBlock = ROWS * 64, kBytes = kBlocks * kBlock;
+  int along[2], across[2];   // by parity of the step; lower and upper rows of a step of 16
+
+  __device__ __forceinline__ void init(int row0) {
+    const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31;
+    const int g = lane >> 4, j = lane & 15;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      along[x] = (row0 + r) * 64 + (((2 * x + half) ^ ((r >> 2) & 3)) << 4);
+      const int row = 4 * (g >> 1) + (j >> 2) + 8 * x;
+      across[x] = (row0 + row) * 64 + (((2 * (g & 1) + ((j & 3) >> 1)) ^ ((row >> 2) & 3)) << 4) + (j & 1) * 8;
+    }
   }
-  // Lane's place in a fragment along d of rows 0 .. 31: row lane & 31, chunk 2 ks + half.
-  static __device__ __forceinline__ int frag(int lane, int ks) {
-    const int r = lane & 31;
-    return r * kRow + (((2 * ks + (lane >> 5)) ^ swz(r)) << 4);
+  // Row lane & 31 of 32, columns 16 ks + 8 half + (0 .. 7).
+  __device__ __forceinline__ v8bf read(const uint8_t* tile, int ks, int row0 = 0) const {
+    return *reinterpret_cast<const v8bf*>(tile + along[ks & 1] + (ks >> 1) * kBlock + row0 * 64);
   }
-  // Lane's place in the transposing read of block db of 32 columns: rows 4 half + (0 .. 3)
-  // of a step of 16, and 8 on (hi).
-  static __device__ __forceinline__ int frag_t(int lane, int db, int hi) {
-    const int g = lane >> 4, j = lane & 15, r = 4 * (g >> 1) + (j >> 2) + 8 * hi;
-    return r * kRow + (((db * 4 + 2 * (g & 1) + ((j & 3) >> 1)) ^ swz(r)) << 4) + (j & 1) * 8;
-  }
-  static __device__ __forceinline__ v8bf read(const uint8_t* at) {
-    return *reinterpret_cast<const v8bf*>(at);
-  }
-  // 8 values of the lane's column: rows of lo, then of hi.
-  static __device__ __forceinline__ v8bf read_t(const uint8_t* lo, const uint8_t* hi) {
-    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)lo);
-    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)hi);
+  // Column 32 db + (lane & 31) of rows 4 half + (0 .. 3) and those 8 on, of step t of 16 rows.
+  __device__ __forceinline__ v8bf read_t(const uint8_t* tile, int db, int t) const {
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tile + across[0] + db * kBlock + t * 1024));
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(tile + across[1] + db * kBlock + t * 1024));
     return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
@@ -279,56 +287,74 @@ __device__ __forceinline__ void tile_landed() {
   asm volatile("s_barrier" ::: "memory");
 }
 
+// How WAVES waves share the loads of a tile: each takes one 1 KiB piece of 16 rows in some
+// of the blocks, so that a lane has one row.
+template <int DP, int ROWS, int WAVES>
+struct Share {
+  static constexpr int kBlocks = DP / 32;
+  static constexpr int kLoads = ROWS / 16 * kBlocks / WAVES;
+  static_assert(kLoads >= 1 && kBlocks % kLoads == 0, "");
+  static __device__ __forceinline__ int block(int wave) { return wave * kLoads % kBlocks; }
+  static __device__ __forceinline__ int group(int wave) { return wave * kLoads / kBlocks; }
+  static __device__ __forceinline__ int row(int wave) { return group(wave) * 16 + ((threadIdx.x & 63) >> 2); }
+  // The lane's source column in its first block; that of load q is 32 q on.
+  static __device__ __forceinline__ int column(int wave) {
+    const int lane = threadIdx.x & 63;
+    return block(wave) * 32 + (((lane & 3) ^ ((lane >> 4) & 3)) << 3);
+  }
+  // off: the lane's bytes from buf, or kDead; columns from D on read zero.
+  static __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buf, uint8_t* tile, int wave, uint32_t off,
+                                              int left) {
+    uint8_t* to = tile + block(wave) * ROWS * 64 + group(wave) * 1024;
+    load_blocks(buf, to, off, left, std::make_integer_sequence<int, kLoads>{});
+  }
+
+ private:
+  template <int... Q>
+  static __device__ __forceinline__ void load_blocks(__amdgpu_buffer_rsrc_t buf, uint8_t* to, uint32_t off, int left,
+                                                     std::integer_sequence<int, Q...>) {
+    (__builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(to + Q * ROWS * 64), 16, left > Q * 32 ? off : kDead,
+                                              Q * 64, 0, 0),
+     ...);
+  }
+};
+
 // Loads ROWS consecutive key rows into LDS, WAVES waves together; rows past the end and
 // columns past D read zero.
 template <int DP, int ROWS, int WAVES>
 struct KeyLoader {
-  using T = Tile<DP>;
-  static constexpr int kLoads = ROWS * T::kRow / 1024 / WAVES;   // per wave, 1 KiB each
+  using S = Share<DP, ROWS, WAVES>;
   const uint16_t* base;
   int64_t ld;
-  int end;
-  uint32_t voff[kLoads];
-  int row[kLoads];
+  uint32_t off;
+  int end, row, left;   // left: columns from the lane's first on
 
   __device__ __forceinline__ void init(const Rows& x, int b, int hk, int rows, int D, int wave) {
-    const int lane = threadIdx.x & 63;
     base = x.p + b * x.batch + hk * x.head;
     ld = x.token;
     end = rows;
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      const int at = (wave * kLoads + q) * 1024 + lane * 16;
-      row[q] = at / T::kRow;
-      const int chunk = (at % T::kRow / 16) ^ T::swz(row[q]);
-      voff[q] = (uint32_t)row[q] * (uint32_t)ld * 2 + chunk * 16;
-      if (chunk * 8 >= D) row[q] = 0x7fffffff;   // always past the end
-    }
+    row = S::row(wave);
+    off = (uint32_t)row * (uint32_t)ld * 2 + S::column(wave) * 2;
+    left = D - S::column(wave);
   }
-  __device__ __forceinline__ void load(uint8_t* lds, int wave, int j0) const {
-    const __amdgpu_buffer_rsrc_t buf = descriptor(base + (int64_t)j0 * ld);
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void)(lds + (wave * kLoads + q) * 1024), 16,
-                                               voff[q] | (row[q] < end - j0 ? 0u : kDead), 0, 0, 0);
+  __device__ __forceinline__ void load(uint8_t* tile, int wave, int j0) const {
+    S::load(descriptor(base + (int64_t)j0 * ld), tile, wave, row < end - j0 ? off : kDead, left);
   }
 };
 
-// Loads ROWS consecutive rows of q and of dout into LDS, WAVES waves together: the rows
-// of a group of heads are tokens and heads in turn.  Each call takes the rows before the last
-// call's.
+// Loads ROWS consecutive rows of q and of dout into two tiles, WAVES waves together: the
+// rows of a group of heads are tokens and heads in turn.  Each call takes the rows before the
+// last call's.
 template <int DP, int ROWS, int WAVES>
 struct RowLoader {
-  using T = Tile<DP>;
-  static constexpr int kLoads = ROWS * T::kRow / 1024 / WAVES;   // per wave and operand
+  using S = Share<DP, ROWS, WAVES>;
   const uint16_t* base[2];
   int64_t ld[2];
-  int step_t, step_g, G, end, t0, g0;   // t0, g0: token and head of the tile's first row
-  int t[kLoads], g[kLoads], row[kLoads], chunk[kLoads];
   uint32_t head[2];
+  int step_t, step_g, G, end, t0, g0;   // t0, g0: token and head of the tile's first row
+  int t, g, row, left;                  // the lane's
 
   __device__ __forceinline__ void init(const Args& a, int b, int hk, int r0, int wave) {
-    const int lane = threadIdx.x & 63;
     G = a.G;
     base[0] = a.q.p + b * a.q.batch + (int64_t)hk * G * a.q.head;
     base[1] = a.dout.p + b * a.dout.batch + (int64_t)hk * G * a.dout.head;
@@ -337,36 +363,24 @@ struct RowLoader {
     step_t = ROWS / G, step_g = ROWS - step_t * G;
     end = a.Tq * G;
     t0 = r0 / G, g0 = r0 - t0 * G;
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      const int at = (wave * kLoads + q) * 1024 + lane * 16;
-      row[q] = r0 + at / T::kRow;
-      chunk[q] = ((at % T::kRow / 16) ^ T::swz(at / T::kRow)) * 16;
-      t[q] = row[q] / G;
-      g[q] = row[q] - t[q] * G;
-      if (chunk[q] >= a.D * 2) chunk[q] = -1;
-    }
+    row = r0 + S::row(wave);
+    t = row / G;
+    g = row - t * G;
+    left = a.D - S::column(wave);
   }
   // The rows at hand to LDS, q's first; then back by ROWS.
-  __device__ __forceinline__ void load(uint8_t* lds, int wave) {
+  __device__ __forceinline__ void load(uint8_t* tiles, int wave) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const __amdgpu_buffer_rsrc_t buf = descriptor(base[x] + (int64_t)t0 * ld[x]);
-#pragma unroll
-      for (int q = 0; q < kLoads; ++q) {
-        const uint32_t off = (uint32_t)(t[q] - t0) * (uint32_t)ld[x] * 2 + (uint32_t)g[q] * head[x] + chunk[q];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            buf, (lds_void)(lds + x * ROWS * T::kRow + (wave * kLoads + q) * 1024), 16,
-            row[q] < end && chunk[q] >= 0 ? off : kDead, 0, 0, 0);
-      }
+      const uint32_t off =
+          (uint32_t)(t - t0) * (uint32_t)ld[x] * 2 + (uint32_t)g * head[x] + (uint32_t)S::column(wave) * 2;
+      S::load(descriptor(base[x] + (int64_t)t0 * ld[x]), tiles + x * ROWS * DP * 2, wave, row < end ? off : kDead,
+              left);
     }
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      row[q] -= ROWS;
-      t[q] -= step_t;
-      g[q] -= step_g;
-      if (g[q] < 0) g[q] += G, --t[q];
-    }
+    row -= ROWS;
+    t -= step_t;
+    g -= step_g;
+    if (g < 0) g += G, --t;
     t0 -= step_t;
     g0 -= step_g;
     if (g0 < 0) g0 += G, --t0;

@@ -44,24 +44,8 @@ Args make_args(const AttnCall& c) {
 }
 
 namespace {
-#ifdef VPRIO
-#define PRIO(x) __builtin_amdgcn_s_setprio(x)
-#else
-#define PRIO(x)
-#endif
-#ifndef AH1
-#define AH1 3
-#define AH2 2
-#define AH3 3
-#define AH4 4
-#endif
-#ifdef VSB
-#define SB __builtin_amdgcn_sched_barrier(0)
-#else
-#define SB
-#endif
-
 constexpr int kWaves = 4;
+constexpr int kAhead = 4;   // reads of LDS ahead of the products (2 and 6 measured the same, 0 a quarter slower)
 constexpr int kRowsWG = 128, kKeys = 64;   // query rows of a workgroup, keys of a tile
 constexpr int kGradRows = 256;   // query rows of a workgroup of the gradient
 constexpr int kPartTiles = 512, kPartKeys = 128;   // see parts_of
@@ -81,8 +65,8 @@ struct Part {   // of a row's softmax, where several workgroups share its keys
 template <int DP, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, Part part) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass drops the stubs of kernels with these builtins
-  using T = Tile<DP>;
-  constexpr int kStage = 2 * kKeys * T::kRow;
+  using T = Tile<DP, kKeys>;
+  constexpr int kStage = 2 * T::kBytes;
   // one array per stage: loads into the next one are not waited for by reads of this one
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kStage], lds1[kStage];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
@@ -115,11 +99,8 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   KeyLoader<DP, kKeys, 4> lk, lv;
   lk.init(a.k, b, hk, a.Tk, a.D, wave);
   lv.init(a.v, b, hk, a.Tk, a.D, wave);
-  int fk[T::kSteps], fv[T::kBlocks][2];
-#pragma unroll
-  for (int ks = 0; ks < T::kSteps; ++ks) fk[ks] = T::frag(lane, ks);
-#pragma unroll
-  for (int db = 0; db < T::kBlocks; ++db) fv[db][0] = T::frag_t(lane, db, 0), fv[db][1] = T::frag_t(lane, db, 1);
+  T frag;
+  frag.init(0);
 
   v16f o[T::kBlocks] = {};
   float m = -INFINITY, l = 0.0f;   // m: of the products, before scale
@@ -136,14 +117,8 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
     const int last = SPLIT ? min(hi, j1) : hi;
     if (j >= last || j + kKeys <= lo) return;
     v16f s[2] = {};
-    PRIO(1);
-#pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) s[kb] = mfma(T::read(at + fk[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
-    interleave<2 * T::kSteps, 1, 6>();
-    __builtin_amdgcn_sched_barrier(0);
-    PRIO(0);
+    pipeline<2 * T::kSteps, kAhead>([&](int i) { return frag.read(at, i >> 1, (i & 1) * 32); },
+                               [&](int i, const v8bf& f) { s[i & 1] = mfma(f, q[i >> 1], s[i & 1]); });
     if (j < all_lo || j + kKeys > (SPLIT ? min(all_hi, j1) : all_hi)) {
       const uint32_t n = (uint32_t)max((SPLIT ? min(mine.hi, j1) : mine.hi) - mine.lo, 0);
 #pragma unroll
@@ -174,16 +149,13 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
         l += s[kb][v];
       }
     const uint8_t* vt = at + kStage / 2;
-    SB;
-    PRIO(1);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const v8bf p = pack_half(s[ks >> 1], ks & 1);
-#pragma unroll
-      for (int db = 0; db < T::kBlocks; ++db)
-        o[db] = mfma(T::read_t(vt + fv[db][0] + ks * 16 * T::kRow, vt + fv[db][1] + ks * 16 * T::kRow), p, o[db]);
-    }
-    PRIO(0);
+    v8bf p;
+    pipeline<4 * T::kBlocks, kAhead>([&](int i) { return frag.read_t(vt, i % T::kBlocks, i / T::kBlocks); },
+                                [&](int i, const v8bf& f) {
+                                  const int db = i % T::kBlocks, ks = i / T::kBlocks;
+                                  if (db == 0) p = pack_half(s[ks >> 1], ks & 1);
+                                  o[db] = mfma(f, p, o[db]);
+                                });
   };
   for (int j = j0; j < j1; j += 2 * kKeys) {
     tile(j, lds, lds1);
@@ -303,8 +275,8 @@ struct GradLds {   // one array per stage: loads into the next are not waited fo
 // rows and find them in their XCD's L2.
 template <int DP>
 __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds, Job job) {
-  using T = Tile<DP>;
-  constexpr int kHalf = 64 * T::kRow;   // of a stage: q, then dout
+  using T = Tile<DP, 64>;
+  constexpr int kHalf = T::kBytes;   // of a stage: q, then dout
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
   const int kg = wave & 3, rg = wave >> 2;
   const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
@@ -326,13 +298,8 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
       *reinterpret_cast<v8bf*>(lds.v + ((kg * T::kSteps + ks) * 64 + lane) * 16) = v[ks];
   }
   const uint8_t* mine_v = lds.v + (kg * T::kSteps * 64 + lane) * 16;
-  int fr[T::kSteps], ft[T::kBlocks][2];
-#pragma unroll
-  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = rg * 32 * T::kRow + T::frag(lane, ks);
-#pragma unroll
-  for (int db = 0; db < T::kBlocks; ++db)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) ft[db][x] = rg * 32 * T::kRow + T::frag_t(lane, db, x);
+  T frag;
+  frag.init(rg * 32);
 
   v16f dk[T::kBlocks] = {}, dv[T::kBlocks] = {};
   const int64_t all_rows = (int64_t)a.Tq * a.G;
@@ -354,13 +321,18 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     if (r0 >= reach.hi || r0 + 32 <= reach.lo) return;
     const uint8_t* td = now + kHalf;
     v16f s{}, dp{};
-#pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks) s = mfma(T::read(now + fr[ks]), k[ks], s);
-    interleave<T::kSteps, 1, AH1>();
-#pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks) dp = mfma(T::read(td + fr[ks]), T::read(mine_v + ks * 1024), dp);
-    interleave<T::kSteps, 2, AH2>();
-    __builtin_amdgcn_sched_barrier(0);
+    struct Two {
+      v8bf a, b;
+    };
+    pipeline<2 * T::kSteps, kAhead>(
+        [&](int i) {
+          if (i & 1) return Two{frag.read(td, i >> 1), *reinterpret_cast<const v8bf*>(mine_v + (i >> 1) * 1024)};
+          return Two{frag.read(now, i >> 1), k[i >> 1]};
+        },
+        [&](int i, const Two& f) {
+          v16f& sum = i & 1 ? dp : s;
+          sum = mfma(f.a, f.b, sum);
+        });
     const uint8_t* st_at = lds.stats + st * 512 + rg * 256 + half * 32;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -378,18 +350,17 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
       for (int v = 0; v < 16; ++v)
         if (first + acc_row(v) >= n) s[v] = dp[v] = 0.0f;
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const v8bf p = pack_half(s, ks), ds = pack_half(dp, ks);
-#pragma unroll
-      for (int db = 0; db < T::kBlocks; ++db) {
-        const int lo = ft[db][0] + ks * 16 * T::kRow, hi = ft[db][1] + ks * 16 * T::kRow;
-        dv[db] = mfma(T::read_t(td + lo, td + hi), p, dv[db]);
-        dk[db] = mfma(T::read_t(now + lo, now + hi), ds, dk[db]);
-      }
-    }
-    interleave<4 * T::kBlocks, 2, AH3>();
+    v8bf p, ds;
+    pipeline<4 * T::kBlocks, kAhead>(
+        [&](int i) { return frag.read_t(i & 1 ? now : td, (i >> 1) % T::kBlocks, (i >> 1) / T::kBlocks); },
+        [&](int i, const v8bf& f) {
+          const int db = (i >> 1) % T::kBlocks, ks = (i >> 1) / T::kBlocks;
+          if (db == 0 && i % 2 == 0) p = pack_half(s, ks), ds = pack_half(dp, ks);
+          if (i & 1)
+            dk[db] = mfma(f, ds, dk[db]);
+          else
+            dv[db] = mfma(f, p, dv[db]);
+        });
   };
   if (all.lo < all.hi) {
     const int last = all.lo + (all.hi - 1 - all.lo) / 64 * 64;
@@ -401,7 +372,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     }
   }
   // the halves' sums
-  uint8_t* part = (kg < 2 ? lds.s0 : lds.s1) + (kg & 1) * 64 * T::kRow + lane * 16;
+  uint8_t* part = (kg < 2 ? lds.s0 : lds.s1) + (kg & 1) * 64 * DP * 2 + lane * 16;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     v16f(&sum)[T::kBlocks] = x ? dv : dk;
@@ -444,8 +415,8 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
 // dS^T as it stands is the second operand of dQ^T = K^T dS^T.
 template <int DP>
 __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& lds, Job job, int tiles) {
-  using T = Tile<DP>;
-  constexpr int kHalf = kKeys * T::kRow;   // of a stage: K, then V
+  using T = Tile<DP, kKeys>;
+  constexpr int kHalf = T::kBytes;   // of a stage: K, then V
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
   const int b = job.pair / a.Hkv, hk = job.pair - b * a.Hkv;
   const int64_t rows = (int64_t)a.Tq * a.G;
@@ -463,11 +434,8 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   KeyLoader<DP, kKeys, 8> lk, lv;
   lk.init(a.k, b, hk, a.Tk, a.D, wave);
   lv.init(a.v, b, hk, a.Tk, a.D, wave);
-  int fr[T::kSteps], ft[T::kBlocks][2];
-#pragma unroll
-  for (int ks = 0; ks < T::kSteps; ++ks) fr[ks] = T::frag(lane, ks);
-#pragma unroll
-  for (int db = 0; db < T::kBlocks; ++db) ft[db][0] = T::frag_t(lane, db, 0), ft[db][1] = T::frag_t(lane, db, 1);
+  T frag;
+  frag.init(0);
 
   v16f dq[T::kBlocks] = {};
   auto tile = [&](int j, uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
@@ -479,15 +447,15 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
     if (j >= reach.hi || j + kKeys <= reach.lo) return;
     const uint8_t* tv = now + kHalf;
     v16f s[2] = {}, dp[2] = {};
-#pragma unroll
-    for (int ks = 0; ks < T::kSteps; ++ks)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        s[kb] = mfma(T::read(now + fr[ks] + kb * 32 * T::kRow), q[ks], s[kb]);
-        dp[kb] = mfma(T::read(tv + fr[ks] + kb * 32 * T::kRow), g[ks], dp[kb]);
-      }
-    interleave<4 * T::kSteps, 1, AH4>();
-    __builtin_amdgcn_sched_barrier(0);
+    pipeline<4 * T::kSteps, kAhead>(
+        [&](int i) { return frag.read(i & 1 ? tv : now, i >> 2, (i & 2) * 16); },
+        [&](int i, const v8bf& f) {
+          const int kb = (i >> 1) & 1;
+          if (i & 1)
+            dp[kb] = mfma(f, g[i >> 2], dp[kb]);
+          else
+            s[kb] = mfma(f, q[i >> 2], s[kb]);
+        });
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -501,15 +469,13 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
         for (int v = 0; v < 16; ++v)
           if (first + kb * 32 + acc_row(v) >= n) dp[kb][v] = 0.0f;
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const v8bf ds = pack_half(dp[ks >> 1], ks & 1);
-#pragma unroll
-      for (int db = 0; db < T::kBlocks; ++db)
-        dq[db] = mfma(T::read_t(now + ft[db][0] + ks * 16 * T::kRow, now + ft[db][1] + ks * 16 * T::kRow), ds, dq[db]);
-    }
-    interleave<4 * T::kBlocks, 2, AH4>();
+    v8bf ds;
+    pipeline<4 * T::kBlocks, kAhead>([&](int i) { return frag.read_t(now, i % T::kBlocks, i / T::kBlocks); },
+                                [&](int i, const v8bf& f) {
+                                  const int db = i % T::kBlocks, ks = i / T::kBlocks;
+                                  if (db == 0) ds = pack_half(dp[ks >> 1], ks & 1);
+                                  dq[db] = mfma(f, ds, dq[db]);
+                                });
   };
   if (all.lo < all.hi) {
     lk.load(lds.s0, wave, all.lo);
@@ -534,7 +500,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
 template <int DP>
 __global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
-  constexpr int kRow = Tile<DP>::kRow;
+  constexpr int kRow = DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t s0[128 * kRow], s1[128 * kRow], v[128 * kRow], stats[1024];
   const GradLds<DP> lds{s0, s1, v, stats};
   const uint32_t id = (uint32_t)block_xz(), keys = (uint32_t)pairs * (uint32_t)key_tiles;

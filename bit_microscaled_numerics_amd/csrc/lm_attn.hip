@@ -44,7 +44,6 @@ Args make_args(const AttnCall& c) {
 }
 
 namespace {
-constexpr int kWaves = 4;
 constexpr int kAhead = 4;   // reads of LDS ahead of the products (2 and 6 measured the same, 0 a quarter slower)
 constexpr int kRowsWG = 128, kKeys = 64;   // query rows of a workgroup, keys of a tile
 constexpr int kGradRows = 256;   // query rows of a workgroup of the gradient
@@ -209,30 +208,52 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 #endif
 }
 
-// The parts of each row joined, in order: one wave a row.
-__global__ __launch_bounds__(kWaves * 64) void k_attn_join(Args a, int64_t rows, Part part) {
-  const int64_t r = block_xz() * kWaves + (threadIdx.x >> 6);
+// The parts of each row joined.  `waves` waves a row (1 or 4): each takes every waves-th part,
+// in order, two columns a lane; 4 are added in order in LDS.
+template <int WAVES>
+__global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part part) {
+  __shared__ float sums[WAVES][128];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, first = WAVES == 1 ? 0 : wave;
+  const uint32_t r = (uint32_t)block_xz() * (4 / WAVES) + (WAVES == 1 ? wave : 0);
   if (r >= rows) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t in_pair = (int64_t)a.Tq * a.G;
-  const int pair = (int)(r / in_pair), rr = (int)(r % in_pair);
-  const int b = pair / a.Hkv, t = rr / a.G, h = pair % a.Hkv * a.G + rr % a.G;
+  const uint32_t in_pair = (uint32_t)a.Tq * a.G, pair = r / in_pair, rr = r - pair * in_pair;
+  const int b = pair / a.Hkv, t = rr / a.G, h = (pair - b * a.Hkv) * a.G + (rr - t * a.G);
+  // the parts' maxima and sums, up to 64 at a time
   float m = -INFINITY;
-  for (int i = 0; i < part.n; ++i) m = fmaxf(m, part.ml[2 * (i * rows + r)]);
-  float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-  for (int i = 0; i < part.n; ++i) {
-    const int64_t at = i * rows + r;
+  for (int i = lane; i < part.n; i += 64) m = fmaxf(m, part.ml[2 * ((int64_t)i * rows + r)]);
+  m = wave_max(m);
+  float l = 0.0f;
+  for (int i = lane; i < part.n; i += 64) {
+    const float* ml = part.ml + 2 * ((int64_t)i * rows + r);
+    l += ml[0] == -INFINITY ? 0.0f : ml[1] * __builtin_amdgcn_exp2f(ml[0] - m);
+  }
+  l = wave_sum(l);
+  float x0 = 0.0f, x1 = 0.0f;
+  const bool lo = 2 * lane < a.D;   // D is even
+#pragma unroll 8
+  for (int i = first; i < part.n; i += WAVES) {
+    const int64_t at = (int64_t)i * rows + r;
     const float mi = part.ml[2 * at];
     const float f = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
-    const float li = part.ml[2 * at + 1];
-    l += li * f;
-    if (lane < a.D) x0 += part.o[at * a.D + lane] * f;
-    if (lane + 64 < a.D) x1 += part.o[at * a.D + lane + 64] * f;
+    const float2 x = lo ? *reinterpret_cast<const float2*>(part.o + at * a.D + 2 * lane) : float2{0.0f, 0.0f};
+    x0 += x.x * f;
+    x1 += x.y * f;
+  }
+  if (WAVES > 1) {
+    sums[wave][2 * lane] = x0;
+    sums[wave][2 * lane + 1] = x1;
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < WAVES; ++w) x0 += sums[w][2 * lane], x1 += sums[w][2 * lane + 1];
   }
   const Range k = keys_of(a, t);
   const bool some = k.lo < k.hi;
-  const RowSum o{x0, x1};
-  o.store(row_of_out(a.out, b, t, h), a.D, some ? 1.0f / l : 0.0f);
+  const float f = some ? 1.0f / l : 0.0f;
+  if (lo) {
+    bf16_t* o = row_of_out(a.out, b, t, h) + 2 * lane;
+    store1(o, x0 * f);
+    store1(o + 1, x1 * f);
+  }
   if (lane == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
@@ -512,7 +533,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key
 }
 
 int64_t sequences(const nvfp4_attn& a) { return a.cu_q == nullptr ? a.batch : 1; }
-int64_t blocks(int64_t rows) { return (rows + kWaves - 1) / kWaves; }
 
 }  // namespace
 }  // namespace attn
@@ -563,7 +583,10 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
     k_attn<64, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
   else
     k_attn<128, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
-  k_attn_join<<<grid_xz(blocks(rows)), kWaves * 64, 0, s>>>(a, rows, part);
+  if (part.n >= 8)
+    k_attn_join<4><<<grid_xz(rows), 256, 0, s>>>(a, (uint32_t)rows, part);
+  else
+    k_attn_join<1><<<grid_xz((rows + 3) / 4), 256, 0, s>>>(a, (uint32_t)rows, part);
   return hipGetLastError();
 }
 

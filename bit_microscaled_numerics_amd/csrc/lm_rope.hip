@@ -2,7 +2,7 @@
 // the same pass, and the gradient (internal to libnvfp4.so).
 //
 // A row of D values is taken as D/2 pairs: the rot/2 rotated ones, then the rest of the
-// row as the pairs of its halves, which are not rotated.  A lane owns 8 pairs; 1 .. 32
+// row as the pairs of its halves, which are not rotated.  A lane owns 4 pairs; 1 .. 64
 // lanes make a row, so that a rotation needs no exchange and a norm a few shuffles.
 // A wave takes all heads of a token (several tokens, where they are few): the
 // sines and cosines of a lane's pairs are formed once for all of them.
@@ -18,7 +18,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWaves = 4;        // waves of a workgroup
-constexpr int kPartials = 1024;  // most workgroups of the gradient, each with sums of dw
+constexpr int kPartials = 4096;  // most workgroups of the gradient, each with a row of sums of dw
 
 struct Side {   // queries or keys
   const uint8_t* x;
@@ -32,24 +32,74 @@ struct Args {
   Side side[2];
   const void* positions;
   const float* inv_freq;
-  float* partials;   // gradient: [workgroup][side][D]
+  float* partials;   // gradient: [workgroup][D]
   int64_t T;
   int Hq, H, D, np, nr;     // np rotated pairs, nr others
   int lanes;                // per row, a power of two
-  int spread, steps, per;   // heads of a token side by side; rounds of them, and per wave
-  int tokens;               // tokens of a wave side by side
+  int spread[2], tokens[2]; // heads of a token, and tokens, that lie side by side in a wave
+  int steps, per;           // rounds of heads, and per wave
+  int blocks[2];            // gradient: workgroups of each side
   int wide_ids, wide_w, norm;
   float eps;
 };
 
+// Four consecutive elements as binary32, at any element alignment.
+typedef uint32_t v2u_any2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void store4(bf16_t* p, v4f v) {
+  *reinterpret_cast<v2u_any2*>(p) = __builtin_bit_cast(v2u_any2, __builtin_convertvector(v, v4bf));
+}
+__device__ __forceinline__ void store4(float* p, v4f v) {
+  *reinterpret_cast<v4u_any4*>(p) = __builtin_bit_cast(v4u, v);
+}
+
+// N consecutive elements as they lie in memory, at any element alignment, and as binary32.
+// Rows are loaded ahead of their use and kept as they lie: unpacked at once they would be waited
+// for at once.
+template <class T, int N> struct Vec;
+template <> struct Vec<bf16_t, 4> {
+  typedef v4f type;
+  typedef v2u_any2 raw;
+  static __device__ __forceinline__ v4f unpack(raw w) { return v4f{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])}; }
+};
+template <> struct Vec<bf16_t, 8> {
+  typedef v8f type;
+  typedef v4u_any2 raw;
+  static __device__ __forceinline__ v8f unpack(raw w) { return unpack8(w); }
+};
+template <> struct Vec<float, 4> {
+  typedef v4f type;
+  typedef v4u_any4 raw;
+  static __device__ __forceinline__ v4f unpack(raw w) { return __builtin_bit_cast(v4f, (v4u)w); }
+};
+template <> struct Vec<float, 8> {
+  typedef v8f type;
+  struct raw { v4u_any4 lo, hi; };
+  static __device__ __forceinline__ v8f unpack(raw w) {
+    return __builtin_shufflevector(__builtin_bit_cast(v4f, (v4u)w.lo), __builtin_bit_cast(v4f, (v4u)w.hi), 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+template <int N> using vfloat = typename Vec<float, N>::type;
+template <class T> __device__ __forceinline__ void storev(T* p, v4f v) { store4(p, v); }
+template <class T> __device__ __forceinline__ void storev(T* p, v8f v) { store8(p, v); }
+
+// N pairs of a row.
+template <int N>
 struct Pairs {
-  v8f a, b;
+  vfloat<N> a, b;
 };
 
-__device__ __forceinline__ int lane_reduce_steps(int lanes) { return __builtin_ctz(lanes); }
-
+// The sum over a row's lanes, in every one of them.
 __device__ __forceinline__ float row_sum(float x, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m);
+#define MOVED(how) __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), how, 15, 15, true))
+  if (lanes > 1) x += MOVED(0xB1);    // the other one of two
+  if (lanes > 2) x += MOVED(0x4E);    // the other two of four
+  if (lanes > 4) x += MOVED(0x141);   // mirrored within 8
+  if (lanes > 8) x += MOVED(0x140);   // mirrored within 16
+#undef MOVED
+  if (lanes > 16) x += __shfl_xor(x, 16);
+  if (lanes > 32) x += __shfl_xor(x, 32);
   return x;
 }
 
@@ -68,38 +118,46 @@ __device__ __forceinline__ void place(const Args& k, int s, int& a, int& b) {
   }
 }
 
-// A lane's pairs: 8 consecutive ones (VEC: all rotated or none, 16-byte pieces of the
-// row), or 8 that lie a row's lanes apart.
-template <class T, bool IL, bool VEC>
+// A lane's pairs: 4 consecutive ones (VEC: all rotated or none, 8-byte pieces of a BF16
+// row), or 4 that lie a row's lanes apart.
+template <bool IL, bool VEC, int N>
 struct Lane {
   const Args& k;
   int first, live;
   __device__ __forceinline__ Lane(const Args& args, int in_row) : k(args) {
-    first = VEC ? in_row * 8 : in_row;
+    first = VEC ? in_row * N : in_row;
     live = (k.np + k.nr) - first;   // pairs from here on
   }
   __device__ __forceinline__ bool has(int i) const { return (VEC ? i : i * k.lanes) < live; }
   __device__ __forceinline__ int pair(int i) const { return first + (VEC ? i : i * k.lanes); }
+  __device__ __forceinline__ bool together() const { return IL && first < k.np; }   // VEC: pairs side by side
+  // VEC: where the lane's two pieces of N begin.
+  __device__ __forceinline__ void pieces(int& a, int& b) const {
+    if (together()) {
+      a = 2 * first;
+      b = a + N;
+    } else {
+      place<false>(k, first, a, b);
+    }
+  }
 
-  template <class U>
-  __device__ __forceinline__ Pairs load(const U* row) const {
-    Pairs p{};
+  template <class T, bool V> struct RawOf { struct type { typename Vec<T, N>::raw a, b; }; };
+  template <class T> struct RawOf<T, false> { typedef Pairs<N> type; };
+  template <class T> using Raw = typename RawOf<T, VEC>::type;
+
+  template <class T>
+  __device__ __forceinline__ Raw<T> load(const T* row) const {
+    Raw<T> p{};
     if constexpr (VEC) {
       if (live > 0) {
-        if (IL && first < k.np) {
-          const v8f lo = load8(row + 2 * first), hi = load8(row + 2 * first + 8);
-          p.a = __builtin_shufflevector(lo, hi, 0, 2, 4, 6, 8, 10, 12, 14);
-          p.b = __builtin_shufflevector(lo, hi, 1, 3, 5, 7, 9, 11, 13, 15);
-        } else {
-          int a, b;
-          place<false>(k, first, a, b);
-          p.a = load8(row + a);
-          p.b = load8(row + b);
-        }
+        int a, b;
+        pieces(a, b);
+        p.a = *reinterpret_cast<const typename Vec<T, N>::raw*>(row + a);
+        p.b = *reinterpret_cast<const typename Vec<T, N>::raw*>(row + b);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (has(i)) {
           int a, b;
           place<IL>(k, pair(i), a, b);
@@ -109,23 +167,43 @@ struct Lane {
     }
     return p;
   }
-  template <class U>
-  __device__ __forceinline__ void store(U* row, const Pairs& p) const {
+  template <class T>
+  __device__ __forceinline__ Pairs<N> unpack(const Raw<T>& w) const {
+    if constexpr (VEC) {
+      const Pairs<N> x{Vec<T, N>::unpack(w.a), Vec<T, N>::unpack(w.b)};
+      if (!together()) return x;
+      Pairs<N> p;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        p.a[i] = i < N / 2 ? x.a[2 * i] : x.b[2 * i - N];
+        p.b[i] = i < N / 2 ? x.a[2 * i + 1] : x.b[2 * i + 1 - N];
+      }
+      return p;
+    } else {
+      return w;
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void store(T* row, Pairs<N> p) const {
     if constexpr (VEC) {
       if (live > 0) {
-        if (IL && first < k.np) {
-          store8(row + 2 * first, __builtin_shufflevector(p.a, p.b, 0, 8, 1, 9, 2, 10, 3, 11));
-          store8(row + 2 * first + 8, __builtin_shufflevector(p.a, p.b, 4, 12, 5, 13, 6, 14, 7, 15));
-        } else {
-          int a, b;
-          place<false>(k, first, a, b);
-          store8(row + a, p.a);
-          store8(row + b, p.b);
+        int a, b;
+        pieces(a, b);
+        if (together()) {
+          Pairs<N> q;   // as they lie
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            q.a[i] = i & 1 ? p.b[i / 2] : p.a[i / 2];
+            q.b[i] = i & 1 ? p.b[(i + N) / 2] : p.a[(i + N) / 2];
+          }
+          p = q;
         }
+        storev(row + a, p.a);
+        storev(row + b, p.b);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (has(i)) {
           int a, b;
           place<IL>(k, pair(i), a, b);
@@ -134,24 +212,26 @@ struct Lane {
         }
     }
   }
-  __device__ __forceinline__ Pairs weights(const void* w) const {
+  __device__ __forceinline__ Pairs<N> weights(const void* w) const {
     if (w == nullptr) {
-      Pairs p;
+      Pairs<N> p;
       p.a = p.b = 1.0f;
       return p;
     }
-    return k.wide_w ? load(static_cast<const float*>(w)) : load(static_cast<const bf16_t*>(w));
+    return k.wide_w ? unpack<float>(load(static_cast<const float*>(w)))
+                    : unpack<bf16_t>(load(static_cast<const bf16_t*>(w)));
   }
 };
 
 // cos and sin of a lane's pairs.  The angle in turns: position * inv_freq in FP64
 // (exact up to positions of 2^29), times 1/(2 pi) in two parts with the whole turns
 // taken off by a fused multiply-add, so a far position costs no accuracy.
-template <class L>
-__device__ __forceinline__ void turns(const Args& k, const L& at, double pos, v8f& c, v8f& s) {
+template <bool IL, bool VEC, int N>
+__device__ __forceinline__ void turns(const Args& k, const Lane<IL, VEC, N>& at, double pos, vfloat<N>& c,
+                                      vfloat<N>& s) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591011e-18;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     c[i] = 1.0f;
     s[i] = 0.0f;
     if (at.has(i) && at.pair(i) < k.np) {
@@ -176,200 +256,237 @@ __device__ __forceinline__ double position(const Args& k, int64_t t) {
 struct Place {
   int in_row, token, head0;
   bool on;
-  __device__ __forceinline__ Place(const Args& k) {
-    const int lane = threadIdx.x & 63, group = lane / k.lanes;
+  __device__ __forceinline__ Place(const Args& k, int side) {
+    const int lane = threadIdx.x & 63, group = lane >> __builtin_ctz(k.lanes);
     in_row = lane & (k.lanes - 1);
-    token = group / k.spread;
-    head0 = group - token * k.spread;
-    on = token < k.tokens;
+    token = group / k.spread[side];
+    head0 = group - token * k.spread[side];
+    on = token < k.tokens[side];
   }
 };
 
-template <class T, bool IL, bool VEC>
+// One row's norm, weight and rotation.
+template <int N, class V>
+__device__ __forceinline__ Pairs<N> forward_row(const Args& k, Pairs<N> x, const Pairs<N>& w, const V& c, const V& s) {
+  if (k.norm) {
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q += x.a[i] * x.a[i] + x.b[i] * x.b[i];
+    const float r = 1.0f / sqrtf(row_sum(q, k.lanes) / (float)k.D + k.eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x.a[i] *= r * w.a[i];
+      x.b[i] *= r * w.b[i];
+    }
+  }
+  Pairs<N> y;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    y.a[i] = x.a[i] * c[i] - x.b[i] * s[i];
+    y.b[i] = x.b[i] * c[i] + x.a[i] * s[i];
+  }
+  return y;
+}
+
+// Queries and keys of a token by one wave; the next row is loaded before one is worked on.
+template <class T, bool IL, bool VEC, int N>
 __global__ __launch_bounds__(kWaves * 64) void k_rope(Args k) {
-  const Place at(k);
+  const Place at(k, 0);
   const int wave = threadIdx.x >> 6;
-  const int64_t t = (block_xz() * kWaves + wave) * k.tokens + at.token;
+  const int64_t t = (block_xz() * kWaves + wave) * k.tokens[0] + at.token;
   if (!at.on || t >= k.T) return;
-  const Lane<T, IL, VEC> lane(k, at.in_row);
-  const int step0 = blockIdx.y * k.per, step1 = min(step0 + k.per, k.steps);
-  const Pairs wq = lane.weights(k.side[0].w), wk = lane.weights(k.side[1].w);
-  v8f c, s;
-  turns(k, lane, k.np ? position(k, t) : 0.0, c, s);
-  for (int step = step0; step < step1; ++step) {
-    const int h = at.head0 + step * k.spread;
-    if (h >= k.H) break;
+  const Lane<IL, VEC, N> lane(k, at.in_row);
+  const int end = min(k.H, at.head0 + min((int)(blockIdx.y + 1) * k.per, k.steps) * k.spread[0]);
+  int h = at.head0 + blockIdx.y * k.per * k.spread[0];
+  auto row = [&](int h) {
     const bool key = h >= k.Hq;
     const Side& side = k.side[key];
-    const int64_t hh = key ? h - k.Hq : h;
-    Pairs x = lane.load(reinterpret_cast<const T*>(side.x + t * side.x_token + hh * side.x_head));
-    if (k.norm) {
-      float q = 0.0f;
+    return lane.load(reinterpret_cast<const T*>(side.x + t * side.x_token + (int64_t)(key ? h - k.Hq : h) * side.x_head));
+  };
+  if (h >= end) return;
+  auto x = row(h);
+  const Pairs<N> wq = lane.weights(k.side[0].w), wk = lane.weights(k.side[1].w);
+  vfloat<N> c, s;
+  turns(k, lane, k.np ? position(k, t) : 0.0, c, s);
+  while (h < end) {
+    const int next = h + k.spread[0];
+    decltype(x) nx{};
+    if (next < end) nx = row(next);
+    const bool key = h >= k.Hq;
+    const Side& side = k.side[key];
+    Pairs<N> w;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q += x.a[i] * x.a[i] + x.b[i] * x.b[i];
-      const float r = 1.0f / sqrtf(row_sum(q, k.lanes) / (float)k.D + k.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x.a[i] *= r * (key ? wk.a[i] : wq.a[i]);
-        x.b[i] *= r * (key ? wk.b[i] : wq.b[i]);
-      }
+    for (int i = 0; i < N; ++i) {
+      w.a[i] = key ? wk.a[i] : wq.a[i];
+      w.b[i] = key ? wk.b[i] : wq.b[i];
     }
-    Pairs y;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y.a[i] = x.a[i] * c[i] - x.b[i] * s[i];
-      y.b[i] = x.b[i] * c[i] + x.a[i] * s[i];
-    }
-    lane.store(reinterpret_cast<T*>(side.out + t * side.out_token + hh * side.out_head), y);
+    lane.store(reinterpret_cast<T*>(side.out + t * side.out_token + (int64_t)(key ? h - k.Hq : h) * side.out_head),
+               forward_row(k, lane.template unpack<T>(x), w, c, s));
+    x = nx;
+    h = next;
   }
 }
 
-// Gradient.  The sums of dw stay in registers over a wave's tokens and heads; a
-// workgroup adds its waves and lane groups in LDS, in order, and leaves one row per
-// side, which k_rope_dw adds up.
-template <class T, bool IL, bool VEC>
+// Gradient; queries and keys by workgroups of their own.  The sums of dw stay in registers
+// over a wave's tokens and heads; a workgroup adds its lane groups and waves in LDS, in order,
+// and leaves one row, which k_rope_dw adds up.
+template <class T, bool IL, bool VEC, int N>
 __global__ __launch_bounds__(kWaves * 64) void k_rope_grad(Args k) {
-  __shared__ float sums[2][512];
-  const Place at(k);
+  __shared__ float sums[512];
+  const int j = (int)blockIdx.x >= k.blocks[0], block = blockIdx.x - (j ? k.blocks[0] : 0);
+  const Side& side = k.side[j];
+  const int H = j ? k.H - k.Hq : k.Hq;
+  const Place at(k, j);
   const int wave = threadIdx.x >> 6;
-  const Lane<T, IL, VEC> lane(k, at.in_row);
-  const Pairs wq = lane.weights(k.side[0].w), wk = lane.weights(k.side[1].w);
-  Pairs dw[2] = {};
-  const int64_t stride = (int64_t)gridDim.x * kWaves * k.tokens;
+  const Lane<IL, VEC, N> lane(k, at.in_row);
+  const Pairs<N> w = lane.weights(side.w);
+  Pairs<N> dw{};
+  const int64_t stride = (int64_t)k.blocks[j] * kWaves * k.tokens[j];
   const float inv_d = 1.0f / (float)k.D;
-  if (at.on)
-    for (int64_t t = ((int64_t)blockIdx.x * kWaves + wave) * k.tokens + at.token; t < k.T; t += stride) {
-      v8f c, s;
-      turns(k, lane, k.np ? position(k, t) : 0.0, c, s);
-      for (int h = at.head0; h < k.H; h += k.spread) {
-        const bool key = h >= k.Hq;
-        const Side& side = k.side[key];
-        const int64_t hh = key ? h - k.Hq : h;
-        const Pairs dy =
-            lane.load(reinterpret_cast<const T*>(side.dy + t * side.dy_token + hh * side.dy_head));
-        Pairs x{};
-        if (k.norm)
-          x = lane.load(reinterpret_cast<const T*>(side.x + t * side.x_token + hh * side.x_head));
-        Pairs g;
+  int64_t t = ((int64_t)block * kWaves + wave) * k.tokens[j] + at.token;
+  if (at.on && at.head0 < H) {
+    struct Row {
+      typename Lane<IL, VEC, N>::template Raw<T> dy, x;
+    };
+    int64_t ahead_t = t;
+    int ahead_h = at.head0;
+    auto fetch = [&]() {   // the row that is two on
+      Row r{};
+      if (ahead_t >= k.T) return r;
+      r.dy = lane.load(reinterpret_cast<const T*>(side.dy + ahead_t * side.dy_token + ahead_h * side.dy_head));
+      if (k.norm) r.x = lane.load(reinterpret_cast<const T*>(side.x + ahead_t * side.x_token + ahead_h * side.x_head));
+      ahead_h += k.spread[j];
+      if (ahead_h >= H) ahead_h = at.head0, ahead_t += stride;
+      return r;
+    };
+    Row first = fetch(), second = fetch();
+    double pos = k.np && t < k.T ? position(k, t) : 0.0;
+    for (; t < k.T; t += stride) {
+      vfloat<N> c, s;
+      turns(k, lane, pos, c, s);
+      if (k.np && t + stride < k.T) pos = position(k, t + stride);
+      for (int h = at.head0; h < H; h += k.spread[j]) {
+        const Pairs<N> dy = lane.template unpack<T>(first.dy);
+        Pairs<N> g, n = lane.template unpack<T>(first.x);
+        first = second;
+        second = fetch();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < N; ++i) {
           g.a[i] = dy.a[i] * c[i] + dy.b[i] * s[i];
           g.b[i] = dy.b[i] * c[i] - dy.a[i] * s[i];
         }
         if (k.norm) {
           float q = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q += x.a[i] * x.a[i] + x.b[i] * x.b[i];
+          for (int i = 0; i < N; ++i) q += n.a[i] * n.a[i] + n.b[i] * n.b[i];
           const float r = 1.0f / sqrtf(row_sum(q, k.lanes) * inv_d + k.eps);
           float m = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x.a[i] *= r;
-            x.b[i] *= r;
-            const float da = g.a[i] * x.a[i], db = g.b[i] * x.b[i];
-            dw[0].a[i] += key ? 0.0f : da;
-            dw[0].b[i] += key ? 0.0f : db;
-            dw[1].a[i] += key ? da : 0.0f;
-            dw[1].b[i] += key ? db : 0.0f;
-            g.a[i] *= key ? wk.a[i] : wq.a[i];
-            g.b[i] *= key ? wk.b[i] : wq.b[i];
-            m += g.a[i] * x.a[i] + g.b[i] * x.b[i];
+          for (int i = 0; i < N; ++i) {
+            n.a[i] *= r;
+            n.b[i] *= r;
+            const float da = g.a[i] * n.a[i], db = g.b[i] * n.b[i];
+            dw.a[i] += da;
+            dw.b[i] += db;
+            m += da * w.a[i] + db * w.b[i];
           }
           m = row_sum(m, k.lanes) * inv_d;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            g.a[i] = r * (g.a[i] - x.a[i] * m);
-            g.b[i] = r * (g.b[i] - x.b[i] * m);
+          for (int i = 0; i < N; ++i) {
+            g.a[i] = r * (g.a[i] * w.a[i] - n.a[i] * m);
+            g.b[i] = r * (g.b[i] * w.b[i] - n.b[i] * m);
           }
         }
-        lane.store(reinterpret_cast<T*>(side.out + t * side.out_token + hh * side.out_head), g);
+        lane.store(reinterpret_cast<T*>(side.out + t * side.out_token + h * side.out_head), g);
       }
     }
+  }
   if (k.partials == nullptr) return;
   // lane groups of a wave, then the waves one after the other
   for (int m = k.lanes; m < 64; m <<= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i) {
+      dw.a[i] += __shfl_xor(dw.a[i], m);
+      dw.b[i] += __shfl_xor(dw.b[i], m);
+    }
+  for (int v = 0; v < kWaves; ++v) {
+    if (wave == v && (int)(threadIdx.x & 63) < k.lanes)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        dw[j].a[i] += __shfl_xor(dw[j].a[i], m);
-        dw[j].b[i] += __shfl_xor(dw[j].b[i], m);
-      }
-  for (int w = 0; w < kWaves; ++w) {
-    if (wave == w && (int)(threadIdx.x & 63) < k.lanes)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (lane.has(i)) {
           int a, b;
           place<IL>(k, lane.pair(i), a, b);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            sums[j][a] = (w ? sums[j][a] : 0.0f) + dw[j].a[i];
-            sums[j][b] = (w ? sums[j][b] : 0.0f) + dw[j].b[i];
-          }
+          sums[a] = (v ? sums[a] : 0.0f) + dw.a[i];
+          sums[b] = (v ? sums[b] : 0.0f) + dw.b[i];
         }
     __syncthreads();
   }
-  for (int i = threadIdx.x; i < 2 * k.D; i += kWaves * 64) {
-    const int j = i >= k.D;
-    k.partials[(int64_t)blockIdx.x * 2 * k.D + i] = sums[j][i - j * k.D];
-  }
+  for (int i = threadIdx.x; i < k.D; i += kWaves * 64) k.partials[(int64_t)blockIdx.x * k.D + i] = sums[i];
 }
 
-// dw of both sides: 32 columns a workgroup, its 32 groups of lanes take the rows in
-// turn; joined in FP64.
-__global__ __launch_bounds__(1024) void k_rope_dw(const float* partials, int rows, int D, void* dwq,
+// dw of both sides (along y): 32 columns a workgroup, its 32 groups of lanes take the
+// side's rows in turn; joined in FP64.
+__global__ __launch_bounds__(1024) void k_rope_dw(const float* partials, int rows_q, int rows_k, int D, void* dwq,
                                                   void* dwk, int wide_w) {
   __shared__ double part[32][33];
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;
+  const int first = blockIdx.y ? rows_q : 0, end = blockIdx.y ? rows_q + rows_k : rows_q;
   double sum = 0.0;
-  if (col < 2 * D) {
+  if (col < D) {
 #pragma unroll 8
-    for (int r = group; r < rows; r += 32) sum += (double)partials[(int64_t)r * 2 * D + col];
+    for (int r = first + group; r < end; r += 32) sum += (double)partials[(int64_t)r * D + col];
   }
   part[group][threadIdx.x & 31] = sum;
   __syncthreads();
-  if (group != 0 || col >= 2 * D) return;
+  void* to = blockIdx.y ? dwk : dwq;
+  if (group != 0 || col >= D || to == nullptr) return;
   for (int g = 1; g < 32; ++g) sum += part[g][threadIdx.x & 31];
-  void* to = col < D ? dwq : dwk;
-  const int at = col < D ? col : col - D;
-  if (to == nullptr) return;
   if (wide_w)
-    store1(static_cast<float*>(to) + at, (float)sum);
+    store1(static_cast<float*>(to) + col, (float)sum);
   else
-    store1(static_cast<bf16_t*>(to) + at, (float)sum);
+    store1(static_cast<bf16_t*>(to) + col, (float)sum);
 }
 
-int row_lanes(int64_t D) {
-  int n = 1;
-  while (n * 16 < D) n *= 2;
-  return n;
+// Pairs of a lane.  Forward 8, 16-byte loads of BF16 (38 us for 8192 tokens of 48 heads of 128, 43 with 4); the
+// gradient, which holds three times the registers, 4 (8 need 166: 110 us instead of 94).
+constexpr int kForward = 8, kGradient = 4;
+
+// Lanes of a row; heads of a token side by side in a wave, and tokens side by side.
+void spread(int64_t H, int64_t D, int pairs, int* lanes, int* width, int* tokens) {
+  *lanes = 1;
+  while (*lanes * 2 * pairs < D) *lanes *= 2;
+  const int64_t groups = 64 / *lanes, steps = H > 0 ? (H + groups - 1) / groups : 1;
+  *width = H > 0 ? (int)((H + steps - 1) / steps) : 1;
+  *tokens = (int)(groups / *width);
 }
 
-// Heads of a token side by side in a wave, rounds of them, tokens side by side.
-void spread(int64_t H, int64_t D, int* lanes, int* width, int* steps, int* tokens) {
-  *lanes = row_lanes(D);
-  const int groups = 64 / *lanes;
-  *steps = (int)((H + groups - 1) / groups);
-  *width = (int)((H + *steps - 1) / *steps);
-  *tokens = groups / *width;
+int64_t token_blocks(int64_t T, int tokens) {
+  return (T + (int64_t)kWaves * tokens - 1) / ((int64_t)kWaves * tokens);
 }
 
-int64_t grad_blocks(int64_t T, int tokens) {
-  const int64_t n = (T + (int64_t)kWaves * tokens - 1) / ((int64_t)kWaves * tokens);
-  return n < kPartials ? n : kPartials;
+// Workgroups of the gradient for queries and keys: at most kPartials, shared out by rows.
+void grad_blocks(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, Args* k) {
+  spread(Hq, D, kGradient, &k->lanes, &k->spread[0], &k->tokens[0]);
+  spread(Hkv, D, kGradient, &k->lanes, &k->spread[1], &k->tokens[1]);
+  const int64_t share = Hq + Hkv > 0 ? (kPartials * Hkv + Hq + Hkv - 1) / (Hq + Hkv) : 0;
+  const int64_t heads[2] = {Hq, Hkv}, most[2] = {kPartials - share > 1 ? kPartials - share : 1, share > 1 ? share : 1};
+  for (int j = 0; j < 2; ++j) {
+    const int64_t n = heads[j] > 0 ? token_blocks(T, k->tokens[j]) : 0;
+    const int64_t rounds = n == 0 ? 1 : (n + most[j] - 1) / most[j];
+    k->blocks[j] = (int)((n + rounds - 1) / rounds);   // as many tokens for each
+  }
 }
 
 template <class T, bool IL, bool VEC>
 void launch(const Args& k, bool grad, int64_t blocks, int y, hipStream_t s) {
   if (grad)
-    k_rope_grad<T, IL, VEC><<<dim3((uint32_t)blocks), kWaves * 64, 0, s>>>(k);
+    k_rope_grad<T, IL, VEC, kGradient><<<dim3((uint32_t)blocks), kWaves * 64, 0, s>>>(k);
   else
-    k_rope<T, IL, VEC><<<grid_xz(blocks, y), kWaves * 64, 0, s>>>(k);
+    k_rope<T, IL, VEC, kForward><<<grid_xz(blocks, y), kWaves * 64, 0, s>>>(k);
 }
 
 template <class T>
-void launch(const Args& k, bool il, bool vec, bool grad, int64_t blocks, int y, hipStream_t s) {
+void launch(const Args& k, bool grad, int64_t blocks, int y, bool il, bool vec, hipStream_t s) {
   if (il)
     vec ? launch<T, true, true>(k, grad, blocks, y, s) : launch<T, true, false>(k, grad, blocks, y, s);
   else
@@ -379,10 +496,9 @@ void launch(const Args& k, bool il, bool vec, bool grad, int64_t blocks, int y, 
 }  // namespace
 
 int64_t rope_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
-  if (T == 0 || Hq + Hkv == 0) return 0;
-  int lanes, width, steps, tokens;
-  spread(Hq + Hkv, D, &lanes, &width, &steps, &tokens);
-  return grad_blocks(T, tokens) * 2 * D * 4;
+  Args k{};
+  grad_blocks(T, Hq, Hkv, D, &k);
+  return (int64_t)(k.blocks[0] + k.blocks[1]) * D * 4;
 }
 
 hipError_t launch_rope(const RopeCall& c, hipStream_t s) {
@@ -409,30 +525,33 @@ hipError_t launch_rope(const RopeCall& c, hipStream_t s) {
     k.D = (int)r.D;
     k.np = (int)(r.rot / 2);
     k.nr = (int)((r.D - r.rot) / 2);
-    spread(k.H, r.D, &k.lanes, &k.spread, &k.steps, &k.tokens);
     k.wide_ids = r.positions_type == NVFP4_TYPE_I64;
     k.wide_w = r.weight_type == NVFP4_TYPE_F32;
     k.norm = r.norm;
     k.eps = r.eps;
-    const bool vec = k.np % 8 == 0 && k.nr % 8 == 0, il = r.interleaved;
+    const int pairs = c.grad ? kGradient : kForward;
+    const bool vec = k.np % pairs == 0 && k.nr % pairs == 0, il = r.interleaved;
     int y = 1;
     if (c.grad) {
-      blocks = grad_blocks(r.T, k.tokens);
+      grad_blocks(r.T, r.Hq, r.Hkv, r.D, &k);
+      blocks = k.blocks[0] + k.blocks[1];
     } else {
-      blocks = (r.T + (int64_t)kWaves * k.tokens - 1) / ((int64_t)kWaves * k.tokens);
+      spread(k.H, r.D, kForward, &k.lanes, &k.spread[0], &k.tokens[0]);
+      k.steps = (k.H + k.spread[0] - 1) / k.spread[0];
+      blocks = token_blocks(r.T, k.tokens[0]);
       // few tokens: their heads are shared out among waves
       k.per = k.steps;
       while (k.per > 1 && blocks * ((k.steps + k.per - 1) / k.per) < 2 * num_cus()) k.per = (k.per + 1) / 2;
       y = (k.steps + k.per - 1) / k.per;
     }
     if (el == 2)
-      launch<bf16_t>(k, il, vec, c.grad, blocks, y, s);
+      launch<bf16_t>(k, c.grad, blocks, y, il, vec, s);
     else
-      launch<float>(k, il, vec, c.grad, blocks, y, s);
+      launch<float>(k, c.grad, blocks, y, il, vec, s);
   }
   if (sums)
-    k_rope_dw<<<(uint32_t)((2 * r.D + 31) / 32), 1024, 0, s>>>(
-        static_cast<const float*>(c.ws), (int)blocks, (int)r.D, c.dq_weight, c.dk_weight,
+    k_rope_dw<<<dim3((uint32_t)((r.D + 31) / 32), 2), 1024, 0, s>>>(
+        static_cast<const float*>(c.ws), k.blocks[0], k.blocks[1], (int)r.D, c.dq_weight, c.dk_weight,
         r.weight_type == NVFP4_TYPE_F32);
   return hipGetLastError();
 }

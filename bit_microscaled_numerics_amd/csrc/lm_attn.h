@@ -403,7 +403,7 @@ __device__ __forceinline__ Reach reach_of(bool live, int lo, int hi) {
   }
   return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi)};
 }
-// The reach of WAVES waves; lds is free before and after.
+// The reach of WAVES waves, {0, 0} if none reaches anything; lds is free before and after.
 template <int WAVES>
 __device__ __forceinline__ Range reach_of_all(uint8_t* lds, const Reach& r, int wave) {
   int* ends = reinterpret_cast<int*>(lds);
@@ -413,7 +413,7 @@ __device__ __forceinline__ Range reach_of_all(uint8_t* lds, const Reach& r, int 
 #pragma unroll
   for (int w = 1; w < WAVES; ++w) lo = min(lo, ends[2 * w]), hi = max(hi, ends[2 * w + 1]);
   __syncthreads();
-  return Range{uniform(lo), uniform(hi)};
+  return lo < hi ? Range{uniform(lo), uniform(hi)} : Range{0, 0};
 }
 
 // Lane's fragments along d of one row of global memory.

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "lm_attn.h"
+#include "lm_kernels.h"
 
 namespace nvfp4 {
 namespace attn {
@@ -55,20 +56,22 @@ struct Part {   // of a row's softmax, where several workgroups share its keys
   int n;
 };
 
-// Forward.  4 waves of 32 query rows each; the keys pass in tiles of 64 through two LDS
+// Forward.  4 waves of 32 query rows each (KH = 2: twice 4, which take every other tile of
+// keys and are added up in LDS at the end); the keys pass in tiles of 64 through two LDS
 // stages filled by loads that write LDS directly.  Scores are formed transposed (S^T = K
 // Q^T): a lane then holds one query's scores of 32 keys, so the softmax needs one
 // exchange (with the lane 32 away), and the probabilities are, as they stand, the second operand of
 // O^T = V^T P^T; V is read transposed from LDS.  The sums are rescaled only when
 // a maximum grows by more than 2^8: until then the probabilities are at most 2^8 and lose nothing.
-template <int DP, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, Part part) {
+template <int DP, int KH, bool SPLIT>
+__global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int tiles, Part part) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass drops the stubs of kernels with these builtins
   using T = Tile<DP, kKeys>;
   constexpr int kStage = 2 * T::kBytes;
   // one array per stage: loads into the next one are not waited for by reads of this one
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStage], lds1[kStage];
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KH * kStage], lds1[KH * kStage];
+  const int wave = uniform(threadIdx.x >> 6) & 3, kh = KH > 1 ? uniform(threadIdx.x >> 8) : 0;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
   const uint32_t block = (uint32_t)block_xz(), id = SPLIT ? block / (uint32_t)part.n : block;
   const int sp = SPLIT ? (int)(block - id * (uint32_t)part.n) : 0;
   if (id >= (uint32_t)pairs * (uint32_t)tiles) return;
@@ -84,7 +87,7 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
   const bool some = mine.lo < mine.hi;
   const Reach reach = reach_of(live, mine.lo, mine.hi);
   const int lo = reach.lo, hi = reach.hi, all_lo = reach.all_lo, all_hi = reach.all_hi;
-  const Range all = reach_of_all<4>(lds, reach, wave);
+  const Range all = reach_of_all<4>(lds, reach, wave);   // both halves write the same
   int j0 = all.lo, j1 = all.hi;
   if (SPLIT && j0 < j1) {
     const int per = ((j1 - j0 + kKeys - 1) / kKeys + part.n - 1) / part.n;
@@ -103,15 +106,17 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 
   v16f o[T::kBlocks] = {};
   float m = -INFINITY, l = 0.0f;   // m: of the products, before scale
-  if (j0 < j1) {
-    lk.load(lds, wave, j0);
-    lv.load(lds + kStage / 2, wave, j0);
+  constexpr int kStep = KH * kKeys;   // the halves take every other tile
+  uint8_t* const own[2] = {lds + kh * kStage, lds1 + kh * kStage};
+  if (j0 + kh * kKeys < j1) {
+    lk.load(own[0], wave, j0 + kh * kKeys);
+    lv.load(own[0] + kStage / 2, wave, j0 + kh * kKeys);
   }
   auto tile = [&](int j, const uint8_t* at, uint8_t* next) __attribute__((always_inline)) {
     tile_landed();
-    if (j + kKeys < j1) {
-      lk.load(next, wave, j + kKeys);
-      lv.load(next + kStage / 2, wave, j + kKeys);
+    if (j + kStep < j1) {
+      lk.load(next, wave, j + kStep);
+      lv.load(next + kStage / 2, wave, j + kStep);
     }
     const int last = SPLIT ? min(hi, j1) : hi;
     if (j >= last || j + kKeys <= lo) return;
@@ -156,11 +161,41 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
                                   o[db] = mfma(f, p, o[db]);
                                 });
   };
-  for (int j = j0; j < j1; j += 2 * kKeys) {
-    tile(j, lds, lds1);
-    if (j + kKeys < j1) tile(j + kKeys, lds1, lds);
+  for (int j = j0; j < j1; j += 2 * kStep) {
+    tile(j + kh * kKeys, own[0], own[1]);
+    if (j + kStep < j1) tile(j + kStep + kh * kKeys, own[1], own[0]);
   }
   l = pair_sum(l);
+  if constexpr (KH > 1) {   // the second half's sums to the first
+    float* to = reinterpret_cast<float*>(lds + wave * (kStage / 2)) + lane * 4;
+    float2* stat = reinterpret_cast<float2*>(lds1) + wave * 64 + lane;
+    __syncthreads();
+    if (kh == 1) {
+#pragma unroll
+      for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<v4f*>(to + (db * 4 + i) * 256) =
+              v4f{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+      *stat = float2{m, l};
+    }
+    __syncthreads();
+    if (kh == 1) return;
+    const float2 other = *stat;
+    const float top = fmaxf(m, other.x);
+    const float f0 = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.scale2);
+    const float f1 = other.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((other.x - top) * a.scale2);
+    m = top;
+    l = l * f0 + other.y * f1;
+#pragma unroll
+    for (int db = 0; db < T::kBlocks; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const v4f y = *reinterpret_cast<const v4f*>(to + (db * 4 + i) * 256);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[db][4 * i + e] = o[db][4 * i + e] * f0 + y[e] * f1;
+      }
+  }
 
   // A value that is not finite may come from a key that a row does not see, multiplied by 0:
   // such rows are formed again, one by one.
@@ -208,17 +243,47 @@ __global__ __launch_bounds__(256, 2) void k_attn(Args a, int pairs, int tiles, P
 #endif
 }
 
-// The parts of each row joined.  `waves` waves a row (1 or 4): each takes every waves-th part,
-// in order, two columns a lane; 4 are added in order in LDS.
-template <int WAVES>
-__global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part part) {
-  __shared__ float sums[WAVES][128];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, first = WAVES == 1 ? 0 : wave;
-  const uint32_t r = (uint32_t)block_xz() * (4 / WAVES) + (WAVES == 1 ? wave : 0);
+// The parts of each row joined, in order.  Few parts: 32 lanes a row, four columns a lane
+// (16 lanes up to 64 columns).
+template <int LANES>
+__global__ __launch_bounds__(256) void k_attn_join_few(Args a, uint32_t rows, Part part) {
+  const int in_row = threadIdx.x & (LANES - 1);
+  const uint32_t r = (uint32_t)block_xz() * (256 / LANES) + threadIdx.x / LANES;
   if (r >= rows) return;
   const uint32_t in_pair = (uint32_t)a.Tq * a.G, pair = r / in_pair, rr = r - pair * in_pair;
   const int b = pair / a.Hkv, t = rr / a.G, h = (pair - b * a.Hkv) * a.G + (rr - t * a.G);
-  // the parts' maxima and sums, up to 64 at a time
+  float m = -INFINITY;
+  for (int i = 0; i < part.n; ++i) m = fmaxf(m, part.ml[2 * ((int64_t)i * rows + r)]);
+  const bool live = 4 * in_row < a.D;
+  float l = 0.0f;
+  v4f x{};
+#pragma unroll 4
+  for (int i = 0; i < part.n; ++i) {
+    const int64_t at = (int64_t)i * rows + r;
+    const float2 ml = *reinterpret_cast<const float2*>(part.ml + 2 * at);
+    const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m);
+    l += ml.y * f;
+    if (live) x += *reinterpret_cast<const v4f*>(part.o + at * a.D + 4 * in_row) * f;
+  }
+  const Range k = keys_of(a, t);
+  const bool some = k.lo < k.hi;
+  const float f = some ? 1.0f / l : 0.0f;
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  if (live)
+    *reinterpret_cast<v4bf*>(row_of_out(a.out, b, t, h) + 4 * in_row) = __builtin_convertvector(x * f, v4bf);
+  if (in_row == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// Many parts, a workgroup a row: each of the 4 waves takes every fourth part, two columns a
+// lane; the waves' sums are added in LDS.
+__global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part part) {
+  __shared__ float2 sums[4][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t r = (uint32_t)block_xz();
+  if (r >= rows) return;
+  const uint32_t in_pair = (uint32_t)a.Tq * a.G, pair = r / in_pair, rr = r - pair * in_pair;
+  const int b = pair / a.Hkv, t = rr / a.G, h = (pair - b * a.Hkv) * a.G + (rr - t * a.G);
+  // the parts' maxima and sums, 64 at a time
   float m = -INFINITY;
   for (int i = lane; i < part.n; i += 64) m = fmaxf(m, part.ml[2 * ((int64_t)i * rows + r)]);
   m = wave_max(m);
@@ -228,31 +293,28 @@ __global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part p
     l += ml[0] == -INFINITY ? 0.0f : ml[1] * __builtin_amdgcn_exp2f(ml[0] - m);
   }
   l = wave_sum(l);
-  float x0 = 0.0f, x1 = 0.0f;
-  const bool lo = 2 * lane < a.D;   // D is even
+  float2 sum{0.0f, 0.0f};
+  const bool live = 2 * lane < a.D;
 #pragma unroll 8
-  for (int i = first; i < part.n; i += WAVES) {
+  for (int i = wave; i < part.n; i += 4) {
     const int64_t at = (int64_t)i * rows + r;
     const float mi = part.ml[2 * at];
     const float f = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
-    const float2 x = lo ? *reinterpret_cast<const float2*>(part.o + at * a.D + 2 * lane) : float2{0.0f, 0.0f};
-    x0 += x.x * f;
-    x1 += x.y * f;
+    const float2 x = live ? *reinterpret_cast<const float2*>(part.o + at * a.D + 2 * lane) : float2{0.0f, 0.0f};
+    sum.x += x.x * f;
+    sum.y += x.y * f;
   }
-  if (WAVES > 1) {
-    sums[wave][2 * lane] = x0;
-    sums[wave][2 * lane + 1] = x1;
-    __syncthreads();
-    if (wave > 0) return;
-    for (int w = 1; w < WAVES; ++w) x0 += sums[w][2 * lane], x1 += sums[w][2 * lane + 1];
-  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave > 0) return;
+  for (int w = 1; w < 4; ++w) sum.x += sums[w][lane].x, sum.y += sums[w][lane].y;
   const Range k = keys_of(a, t);
   const bool some = k.lo < k.hi;
   const float f = some ? 1.0f / l : 0.0f;
-  if (lo) {
+  if (live) {
     bf16_t* o = row_of_out(a.out, b, t, h) + 2 * lane;
-    store1(o, x0 * f);
-    store1(o + 1, x1 * f);
+    store1(o, sum.x * f);
+    store1(o + 1, sum.y * f);
   }
   if (lane == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
@@ -541,14 +603,25 @@ using namespace attn;
 
 namespace {
 
-// Workgroups that share a row's keys: while the tiles of queries leave most of the
-// chip idle, parts of at least 128 keys.
+// Keys of a sequence, on average.
+int64_t keys_in(const nvfp4_attn& a) { return a.cu_q == nullptr || a.batch < 2 ? a.Tk : a.Tk / a.batch; }
+
+// Workgroups that share a row's keys, at most 512 in all and parts of at least 128 keys.  A part
+// costs its sums' way through memory (4.5 TB/s there and back) and the join a launch; the key
+// tiles one after the other take 0.8 us each.  The n with the least sum of both.
 int parts_of(const nvfp4_attn& a) {
   const int64_t G = a.Hq / a.Hkv, tiles = (a.Tq * G + kRowsWG - 1) / kRowsWG * sequences(a) * a.Hkv;
   if (tiles == 0 || tiles >= kPartTiles) return 1;
-  const int64_t keys = a.Tk / kPartKeys, want = kPartTiles / tiles;
-  const int64_t n = keys < want ? keys : want;
-  return n < 1 ? 1 : (int)n;
+  const int64_t keys = keys_in(a);
+  const int64_t most = keys / kPartKeys < kPartTiles / tiles ? keys / kPartKeys : kPartTiles / tiles;
+  const double chain = (double)keys / kKeys * 0.8, part = (double)sequences(a) * a.Tq * a.Hq * a.D * 8 / 4.5e6;
+  int best = 1;
+  double least = chain;
+  for (int64_t n = 2; n <= most; ++n) {
+    const double t = chain / n + 8.0 + 1.3 * n * part;
+    if (t < least) least = t, best = (int)n;
+  }
+  return best;
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -570,23 +643,29 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
   const int tiles = (int)(((int64_t)a.Tq * a.G + kRowsWG - 1) / kRowsWG);
   Part part{nullptr, nullptr, parts_of(c.a)};
   const int64_t n = (int64_t)pairs * tiles;
-  if (part.n == 1) {
-    if (a.D <= 64)
-      k_attn<64, false><<<grid_xz(n), 256, 0, s>>>(a, pairs, tiles, part);
-    else
-      k_attn<128, false><<<grid_xz(n), 256, 0, s>>>(a, pairs, tiles, part);
-    return hipGetLastError();
+  // Eight waves a workgroup where there is at most one for each compute unit and its keys
+  // are many tiles (188 of 24 tiles of width 64: 30 -> 26 us; 128 of 32 of width 128: 47 -> 41; 96
+  // of 5: 17 -> 18; 512 of 64: 45 -> 57).
+  const bool halves = part.n == 1 && n <= num_cus() && keys_in(c.a) >= 8 * kKeys;
+  if (part.n > 1) {
+    part.o = static_cast<float*>(c.ws);
+    part.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * part.n * a.D * 4));
   }
-  part.o = static_cast<float*>(c.ws);
-  part.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * part.n * a.D * 4));
+  const dim3 grid = grid_xz(n * part.n), block(halves ? 512 : 256);
+  auto launch = [&](auto one, auto two) { (halves ? two : one)<<<grid, block, 0, s>>>(a, pairs, tiles, part); };
   if (a.D <= 64)
-    k_attn<64, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
+    part.n == 1 ? launch(k_attn<64, 1, false>, k_attn<64, 2, false>)
+                : launch(k_attn<64, 1, true>, k_attn<64, 2, true>);
   else
-    k_attn<128, true><<<grid_xz(n * part.n), 256, 0, s>>>(a, pairs, tiles, part);
-  if (part.n >= 8)
-    k_attn_join<4><<<grid_xz(rows), 256, 0, s>>>(a, (uint32_t)rows, part);
+    part.n == 1 ? launch(k_attn<128, 1, false>, k_attn<128, 2, false>)
+                : launch(k_attn<128, 1, true>, k_attn<128, 2, true>);
+  if (part.n == 1) return hipGetLastError();
+  if (part.n > 8)
+    k_attn_join<<<grid_xz(rows), 256, 0, s>>>(a, (uint32_t)rows, part);
+  else if (a.D <= 64)
+    k_attn_join_few<16><<<grid_xz((rows + 15) / 16), 256, 0, s>>>(a, (uint32_t)rows, part);
   else
-    k_attn_join<1><<<grid_xz((rows + 3) / 4), 256, 0, s>>>(a, (uint32_t)rows, part);
+    k_attn_join_few<32><<<grid_xz((rows + 7) / 8), 256, 0, s>>>(a, (uint32_t)rows, part);
   return hipGetLastError();
 }
 

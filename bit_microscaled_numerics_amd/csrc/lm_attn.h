@@ -142,6 +142,11 @@ struct RowSum {   // columns lane and lane + 64
     if (lane < D) store1(row + lane, x0 * f);
     if (lane + 64 < D) store1(row + lane + 64, x1 * f);
   }
+  __device__ __forceinline__ void store(float* row, int D) const {
+    const int lane = threadIdx.x & 63;
+    if (lane < D) row[lane] = x0;
+    if (lane + 64 < D) row[lane + 64] = x1;
+  }
 };
 
 struct Soft {   // scores in log2: the running maximum, the sum relative to it
@@ -442,6 +447,19 @@ __device__ __forceinline__ void store_columns(bf16_t* row, const v16f (&o)[BLOCK
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = o[db][4 * i + e] * f;
       *reinterpret_cast<v4bf*>(row + d) = __builtin_convertvector(x, v4bf);
+    }
+}
+
+// The same as FP32.
+template <int BLOCKS>
+__device__ __forceinline__ void store_sums(float* row, const v16f (&o)[BLOCKS], int D, int half) {
+#pragma unroll
+  for (int db = 0; db < BLOCKS; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = db * 32 + 8 * i + 4 * half;
+      if (d < D)
+        *reinterpret_cast<v4f*>(row + d) = v4f{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
     }
 }
 

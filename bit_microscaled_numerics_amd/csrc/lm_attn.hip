@@ -204,15 +204,7 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   const int64_t at = SPLIT ? (int64_t)sp * pairs * rows + job.pair * rows + r : 0;
   if (live) {
     if (SPLIT) {
-#pragma unroll
-      for (int db = 0; db < T::kBlocks; ++db)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = db * 32 + 8 * i + 4 * half;
-          if (d < a.D)
-            *reinterpret_cast<v4f*>(part.o + at * a.D + d) =
-                v4f{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
-        }
+      store_sums(part.o + at * a.D, o, a.D, half);
     } else {
       store_columns(row_of_out(a.out, b, t, h), o, some ? 1.0f / l : 0.0f, a.D, half);
     }
@@ -231,8 +223,7 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
     const int64_t at1 = at - (lane & 31) + from;
     const Soft x = row_forward(a, b, tt, hh, SPLIT ? max(lo1, j0) : lo1, SPLIT ? min(hi1, j1) : hi1);
     if (SPLIT) {
-      if (lane < a.D) part.o[at1 * a.D + lane] = x.o.x0;
-      if (lane + 64 < a.D) part.o[at1 * a.D + lane + 64] = x.o.x1;
+      x.o.store(part.o + at1 * a.D, a.D);
       if (lane == 0) part.ml[2 * at1] = x.m, part.ml[2 * at1 + 1] = x.l;
     } else {
       x.o.store(row_of_out(a.out, b, tt, hh), a.D, lo1 < hi1 ? 1.0f / x.l : 0.0f);
@@ -356,8 +347,10 @@ struct GradLds {   // one array per stage: loads into the next are not waited fo
 // dV^T = dO^T P and dK^T = Q^T dS.  The rows pass from the last one down: the last
 // rows of a causal sequence see all keys, so the workgroups of a key head start on the same
 // rows and find them in their XCD's L2.
-template <int DP>
-__device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds, Job job) {
+// parts > 1: each takes a piece of the rows and leaves FP32 sums, which k_attn_join_keys adds up.
+template <int DP, bool PARTS>
+__device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds, Job job, int part, int parts,
+                                          float* sums, int64_t all_keys) {
   using T = Tile<DP, 64>;
   constexpr int kHalf = T::kBytes;   // of a stage: q, then dout
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
@@ -369,7 +362,12 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   const Range seen = queries_of(a, j);
   const int rlo = seen.lo * a.G, rhi = seen.hi * a.G;
   const Reach reach = reach_of(live, rlo, rhi);
-  const Range all = reach_of_all<8>(lds.s0, reach, wave);
+  Range all = reach_of_all<8>(lds.s0, reach, wave);
+  if (PARTS) {
+    const int per = ((all.hi - all.lo + 63) / 64 + parts - 1) / parts * 64;
+    const int64_t from = all.lo + (int64_t)part * per;
+    all = Range{(int)min(from, (int64_t)all.hi), (int)min(from + per, (int64_t)all.hi)};
+  }
 
   v8bf k[T::kSteps];
   row_frags<DP>(k, row_of(a.k, b, live ? j : 0, hk), live, a.D, half);
@@ -401,7 +399,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     tile_landed();
     if (r > all.lo) load(next, st ^ 1, r - 64);
     const int r0 = r + rg * 32;
-    if (r0 >= reach.hi || r0 + 32 <= reach.lo) return;
+    if (r0 >= min(reach.hi, all.hi) || r0 + 32 <= reach.lo) return;
     const uint8_t* td = now + kHalf;
     v16f s{}, dp{};
     struct Two {
@@ -427,8 +425,8 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
         dp[v] = s[v] * (dp[v] - x[e >> 1][2 * (e & 1) + 1]);
       }
     }
-    if (r0 < reach.all_lo || r0 + 32 > reach.all_hi) {
-      const uint32_t first = (uint32_t)(r0 + 4 * half - rlo), n = (uint32_t)max(rhi - rlo, 0);
+    if (r0 < reach.all_lo || r0 + 32 > min(reach.all_hi, all.hi)) {
+      const uint32_t first = (uint32_t)(r0 + 4 * half - rlo), n = (uint32_t)max(min(rhi, all.hi) - rlo, 0);
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         if (first + acc_row(v) >= n) s[v] = dp[v] = 0.0f;
@@ -455,7 +453,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     }
   }
   // the halves' sums
-  uint8_t* part = (kg < 2 ? lds.s0 : lds.s1) + (kg & 1) * 64 * DP * 2 + lane * 16;
+  uint8_t* other = (kg < 2 ? lds.s0 : lds.s1) + (kg & 1) * 64 * DP * 2 + lane * 16;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     v16f(&sum)[T::kBlocks] = x ? dv : dk;
@@ -465,7 +463,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (rg == 1)
-          *reinterpret_cast<v4f*>(part + (db * 4 + i) * 1024) =
+          *reinterpret_cast<v4f*>(other + (db * 4 + i) * 1024) =
               v4f{sum[db][4 * i], sum[db][4 * i + 1], sum[db][4 * i + 2], sum[db][4 * i + 3]};
     __syncthreads();
     if (rg == 1) continue;
@@ -473,7 +471,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     for (int db = 0; db < T::kBlocks; ++db)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const v4f y = *reinterpret_cast<const v4f*>(part + (db * 4 + i) * 1024);
+        const v4f y = *reinterpret_cast<const v4f*>(other + (db * 4 + i) * 1024);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[db][4 * i + e] += y[e];
       }
@@ -481,14 +479,24 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   if (rg == 1) return;
   const float odd = odd_of(dk) + odd_of(dv);
   uint64_t again = __ballot(live && odd != 0.0f);
-  if (live) {
+  float* to = PARTS ? sums + (((int64_t)part * all_keys + (int64_t)job.pair * a.Tk + key) * 2) * a.D : nullptr;
+  if (live && !PARTS) {
     store_columns(row_of_out(a.dk, b, j, hk), dk, a.scale, a.D, half);
     store_columns(row_of_out(a.dv, b, j, hk), dv, 1.0f, a.D, half);
+  } else if (live) {
+    store_sums(to, dk, a.D, half);
+    store_sums(to + a.D, dv, a.D, half);
   }
   for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
-    const int from = __builtin_ctzll(again), jj = __shfl(j, from);
+    const int from = __builtin_ctzll(again), jj = __shfl(j, from), lo = __shfl(rlo, from), hi = __shfl(rhi, from);
     RowSum xk, xv;
-    row_dkv(a, b, jj, hk, __shfl(rlo, from), __shfl(rhi, from), xk, xv);
+    row_dkv(a, b, jj, hk, PARTS ? max(lo, all.lo) : lo, PARTS ? min(hi, all.hi) : hi, xk, xv);
+    if (PARTS) {
+      float* row = to + 2 * (int64_t)(from - (lane & 31)) * a.D;
+      xk.store(row, a.D);
+      xv.store(row + a.D, a.D);
+      continue;
+    }
     xk.store(row_of_out(a.dk, b, jj, hk), a.D, a.scale);
     xv.store(row_of_out(a.dv, b, jj, hk), a.D, 1.0f);
   }
@@ -580,18 +588,44 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
 
 // One launch for both halves of the gradient: the keys' workgroups, which are few and
 // long, come first, the queries' fill what they leave.
-template <int DP>
-__global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles) {
+template <int DP, bool PARTS>
+__global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles, int parts,
+                                                      float* sums) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kRow = DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t s0[128 * kRow], s1[128 * kRow], v[128 * kRow], stats[1024];
   const GradLds<DP> lds{s0, s1, v, stats};
-  const uint32_t id = (uint32_t)block_xz(), keys = (uint32_t)pairs * (uint32_t)key_tiles;
-  if (id < keys)
-    grad_keys<DP>(a, lds, job_of(id, pairs, key_tiles));
-  else if (id - keys < (uint32_t)pairs * (uint32_t)row_tiles)
+  const uint32_t id = (uint32_t)block_xz(), tiles = (uint32_t)pairs * (uint32_t)key_tiles;
+  const uint32_t keys = PARTS ? tiles * (uint32_t)parts : tiles;
+  if (id < keys) {
+    const uint32_t part = PARTS ? id / tiles : 0;
+    grad_keys<DP, PARTS>(a, lds, job_of(id - part * tiles, pairs, key_tiles), (int)part, parts, sums,
+                         (int64_t)pairs * a.Tk);
+  } else if (id - keys < (uint32_t)pairs * (uint32_t)row_tiles) {
     grad_queries<DP>(a, lds, job_of(id - keys, pairs, row_tiles), row_tiles);
+  }
 #endif
+}
+
+// dk and dv of each key from the parts' sums, in order: 32 lanes a key (16 up to 64 columns), four
+// columns a lane.
+template <int LANES>
+__global__ __launch_bounds__(256) void k_attn_join_keys(Args a, uint32_t keys, int parts, const float* sums) {
+  const uint32_t r = (uint32_t)block_xz() * (256 / LANES) + threadIdx.x / LANES;
+  const int d = 4 * (threadIdx.x & (LANES - 1));
+  if (r >= keys || d >= a.D) return;
+  v4f dk{}, dv{};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float* at = sums + ((int64_t)i * keys + r) * 2 * a.D + d;
+    dk += *reinterpret_cast<const v4f*>(at);
+    dv += *reinterpret_cast<const v4f*>(at + a.D);
+  }
+  const uint32_t pair = r / a.Tk;
+  const int j = (int)(r - pair * a.Tk), b = pair / a.Hkv, hk = pair - b * a.Hkv;
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<v4bf*>(row_of_out(a.dk, b, j, hk) + d) = __builtin_convertvector(dk * a.scale, v4bf);
+  *reinterpret_cast<v4bf*>(row_of_out(a.dv, b, j, hk) + d) = __builtin_convertvector(dv, v4bf);
 }
 
 int64_t sequences(const nvfp4_attn& a) { return a.cu_q == nullptr ? a.batch : 1; }
@@ -624,13 +658,34 @@ int parts_of(const nvfp4_attn& a) {
   return best;
 }
 
+// Workgroups that share a key tile's query rows in the gradient, by the same rule: 1.1 us a step
+// of 64 rows, and at most 256 in all, one for each compute unit (2048 queries of 40 heads over 8
+// key heads, 128 tiles: 275 us whole, 215 in two parts, 238 in four; 4096: 628 and 682).
+int key_parts_of(const nvfp4_attn& a) {
+  const int64_t tiles = (a.Tk + 127) / 128 * sequences(a) * a.Hkv;
+  if (tiles == 0) return 1;
+  const int64_t queries = a.cu_q == nullptr || a.batch < 2 ? a.Tq : a.Tq / a.batch, steps = queries * (a.Hq / a.Hkv) / 64;
+  const int64_t most = steps / 4 < 256 / tiles ? steps / 4 : 256 / tiles;
+  const double chain = steps * 1.1, part = (double)sequences(a) * a.Tk * a.Hkv * a.D * 16 / 4.5e6;
+  int best = 1;
+  double least = chain;
+  for (int64_t n = 2; n <= most; ++n) {
+    const double t = chain / n + 8.0 + 1.3 * n * part;
+    if (t < least) least = t, best = (int)n;
+  }
+  return best;
+}
+
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
 int64_t attn_workspace_bytes(const nvfp4_attn& a, bool grad) {
   const int64_t rows = sequences(a) * a.Tq * a.Hq;
-  if (grad) return rows * 8;
+  if (grad) {
+    const int parts = key_parts_of(a);
+    return parts > 1 ? up256(rows * 8) + sequences(a) * a.Tk * a.Hkv * a.D * 8 * parts : rows * 8;
+  }
   const int n = parts_of(a);
   return n > 1 ? up256(rows * n * a.D * 4) + rows * n * 8 : 0;
 }
@@ -675,13 +730,23 @@ hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
   const int pairs = (int)(sequences(c.a) * a.Hkv);
   const int row_tiles = (int)(((int64_t)a.Tq * a.G + kGradRows - 1) / kGradRows);
   const int key_tiles = (int)(((int64_t)a.Tk + 127) / 128);
-  const int64_t n = (int64_t)pairs * row_tiles + (int64_t)pairs * key_tiles;
+  const int parts = key_parts_of(c.a);
+  const int64_t n = (int64_t)pairs * row_tiles + (int64_t)pairs * key_tiles * parts;
   if (n == 0) return hipSuccess;
   if (rows > 0) k_attn_stats<<<grid_xz((rows + 31) / 32), 256, 0, s>>>(a, rows);
+  float* sums = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * 8)) : nullptr;
+  const dim3 grid = grid_xz(n);
+  auto launch = [&](auto k) { k<<<grid, 512, 0, s>>>(a, pairs, key_tiles, row_tiles, parts, sums); };
+  if (parts == 1) {
+    a.D <= 64 ? launch(k_attn_grad<64, false>) : launch(k_attn_grad<128, false>);
+    return hipGetLastError();
+  }
+  a.D <= 64 ? launch(k_attn_grad<64, true>) : launch(k_attn_grad<128, true>);
+  const uint32_t keys = (uint32_t)((int64_t)pairs * a.Tk);
   if (a.D <= 64)
-    k_attn_grad<64><<<grid_xz(n), 512, 0, s>>>(a, pairs, key_tiles, row_tiles);
+    k_attn_join_keys<16><<<grid_xz((keys + 15) / 16), 256, 0, s>>>(a, keys, parts, sums);
   else
-    k_attn_grad<128><<<grid_xz(n), 512, 0, s>>>(a, pairs, key_tiles, row_tiles);
+    k_attn_join_keys<32><<<grid_xz((keys + 7) / 8), 256, 0, s>>>(a, keys, parts, sums);
   return hipGetLastError();
 }
 

@@ -1,11 +1,13 @@
-"""The ends of a language model's training step around its NVFP4 linear layers, as
-torch modules: the token embedding, the output head with its loss, and gradient
-clipping.  The recipe leaves them in BF16 ("Pretraining Large Language Models with
-NVFP4", summary page, recipe paragraph); every step runs in the library's HIP
-kernels, on the current stream.  There is no CPU path.
+"""A language model's training step around its NVFP4 linear layers, as torch modules:
+the token embedding, the output head with its loss, gradient clipping, and
+self-attention with the norms and rotation of its queries and keys.  The recipe leaves
+them in BF16 ("Pretraining Large Language Models with NVFP4", summary page, recipe
+paragraph); every step runs in the library's HIP kernels, on the current stream.  There
+is no CPU path.
 
   x = ScaledEmbedding(vocab, hidden, scale)(ids)           [.., hidden] BF16
-  ... NVFP4Linear layers, norms, attention ...
+  ... NVFP4Linear layers, norms ...
+  y = SelfAttention(heads, dim, kv_heads)(qkv)             [.., heads * dim] BF16
   loss = CrossEntropyHead(hidden, vocab)(x, targets)       mean over the targets
   loss.backward()
   norm = clip_grad_norm(model.parameters(), 1.0)
@@ -24,8 +26,10 @@ from typing import Iterable, Optional, Union
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (NVFP4_SUMSQ_WORDS, clip_grads, embed, embed_grad, grad_sumsq, linear_ce,
-               linear_ce_grad, scale_grads)
+from . import (NVFP4_SUMSQ_WORDS, attention_grad, clip_grads, embed, embed_grad, grad_sumsq,
+               linear_ce, linear_ce_grad, qk_norm_rope_grad, scale_grads)
+from . import attention as attention_forward
+from . import qk_norm_rope as qk_norm_rope_forward
 
 
 class EmbeddingFunction(torch.autograd.Function):
@@ -230,3 +234,178 @@ def clip_grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_
         return (torch.zeros(1, device="cuda") if partials is None
                 else partials.sum().sqrt().float().reshape(1))
     return clip_grads(grads, max_norm, partials=partials)
+
+
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """Heads of tokens as the norm and rotation take them: contiguous rows that do not
+    overlap; copied otherwise (expanded gradients, transposed rows)."""
+    sizes = sorted((st, n) for st, n in zip(x.stride()[:-1], x.shape[:-1]) if n > 1)
+    span, apart = x.shape[-1], x.stride(-1) == 1 or x.shape[-1] == 1
+    for st, n in sizes:
+        apart = apart and st >= span
+        span = st * (n - 1) + span
+    return x if apart or x.numel() == 0 else x.clone(memory_format=torch.contiguous_format)
+
+
+def _rows16(x: torch.Tensor) -> torch.Tensor:
+    """Heads of tokens as attention takes them: on 16 bytes besides."""
+    x = _rows(x)
+    if x.data_ptr() % 16 or any(n > 1 and st % 8 for st, n in zip(x.stride()[:-1], x.shape[:-1])):
+        return x.clone(memory_format=torch.contiguous_format)
+    return x
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """The functional ``qk_norm_rope`` on [tokens][heads][D], differentiable by q, k and
+    the weights."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.how = (eps, interleaved, norm)
+        return qk_norm_rope_forward(q, k, q_weight, k_weight, positions, inv_freq, *ctx.how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        grads = qk_norm_rope_grad(_rows(dq), _rows(dk), *ctx.saved_tensors, *ctx.how)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)),
+                None, None, None, None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, norm: bool = True):
+    """Norms and rotation of queries [.., heads, D] and keys [.., key heads, D]: each row
+    divided by its root mean square, times its side's weight, and rotated by its token's
+    position.  positions: integers that broadcast to the leading dimensions; inv_freq float32
+    [rot/2], pairs (j, j + rot/2) or, interleaved, (2j, 2j + 1) of each row."""
+    lead = q.shape[:-2]
+    if k.shape[:-2] != lead:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not match")
+    if positions is not None:
+        positions = positions.expand(lead).reshape(-1).contiguous()
+    flat = [_rows(x.reshape(lead.numel(), *x.shape[-2:])) for x in (q, k)]
+    a, b = QKNormRopeFunction.apply(*flat, q_weight, k_weight, positions, inv_freq, eps, interleaved,
+                                    norm)
+    return a.view(q.shape), b.view(k.shape)
+
+
+class AttentionFunction(torch.autograd.Function):
+    """(out, lse) of the functional ``attention``; out is differentiable by q, k and v.  The
+    backward pass forms the probabilities again from lse."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, scale, causal, window, cu_q, cu_k):
+        out, lse = attention_forward(q, k, v, scale, causal, window, cu_q, cu_k)
+        ctx.save_for_backward(q, k, v, out, lse, cu_q, cu_k)
+        ctx.how = (scale, causal, window)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, _):
+        *saved, cu_q, cu_k = ctx.saved_tensors
+        grads = attention_grad(_rows16(dout), *saved, *ctx.how, cu_q, cu_k)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)),
+                None, None, None, None, None)
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
+              causal: bool = False, window: int = 0, cu_q: Optional[torch.Tensor] = None,
+              cu_k: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Softmax attention, like q: [sequences, tokens, heads, D], or [tokens, heads, D] of one
+    sequence or, with cu_q, of several one after the other.  bf16; operands that do not lie on
+    16 bytes are copied.  See the functional form for the arguments."""
+    return AttentionFunction.apply(_rows16(q), _rows16(k), _rows16(v), scale, causal, window, cu_q,
+                                   cu_k)[0]
+
+
+class SelfAttentionFunction(torch.autograd.Function):
+    """Norm, rotation and attention of the rows [.., (heads + 2 * kv_heads) * D] of one
+    projection, whose gradient is formed in one buffer of its shape: attention's gradients are
+    written into its pieces, and the norm's and rotation's take them in place."""
+
+    @staticmethod
+    def forward(ctx, qkv, q_weight, k_weight, positions, inv_freq, how, cu):
+        heads, kv_heads, dim, eps, interleaved, norm, scale, causal, window = how
+        q, k, v = SelfAttentionFunction.pieces(qkv, heads, kv_heads, dim)
+        tokens = qkv.shape[:-1].numel()
+        qn, kn = qk_norm_rope_forward(q.reshape(tokens, heads, dim), k.reshape(tokens, kv_heads, dim),
+                                      q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+        qn, kn = qn.view(q.shape), kn.view(k.shape)
+        out, lse = attention_forward(qn, kn, v, scale, causal, window, cu)
+        ctx.save_for_backward(qkv, q_weight, k_weight, positions, inv_freq, qn, kn, out, lse, cu)
+        ctx.how = how
+        return out.view(*qkv.shape[:-1], heads * dim)
+
+    @staticmethod
+    def pieces(qkv, heads, kv_heads, dim):
+        """q, k and v in a projection's rows: views [.., heads, dim]."""
+        split = qkv.split((heads * dim, kv_heads * dim, kv_heads * dim), -1)
+        return [x.view(*x.shape[:-1], -1, dim) for x in split]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        heads, kv_heads, dim, eps, interleaved, norm, scale, causal, window = ctx.how
+        qkv, q_weight, k_weight, positions, inv_freq, qn, kn, out, lse, cu = ctx.saved_tensors
+        q, k, v = SelfAttentionFunction.pieces(qkv, heads, kv_heads, dim)
+        dqkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
+        dq, dk, dv = SelfAttentionFunction.pieces(dqkv, heads, kv_heads, dim)
+        attention_grad(_rows16(dout.reshape(out.shape)), qn, kn, v, out, lse, scale, causal, window, cu,
+                       grads=(dq, dk, dv))
+        tokens = qkv.shape[:-1].numel()
+        flat = [x.reshape(tokens, *x.shape[-2:]) for x in (dq, dk, q, k)]   # views of dqkv and qkv
+        _, _, dwq, dwk = qk_norm_rope_grad(*flat, q_weight, k_weight, positions, inv_freq, eps,
+                                           interleaved, norm, out=(flat[0], flat[1]))
+        return dqkv, dwq, dwk, None, None, None, None
+
+
+class SelfAttention(torch.nn.Module):
+    """Causal self-attention of a projection's rows [.., tokens, (heads + 2 * kv_heads) * dim]
+    (queries, keys, values), bf16, to [.., tokens, heads * dim]: norms of queries and keys
+    for each head (norm=False: none), rotation of the first `rot` of their dim values, softmax
+    attention over all earlier tokens or the last `window`."""
+
+    def __init__(self, heads: int, dim: int, kv_heads: Optional[int] = None, rot: Optional[int] = None,
+                 base: float = 10000.0, norm: bool = True, eps: float = 1e-6,
+                 interleaved: bool = False, causal: bool = True, window: int = 0, device=None):
+        super().__init__()
+        kv_heads = heads if kv_heads is None else kv_heads
+        rot = dim if rot is None else rot
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
+            raise ValueError(f"{heads} heads are no multiple of {kv_heads} key heads")
+        if dim % 8 or not 8 <= dim <= 128 or rot % 2 or not 0 <= rot <= dim:
+            raise ValueError("dim must be a multiple of 8 up to 128, rot even and at most dim")
+        self.how = (heads, kv_heads, dim, eps, interleaved, norm, dim ** -0.5, causal, window)
+        for name in ("q_weight", "k_weight"):
+            self.register_parameter(name, torch.nn.Parameter(
+                torch.ones(dim, dtype=torch.bfloat16, device=device)) if norm else None)
+        inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+        self.register_buffer("inv_freq", inv.float().to(device), persistent=False)
+
+    def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                cu: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """qkv [sequences, tokens, ..] or [tokens, ..]; cu (int32 or int64, on the GPU): where
+        the sequences of one row of tokens begin, and the end.  positions: of the tokens,
+        broadcast to qkv's leading dimensions (None: counted from each sequence's start)."""
+        heads, kv_heads, dim = self.how[:3]
+        if qkv.shape[-1] != (heads + 2 * kv_heads) * dim or qkv.dim() not in (2, 3):
+            raise ValueError(f"qkv must be [.., tokens, {(heads + 2 * kv_heads) * dim}]")
+        if cu is not None and qkv.dim() != 2:
+            raise ValueError("cu goes with qkv [tokens, ..]")
+        if positions is None:
+            positions = torch.arange(qkv.shape[-2], device=qkv.device)
+            if cu is not None:
+                at = torch.searchsorted(cu.long(), positions, right=True) - 1
+                positions = positions - cu.long()[at.clamp(min=0)]
+        positions = positions.expand(qkv.shape[:-1]).reshape(-1).contiguous()
+        inv = self.inv_freq if self.inv_freq.numel() else None
+        if qkv.stride(-1) != 1 or qkv.data_ptr() % 16 or any(
+                n > 1 and (st % 8 or st < qkv.shape[-1]) for st, n in zip(qkv.stride()[:-1], qkv.shape[:-1])):
+            qkv = qkv.contiguous() if not qkv.is_contiguous() else qkv.clone()
+        return SelfAttentionFunction.apply(qkv, self.q_weight, self.k_weight,
+                                           None if inv is None else positions, inv, self.how, cu)

@@ -872,44 +872,54 @@ def scale_grads(grads, factor: torch.Tensor):
 
 
 # ------------------------------------------------------- attention, and what feeds it
-def _heads(x: torch.Tensor, dims: int, dtype, name: str) -> bytes:
-    """The nvfp4_heads of a GPU tensor [tokens][heads][D], or [sequences] of them."""
-    if not x.is_cuda or x.dtype != dtype or x.dim() != dims:
+_pack_heads, _pack_rope, _pack_attn = (struct.Struct(f).pack for f in ("4q", "5q5if4q", "8qiiqf4x"))
+
+
+def _heads(x: torch.Tensor, dims: int, dtype, dev: int, name: str) -> bytes:
+    """The nvfp4_heads of a tensor [tokens][heads][D], or [sequences] of them, on device dev."""
+    if x.get_device() != dev or x.dtype != dtype or x.dim() != dims:
+        if x.is_cuda and x.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
         raise ValueError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
     st = x.stride()
     if st[-1] != 1 and x.shape[-1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return struct.pack("4q", x.data_ptr(), st[0] if dims == 4 else 0, st[-3], st[-2])
+    return _pack_heads(x.data_ptr(), st[0] if dims == 4 else 0, st[-3], st[-2])
 
 
-def _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm) -> bytes:
-    """The nvfp4_rope of a call whose q and k are checked by ``_heads``."""
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+def _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm):
+    """(the nvfp4_rope of a call, the device); q and k themselves are checked by ``_heads``."""
+    T, Hq, D = q.shape if q.dim() == 3 else (-1, 0, 0)
+    if k.dim() != 3 or T != k.shape[0] or D != k.shape[2]:
         raise ValueError("q and k must be [tokens][heads][D] of the same tokens and D")
-    T, D = q.shape[0], q.shape[2]
     kind = _FLOATS.get(q.dtype)
     if kind is None:
         raise ValueError("q and k must be bf16 or float32")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    dev = torch.cuda.current_device()
     wt, ids, rot = NVFP4_TYPE_F32, NVFP4_TYPE_I32, 0
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            continue
-        if not w.is_cuda or w.dtype not in _FLOATS or w.numel() != D or not w.is_contiguous():
-            raise ValueError(f"{name} must be {D} contiguous bf16 or float32 CUDA values")
-        wt = _FLOATS[w.dtype]
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one type")
+    wq = wk = at = inv = 0
+    if q_weight is not None or k_weight is not None:
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None and (w.get_device() != dev or w.dtype not in _FLOATS or w.numel() != D
+                                  or not w.is_contiguous()):
+                raise ValueError(f"{name} must be {D} contiguous bf16 or float32 values on the "
+                                 "current CUDA device")
+        wt = _FLOATS[(k_weight if q_weight is None else q_weight).dtype]
+        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError("q_weight and k_weight must have one type")
+        wq, wk = _p(q_weight) or 0, _p(k_weight) or 0
     if inv_freq is not None:
         ids, rot = _dev_ids(positions, "positions"), 2 * inv_freq.numel()
         if positions.numel() != T:
             raise ValueError("one position for each token")
         _dev_f32(inv_freq, inv_freq.numel(), "inv_freq")
-    elif positions is not None:
-        raise ValueError("positions go with inv_freq")
-    _one_device(q, k, q_weight, k_weight, positions, inv_freq)
-    return struct.pack("5q5if4q", T, q.shape[1], k.shape[1], D, rot, kind, wt, ids, int(interleaved),
-                       int(norm), eps, _p(q_weight) or 0, _p(k_weight) or 0, _p(positions) or 0,
-                       _p(inv_freq) or 0)
+        if positions.get_device() != dev or inv_freq.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
+        at, inv = positions.data_ptr(), inv_freq.data_ptr()
+    return _pack_rope(T, Hq, k.shape[1], D, rot, kind, wt, ids, int(interleaved), int(norm), eps, wq, wk,
+                      at, inv), dev
 
 
 def _like(x, shape, name):
@@ -919,14 +929,13 @@ def _like(x, shape, name):
 
 def nvfp4_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm, q_out,
                        k_out, stream=None):
-    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    r, dev = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
     _like(q_out, q.shape, "q_out")
     _like(k_out, k.shape, "k_out")
-    _one_device(q_out, k_out)
     dt = q.dtype
     _check(load_library().nvfp4_qk_norm_rope(
-        r, _heads(q, 3, dt, "q"), _heads(k, 3, dt, "k"), _heads(q_out, 3, dt, "q_out"),
-        _heads(k_out, 3, dt, "k_out"), _stream(stream)))
+        r, _heads(q, 3, dt, dev, "q"), _heads(k, 3, dt, dev, "k"), _heads(q_out, 3, dt, dev, "q_out"),
+        _heads(k_out, 3, dt, dev, "k_out"), _stream(stream)))
 
 
 def nvfp4_qk_norm_rope_grad_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -938,18 +947,18 @@ def nvfp4_qk_norm_rope_grad_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -
 
 def nvfp4_qk_norm_rope_grad(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
                             norm, dq_in, dk_in, dq_weight, dk_weight, workspace, stream=None):
-    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    r, dev = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
     for x, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dq_in, q, "dq_in"), (dk_in, k, "dk_in")):
         _like(x, like.shape, name)
     for x, w, name in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
         if x is not None and (w is None or x.dtype != w.dtype or x.numel() != w.numel()
                               or not x.is_contiguous()):
             raise ValueError(f"{name} must be contiguous, of its weight's size and type")
-    _one_device(dq, dk, dq_in, dk_in, dq_weight, dk_weight, workspace)
+    _one_device(dq_weight, dk_weight, workspace)
     dt = q.dtype
     _check(load_library().nvfp4_qk_norm_rope_grad(
-        r, _heads(dq, 3, dt, "dq"), _heads(dk, 3, dt, "dk"), _heads(q, 3, dt, "q"),
-        _heads(k, 3, dt, "k"), _heads(dq_in, 3, dt, "dq_in"), _heads(dk_in, 3, dt, "dk_in"),
+        r, _heads(dq, 3, dt, dev, "dq"), _heads(dk, 3, dt, dev, "dk"), _heads(q, 3, dt, dev, "q"),
+        _heads(k, 3, dt, dev, "k"), _heads(dq_in, 3, dt, dev, "dq_in"), _heads(dk_in, 3, dt, dev, "dk_in"),
         _p(dq_weight), _p(dk_weight), _p(workspace), _nbytes(workspace), _stream(stream)))
 
 
@@ -963,13 +972,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     of inv_freq (float32).  q [tokens][heads][D] and k [tokens][key heads][D], both bf16
     or float32, with strides (pieces of a projection's rows); the results are contiguous.
     Without inv_freq nothing is rotated; norm=False leaves the norm out."""
-    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
-    dt, dev = q.dtype, q.device
-    qo, ko = _empty(*q.shape, dtype=dt, device=dev), _empty(*k.shape, dtype=dt, device=dev)
+    r, dev = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    dt = q.dtype
+    hq, hk = _heads(q, 3, dt, dev, "q"), _heads(k, 3, dt, dev, "k")
+    (T, H, D), Hk = q.shape, k.shape[1]
+    qo, ko = _empty(T, H, D, dtype=dt, device=q.device), _empty(T, Hk, D, dtype=dt, device=q.device)
     # its own call of the entry point: a single token's rows are bound by the host
     _check(load_library().nvfp4_qk_norm_rope(
-        r, _heads(q, 3, dt, "q"), _heads(k, 3, dt, "k"), _heads(qo, 3, dt, "q"),
-        _heads(ko, 3, dt, "k"), _stream(None)))
+        r, hq, hk, _pack_heads(qo.data_ptr(), 0, H * D, D), _pack_heads(ko.data_ptr(), 0, Hk * D, D),
+        _raw_stream(dev)))
     return qo, ko
 
 
@@ -983,51 +994,55 @@ def qk_norm_rope_grad(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: to
     """(dq, dk, dq_weight, dk_weight): the gradient of ``qk_norm_rope`` from the gradients
     of its results and its own inputs; None for a weight that is not there.  out: the
     tensors that take the first two, such as pieces of a projection's gradient."""
-    r = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
-    dt, dev = q.dtype, q.device
-    _like(dq, q.shape, "dq")
-    _like(dk, k.shape, "dk")
+    r, dev = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
+    dt, place, (T, H, D), Hk = q.dtype, q.device, q.shape, k.shape[1]
+    h = (_heads(dq, 3, dt, dev, "dq"), _heads(dk, 3, dt, dev, "dk"), _heads(q, 3, dt, dev, "q"),
+         _heads(k, 3, dt, dev, "k"))
+    if dq.shape != q.shape or dk.shape != k.shape:
+        raise ValueError("dq and dk must be of the shapes of q and k")
     if out is None:
-        qi, ki = _empty(*q.shape, dtype=dt, device=dev), _empty(*k.shape, dtype=dt, device=dev)
+        qi, ki = _empty(T, H, D, dtype=dt, device=place), _empty(T, Hk, D, dtype=dt, device=place)
+        to = _pack_heads(qi.data_ptr(), 0, H * D, D), _pack_heads(ki.data_ptr(), 0, Hk * D, D)
     else:
         qi, ki = out
         _like(qi, q.shape, "out[0]")
         _like(ki, k.shape, "out[1]")
-    dwq, dwk = (None if w is None else _empty(w.numel(), dtype=w.dtype, device=dev).view(w.shape)
+        to = _heads(qi, 3, dt, dev, "out[0]"), _heads(ki, 3, dt, dev, "out[1]")
+    dwq, dwk = (None if w is None else _empty(*w.shape, dtype=w.dtype, device=place)
                 for w in (q_weight, k_weight))
-    _one_device(dq, dk, qi, ki)
-    n = nvfp4_qk_norm_rope_grad_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2])
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _check(load_library().nvfp4_qk_norm_rope_grad(
-        r, _heads(dq, 3, dt, "dq"), _heads(dk, 3, dt, "dk"), _heads(q, 3, dt, "q"),
-        _heads(k, 3, dt, "k"), _heads(qi, 3, dt, "out[0]"), _heads(ki, 3, dt, "out[1]"), _p(dwq),
-        _p(dwk), _p(ws), n, _stream(None)))
+    n = nvfp4_qk_norm_rope_grad_workspace_bytes(T, H, Hk, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=place) if n else None
+    _check(load_library().nvfp4_qk_norm_rope_grad(r, *h, *to, _p(dwq), _p(dwk), _p(ws), n,
+                                                  _raw_stream(dev)))
     return qi, ki, dwq, dwk
 
 
 def _attn(q, k, v, scale, causal, window, cu_q, cu_k):
-    """(the nvfp4_attn of a call, the operands' number of dimensions)."""
-    dims = 3 if cu_q is not None else q.dim()
-    if dims not in (3, 4) or q.dim() != dims or k.dim() != dims or v.shape != k.shape:
+    """(the nvfp4_attn of a call, the operands' number of dimensions, the device); q, k and v
+    themselves are checked by ``_heads``."""
+    dims, qs, ks = q.dim(), q.shape, k.shape
+    if (dims != 3 and (dims != 4 or cu_q is not None)) or len(ks) != dims or v.shape != ks:
         raise ValueError("q, k and v must be [tokens][heads][D], or without cu_q also "
                          "[sequences][tokens][heads][D], k and v of one shape")
-    if q.shape[-1] != k.shape[-1] or (dims == 4 and q.shape[0] != k.shape[0]):
+    D = qs[-1]
+    if D != ks[-1] or (dims == 4 and qs[0] != ks[0]):
         raise ValueError("q and k must have the same D and number of sequences")
-    batch, at, kind = (q.shape[0] if dims == 4 else 1), (0, 0), 0
-    if cu_q is not None:
+    if cu_k is not None and cu_q is None:
+        raise ValueError("cu_k goes with cu_q")
+    dev, batch, kind, at_q, at_k = torch.cuda.current_device(), 1, 0, 0, 0
+    if dims == 4:
+        batch = qs[0]
+    elif cu_q is not None:
         cu_k = cu_q if cu_k is None else cu_k
         kind = _dev_ids(cu_q, "cu_q")
         if _dev_ids(cu_k, "cu_k") != kind or cu_k.numel() != cu_q.numel() or cu_q.numel() < 1:
             raise ValueError("cu_q and cu_k must be of one type and of one length, sequences + 1")
-        batch, at = cu_q.numel() - 1, (cu_q.data_ptr(), cu_k.data_ptr())
-    elif cu_k is not None:
-        raise ValueError("cu_k goes with cu_q")
-    _one_device(q, k, v, cu_q, cu_k)
-    D = q.shape[-1]
+        _one_device(cu_q, cu_k)
+        batch, at_q, at_k = cu_q.numel() - 1, cu_q.data_ptr(), cu_k.data_ptr()
     if scale is None:
         scale = D ** -0.5 if D else 1.0
-    return struct.pack("8qiiqf4x", batch, q.shape[-3], k.shape[-3], q.shape[-2], k.shape[-2], D, *at,
-                       kind, int(causal), window, scale), dims
+    return _pack_attn(batch, qs[-3], ks[-3], qs[-2], ks[-2], D, at_q, at_k, kind, int(causal), window,
+                      scale), dims, dev
 
 
 def nvfp4_attention_workspace_bytes(a: bytes, grad: bool) -> int:
@@ -1038,27 +1053,32 @@ def nvfp4_attention_workspace_bytes(a: bytes, grad: bool) -> int:
 
 
 def nvfp4_attention(q, k, v, scale, causal, window, cu_q, cu_k, out, lse, workspace, stream=None):
-    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    a, dims, dev = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
     _like(out, q.shape, "out")
     _dev_f32(lse, q.shape[:-1].numel(), "lse")
-    _one_device(out, lse, workspace)
+    _one_device(lse, workspace)
     bf = torch.bfloat16
     _check(load_library().nvfp4_attention(
-        a, _heads(q, dims, bf, "q"), _heads(k, dims, bf, "k"), _heads(v, dims, bf, "v"),
-        _heads(out, dims, bf, "out"), _p(lse), _p(workspace), _nbytes(workspace), _stream(stream)))
+        a, _heads(q, dims, bf, dev, "q"), _heads(k, dims, bf, dev, "k"), _heads(v, dims, bf, dev, "v"),
+        _heads(out, dims, bf, dev, "out"), _p(lse), _p(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def nvfp4_attention_grad(dout, q, k, v, out, lse, scale, causal, window, cu_q, cu_k, dq, dk, dv,
                          workspace, stream=None):
-    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    a, dims, dev = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
     for x, like, name in ((dout, q, "dout"), (out, q, "out"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         _like(x, like.shape, name)
     _dev_f32(lse, q.shape[:-1].numel(), "lse")
-    _one_device(dout, out, lse, dq, dk, dv, workspace)
-    h = [_heads(x, dims, torch.bfloat16, name) for x, name in
+    _one_device(lse, workspace)
+    h = [_heads(x, dims, torch.bfloat16, dev, name) for x, name in
          ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
     _check(load_library().nvfp4_attention_grad(a, *h[:5], _p(lse), *h[5:], _p(workspace),
                                                _nbytes(workspace), _stream(stream)))
+
+
+def _whole(x: torch.Tensor, T: int, H: int, D: int) -> bytes:
+    """The nvfp4_heads of a contiguous tensor."""
+    return _pack_heads(x.data_ptr(), T * H * D, H * D, D)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
@@ -1072,16 +1092,16 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional
     are multiples of 8, D one up to 128.  scale: of the products (1/sqrt(D) if None).  causal: query
     i of nq sees keys up to i + nk - nq; window > 0: only the last `window` of those.  A
     query that sees no key has a row of zeros and an lse of -inf."""
-    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
-    bf, dev = torch.bfloat16, q.device
-    out = _empty(*q.shape, dtype=bf, device=dev)
-    lse = _empty(*q.shape[:-1], dtype=torch.float32, device=dev)
+    a, dims, dev = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    bf, place, shape = torch.bfloat16, q.device, q.shape
+    h = (_heads(q, dims, bf, dev, "q"), _heads(k, dims, bf, dev, "k"), _heads(v, dims, bf, dev, "v"))
+    out = _empty(*shape, dtype=bf, device=place)
+    lse = _empty(*shape[:-1], dtype=torch.float32, device=place)
     n = nvfp4_attention_workspace_bytes(a, False)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    ws = torch.empty(n, dtype=torch.uint8, device=place) if n else None
     # its own call of the entry point: a single token's attention is bound by the host
-    _check(load_library().nvfp4_attention(
-        a, _heads(q, dims, bf, "q"), _heads(k, dims, bf, "k"), _heads(v, dims, bf, "v"),
-        _heads(out, dims, bf, "out"), lse.data_ptr(), _p(ws), n, _stream(None)))
+    _check(load_library().nvfp4_attention(a, *h, _whole(out, *shape[-3:]), lse.data_ptr(), _p(ws), n,
+                                          _raw_stream(dev)))
     return out, lse
 
 
@@ -1091,22 +1111,28 @@ def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
                    cu_k: Optional[torch.Tensor] = None, grads: Optional[tuple] = None):
     """(dq, dk, dv): the gradient of ``attention`` from the gradient of its out, with the
     out and lse that it returned for the same arguments.  grads: the tensors that take them."""
-    a, dims = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
-    bf, dev = torch.bfloat16, q.device
+    a, dims, dev = _attn(q, k, v, scale, causal, window, cu_q, cu_k)
+    bf, place, qs, ks = torch.bfloat16, q.device, q.shape, k.shape
+    if dout.shape != qs or out.shape != qs:
+        raise ValueError("dout and out must be of the shape of q")
+    _dev_f32(lse, qs[:-1].numel(), "lse")
+    if lse.get_device() != dev:
+        raise ValueError("all tensors must be on the current CUDA device")
+    h = (_heads(dout, dims, bf, dev, "dout"), _heads(q, dims, bf, dev, "q"), _heads(k, dims, bf, dev, "k"),
+         _heads(v, dims, bf, dev, "v"), _heads(out, dims, bf, dev, "out"))
     if grads is None:
-        grads = tuple(_empty(*x.shape, dtype=bf, device=dev) for x in (q, k, v))
-    dq, dk, dv = grads
-    for x, like, name in ((dout, q, "dout"), (out, q, "out"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        _like(x, like.shape, name)
-    _dev_f32(lse, q.shape[:-1].numel(), "lse")
-    _one_device(dout, out, lse, dq, dk, dv)
-    h = [_heads(x, dims, bf, name) for x, name in
-         ((dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+        dq, dk, dv = grads = (_empty(*qs, dtype=bf, device=place), _empty(*ks, dtype=bf, device=place),
+                              _empty(*ks, dtype=bf, device=place))
+        to = _whole(dq, *qs[-3:]), _whole(dk, *ks[-3:]), _whole(dv, *ks[-3:])
+    else:
+        dq, dk, dv = grads = tuple(grads)
+        if dq.shape != qs or dk.shape != ks or dv.shape != ks:
+            raise ValueError("grads must be of the shapes of q, k and v")
+        to = [_heads(x, dims, bf, dev, "grads") for x in grads]
     n = nvfp4_attention_workspace_bytes(a, True)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _check(load_library().nvfp4_attention_grad(a, *h[:5], lse.data_ptr(), *h[5:], _p(ws), n,
-                                               _stream(None)))
-    return dq, dk, dv
+    ws = torch.empty(n, dtype=torch.uint8, device=place) if n else None
+    _check(load_library().nvfp4_attention_grad(a, *h, lse.data_ptr(), *to, _p(ws), n, _raw_stream(dev)))
+    return grads
 
 
 PROBE_ZEROS, PROBE_NVFP4_LIKE, PROBE_UNIFORM = 0, 1, 2

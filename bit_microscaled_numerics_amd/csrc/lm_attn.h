@@ -252,7 +252,7 @@ __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A tile of ROWS rows of DP values (64 or 128) in LDS: blocks of 32 columns, in each 64
+// A tile of ROWS rows of DP values (64, 96 or 128) in LDS: blocks of 32 columns, in each 64
 // bytes a row, whose 16-byte chunk c lies at c ^ ((row >> 2) & 3).  Both reads are free of bank
 // conflicts: the same chunk of 16 rows (fragments along d) and the transposing read, where 32
 // lanes take 64 bytes of 4 rows, cover 256 bytes each.  Two lane addresses serve all reads of a kind;
@@ -347,24 +347,23 @@ struct KeyLoader {
   }
 };
 
-// Loads ROWS consecutive rows of q and of dout into two tiles, WAVES waves together: the
-// rows of a group of heads are tokens and heads in turn.  Each call takes the rows before the
-// last call's.
+// Loads ROWS consecutive rows of q or of dout into a tile, WAVES waves together: the rows
+// of a group of heads are tokens and heads in turn.  Each call takes the rows before the last
+// call's.
 template <int DP, int ROWS, int WAVES>
 struct RowLoader {
   using S = Share<DP, ROWS, WAVES>;
-  const uint16_t* base[2];
-  int64_t ld[2];
-  uint32_t head[2];
+  const uint16_t* base;
+  int64_t ld;
+  uint32_t head;
   int step_t, step_g, G, end, t0, g0;   // t0, g0: token and head of the tile's first row
   int t, g, row, left;                  // the lane's
 
-  __device__ __forceinline__ void init(const Args& a, int b, int hk, int r0, int wave) {
+  __device__ __forceinline__ void init(const Rows& x, const Args& a, int b, int hk, int r0, int wave) {
     G = a.G;
-    base[0] = a.q.p + b * a.q.batch + (int64_t)hk * G * a.q.head;
-    base[1] = a.dout.p + b * a.dout.batch + (int64_t)hk * G * a.dout.head;
-    ld[0] = a.q.token, ld[1] = a.dout.token;
-    head[0] = (uint32_t)a.q.head * 2, head[1] = (uint32_t)a.dout.head * 2;
+    base = x.p + b * x.batch + (int64_t)hk * G * x.head;
+    ld = x.token;
+    head = (uint32_t)x.head * 2;
     step_t = ROWS / G, step_g = ROWS - step_t * G;
     end = a.Tq * G;
     t0 = r0 / G, g0 = r0 - t0 * G;
@@ -373,15 +372,10 @@ struct RowLoader {
     g = row - t * G;
     left = a.D - S::column(wave);
   }
-  // The rows at hand to LDS, q's first; then back by ROWS.
-  __device__ __forceinline__ void load(uint8_t* tiles, int wave) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t off =
-          (uint32_t)(t - t0) * (uint32_t)ld[x] * 2 + (uint32_t)g * head[x] + (uint32_t)S::column(wave) * 2;
-      S::load(descriptor(base[x] + (int64_t)t0 * ld[x]), tiles + x * ROWS * DP * 2, wave, row < end ? off : kDead,
-              left);
-    }
+  // The rows at hand to LDS; then back by ROWS.
+  __device__ __forceinline__ void load(uint8_t* tile, int wave) {
+    const uint32_t off = (uint32_t)(t - t0) * (uint32_t)ld * 2 + (uint32_t)g * head + (uint32_t)S::column(wave) * 2;
+    S::load(descriptor(base + (int64_t)t0 * ld), tile, wave, row < end ? off : kDead, left);
     row -= ROWS;
     t -= step_t;
     g -= step_g;

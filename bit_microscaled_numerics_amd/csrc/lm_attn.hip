@@ -385,9 +385,9 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   v16f dk[T::kBlocks] = {}, dv[T::kBlocks] = {};
   const int64_t all_rows = (int64_t)a.Tq * a.G;
   const float2* stats = a.stats + job.pair * all_rows;
-  RowLoader<DP, 64, 8> rows;
+  RowLoader<DP, 64, 4> rows;   // waves 0 .. 3 load q, the others dout
   auto load = [&](uint8_t* stage, int st, int r) __attribute__((always_inline)) {
-    rows.load(stage, wave);
+    rows.load(stage + rg * kHalf, kg);
     if (wave < 2) {   // the statistics of 32 rows
       const int r0 = r + wave * 32;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -445,7 +445,7 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   };
   if (all.lo < all.hi) {
     const int last = all.lo + (all.hi - 1 - all.lo) / 64 * 64;
-    rows.init(a, b, hk, last, wave);
+    rows.init(rg ? a.dout : a.q, a, b, hk, last, kg);
     load(lds.s0, 0, last);
     for (int r = last; r >= all.lo; r -= 128) {
       tile(r, lds.s0, lds.s1, 0);
@@ -522,19 +522,16 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   v8bf q[T::kSteps], g[T::kSteps];
   row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
   row_frags<DP>(g, row_of(a.dout, b, live ? t : 0, h), live, a.D, half);
-  KeyLoader<DP, kKeys, 8> lk, lv;
-  lk.init(a.k, b, hk, a.Tk, a.D, wave);
-  lv.init(a.v, b, hk, a.Tk, a.D, wave);
+  KeyLoader<DP, kKeys, 4> keys;   // waves 0 .. 3 load K, the others V
+  const int lw = wave & 3, second = wave >> 2;
+  keys.init(second ? a.v : a.k, b, hk, a.Tk, a.D, lw);
   T frag;
   frag.init(0);
 
   v16f dq[T::kBlocks] = {};
   auto tile = [&](int j, uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
     tile_landed();
-    if (j + kKeys < all.hi) {
-      lk.load(next, wave, j + kKeys);
-      lv.load(next + kHalf, wave, j + kKeys);
-    }
+    if (j + kKeys < all.hi) keys.load(next + second * kHalf, lw, j + kKeys);
     if (j >= reach.hi || j + kKeys <= reach.lo) return;
     const uint8_t* tv = now + kHalf;
     v16f s[2] = {}, dp[2] = {};
@@ -568,10 +565,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
                                   dq[db] = mfma(f, ds, dq[db]);
                                 });
   };
-  if (all.lo < all.hi) {
-    lk.load(lds.s0, wave, all.lo);
-    lv.load(lds.s0 + kHalf, wave, all.lo);
-  }
+  if (all.lo < all.hi) keys.load(lds.s0 + second * kHalf, lw, all.lo);
   for (int j = all.lo; j < all.hi; j += 2 * kKeys) {
     tile(j, lds.s0, lds.s1);
     if (j + kKeys < all.hi) tile(j + kKeys, lds.s1, lds.s0);
@@ -676,6 +670,17 @@ int key_parts_of(const nvfp4_attn& a) {
   return best;
 }
 
+// f(columns of the tiles): 64, 96 or 128.
+template <class F>
+void by_width(int D, F f) {
+  if (D <= 64)
+    f(std::integral_constant<int, 64>{});
+  else if (D <= 96)
+    f(std::integral_constant<int, 96>{});
+  else
+    f(std::integral_constant<int, 128>{});
+}
+
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -708,12 +713,11 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
   }
   const dim3 grid = grid_xz(n * part.n), block(halves ? 512 : 256);
   auto launch = [&](auto one, auto two) { (halves ? two : one)<<<grid, block, 0, s>>>(a, pairs, tiles, part); };
-  if (a.D <= 64)
-    part.n == 1 ? launch(k_attn<64, 1, false>, k_attn<64, 2, false>)
-                : launch(k_attn<64, 1, true>, k_attn<64, 2, true>);
-  else
-    part.n == 1 ? launch(k_attn<128, 1, false>, k_attn<128, 2, false>)
-                : launch(k_attn<128, 1, true>, k_attn<128, 2, true>);
+  auto width = [&](auto dp) {
+    constexpr int DP = decltype(dp)::value;
+    part.n == 1 ? launch(k_attn<DP, 1, false>, k_attn<DP, 2, false>) : launch(k_attn<DP, 1, true>, k_attn<DP, 1, true>);
+  };
+  by_width(a.D, width);
   if (part.n == 1) return hipGetLastError();
   if (part.n > 8)
     k_attn_join<<<grid_xz(rows), 256, 0, s>>>(a, (uint32_t)rows, part);
@@ -737,11 +741,11 @@ hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
   float* sums = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * 8)) : nullptr;
   const dim3 grid = grid_xz(n);
   auto launch = [&](auto k) { k<<<grid, 512, 0, s>>>(a, pairs, key_tiles, row_tiles, parts, sums); };
-  if (parts == 1) {
-    a.D <= 64 ? launch(k_attn_grad<64, false>) : launch(k_attn_grad<128, false>);
-    return hipGetLastError();
-  }
-  a.D <= 64 ? launch(k_attn_grad<64, true>) : launch(k_attn_grad<128, true>);
+  by_width(a.D, [&](auto dp) {
+    constexpr int DP = decltype(dp)::value;
+    parts == 1 ? launch(k_attn_grad<DP, false>) : launch(k_attn_grad<DP, true>);
+  });
+  if (parts == 1) return hipGetLastError();
   const uint32_t keys = (uint32_t)((int64_t)pairs * a.Tk);
   if (a.D <= 64)
     k_attn_join_keys<16><<<grid_xz((keys + 15) / 16), 256, 0, s>>>(a, keys, parts, sums);

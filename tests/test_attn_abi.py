@@ -141,8 +141,7 @@ def test_binding_refuses():
         nv.qk_norm_rope(x, x)   # not on a GPU
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         nv.attention(x, x, x)
-    for bad in (dict(positions=torch.zeros(4, dtype=torch.int64)), dict(q_weight=torch.ones(16)),
-                dict(inv_freq=torch.ones(8), positions=torch.zeros(4))):
+    for bad in (dict(positions=torch.zeros(4, dtype=torch.int64)), dict(inv_freq=torch.ones(8))):
         with pytest.raises(ValueError):
             nv.qk_norm_rope(x, x, **bad)
     with pytest.raises(ValueError):

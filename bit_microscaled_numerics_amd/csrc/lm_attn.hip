@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   // long rows of a causal sequence first
   const int64_t r = (int64_t)(tiles - 1 - job.tile) * kRowsWG + wave * 32 + (lane & 31);
   const bool live = r < rows;
-  const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
+  const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
   const Range mine = keys_of(a, t);
 
   const bool some = mine.lo < mine.hi;
@@ -315,9 +315,8 @@ __global__ __launch_bounds__(256) void k_attn_stats(Args a, int64_t rows) {
   const int64_t r = block_xz() * 32 + (threadIdx.x >> 3);
   const int in_row = threadIdx.x & 7;
   if (r >= rows) return;
-  const int64_t in_pair = (int64_t)a.Tq * a.G;
-  const int pair = (int)(r / in_pair), rr = (int)(r % in_pair);
-  const int b = pair / a.Hkv, t = rr / a.G, h = pair % a.Hkv * a.G + rr % a.G;
+  const uint32_t in_pair = (uint32_t)a.Tq * a.G, pair = (uint32_t)r / in_pair, rr = (uint32_t)r - pair * in_pair;
+  const int b = pair / a.Hkv, t = rr / a.G, h = (pair - b * a.Hkv) * a.G + (rr - t * a.G);
   const bf16_t* o = row_of(a.out, b, t, h);
   const bf16_t* d = row_of(a.dout, b, t, h);
   float s = 0.0f;
@@ -513,7 +512,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   const int64_t rows = (int64_t)a.Tq * a.G;
   const int64_t r = (int64_t)(tiles - 1 - job.tile) * kGradRows + wave * 32 + (lane & 31);
   const bool live = r < rows;
-  const int t = live ? (int)(r / a.G) : a.Tq, h = hk * a.G + (live ? (int)(r % a.G) : 0);
+  const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
   const Range mine = keys_of(a, t);
   const Reach reach = reach_of(live, mine.lo, mine.hi);
   const Range all = reach_of_all<8>(lds.s0, reach, wave);

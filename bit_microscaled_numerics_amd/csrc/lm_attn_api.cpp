@@ -174,6 +174,19 @@ int take_k_side(const nvfp4_attn* a, const nvfp4_heads* x, nvfp4_heads* to, cons
   return check_tile(to, a->Tk, 1, name);
 }
 
+// Results are written while operands are still read.
+int check_apart(const nvfp4_heads* results, int n, const nvfp4_heads* operands, int m) {
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < m; ++j)
+      if (results[i].p != nullptr && results[i].p == operands[j].p)
+        return fail(NVFP4_ERR_ARG, "a result may not be an operand (no attention in place)");
+    for (int j = 0; j < i; ++j)
+      if (results[i].p != nullptr && results[i].p == results[j].p)
+        return fail(NVFP4_ERR_ARG, "two results at one place");
+  }
+  return NVFP4_OK;
+}
+
 int check_lse(const nvfp4_attn* a, const float* lse) {
   const int64_t n = a->cu_q == nullptr ? a->batch : 1;
   if (n * a->Tq > 0 && lse == nullptr) return fail(NVFP4_ERR_NULL, "lse is NULL");
@@ -268,6 +281,8 @@ int nvfp4_attention(const nvfp4_attn* a, const nvfp4_heads* q, const nvfp4_heads
   if ((st = take_k_side(a, v, &c.v, "v"))) return st;
   if ((st = take_q_side(a, out, &c.out, "out"))) return st;
   if ((st = check_lse(a, lse))) return st;
+  const nvfp4_heads operands[] = {c.q, c.k, c.v};
+  if ((st = check_apart(&c.out, 1, operands, 3))) return st;
   if ((st = check_workspace(workspace, workspace_bytes, nvfp4::attn_workspace_bytes(*a, false),
                             "nvfp4_attention_workspace_bytes")))
     return st;
@@ -294,6 +309,8 @@ int nvfp4_attention_grad(const nvfp4_attn* a, const nvfp4_heads* dout, const nvf
   if ((st = take_q_side(a, dq, &c.dq, "dq"))) return st;
   if ((st = take_k_side(a, dk, &c.dk, "dk"))) return st;
   if ((st = take_k_side(a, dv, &c.dv, "dv"))) return st;
+  const nvfp4_heads operands[] = {c.q, c.k, c.v, c.out, c.dout}, results[] = {c.dq, c.dk, c.dv};
+  if ((st = check_apart(results, 3, operands, 5))) return st;
   if ((st = check_workspace(workspace, workspace_bytes, nvfp4::attn_workspace_bytes(*a, true),
                             "nvfp4_attention_workspace_bytes")))
     return st;

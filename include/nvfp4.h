@@ -476,14 +476,17 @@ int nvfp4_qk_norm_rope_grad(const nvfp4_rope* r, const nvfp4_heads* dq, const nv
  * results are zeros.  Values of cu that do not ascend or exceed Tq, Tk give unspecified
  * results, without an access outside the operands.
  * What a query does not see (infinities, NaN) does not reach its results, nor its
- * gradients those of the keys that it does not see.
- * q, k, v, out and gradients BF16, 16-byte aligned with strides that are multiples of 8;
+ * gradients those of the keys that it does not see.  Rows and keys whose results are not
+ * finite are formed one by one, at a hundredth of the speed.
+ * Results may not overlap operands or each other.
+ * q, k, v, out and gradients BF16, 16-byte aligned with strides that are multiples of 8 (token
+ * strides below 2^22, the heads of a group within 2^29 elements);
  * lse FP32 [batch][Tq][Hq] ([Tq][Hq] with cu_q).  Accumulation is FP32; the
  * probabilities (and in the gradient the scores' gradients) enter their products rounded to BF16. */
 typedef struct {
   int64_t batch, Tq, Tk;     /* 0 or more */
   int64_t Hq, Hkv;           /* Hq a multiple of Hkv */
-  int64_t D;                 /* a multiple of 8, 8 .. 128 */
+  int64_t D;                 /* a multiple of 8, 8 .. 128; columns are taken in 64, 96 or 128 */
   const void* cu_q;          /* NULL: sequences of one length */
   const void* cu_k;
   int32_t cu_type;           /* I32 or I64 */
@@ -493,8 +496,8 @@ typedef struct {
 } nvfp4_attn;
 
 /* workspace (also of the gradient): 256-byte aligned, of at least
- * nvfp4_attention_workspace_bytes(a, grad) bytes, which depends on the sizes alone; NULL
- * where that is 0. */
+ * nvfp4_attention_workspace_bytes(a, grad) bytes, which depends on the sizes and on whether
+ * there is a cu_q; NULL where that is 0.  Calls that use one workspace at the same time race. */
 int64_t nvfp4_attention_workspace_bytes(const nvfp4_attn* a, int grad);
 int nvfp4_attention(const nvfp4_attn* a, const nvfp4_heads* q, const nvfp4_heads* k,
                     const nvfp4_heads* v, const nvfp4_heads* out, float* lse, void* workspace,

@@ -48,29 +48,30 @@ int main() {
     EXPECT(nvfp4_qk_norm_rope_grad_workspace_bytes(4, 1, 1, w), S);
   }
   const nvfp4_attn a{2, 4, 6, 4, 2, 16, nullptr, nullptr, 0, 1, 0, 0.25f};
-  const nvfp4_heads q{P, 256, 64, 16}, k{P, 192, 32, 16};
-  EXPECT(nvfp4_attention(&a, &q, &k, &k, &q, F, P, 4096, nullptr), OK);
-  EXPECT(nvfp4_attention_grad(&a, &q, &q, &k, &k, &q, F, &q, &k, &k, P, 4096, nullptr), OK);
+  const nvfp4_heads q{P, 256, 64, 16}, k{P, 192, 32, 16}, o{dev + 1024, 256, 64, 16}, gq{dev + 2048, 256, 64, 16};
+  const nvfp4_heads gk{dev + 3072, 192, 32, 16}, gv{dev + 3584, 192, 32, 16};
+  EXPECT(nvfp4_attention(&a, &q, &k, &k, &o, F, P, 4096, nullptr), OK);
+  EXPECT(nvfp4_attention_grad(&a, &q, &q, &k, &k, &o, F, &gq, &gk, &gv, P, 4096, nullptr), OK);
   for (int64_t w : wild) {
     for (int64_t nvfp4_attn::*f : {&nvfp4_attn::batch, &nvfp4_attn::Tq, &nvfp4_attn::Tk, &nvfp4_attn::Hq,
                                    &nvfp4_attn::Hkv, &nvfp4_attn::D}) {
       nvfp4_attn b = a;
       b.*f = w;
-      EXPECT(nvfp4_attention(&b, &q, &k, &k, &q, F, P, 4096, nullptr), S);
+      EXPECT(nvfp4_attention(&b, &q, &k, &k, &o, F, P, 4096, nullptr), S);
       EXPECT(nvfp4_attention_workspace_bytes(&b, 1), S);
     }
     for (int64_t nvfp4_heads::*f : {&nvfp4_heads::batch, &nvfp4_heads::token, &nvfp4_heads::head}) {
       nvfp4_heads b = q;
       b.*f = w;
-      EXPECT(nvfp4_attention(&a, &b, &k, &k, &q, F, P, 4096, nullptr), S);
+      EXPECT(nvfp4_attention(&a, &b, &k, &k, &o, F, P, 4096, nullptr), S);
       b = k;
       b.*f = w;
-      EXPECT(nvfp4_attention_grad(&a, &q, &q, &k, &k, &q, F, &q, &k, &b, P, 4096, nullptr), S);
+      EXPECT(nvfp4_attention_grad(&a, &q, &q, &k, &k, &o, F, &gq, &gk, &b, P, 4096, nullptr), S);
     }
   }
   nvfp4_attn b = a;
   b.window = INT64_MAX;
-  EXPECT(nvfp4_attention(&b, &q, &k, &k, &q, F, P, 4096, nullptr), OK);
+  EXPECT(nvfp4_attention(&b, &q, &k, &k, &o, F, P, 4096, nullptr), OK);
   std::printf("unexpected statuses: %d, launches %d\n", failures, launches);
   return failures != 0;
 }

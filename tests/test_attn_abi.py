@@ -84,13 +84,16 @@ def attn(batch=2, Tq=4, Tk=6, Hq=4, Hkv=2, D=16, cu_q=0, cu_k=0, it=I4, causal=0
 
 
 AQ, AK = heads(batch=256, token=64, head=16), heads(batch=192, token=32, head=16)
+OQ = heads(p=FAKE + 0x8000, batch=256, token=64, head=16)
+GQ = heads(p=FAKE + 0x10000, batch=256, token=64, head=16)
+GK, GV = (heads(p=FAKE + n, batch=192, token=32, head=16) for n in (0x18000, 0x20000))
 
 
-def _attn(lib, q=AQ, k=AK, v=AK, out=AQ, lse=FAKE, ws=FAKE, nb=1 << 40, a=None, **kw):
+def _attn(lib, q=AQ, k=AK, v=AK, out=OQ, lse=FAKE, ws=FAKE, nb=1 << 40, a=None, **kw):
     return lib.nvfp4_attention(attn(**kw) if a is None else a, q, k, v, out, lse, ws, nb, None)
 
 
-def _attn_grad(lib, q=AQ, k=AK, v=AK, out=AQ, lse=FAKE, ws=FAKE, nb=1 << 40, dout=AQ, dq=AQ, dk=AK, dv=AK, **kw):
+def _attn_grad(lib, q=AQ, k=AK, v=AK, out=OQ, lse=FAKE, ws=FAKE, nb=1 << 40, dout=AQ, dq=GQ, dk=GK, dv=GV, **kw):
     return lib.nvfp4_attention_grad(attn(**kw), dout, q, k, v, out, lse, dq, dk, dv, ws, nb, None)
 
 
@@ -122,9 +125,14 @@ def test_attention_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(ws=None), NULL), (dict(ws=FAKE + 64), ALIGN), (dict(nb=16), ARG), (dict(dout=None), NULL),
     (dict(dq=heads(p=0, batch=256, token=64, head=16)), NULL), (dict(dk=heads(batch=192, token=36, head=16)), ALIGN),
-    (dict(dv=heads(batch=192, token=8, head=16)), SHAPE)])
+    (dict(dv=heads(batch=192, token=8, head=16)), SHAPE), (dict(dq=AQ), ARG), (dict(dq=OQ), ARG),
+    (dict(dk=AK), ARG), (dict(dv=GK), ARG)])
 def test_attention_grad_refusals(lib, kw, status):
     assert _attn_grad(lib, **kw) == status
+
+
+def test_attention_is_not_in_place(lib):
+    assert _attn(lib, out=AQ) == ARG
 
 
 def test_attention_workspace(lib):

@@ -247,3 +247,95 @@ def test_replayed_graph_and_streams():
         g2 = nv.attention_grad(dout, q, k, v, o2, l2, causal=True)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
         assert all(torch.equal(x, y) for x, y in zip(g2, grads))
+
+
+@pytest.mark.parametrize("D", [88, 96, 104])
+def test_widths_between_the_tiles(D):
+    say("attention width", D)
+    g = torch.Generator().manual_seed(D)
+    _check(_rand(g, 1, 300, 4, D), _rand(g, 1, 300, 2, D), _rand(g, 1, 300, 2, D), _rand(g, 1, 300, 4, D), True)
+
+
+def test_offsets_past_32_bits():
+    """Keys and values 2^22 - 8 elements apart: the last ones lie more than 2^33 bytes in."""
+    say("attention far offsets")
+    T, D, stride = 1100, 64, (1 << 22) - 8
+    g = torch.Generator().manual_seed(11)
+    flat = torch.empty(T * stride, dtype=BF, device="cuda")
+    far = flat.view(T, stride)
+    q, k, v, dout = (_rand(g, T, 1, D) for _ in range(4))
+    views = [far[:, i * D:(i + 1) * D].unsqueeze(1) for i in range(3)]
+    for x, y in zip(views, (q, k, v)):
+        x.copy_(y)
+    out, lse = nv.attention(q, k, v, causal=True)
+    grads = nv.attention_grad(dout, q, k, v, out, lse, causal=True)
+    o2, l2 = nv.attention(*views, causal=True)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    to = tuple(far[:, (3 + i) * D:(4 + i) * D].unsqueeze(1) for i in range(3))
+    g2 = nv.attention_grad(dout, *views, out, lse, causal=True, grads=to)
+    assert all(torch.equal(x, y) for x, y in zip(g2, grads))
+
+
+def test_many_heads_of_one_key_head():
+    """300 query heads on one key head, more than a step of rows; two calls at once on two streams."""
+    say("attention many heads")
+    g = torch.Generator().manual_seed(12)
+    q, k, v, dout = (_rand(g, 20, H, 32) for H in (300, 1, 1, 300))
+    out, lse, grads = _check(q, k, v, dout, True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            o, l = nv.attention(q, k, v, causal=True)
+            got.append((o, l, *nv.attention_grad(dout, q, k, v, o, l, causal=True)))
+    torch.cuda.synchronize()
+    for x in got:
+        assert all(torch.equal(a, b) for a, b in zip(x, (out, lse, *grads)))
+
+
+def test_nothing_finite():
+    """A step that has diverged: every value NaN, results NaN, every loop ends."""
+    say("attention all NaN")
+    x = torch.full((400, 2, 64), float("nan"), dtype=BF, device="cuda")
+    out, lse = nv.attention(x, x, x, causal=True)
+    grads = nv.attention_grad(x, x, x, x, out, lse, causal=True)
+    assert all(torch.isnan(y).all() for y in (out, lse, *grads))
+
+
+@pytest.mark.parametrize("cu", [[5, 2, 9, 40], [0, 1000, 30, 50], [-7, 20, 10, 50], [3, 50, 50, 50]])
+def test_sequence_bounds_that_make_no_sense_stay_inside(cu):
+    """Unspecified results, but none outside the operands (the outputs' guard bands) and no
+    endless loop."""
+    say("attention cu", cu)
+    g = torch.Generator().manual_seed(13)
+    q, k, v, dout = (_rand(g, 50, H, 64) for H in (2, 1, 1, 2))
+    b = torch.tensor(cu, dtype=torch.int64, device="cuda")
+    out, lse = nv.attention(q, k, v, causal=True, cu_q=b)
+    nv.attention_grad(dout, q, k, v, out, lse, causal=True, cu_q=b)
+    torch.cuda.synchronize()
+
+
+def test_shared_out_parts_of_keys_with_hidden_values():
+    """Few queries over many keys and few keys under many queries: the parts' joins, with values
+    that only some rows see."""
+    say("attention parts")
+    g = torch.Generator().manual_seed(14)
+    q, k, v, dout = (_rand(g, T, H, 64) for T, H in ((3, 4), (3000, 2), (3000, 2), (3, 4)))
+    r, t = ref.attention(q, k, v, 0.125, True, 0, None, dout)
+    v[2999] = float("inf")   # only the last query sees it
+    out, lse = nv.attention(q, k, v, causal=True)
+    _close(out[:2], r["out"][:2], t["out"][:2], "out")
+    _close(lse, r["lse"], t["lse"], "lse")
+    assert not torch.isfinite(out[2]).any()
+    q, k, v, dout = (_rand(g, T, H, 64) for T, H in ((2000, 8), (2000, 1), (2000, 1), (2000, 8)))
+    r, t = ref.attention(q, k, v, 0.125, True, 0, None, dout)
+    out, lse = nv.attention(q, k, v, causal=True)
+    dout[700, 3] = float("nan")   # keys behind token 700 do not see it
+    dq, dk, dv = nv.attention_grad(dout, q, k, v, out, lse, causal=True)
+    _close(dk[701:], r["dk"][701:], t["dk"][701:], "dk")
+    _close(dv[701:], r["dv"][701:], t["dv"][701:], "dv")
+    assert torch.isnan(dv[:701]).all()
+    keep = torch.ones(2000, 8, dtype=torch.bool, device="cuda")
+    keep[700, 3] = False
+    _close(dq[keep], r["dq"][keep], t["dq"][keep], "dq")

@@ -27,6 +27,7 @@ struct Args {
   int wide_cu, causal;
   int batch;       // sequences behind one another (cu), or the operands' first dimension
   int Tq, Tk, Hq, Hkv, G, D;
+  int pairs;       // sequences (of one length; else 1) times key heads
   int64_t window;
   float scale, scale2;   // scale2 = scale * log2(e)
 };
@@ -103,6 +104,15 @@ __device__ __forceinline__ bf16_t* row_of_out(const Rows& r, int b, int t, int h
   return const_cast<bf16_t*>(row_of(r, b, t, h));
 }
 
+// The sum over aligned groups of 8 lanes, in each of them.
+__device__ __forceinline__ float sum_of_8(float x) {
+#define MOVED(how) __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), how, 15, 15, true))
+  x += MOVED(0xB1);    // the other one of two
+  x += MOVED(0x4E);    // the other two of four
+  x += MOVED(0x141);   // mirrored within 8
+#undef MOVED
+  return x;
+}
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
@@ -415,16 +425,18 @@ __device__ __forceinline__ Range reach_of_all(uint8_t* lds, const Reach& r, int 
   return lo < hi ? Range{uniform(lo), uniform(hi)} : Range{0, 0};
 }
 
+// Eight values of global memory, or zeros.
+__device__ __forceinline__ v8bf piece(const bf16_t* at, bool there) {
+  v4u x{};
+  if (there) x = *reinterpret_cast<const v4u*>(at);
+  return __builtin_bit_cast(v8bf, x);
+}
+
 // Lane's fragments along d of one row of global memory.
 template <int DP>
 __device__ __forceinline__ void row_frags(v8bf (&f)[DP / 16], const bf16_t* row, bool live, int D, int half) {
 #pragma unroll
-  for (int ks = 0; ks < DP / 16; ++ks) {
-    const int d = 16 * ks + 8 * half;
-    v4u x{};
-    if (live && d < D) x = *reinterpret_cast<const v4u*>(row + d);
-    f[ks] = __builtin_bit_cast(v8bf, x);
-  }
+  for (int ks = 0; ks < DP / 16; ++ks) f[ks] = piece(row + 16 * ks + 8 * half, live && 16 * ks + 8 * half < D);
 }
 
 // An accumulator of columns lane & 31 as rows of global memory, times f.

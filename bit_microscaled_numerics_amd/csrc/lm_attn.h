@@ -192,17 +192,17 @@ __device__ __forceinline__ void pair_grad(const Args& a, int b, int t, int h, in
   ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) - st.y);
 }
 
-__device__ inline void row_dq(const Args& a, int b, int t, int h) {
+// Keys lo .. hi - 1's part of a query's dq, before the scale.
+__device__ inline RowSum row_dq(const Args& a, int b, int t, int h, int lo, int hi) {
   const int lane = threadIdx.x & 63, hk = h / a.G;
-  const Range r = keys_of(a, t);
   RowSum dq;
-  for (int j0 = r.lo; j0 < r.hi; j0 += 64) {
-    const int j = j0 + lane, n = min(64, r.hi - j0);
+  for (int j0 = lo; j0 < hi; j0 += 64) {
+    const int j = j0 + lane, n = min(64, hi - j0);
     float p = 0.0f, ds = 0.0f;
-    if (j < r.hi) pair_grad(a, b, t, h, j, p, ds);
+    if (j < hi) pair_grad(a, b, t, h, j, p, ds);
     for (int i = 0; i < n; ++i) dq.add(row_of(a.k, b, j0 + i, hk), a.D, __shfl(ds, i));
   }
-  dq.store(row_of_out(a.dq, b, t, h), a.D, a.scale);
+  return dq;
 }
 
 // Query rows lo .. hi - 1 (token * G + head of the group), added to dk and dv.

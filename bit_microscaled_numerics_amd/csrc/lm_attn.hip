@@ -1,6 +1,15 @@
-// lm_attn.hip -- softmax attention and its gradient (internal to libnvfp4.so).
+// lm_attn.hip -- softmax attention and its gradient (internal to libnvfp4.so): which
+// workgroup takes what, and the kernels.  lm_attn.h has the tiles and the arithmetic of rows.
 //
-// One wave a row: right for every case, bound by the vector units.
+// The forward pass is one pass over the keys with a running maximum and sum.  The gradient
+// forms the probabilities again from lse, twice: once with the sums of dk and dv in registers, once with
+// those of dq (7 products where 5 would do with dq added up by atomics in memory: those
+// would change their order from run to run, and 64 key tiles adding to 21 MB of dq for each
+// key head pass the L2).  Long products are bound by power: at 8192 tokens, 40 heads of 128 over 8
+// key heads, causal, the clock is at 1.7 - 1.9 GHz with the matrix cores busy for 52 - 54% (zeros
+// as data: 2.2 GHz and three quarters of the time); 680 - 740 us forward (0.93 - 1.0 PFLOP/s), 2100 - 2200
+// the gradient (1.1 PFLOP/s with what is formed again).  Heads of 64 are bound by the
+// exponentials and sums on the vector units, small calls by launches and the chain of a tile's steps.
 #include <hip/hip_runtime.h>
 
 #include "lm_attn.h"
@@ -576,9 +585,11 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
 }
 
 // dq of 256 query rows, laid out as the forward kernel: S^T = K Q^T, dP^T = V dO^T, and
-// dS^T as it stands is the second operand of dQ^T = K^T dS^T.
-template <int DP>
-__device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& lds, Job job, int tiles) {
+// dS^T as it stands is the second operand of dQ^T = K^T dS^T.  parts > 1: each takes a piece of
+// the keys and leaves FP32 sums, which k_attn_join_rows adds up.
+template <int DP, bool PARTS>
+__device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& lds, Job job, int tiles, int part,
+                                             int parts, float* sums) {
   using T = Tile<DP, kKeys>;
   constexpr int kHalf = T::kBytes;   // of a stage: K, then V
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
@@ -589,7 +600,12 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
   const Range mine = keys_of(a, t);
   const Reach reach = reach_of(live, mine.lo, mine.hi);
-  const Range all = reach_of_all<8>(lds.s0, reach, wave);
+  Range all = reach_of_all<8>(lds.s0, reach, wave);
+  if (PARTS) {
+    const int per = ((all.hi - all.lo + kKeys - 1) / kKeys + parts - 1) / parts * kKeys;
+    const int64_t from = all.lo + (int64_t)part * per;
+    all = Range{(int)min(from, (int64_t)all.hi), (int)min(from + per, (int64_t)all.hi)};
+  }
   const float2 st = live ? a.stats[job.pair * rows + r] : float2{0.0f, 0.0f};
 
   v8bf q[T::kSteps], g[T::kSteps];
@@ -605,7 +621,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   auto tile = [&](int j, uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
     tile_landed();
     if (j + kKeys < all.hi) keys.load(next + second * kHalf, lw, j + kKeys);
-    if (j >= reach.hi || j + kKeys <= reach.lo) return;
+    if (j >= min(reach.hi, all.hi) || j + kKeys <= reach.lo) return;
     const uint8_t* tv = now + kHalf;
     v16f s[2] = {}, dp[2] = {};
     pipeline<4 * T::kSteps, kAhead>(
@@ -622,8 +638,8 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         dp[kb][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][v], a.scale2, -st.x)) * (dp[kb][v] - st.y);
-    if (j < reach.all_lo || j + kKeys > reach.all_hi) {
-      const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(mine.hi - mine.lo, 0);
+    if (j < reach.all_lo || j + kKeys > min(reach.all_hi, all.hi)) {
+      const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(min(mine.hi, all.hi) - mine.lo, 0);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -645,33 +661,63 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   }
   const float odd = odd_of(dq);
   uint64_t again = __ballot(live && odd != 0.0f);
-  if (live) store_columns(row_of_out(a.dq, b, t, h), dq, a.scale, a.D, half);
+  float* to = PARTS ? sums + (((int64_t)part * a.pairs + job.pair) * rows + r) * a.D : nullptr;
+  if (live && !PARTS) store_columns(row_of_out(a.dq, b, t, h), dq, a.scale, a.D, half);
+  if (live && PARTS) store_sums(to, dq, a.D, half);
   for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
-    const int from = __builtin_ctzll(again);
-    row_dq(a, b, __shfl(t, from), __shfl(h, from));
+    const int from = __builtin_ctzll(again), tt = __shfl(t, from), hh = __shfl(h, from);
+    const int lo = __shfl(mine.lo, from), hi = __shfl(mine.hi, from);
+    const RowSum x = row_dq(a, b, tt, hh, PARTS ? max(lo, all.lo) : lo, PARTS ? min(hi, all.hi) : hi);
+    if (PARTS)
+      x.store(to + (int64_t)(from - (lane & 31)) * a.D, a.D);
+    else
+      x.store(row_of_out(a.dq, b, tt, hh), a.D, a.scale);
   }
 }
 #endif
 
+// How the gradient's workgroups are shared out; sums of parts in the workspace.
+struct Shares {
+  int key_tiles, key_parts, row_tiles, row_parts;
+  float *key_sums, *row_sums;
+};
+
 // One launch for both halves of the gradient: the keys' workgroups, which are few and
 // long, come first, the queries' fill what they leave.
-template <int DP, bool PARTS>
-__global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, int pairs, int key_tiles, int row_tiles, int parts,
-                                                      float* sums) {
+template <int DP, bool KP, bool RP>
+__global__ __launch_bounds__(512, 2) void k_attn_grad(Args a, Shares sh) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kRow = DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t s0[128 * kRow], s1[128 * kRow], v[128 * kRow], stats[1024];
   const GradLds<DP> lds{s0, s1, v, stats};
-  const uint32_t id = (uint32_t)block_xz(), tiles = (uint32_t)pairs * (uint32_t)key_tiles;
-  const uint32_t keys = PARTS ? tiles * (uint32_t)parts : tiles;
+  const uint32_t id = (uint32_t)block_xz(), kt = (uint32_t)a.pairs * (uint32_t)sh.key_tiles;
+  const uint32_t keys = KP ? kt * (uint32_t)sh.key_parts : kt;
   if (id < keys) {
-    const uint32_t part = PARTS ? id / tiles : 0;
-    grad_keys<DP, PARTS>(a, lds, job_of(id - part * tiles, pairs, key_tiles), (int)part, parts, sums,
-                         (int64_t)pairs * a.Tk);
-  } else if (id - keys < (uint32_t)pairs * (uint32_t)row_tiles) {
-    grad_queries<DP>(a, lds, job_of(id - keys, pairs, row_tiles), row_tiles);
+    const uint32_t part = KP ? id / kt : 0;
+    grad_keys<DP, KP>(a, lds, job_of(id - part * kt, a.pairs, sh.key_tiles), (int)part, sh.key_parts, sh.key_sums,
+                      (int64_t)a.pairs * a.Tk);
+    return;
   }
+  const uint32_t rt = (uint32_t)a.pairs * (uint32_t)sh.row_tiles, part = RP ? (id - keys) / rt : 0;
+  if (id - keys < (RP ? rt * (uint32_t)sh.row_parts : rt))
+    grad_queries<DP, RP>(a, lds, job_of(id - keys - part * rt, a.pairs, sh.row_tiles), sh.row_tiles, (int)part,
+                         sh.row_parts, sh.row_sums);
 #endif
+}
+
+// dq of each row from the parts' sums, in order, laid out as k_attn_join_keys.
+template <int LANES>
+__global__ __launch_bounds__(256) void k_attn_join_rows(Args a, uint32_t rows, int parts, const float* sums) {
+  const uint32_t r = (uint32_t)block_xz() * (256 / LANES) + threadIdx.x / LANES;
+  const int d = 4 * (threadIdx.x & (LANES - 1));
+  if (r >= rows || d >= a.D) return;
+  v4f dq{};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) dq += *reinterpret_cast<const v4f*>(sums + ((int64_t)i * rows + r) * a.D + d);
+  const uint32_t in_pair = (uint32_t)a.Tq * a.G, pair = r / in_pair, rr = r - pair * in_pair;
+  const int b = pair / a.Hkv, t = rr / a.G, h = (pair - b * a.Hkv) * a.G + (rr - t * a.G);
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<v4bf*>(row_of_out(a.dq, b, t, h) + d) = __builtin_convertvector(dq * a.scale, v4bf);
 }
 
 // dk and dv of each key from the parts' sums, in order: 32 lanes a key (16 up to 64 columns), four
@@ -707,15 +753,8 @@ namespace {
 // Keys of a sequence, on average.
 int64_t keys_in(const nvfp4_attn& a) { return a.cu_q == nullptr || a.batch < 2 ? a.Tk : a.Tk / a.batch; }
 
-// Workgroups that share a row's keys, at most 512 in all and parts of at least 128 keys.  A part
-// costs its sums' way through memory (4.5 TB/s there and back) and the join a launch; the key
-// tiles one after the other take 0.8 us each.  The n with the least sum of both.
-int parts_of(const nvfp4_attn& a) {
-  const int64_t G = a.Hq / a.Hkv, tiles = (a.Tq * G + kRowsWG - 1) / kRowsWG * sequences(a) * a.Hkv;
-  if (tiles == 0 || tiles >= kPartTiles) return 1;
-  const int64_t keys = keys_in(a);
-  const int64_t most = keys / kPartKeys < kPartTiles / tiles ? keys / kPartKeys : kPartTiles / tiles;
-  const double chain = (double)keys / kKeys * 0.8, part = (double)sequences(a) * a.Tq * a.Hq * a.D * 8 / 4.5e6;
+// The n of at most `most` with the least chain / n + 8 + 1.3 n part (us).
+int least_parts(double chain, double part, int64_t most) {
   int best = 1;
   double least = chain;
   for (int64_t n = 2; n <= most; ++n) {
@@ -725,6 +764,18 @@ int parts_of(const nvfp4_attn& a) {
   return best;
 }
 
+// Workgroups that share a row's keys, at most 512 in all and parts of at least 128 keys.  A part
+// costs its sums' way through memory (4.5 TB/s there and back) and the join a launch; the key
+// tiles one after the other take 0.8 us each.  The n with the least sum of both.
+int parts_of(const nvfp4_attn& a) {
+  const int64_t G = a.Hq / a.Hkv, tiles = (a.Tq * G + kRowsWG - 1) / kRowsWG * sequences(a) * a.Hkv;
+  if (tiles == 0 || tiles >= kPartTiles) return 1;
+  const int64_t keys = keys_in(a);
+  const int64_t most = keys / kPartKeys < kPartTiles / tiles ? keys / kPartKeys : kPartTiles / tiles;
+  const double chain = (double)keys / kKeys * 0.8, part = (double)sequences(a) * a.Tq * a.Hq * a.D * 8 / 4.5e6;
+  return least_parts(chain, part, most);
+}
+
 // Workgroups that share a key tile's query rows in the gradient, by the same rule: 1.1 us a step
 // of 64 rows, and at most 256 in all, one for each compute unit (2048 queries of 40 heads over 8
 // key heads, 128 tiles: 275 us whole, 215 in two parts, 238 in four; 4096: 628 and 682).
@@ -732,16 +783,23 @@ int key_parts_of(const nvfp4_attn& a) {
   const int64_t tiles = (a.Tk + 127) / 128 * sequences(a) * a.Hkv;
   if (tiles == 0) return 1;
   const int64_t queries = a.cu_q == nullptr || a.batch < 2 ? a.Tq : a.Tq / a.batch, steps = queries * (a.Hq / a.Hkv) / 64;
-  const int64_t most = steps / 4 < 256 / tiles ? steps / 4 : 256 / tiles;
-  const double chain = steps * 1.1, part = (double)sequences(a) * a.Tk * a.Hkv * a.D * 16 / 4.5e6;
-  int best = 1;
-  double least = chain;
-  for (int64_t n = 2; n <= most; ++n) {
-    const double t = chain / n + 8.0 + 1.3 * n * part;
-    if (t < least) least = t, best = (int)n;
-  }
-  return best;
+  return least_parts(steps * 1.1, (double)sequences(a) * a.Tk * a.Hkv * a.D * 16 / 4.5e6,
+                     steps / 4 < 256 / tiles ? steps / 4 : 256 / tiles);
 }
+
+// Those that share a tile of query rows: 1.3 us a tile of keys.
+int row_parts_of(const nvfp4_attn& a) {
+  const int64_t tiles = (a.Tq * (a.Hq / a.Hkv) + kGradRows - 1) / kGradRows * sequences(a) * a.Hkv;
+  if (tiles == 0) return 1;
+  const int64_t steps = keys_in(a) / kKeys;
+  return least_parts(steps * 1.3, (double)sequences(a) * a.Tq * a.Hq * a.D * 8 / 4.5e6,
+                     steps / 4 < 256 / tiles ? steps / 4 : 256 / tiles);
+}
+
+// Bytes of the gradient's workspace, in this order: statistics, the keys' parts, the rows' parts.
+struct GradSpace {
+  int64_t stats, key_sums, row_sums;
+};
 
 // f(columns of the tiles): 64, 96 or 128.
 template <class F>
@@ -756,13 +814,19 @@ void by_width(int D, F f) {
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
+GradSpace grad_space(const nvfp4_attn& a) {
+  const int64_t rows = sequences(a) * a.Tq * a.Hq, keys = sequences(a) * a.Tk * a.Hkv;
+  const int kp = key_parts_of(a), rp = row_parts_of(a);
+  return GradSpace{up256(rows * 8), kp > 1 ? up256(keys * a.D * 8 * kp) : 0, rp > 1 ? rows * a.D * 4 * rp : 0};
+}
+
 }  // namespace
 
 int64_t attn_workspace_bytes(const nvfp4_attn& a, bool grad) {
   const int64_t rows = sequences(a) * a.Tq * a.Hq;
   if (grad) {
-    const int parts = key_parts_of(a);
-    return parts > 1 ? up256(rows * 8) + sequences(a) * a.Tk * a.Hkv * a.D * 8 * parts : rows * 8;
+    const GradSpace g = grad_space(a);
+    return g.stats + g.key_sums + g.row_sums;
   }
   const int n = parts_of(a);
   return n > 1 ? up256(rows * n * a.D * 4) + rows * n * 8 : 0;
@@ -804,27 +868,34 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
 hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
   const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq;
   const Args a = make_args(c);
-  const int pairs = (int)(sequences(c.a) * a.Hkv);
-  const int row_tiles = (int)(((int64_t)a.Tq * a.G + kGradRows - 1) / kGradRows);
-  const int key_tiles = (int)(((int64_t)a.Tk + 127) / 128);
-  const int parts = key_parts_of(c.a);
-  const int64_t n = (int64_t)pairs * row_tiles + (int64_t)pairs * key_tiles * parts;
+  const GradSpace g = grad_space(c.a);
+  Shares sh{(int)(((int64_t)a.Tk + 127) / 128),
+            key_parts_of(c.a),
+            (int)(((int64_t)a.Tq * a.G + kGradRows - 1) / kGradRows),
+            row_parts_of(c.a),
+            reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + g.stats),
+            reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + g.stats + g.key_sums)};
+  const int64_t n = (int64_t)a.pairs * sh.row_tiles * sh.row_parts + (int64_t)a.pairs * sh.key_tiles * sh.key_parts;
   if (n == 0) return hipSuccess;
-  float* sums = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + up256(rows * 8)) : nullptr;
   const dim3 grid = grid_xz(n);
-  auto launch = [&](auto k) { k<<<grid, 512, 0, s>>>(a, pairs, key_tiles, row_tiles, parts, sums); };
+  auto launch = [&](auto k) { k<<<grid, 512, 0, s>>>(a, sh); };
   const int stat_tiles = (int)(((int64_t)a.Tq * a.G + 127) / 128);
+  const bool kp = sh.key_parts > 1, rp = sh.row_parts > 1;
   by_width(a.D, [&](auto dp) {
-    constexpr int DP = decltype(dp)::value;
-    if (rows > 0) k_attn_stats<DP><<<grid_xz((int64_t)pairs * stat_tiles), 256, 0, s>>>(a, stat_tiles);
-    parts == 1 ? launch(k_attn_grad<DP, false>) : launch(k_attn_grad<DP, true>);
+    constexpr int DP = decltype(dp)::value, kLanes = DP == 64 ? 16 : 32;
+    if (rows > 0) k_attn_stats<DP><<<grid_xz((int64_t)a.pairs * stat_tiles), 256, 0, s>>>(a, stat_tiles);
+    if (kp)
+      rp ? launch(k_attn_grad<DP, true, true>) : launch(k_attn_grad<DP, true, false>);
+    else
+      rp ? launch(k_attn_grad<DP, false, true>) : launch(k_attn_grad<DP, false, false>);
+    const int64_t keys = (int64_t)a.pairs * a.Tk;
+    if (kp)
+      k_attn_join_keys<kLanes><<<grid_xz((keys * kLanes + 255) / 256), 256, 0, s>>>(a, (uint32_t)keys, sh.key_parts,
+                                                                                 sh.key_sums);
+    if (rp)
+      k_attn_join_rows<kLanes><<<grid_xz((rows * kLanes + 255) / 256), 256, 0, s>>>(a, (uint32_t)rows, sh.row_parts,
+                                                                                 sh.row_sums);
   });
-  if (parts == 1) return hipGetLastError();
-  const uint32_t keys = (uint32_t)((int64_t)pairs * a.Tk);
-  if (a.D <= 64)
-    k_attn_join_keys<16><<<grid_xz((keys + 15) / 16), 256, 0, s>>>(a, keys, parts, sums);
-  else
-    k_attn_join_keys<32><<<grid_xz((keys + 7) / 8), 256, 0, s>>>(a, keys, parts, sums);
   return hipGetLastError();
 }
 

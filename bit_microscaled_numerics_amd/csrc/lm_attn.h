@@ -21,7 +21,10 @@ struct Rows {   // strides in elements
 struct Args {
   Rows q, k, v, out, dout, dq, dk, dv;
   float* lse;      // [sequence][Tq][Hq], or [Tq][Hq]
-  float2* stats;   // gradient: {lse in log2, delta} of [sequence * key head][row]
+  // gradient, of [sequence * key head][row]: -lse / scale and -delta, where the sums of the
+  // scores and of dout . v begin: both come out of their products shifted
+  float* neg_lse;
+  float* neg_delta;
   const void* cu_q;
   const void* cu_k;
   int wide_cu, causal;
@@ -187,9 +190,9 @@ __device__ inline Soft row_forward(const Args& a, int b, int t, int h, int lo, i
 // p and ds of one query and key.
 __device__ __forceinline__ void pair_grad(const Args& a, int b, int t, int h, int j, float& p, float& ds) {
   const int hk = h / a.G;
-  const float2 st = a.stats[((int64_t)b * a.Hkv + hk) * a.Tq * a.G + (int64_t)t * a.G + (h - hk * a.G)];
-  p = exp2f(fmaf(dot(row_of(a.q, b, t, h), row_of(a.k, b, j, hk), a.D), a.scale2, -st.x));
-  ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) - st.y);
+  const int64_t r = ((int64_t)b * a.Hkv + hk) * a.Tq * a.G + (int64_t)t * a.G + (h - hk * a.G);
+  p = exp2f((dot(row_of(a.q, b, t, h), row_of(a.k, b, j, hk), a.D) + a.neg_lse[r]) * a.scale2);
+  ds = p * (dot(row_of(a.dout, b, t, h), row_of(a.v, b, j, hk), a.D) + a.neg_delta[r]);
 }
 
 // Keys lo .. hi - 1's part of a query's dq, before the scale.

@@ -35,7 +35,7 @@ Args make_args(const AttnCall& c) {
   a.dk = rows(c.dk);
   a.dv = rows(c.dv);
   a.lse = c.lse;
-  a.stats = static_cast<float2*>(c.ws);
+  a.neg_lse = static_cast<float*>(c.ws);   // the gradient's; launch_attn_grad places the other
   a.cu_q = n.cu_q;
   a.cu_k = n.cu_k;
   a.wide_cu = n.cu_type == NVFP4_TYPE_I64;
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part p
   if (lane == 0) a.lse[stat_at(a, b, t, h)] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-// lse in log2 and delta of every row, in the order of the rows of a key head: a wave 32 rows.
+// -lse / scale and -delta of every row, in the order of the rows of a key head: a wave 32 rows.
 // delta = dout . out takes over out's rounding to BF16, which is small beside the rounding of
 // ds where many keys share a row, and as large where few do.  Rows of at most 64 keys that
 // fit a window of 64 therefore take delta = sum p dp, formed from the scores again: the error of
@@ -412,7 +412,10 @@ __global__ __launch_bounds__(256) void k_attn_stats(Args a, int tiles) {
     sum = pair_sum(sum);
     if (few && mine.hi - from <= 64 && __builtin_isfinite(sum)) delta = sum;
   }
-  if (live && half == 0) a.stats[pair * rows + r] = float2{lse, delta};
+  if (live && half == 0) {
+    a.neg_lse[pair * rows + r] = -lse / a.scale2;
+    a.neg_delta[pair * rows + r] = -delta;
+  }
 #endif
 }
 
@@ -466,16 +469,14 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
 
   v16f dk[T::kBlocks] = {}, dv[T::kBlocks] = {};
   const int64_t all_rows = (int64_t)a.Tq * a.G;
-  const float2* stats = a.stats + job.pair * all_rows;
+  const float* stats = (wave == 0 ? a.neg_lse : a.neg_delta) + job.pair * all_rows;
   RowLoader<DP, 64, 4> rows;   // waves 0 .. 3 load q, the others dout
   auto load = [&](uint8_t* stage, int st, int r) __attribute__((always_inline)) {
     rows.load(stage + rg * kHalf, kg);
-    if (wave < 2) {   // the statistics of 32 rows
-      const int r0 = r + wave * 32;
+    if (wave < 2)   // -lse / scale, -delta of the rows
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          descriptor(reinterpret_cast<const uint16_t*>(stats + r0)), (lds_void)(lds.stats + st * 512 + wave * 256),
-          4, r0 + (lane >> 1) < all_rows ? (uint32_t)lane * 4 : kDead, 0, 0, 0);
-    }
+          descriptor(reinterpret_cast<const uint16_t*>(stats + r)), (lds_void)(lds.stats + st * 512 + wave * 256), 4,
+          r + lane < all_rows ? (uint32_t)lane * 4 : kDead, 0, 0, 0);
   };
   auto tile = [&](int r, uint8_t* now, uint8_t* next, int st) __attribute__((always_inline)) {
     tile_landed();
@@ -483,7 +484,14 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     const int r0 = r + rg * 32;
     if (r0 >= min(reach.hi, all.hi) || r0 + 32 <= reach.lo) return;
     const uint8_t* td = now + kHalf;
-    v16f s{}, dp{};
+    v16f s, dp;   // from -lse / scale and -delta on
+    const uint8_t* st_at = lds.stats + st * 512 + rg * 128 + half * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v4f x = *reinterpret_cast<const v4f*>(st_at + i * 32), y = *reinterpret_cast<const v4f*>(st_at + 256 + i * 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * i + e] = x[e], dp[4 * i + e] = y[e];
+    }
     struct Two {
       v8bf a, b;
     };
@@ -496,16 +504,10 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
           v16f& sum = i & 1 ? dp : s;
           sum = mfma(f.a, f.b, sum);
         });
-    const uint8_t* st_at = lds.stats + st * 512 + rg * 256 + half * 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v4f x[2] = {*reinterpret_cast<const v4f*>(st_at + i * 64), *reinterpret_cast<const v4f*>(st_at + i * 64 + 16)};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int v = 4 * i + e;
-        s[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], a.scale2, -x[e >> 1][2 * (e & 1)]));
-        dp[v] = s[v] * (dp[v] - x[e >> 1][2 * (e & 1) + 1]);
-      }
+    for (int v = 0; v < 16; ++v) {
+      s[v] = __builtin_amdgcn_exp2f(s[v] * a.scale2);
+      dp[v] *= s[v];
     }
     if (r0 < reach.all_lo || r0 + 32 > min(reach.all_hi, all.hi)) {
       const uint32_t first = (uint32_t)(r0 + 4 * half - rlo), n = (uint32_t)max(min(rhi, all.hi) - rlo, 0);
@@ -606,7 +608,13 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
     const int64_t from = all.lo + (int64_t)part * per;
     all = Range{(int)min(from, (int64_t)all.hi), (int)min(from + per, (int64_t)all.hi)};
   }
-  const float2 st = live ? a.stats[job.pair * rows + r] : float2{0.0f, 0.0f};
+  // The products begin from -lse / scale and -delta (heads of 64: gradient 521 -> 496 us at 8192 x
+  // 16/8 heads); with 128 columns, where 32 registers for two values would spill, they are added.
+  constexpr bool kFrom = DP < 128;
+  const float nl = live ? a.neg_lse[job.pair * rows + r] : 0.0f, nd = live ? a.neg_delta[job.pair * rows + r] : 0.0f;
+  v16f first_s{}, first_dp{};
+  if (kFrom) first_s = nl, first_dp = nd;
+  const float shift = kFrom ? 0.0f : nl * a.scale2, more = kFrom ? 0.0f : nd;
 
   v8bf q[T::kSteps], g[T::kSteps];
   row_frags<DP>(q, row_of(a.q, b, live ? t : 0, h), live, a.D, half);
@@ -623,21 +631,22 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
     if (j + kKeys < all.hi) keys.load(next + second * kHalf, lw, j + kKeys);
     if (j >= min(reach.hi, all.hi) || j + kKeys <= reach.lo) return;
     const uint8_t* tv = now + kHalf;
-    v16f s[2] = {}, dp[2] = {};
+    v16f s[2], dp[2];
     pipeline<4 * T::kSteps, kAhead>(
         [&](int i) { return frag.read(i & 1 ? tv : now, i >> 2, (i & 2) * 16); },
         [&](int i, const v8bf& f) {
           const int kb = (i >> 1) & 1;
           if (i & 1)
-            dp[kb] = mfma(f, g[i >> 2], dp[kb]);
+            dp[kb] = mfma(f, g[i >> 2], i < 4 ? first_dp : dp[kb]);
           else
-            s[kb] = mfma(f, q[i >> 2], s[kb]);
+            s[kb] = mfma(f, q[i >> 2], i < 4 ? first_s : s[kb]);
         });
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int v = 0; v < 16; ++v)
-        dp[kb][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][v], a.scale2, -st.x)) * (dp[kb][v] - st.y);
+        dp[kb][v] = __builtin_amdgcn_exp2f(kFrom ? s[kb][v] * a.scale2 : __builtin_fmaf(s[kb][v], a.scale2, shift)) *
+                    (kFrom ? dp[kb][v] : dp[kb][v] + more);
     if (j < reach.all_lo || j + kKeys > min(reach.all_hi, all.hi)) {
       const uint32_t first = (uint32_t)(j + 4 * half - mine.lo), n = (uint32_t)max(min(mine.hi, all.hi) - mine.lo, 0);
 #pragma unroll
@@ -867,8 +876,9 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
 
 hipError_t launch_attn_grad(const AttnCall& c, hipStream_t s) {
   const int64_t rows = sequences(c.a) * c.a.Tq * c.a.Hq;
-  const Args a = make_args(c);
+  Args a = make_args(c);
   const GradSpace g = grad_space(c.a);
+  a.neg_delta = a.neg_lse + g.stats / 8;
   Shares sh{(int)(((int64_t)a.Tk + 127) / 128),
             key_parts_of(c.a),
             (int)(((int64_t)a.Tq * a.G + kGradRows - 1) / kGradRows),

@@ -137,8 +137,9 @@ int check_attn(const nvfp4_attn* a) {
     return fail(NVFP4_ERR_ARG, "causal=%d must be 0 or 1", a->causal);
   if (a->window < 0 || (a->window > 0 && !a->causal))
     return fail(NVFP4_ERR_ARG, "window=%lld must be 0, or positive and causal", (long long)a->window);
-  if (!(a->scale > 0.f) || std::isinf(a->scale))
-    return fail(NVFP4_ERR_ARG, "scale=%g must be positive and finite", (double)a->scale);
+  // the gradient holds lse / scale, which stays in FP32's range between these
+  if (!(a->scale >= 0x1p-64f && a->scale <= 0x1p64f))
+    return fail(NVFP4_ERR_ARG, "scale=%g must lie within 2^-64 .. 2^64", (double)a->scale);
   if (a->cu_q != nullptr) {
     if (!index_type(a->cu_type))
       return fail(NVFP4_ERR_ARG, "cu_q, cu_k: type %d is not I32 or I64", a->cu_type);

@@ -492,7 +492,7 @@ typedef struct {
   int32_t cu_type;           /* I32 or I64 */
   int32_t causal;            /* 0 or 1 */
   int64_t window;            /* 0: none */
-  float scale;
+  float scale;               /* 2^-64 .. 2^64 */
 } nvfp4_attn;
 
 /* workspace (also of the gradient): 256-byte aligned, of at least

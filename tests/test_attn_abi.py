@@ -106,6 +106,7 @@ BAD_ATTN = [
     (dict(cu_q=FAKE + 2, cu_k=FAKE), ALIGN), (dict(cu_q=FAKE, cu_k=FAKE + 4, it=I8), ALIGN),
     (dict(causal=2), ARG), (dict(window=3), ARG), (dict(window=-1, causal=1), ARG), (dict(scale=0.0), ARG),
     (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
+    (dict(scale=2.0 ** -65), ARG), (dict(scale=2.0 ** 65), ARG),
     (dict(q=None), NULL), (dict(k=heads(p=0, batch=192, token=32, head=16)), NULL), (dict(lse=None), NULL),
     (dict(lse=FAKE + 2), ALIGN), (dict(v=heads(p=FAKE + 8, batch=192, token=32, head=16)), ALIGN),
     (dict(q=heads(batch=256, token=68, head=16)), ALIGN), (dict(q=heads(batch=256, token=56, head=16)), SHAPE),

@@ -188,6 +188,15 @@ def test_large_scores_and_scale():
     _check(q, k, v, dout, False, scale=1e-3)
 
 
+@pytest.mark.parametrize("power", [-64, 64])
+def test_largest_and_smallest_scale(power):
+    say("attention scale", power)
+    g = torch.Generator().manual_seed(power + 100)
+    std = 1.0 if power < 0 else 2.0 ** -33
+    q, k, v, dout = (_rand(g, 150, 2, 64, std=s) for s in (std, std, 1.0, 1.0))
+    _check(q, k, v, dout, True, scale=2.0 ** power)
+
+
 def test_same_bits_every_time():
     say("attention repeat")
     g = torch.Generator().manual_seed(4)

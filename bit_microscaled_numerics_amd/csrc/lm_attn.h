@@ -58,6 +58,29 @@ __device__ __forceinline__ int sequence_of(const void* cu, int wide, int n, int 
   return lo - 1;
 }
 
+// The same, formed by a whole wave, all lanes present: 64 entries are loaded at once and looked
+// through by shuffles, and only what lies between two of them is searched in memory.  Up to 63
+// sequences that is one load instead of six, each waiting for the last.
+__device__ __forceinline__ int sequence_by_wave(const void* cu, int wide, int n, int t, int most) {
+  const int lane = threadIdx.x & 63, step = n / 64 + 1;
+  const int mine = cu_at(cu, wide, min(lane * step, n), most);
+  int below = 0;   // of the 64, those at or before t
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1)
+    if (__shfl(mine, below + m - 1) <= t) below += m;
+  if (__shfl(mine, below) <= t) ++below;
+  if (below == 0) return -1;
+  int lo = min((below - 1) * step + 1, n + 1), hi = min(below * step, n + 1);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu_at(cu, wide, mid, most) <= t)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo - 1;
+}
+
 __device__ __forceinline__ int clamp64(int64_t x, int lo, int hi) {
   return (int)(x < lo ? lo : x > hi ? hi : x);
 }
@@ -71,12 +94,14 @@ __device__ __forceinline__ Span span_of(const Args& a, int s) {
               cu_at(a.cu_k, a.wide_cu, s, a.Tk), cu_at(a.cu_k, a.wide_cu, s + 1, a.Tk)};
 }
 
-// The keys that query token t sees; empty for a t past the end.
+// The keys that query token t sees; empty for a t past the end.  WAVE: all lanes call.
+template <bool WAVE>
 __device__ __forceinline__ Range keys_of(const Args& a, int t) {
-  if (t >= a.Tq) return Range{0, 0};
   Span s{0, a.Tq, 0, a.Tk};
-  if (a.cu_q != nullptr) s = span_of(a, sequence_of(a.cu_q, a.wide_cu, a.batch, t, a.Tq));
-  if (t < s.q0 || t >= s.q1 || s.k1 <= s.k0) return Range{0, 0};
+  if (a.cu_q != nullptr)
+    s = span_of(a, WAVE ? sequence_by_wave(a.cu_q, a.wide_cu, a.batch, t, a.Tq)
+                        : sequence_of(a.cu_q, a.wide_cu, a.batch, t, a.Tq));
+  if (t >= a.Tq || t < s.q0 || t >= s.q1 || s.k1 <= s.k0) return Range{0, 0};
   if (!a.causal) return Range{s.k0, s.k1};
   const int64_t end = (int64_t)(t - s.q0) + 1 + (s.k1 - s.k0) - (s.q1 - s.q0);
   const int hi = s.k0 + clamp64(end, 0, s.k1 - s.k0);
@@ -84,12 +109,11 @@ __device__ __forceinline__ Range keys_of(const Args& a, int t) {
   return Range{lo, hi};
 }
 
-// The query tokens that see key j.
+// The query tokens that see key j.  All lanes call.
 __device__ __forceinline__ Range queries_of(const Args& a, int j) {
-  if (j >= a.Tk) return Range{0, 0};
   Span s{0, a.Tq, 0, a.Tk};
-  if (a.cu_q != nullptr) s = span_of(a, sequence_of(a.cu_k, a.wide_cu, a.batch, j, a.Tk));
-  if (j < s.k0 || j >= s.k1 || s.q1 <= s.q0) return Range{0, 0};
+  if (a.cu_q != nullptr) s = span_of(a, sequence_by_wave(a.cu_k, a.wide_cu, a.batch, j, a.Tk));
+  if (j >= a.Tk || j < s.k0 || j >= s.k1 || s.q1 <= s.q0) return Range{0, 0};
   if (!a.causal) return Range{s.q0, s.q1};
   const int64_t first = (int64_t)(j - s.k0) - ((s.k1 - s.k0) - (s.q1 - s.q0));
   const int lo = s.q0 + clamp64(first, 0, s.q1 - s.q0);

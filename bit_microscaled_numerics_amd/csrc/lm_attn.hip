@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   const int64_t r = (int64_t)(tiles - 1 - job.tile) * kRowsWG + wave * 32 + (lane & 31);
   const bool live = r < rows;
   const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
-  const Range mine = keys_of(a, t);
+  const Range mine = keys_of<true>(a, t);
 
   const bool some = mine.lo < mine.hi;
   const Reach reach = reach_of(live, mine.lo, mine.hi);
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(Args a, uint32_t rows, Pa
     l += ml.y * f;
     if (live) x += *reinterpret_cast<const v4f*>(part.o + at * a.D + 4 * in_row) * f;
   }
-  const Range k = keys_of(a, t);
+  const Range k = keys_of<false>(a, t);
   const bool some = k.lo < k.hi;
   const float f = some ? 1.0f / l : 0.0f;
   typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part p
   __syncthreads();
   if (wave > 0) return;
   for (int w = 1; w < 4; ++w) sum.x += sums[w][lane].x, sum.y += sums[w][lane].y;
-  const Range k = keys_of(a, t);
+  const Range k = keys_of<false>(a, t);
   const bool some = k.lo < k.hi;
   const float f = some ? 1.0f / l : 0.0f;
   if (live) {
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256) void k_attn_stats(Args a, int tiles) {
   const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
   // dout . out: 8 lanes a row, 8 rows at a time, then to the lanes of the row
   const float lse = live ? a.lse[stat_at(a, b, t, h)] * kLog2e : 0.0f;
-  const Range mine = keys_of(a, t);
+  const Range mine = keys_of<true>(a, t);
   constexpr int kParts = (DP + 63) / 64;
   v4u x[4][kParts], y[4][kParts];
 #pragma unroll
@@ -600,7 +600,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   const int64_t r = (int64_t)(tiles - 1 - job.tile) * kGradRows + wave * 32 + (lane & 31);
   const bool live = r < rows;
   const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
-  const Range mine = keys_of(a, t);
+  const Range mine = keys_of<true>(a, t);
   const Reach reach = reach_of(live, mine.lo, mine.hi);
   Range all = reach_of_all<8>(lds.s0, reach, wave);
   if (PARTS) {
@@ -787,11 +787,15 @@ int parts_of(const nvfp4_attn& a) {
 
 // Workgroups that share a key tile's query rows in the gradient, by the same rule: 1.1 us a step
 // of 64 rows, and at most 256 in all, one for each compute unit (2048 queries of 40 heads over 8
-// key heads, 128 tiles: 275 us whole, 215 in two parts, 238 in four; 4096: 628 and 682).
+// key heads, 128 tiles: 275 us whole, 215 in two parts, 238 in four; 4096: 628 and 682).  The
+// longest chain counts, which the host does not know of packed sequences: it is taken as twice the
+// average (gradient, by the average, twice and four times it: 12 documents of 1 .. 1371 in 4096, 8/2
+// heads of 128: 154, 120, 130 us; 9 in 2048, 16/4 heads of 64: 79, 69, 68; of equal ones 8 in 2048: 44,
+// 52, 51; 32 in 4096: 49, 49, 64).
 int key_parts_of(const nvfp4_attn& a) {
   const int64_t tiles = (a.Tk + 127) / 128 * sequences(a) * a.Hkv;
   if (tiles == 0) return 1;
-  const int64_t queries = a.cu_q == nullptr || a.batch < 2 ? a.Tq : a.Tq / a.batch, steps = queries * (a.Hq / a.Hkv) / 64;
+  const int64_t queries = a.cu_q == nullptr || a.batch < 2 ? a.Tq : a.Tq / a.batch * 2, steps = queries * (a.Hq / a.Hkv) / 64;
   return least_parts(steps * 1.1, (double)sequences(a) * a.Tk * a.Hkv * a.D * 16 / 4.5e6,
                      steps / 4 < 256 / tiles ? steps / 4 : 256 / tiles);
 }

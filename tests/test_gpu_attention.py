@@ -110,6 +110,20 @@ def test_packed(nq, nk, extra, it, causal, window, Hq, Hkv, D):
         _close(x, r[name], t[name], name)
 
 
+@pytest.mark.parametrize("n", [1, 62, 63, 64, 65, 127, 128, 129, 500])
+def test_number_of_sequences(n):
+    """The sequence of a row is found whatever their number, with empty ones at both ends and between."""
+    say("attention sequences", n)
+    g = torch.Generator().manual_seed(n)
+    lengths = torch.randint(0, 6, (2, n), generator=g)
+    lengths[:, :min(2, n - 1)] = 0
+    lengths[:, n - 1] *= n % 2
+    cu = torch.cat((torch.zeros(2, 1, dtype=torch.int64), lengths.cumsum(1)), 1).tolist()
+    (Tq, Tk), Hq, Hkv, D = (c[-1] + 2 for c in cu), 2, 1, 64
+    _check(_rand(g, Tq, Hq, D), _rand(g, Tk, Hkv, D), _rand(g, Tk, Hkv, D), _rand(g, Tq, Hq, D), n % 4 == 1,
+           cu=(*cu, torch.int32 if n % 2 else torch.int64))
+
+
 def _view(x, kind):
     """The same values in another layout."""
     B, T, H, D = x.shape

@@ -6,7 +6,7 @@
 // those of dq (7 products where 5 would do with dq added up by atomics in memory: those
 // would change their order from run to run, and 64 key tiles adding to 21 MB of dq for each
 // key head pass the L2).  Long products are bound by power: at 8192 tokens, 40 heads of 128 over 8
-// key heads, causal, the clock is at 1.7 - 1.9 GHz with the matrix cores busy for 52 - 54% (zeros
+// key heads, causal, the clock is at 1.7 - 1.9 GHz with the matrix cores busy for 53 - 55% (zeros
 // as data: 2.2 GHz and three quarters of the time); 680 - 740 us forward (0.93 - 1.0 PFLOP/s), 2100 - 2200
 // the gradient (1.1 PFLOP/s with what is formed again).  Heads of 64 are bound by the
 // exponentials and sums on the vector units, small calls by launches and the chain of a tile's steps.

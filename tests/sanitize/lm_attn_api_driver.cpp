@@ -49,7 +49,7 @@ int main() {
   }
   const nvfp4_attn a{2, 4, 6, 4, 2, 16, nullptr, nullptr, 0, 1, 0, 0.25f};
   const nvfp4_heads q{P, 256, 64, 16}, k{P, 192, 32, 16}, o{dev + 1024, 256, 64, 16}, gq{dev + 2048, 256, 64, 16};
-  const nvfp4_heads gk{dev + 3072, 192, 32, 16}, gv{dev + 3584, 192, 32, 16};
+  const nvfp4_heads gk{dev + 3088, 192, 32, 16}, gv{dev + 3600, 192, 32, 16};
   EXPECT(nvfp4_attention(&a, &q, &k, &k, &o, F, P, 4096, nullptr), OK);
   EXPECT(nvfp4_attention_grad(&a, &q, &q, &k, &k, &o, F, &gq, &gk, &gv, P, 4096, nullptr), OK);
   for (int64_t w : wild) {

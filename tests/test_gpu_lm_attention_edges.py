@@ -1,0 +1,84 @@
+"""SelfAttention against float64 autograd away from its defaults: without norms, adjacent pairs, both
+directions, and calls at the edges of what it takes."""
+import pytest
+import torch
+
+import attn_reference as ref
+from bit_microscaled_numerics_amd import lm
+from parity import say
+
+pytestmark = pytest.mark.gpu
+BF, HALF = torch.bfloat16, 2.0 ** -8
+
+
+def _rand(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(BF).cuda()
+
+
+def _near(got, want, rel):
+    """Norm-wise: rounding errors of independent sign, each at most `rel` of its entry."""
+    assert got.shape == want.shape
+    assert (got.double() - want).norm() <= rel * want.norm()
+
+
+def _reference(m, qkv, bounds, dout):
+    """Float64 autograd of one row of tokens; (out, dqkv, and dq_weight, dk_weight if there are norms)."""
+    heads, kv, D, eps, il, norm, scale, causal, window = m.how
+    x = qkv.double().requires_grad_()
+    w = [p.double().detach().requires_grad_() for p in (m.q_weight, m.k_weight)] if norm else []
+    T, n = x.shape[0], m.inv_freq.numel()
+    q, k, v = (y.view(T, -1, D) for y in x.split((heads * D, kv * D, kv * D), -1))
+    pos = torch.cat([torch.arange(b - a) for a, b in bounds]).double().cuda()
+    t = (pos.unsqueeze(1) * m.inv_freq.double()).unsqueeze(1)
+
+    def turn(y, side):
+        if norm:
+            y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + eps) * w[side]
+        pairs = y[..., :2 * n].unflatten(-1, (n, 2) if il else (2, n))
+        a, b = pairs.unbind(-1 if il else -2)
+        turned = torch.stack((a * t.cos() - b * t.sin(), b * t.cos() + a * t.sin()), -1 if il else -2)
+        return torch.cat((turned.flatten(-2), y[..., 2 * n:]), -1)
+
+    q, k = turn(q, 0), turn(k, 1)
+    rows = []
+    for a, b in bounds:
+        seen = ref.seen_mask(b - a, b - a, causal, window, "cuda")
+        for h in range(heads):
+            z = (scale * q[a:b, h] @ k[a:b, h * kv // heads].T).masked_fill(~seen, -torch.inf)
+            rows.append(torch.softmax(z, -1) @ v[a:b, h * kv // heads])
+    out = torch.cat([torch.stack(rows[i * heads:(i + 1) * heads], 1) for i in range(len(bounds))])
+    out = out.reshape(T, heads * D)
+    return (out.detach(), *torch.autograd.grad((out * dout.double()).sum(), (x, *w)))
+
+
+def _results(m, qkv, dout, **kw):
+    x = qkv.detach().requires_grad_()
+    out = m(x, **kw)
+    params = list(m.parameters())
+    return (out.detach(), *torch.autograd.grad(out, (x, *params), dout))
+
+
+# Roundings to BF16 on the way: q and k after the norm and rotation (they move the scores by scale *
+# sum |q||k| 2^-8 / sqrt(D), some 2^-8 of p), p, ds, the intermediate gradients and the results: six of
+# independent sign, the most of each HALF of its entry.
+REL = 6 ** 0.5 * HALF
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("il,rot", [(False, 32), (True, 32), (True, 20), (False, 0)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_variants(norm, il, rot, causal):
+    say("lm module variant", norm, il, rot, causal)
+    g = torch.Generator().manual_seed(7)
+    T, heads, kv, D = 130, 4, 2, 32
+    m = lm.SelfAttention(heads, D, kv, rot=rot, norm=norm, interleaved=il, causal=causal, device="cuda")
+    with torch.no_grad():
+        for p in m.parameters():
+            p.add_(_rand(g, D, std=0.2))
+    qkv, dout = _rand(g, T, (heads + 2 * kv) * D), _rand(g, T, heads * D)
+    cu = torch.tensor([0, 50, T], dtype=torch.int32, device="cuda")
+    got = _results(m, qkv, dout, cu=cu)
+    want = _reference(m, qkv, [(0, 50), (50, T)], dout)
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        _near(a, b, REL)

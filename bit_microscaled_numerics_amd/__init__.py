@@ -992,8 +992,9 @@ def qk_norm_rope_grad(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: to
                       interleaved: bool = False, norm: bool = True,
                       out: Optional[tuple] = None):
     """(dq, dk, dq_weight, dk_weight): the gradient of ``qk_norm_rope`` from the gradients
-    of its results and its own inputs; None for a weight that is not there.  out: the
-    tensors that take the first two, such as pieces of a projection's gradient."""
+    of its results and its own inputs; None for a weight that is not there.  Rows whose
+    incoming gradient is all zero take no part, whatever they hold.  out: the tensors that
+    take the first two, such as pieces of a projection's gradient."""
     r, dev = _rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, norm)
     dt, place, (T, H, D), Hk = q.dtype, q.device, q.shape, k.shape[1]
     h = (_heads(dq, 3, dt, dev, "dq"), _heads(dk, 3, dt, dev, "dk"), _heads(q, 3, dt, dev, "q"),

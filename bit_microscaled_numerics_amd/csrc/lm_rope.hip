@@ -379,20 +379,29 @@ __global__ __launch_bounds__(kWaves * 64) void k_rope_grad(Args k) {
           float q = 0.0f;
 #pragma unroll
           for (int i = 0; i < N; ++i) q += n.a[i] * n.a[i] + n.b[i] * n.b[i];
-          const float r = 1.0f / sqrtf(row_sum(q, k.lanes) * inv_d + k.eps);
-          float m = 0.0f;
+          float r = 1.0f / sqrtf(row_sum(q, k.lanes) * inv_d + k.eps), m = 0.0f;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             n.a[i] *= r;
             n.b[i] *= r;
-            const float da = g.a[i] * n.a[i], db = g.b[i] * n.b[i];
-            dw.a[i] += da;
-            dw.b[i] += db;
-            m += da * w.a[i] + db * w.b[i];
+            m += g.a[i] * n.a[i] * w.a[i] + g.b[i] * n.b[i] * w.b[i];
           }
           m = row_sum(m, k.lanes) * inv_d;
+          // A row that takes no gradient (a token of no sequence) adds nothing, whatever it holds: 0
+          // times NaN would reach dw through it.  m is the row's, so all its lanes are here or none.
+          if (m != m) {
+            float some = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) some += (g.a[i] != 0.0f || g.b[i] != 0.0f) ? 1.0f : 0.0f;
+            if (row_sum(some, k.lanes) == 0.0f) {
+              n.a = n.b = 0.0f;
+              m = r = 0.0f;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < N; ++i) {
+            dw.a[i] += g.a[i] * n.a[i];
+            dw.b[i] += g.b[i] * n.b[i];
             g.a[i] = r * (g.a[i] * w.a[i] - n.a[i] * m);
             g.b[i] = r * (g.b[i] * w.b[i] - n.b[i] * m);
           }

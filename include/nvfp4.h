@@ -453,7 +453,9 @@ int nvfp4_qk_norm_rope(const nvfp4_rope* r, const nvfp4_heads* q, const nvfp4_he
 /* Its gradient: dq, dk (the incoming ones) to dq_in, dk_in, which may be dq and dk (in place, the
  * same strides), and dq_weight, dk_weight [D] of weight_type (nullable: not formed; must
  * be NULL without their weight), FP32 sums over tokens and heads in an order fixed by the sizes,
- * joined in FP64.  q and k are the unchanged inputs.  workspace: 256-byte aligned, of at least
+ * joined in FP64.  q and k are the unchanged inputs; a row of theirs whose incoming gradient is all
+ * zero may hold anything: its gradient is zero and it adds nothing to the weights'.
+ * workspace: 256-byte aligned, of at least
  * nvfp4_qk_norm_rope_grad_workspace_bytes(T, Hq, Hkv, D). */
 int64_t nvfp4_qk_norm_rope_grad_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
 int nvfp4_qk_norm_rope_grad(const nvfp4_rope* r, const nvfp4_heads* dq, const nvfp4_heads* dk,

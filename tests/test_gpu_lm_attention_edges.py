@@ -82,3 +82,25 @@ def test_variants(norm, il, rot, causal):
     assert len(got) == len(want)
     for a, b in zip(got, want):
         _near(a, b, REL)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("before", [0, 5])
+def test_tokens_of_no_sequence_reach_nothing(before, value):
+    """Rows before the first and behind the last sequence hold what was there: neither the other rows'
+    results nor the gradients of the norms' weights take it over; their own are zeros."""
+    say("lm module padding", before, value)
+    g = torch.Generator().manual_seed(8)
+    T, extra, heads, kv, D = 150, 11, 4, 2, 32
+    m = lm.SelfAttention(heads, D, kv, device="cuda")
+    qkv, dout = _rand(g, before + T + extra, (heads + 2 * kv) * D), _rand(g, before + T + extra, heads * D)
+    real = slice(before, before + T)
+    none = torch.ones(before + T + extra, dtype=torch.bool, device="cuda")
+    none[real] = False
+    qkv[none] = value
+    cu = torch.tensor([before, before + 60, before + T], dtype=torch.int32, device="cuda")
+    out, dqkv, dwq, dwk = _results(m, qkv, dout, cu=cu)
+    assert not out[none].any() and not dqkv[none].any()
+    want = _reference(m, qkv[real], [(0, 60), (60, T)], dout[real])
+    for a, b in zip((out[real], dqkv[real], dwq, dwk), want):
+        _near(a, b, REL)

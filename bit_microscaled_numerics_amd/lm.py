@@ -368,7 +368,8 @@ class SelfAttention(torch.nn.Module):
     """Causal self-attention of a projection's rows [.., tokens, (heads + 2 * kv_heads) * dim]
     (queries, keys, values), bf16, to [.., tokens, heads * dim]: norms of queries and keys
     for each head (norm=False: none), rotation of the first `rot` of their dim values, softmax
-    attention over all earlier tokens or the last `window`."""
+    attention over all earlier tokens or the last `window`.  Its weights may be cast to float32;
+    the rotation's frequencies are float32 whatever the module is cast to."""
 
     def __init__(self, heads: int, dim: int, kv_heads: Optional[int] = None, rot: Optional[int] = None,
                  base: float = 10000.0, norm: bool = True, eps: float = 1e-6,
@@ -384,8 +385,25 @@ class SelfAttention(torch.nn.Module):
         for name in ("q_weight", "k_weight"):
             self.register_parameter(name, torch.nn.Parameter(
                 torch.ones(dim, dtype=torch.bfloat16, device=device)) if norm else None)
-        inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
-        self.register_buffer("inv_freq", inv.float().to(device), persistent=False)
+        self.rotation = (rot, base)
+        self.register_buffer("inv_freq", self._frequencies(
+            torch.get_default_device() if device is None else device), persistent=False)
+
+    def _frequencies(self, device) -> torch.Tensor:
+        rot, base = self.rotation
+        at = torch.arange(0, rot, 2, dtype=torch.float64, device="cpu")
+        return (base ** (-at / max(rot, 1))).float().to(device)
+
+    def _apply(self, fn, recurse=True):
+        """Casts and moves of the module.  The frequencies move, but keep their type: rounded to 8 bits
+        they turn rows at positions in the thousands by radians too much.  Where a module made without
+        memory is given some, they are formed now."""
+        before = self.inv_freq
+        super()._apply(fn, recurse)
+        device = self.inv_freq.device
+        if self.inv_freq is not before:
+            self.inv_freq = self._frequencies(device) if before.is_meta else before.to(device)
+        return self
 
     def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor] = None,
                 cu: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -104,3 +104,13 @@ def test_tokens_of_no_sequence_reach_nothing(before, value):
     want = _reference(m, qkv[real], [(0, 60), (60, T)], dout[real])
     for a, b in zip((out[real], dqkv[real], dwq, dwk), want):
         _near(a, b, REL)
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.to(BF), lambda m: m.bfloat16().float(), lambda m: m.cpu().half().float().cuda()])
+def test_module_that_was_cast(cast):
+    """Positions in the tens of thousands: frequencies with fewer bits would turn rows elsewhere."""
+    say("lm module cast")
+    g = torch.Generator().manual_seed(9)
+    qkv, pos = _rand(g, 90, 6 * 32), 50000 + torch.arange(90, device="cuda")
+    want = lm.SelfAttention(2, 32, device="cuda")(qkv, positions=pos)
+    assert torch.equal(cast(lm.SelfAttention(2, 32, device="cuda"))(qkv, positions=pos), want)

@@ -344,8 +344,8 @@ class SelfAttentionFunction(torch.autograd.Function):
     @staticmethod
     def pieces(qkv, heads, kv_heads, dim):
         """q, k and v in a projection's rows: views [.., heads, dim]."""
-        split = qkv.split((heads * dim, kv_heads * dim, kv_heads * dim), -1)
-        return [x.view(*x.shape[:-1], -1, dim) for x in split]
+        counts = (heads, kv_heads, kv_heads)
+        return [x.view(*x.shape[:-1], n, dim) for x, n in zip(qkv.split([n * dim for n in counts], -1), counts)]
 
     @staticmethod
     @once_differentiable

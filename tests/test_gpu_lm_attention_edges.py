@@ -114,3 +114,17 @@ def test_module_that_was_cast(cast):
     qkv, pos = _rand(g, 90, 6 * 32), 50000 + torch.arange(90, device="cuda")
     want = lm.SelfAttention(2, 32, device="cuda")(qkv, positions=pos)
     assert torch.equal(cast(lm.SelfAttention(2, 32, device="cuda"))(qkv, positions=pos), want)
+
+
+@pytest.mark.parametrize("shape", [(0,), (2, 0), (0, 3)])
+@pytest.mark.parametrize("norm,rot", [(True, 32), (False, 0)])
+def test_no_tokens(shape, norm, rot):
+    """As the functions below: results without rows, gradients of the weights that are zero."""
+    say("lm module no tokens", shape, norm, rot)
+    m = lm.SelfAttention(4, 32, 2, norm=norm, rot=rot, device="cuda")
+    calls = [dict()] + [dict(cu=torch.zeros(n, dtype=torch.int32, device="cuda")) for n in (1, 3) if len(shape) == 1]
+    for kw in calls:
+        out, dqkv, *dw = _results(m, torch.zeros(*shape, 256, dtype=BF, device="cuda"),
+                                  torch.zeros(*shape, 128, dtype=BF, device="cuda"), **kw)
+        assert out.shape == (*shape, 128) and dqkv.shape == (*shape, 256)
+        assert len(dw) == (2 if norm else 0) and not any(x.any() for x in dw)

@@ -56,3 +56,48 @@ def test_frequencies_put_in_are_kept():
     for change in (lambda: m.to(BF), m.half, m.float, lambda: m.to_empty(device="cpu")):
         change()
         assert m.inv_freq.dtype == torch.float32 and torch.equal(m.inv_freq, own)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The module's calls of the library, with results of the right shapes."""
+    log = []
+
+    def rope(q, k, *rest, **kw):
+        assert q.shape[0] == k.shape[0] and (rest[2] is None or rest[2].numel() == q.shape[0])
+        return (q.clone(memory_format=torch.contiguous_format), k.clone(memory_format=torch.contiguous_format))
+
+    def rope_grad(dq, dk, q, k, q_weight=None, k_weight=None, *rest, out=None, **kw):
+        dw = [None if w is None else torch.zeros_like(w) for w in (q_weight, k_weight)]
+        return (*((dq, dk) if out is None else out), *dw)
+
+    def forward(q, k, v, *rest, **kw):
+        log.append((q, k, v))
+        return torch.zeros(q.shape, dtype=q.dtype), torch.zeros(q.shape[:-1])
+
+    def grad(dout, q, k, v, out, lse, *rest, grads=None, **kw):
+        assert dout.shape == q.shape
+        for x, like in zip(grads, (q, k, v)):
+            assert x.shape == like.shape
+            x.zero_()
+        return grads
+
+    for name, fn in (("qk_norm_rope_forward", rope), ("qk_norm_rope_grad", rope_grad),
+                     ("attention_forward", forward), ("attention_grad", grad)):
+        monkeypatch.setattr(lm, name, fn)
+    return log
+
+
+@pytest.mark.parametrize("shape", [(0,), (2, 0), (0, 3), (0, 0)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_no_tokens(calls, shape, norm):
+    m = _fresh(norm=norm)
+    x = torch.zeros(*shape, 128, dtype=BF, requires_grad=True)
+    for kw in (dict(), dict(positions=torch.zeros((), dtype=torch.int64))):
+        out = m(x, **kw)
+        assert out.shape == (*shape, 64)
+        out.backward(torch.zeros_like(out))
+        assert x.grad.shape == x.shape and all(not p.grad.any() for p in m.parameters())
+    if len(shape) == 1:
+        for cu in ([0], [0, 0], [0, 0, 0]):
+            assert m(x, cu=torch.tensor(cu, dtype=torch.int32)).shape == (0, 64)

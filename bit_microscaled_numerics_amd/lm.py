@@ -422,8 +422,5 @@ class SelfAttention(torch.nn.Module):
                 positions = positions - cu.long()[at.clamp(min=0)]
         positions = positions.expand(qkv.shape[:-1]).reshape(-1).contiguous()
         inv = self.inv_freq if self.inv_freq.numel() else None
-        if qkv.stride(-1) != 1 or qkv.data_ptr() % 16 or any(
-                n > 1 and (st % 8 or st < qkv.shape[-1]) for st, n in zip(qkv.stride()[:-1], qkv.shape[:-1])):
-            qkv = qkv.contiguous() if not qkv.is_contiguous() else qkv.clone()
-        return SelfAttentionFunction.apply(qkv, self.q_weight, self.k_weight,
+        return SelfAttentionFunction.apply(_rows16(qkv), self.q_weight, self.k_weight,
                                            None if inv is None else positions, inv, self.how, cu)

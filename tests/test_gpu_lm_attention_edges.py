@@ -128,3 +128,13 @@ def test_no_tokens(shape, norm, rot):
                                   torch.zeros(*shape, 128, dtype=BF, device="cuda"), **kw)
         assert out.shape == (*shape, 128) and dqkv.shape == (*shape, 256)
         assert len(dw) == (2 if norm else 0) and not any(x.any() for x in dw)
+
+
+def test_windows_over_one_row_of_tokens():
+    say("lm module windows")
+    g = torch.Generator().manual_seed(10)
+    m = lm.SelfAttention(4, 32, 2, device="cuda")
+    tokens, dout = _rand(g, 50, 256), _rand(g, 7, 20, 128)
+    windows = tokens.unfold(0, 20, 5).transpose(1, 2)
+    for a, b in zip(_results(m, windows, dout), _results(m, windows.contiguous(), dout)):
+        assert torch.equal(a, b)

@@ -101,3 +101,20 @@ def test_no_tokens(calls, shape, norm):
     if len(shape) == 1:
         for cu in ([0], [0, 0], [0, 0, 0]):
             assert m(x, cu=torch.tensor(cu, dtype=torch.int32)).shape == (0, 64)
+
+
+def test_rows_that_overlap_are_copied(calls):
+    """Windows that slide over one row of tokens share its rows; attention takes rows apart."""
+    tokens = torch.zeros(10, 128, dtype=BF, requires_grad=True)
+    windows = tokens.unfold(0, 4, 2).transpose(1, 2)   # [4][4][128], every second token in two of them
+    assert windows.stride() == (256, 128, 1)
+    m = _fresh()
+    out = m(windows)
+    out.backward(torch.zeros_like(out))
+    assert tokens.grad.shape == tokens.shape
+    m(windows.expand(4, 4, 128)[:1].expand(3, 4, 128))
+    for q, k, v in calls:
+        assert v.stride() == (4 * 128, 128, 16, 1)
+    apart = torch.zeros(4, 3, 128, dtype=BF).transpose(0, 1)
+    m(apart)
+    assert calls[-1][2].stride() == (128, 3 * 128, 16, 1)   # taken as it lies

@@ -295,7 +295,8 @@ __global__ __launch_bounds__(256) void k_attn_join(Args a, uint32_t rows, Part p
   float l = 0.0f;
   for (int i = lane; i < part.n; i += 64) {
     const float* ml = part.ml + 2 * ((int64_t)i * rows + r);
-    l += ml[0] == -INFINITY ? 0.0f : ml[1] * __builtin_amdgcn_exp2f(ml[0] - m);
+    // a part whose scores are all NaN has no maximum, and a sum of NaN that counts
+    l += ml[1] * (ml[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[0] - m));
   }
   l = wave_sum(l);
   float2 sum{0.0f, 0.0f};

@@ -232,6 +232,36 @@ __device__ inline RowSum row_dq(const Args& a, int b, int t, int h, int lo, int 
   return dq;
 }
 
+__device__ __forceinline__ bool nan_throughout(const bf16_t* row, int D) {
+  const int lane = threadIdx.x & 63;
+  const float x = lane < D ? load1(row + lane) : NAN, y = lane + 64 < D ? load1(row + lane + 64) : NAN;
+  return __all(x != x && y != y);
+}
+
+// Whether query rows lo .. hi - 1 make a key that they see NaN throughout: dk and dv by an lse, dk by a
+// delta, dv by a row of dout (of 64 in a row with such deltas one is looked at).  By the statistics, 64
+// rows at a time: a step that has diverged is told by its first rows, where forming its keys again would
+// take hundreds of times an ordinary gradient.
+struct NanRows {
+  bool dk, dv;
+};
+__device__ inline NanRows nan_rows(const Args& a, int b, int hk, int64_t lo, int64_t hi, bool dv_too) {
+  const int lane = threadIdx.x & 63;
+  const int64_t first = ((int64_t)b * a.Hkv + hk) * a.Tq * a.G;
+  NanRows is{false, false};
+  for (int64_t r0 = lo; r0 < hi && !(is.dk && (is.dv || !dv_too)); r0 += 64) {
+    const bool there = r0 + lane < hi;
+    const float l = there ? a.neg_lse[first + r0 + lane] : 0.0f, d = there ? a.neg_delta[first + r0 + lane] : 0.0f;
+    if (__any(l != l)) return NanRows{true, true};
+    const uint64_t lost = __ballot(d != d);
+    if (lost == 0) continue;
+    const int64_t r = r0 + __builtin_ctzll(lost);
+    is.dk = true;
+    is.dv = nan_throughout(row_of(a.dout, b, (int)(r / a.G), hk * a.G + (int)(r % a.G)), a.D);
+  }
+  return is;
+}
+
 // Query rows lo .. hi - 1 (token * G + head of the group), added to dk and dv.
 __device__ inline void row_dkv(const Args& a, int b, int j, int hk, int64_t lo, int64_t hi, RowSum& dk,
                                RowSum& dv) {

@@ -212,9 +212,10 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   }
 
   // A value that is not finite may come from a key that a row does not see, multiplied by 0:
-  // such rows are formed again, one by one.
+  // such rows are formed again, one by one, unless they are NaN throughout anyway: where l is, which
+  // only keys that the row sees are part of, or the first of their values is.
   const float odd = odd_of(o);
-  uint64_t again = __ballot(live && odd != 0.0f);
+  uint64_t again = __ballot(live && odd != 0.0f && l == l);
   const int64_t at = SPLIT ? (int64_t)sp * pairs * rows + job.pair * rows + r : 0;
   if (live) {
     if (SPLIT) {
@@ -233,9 +234,12 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   }
   for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
     const int from = __builtin_ctzll(again);
-    const int tt = __shfl(t, from), hh = __shfl(h, from), lo1 = __shfl(mine.lo, from), hi1 = __shfl(mine.hi, from);
+    const int tt = __shfl(t, from), hh = __shfl(h, from);
+    const int lo1 = SPLIT ? max(__shfl(mine.lo, from), j0) : __shfl(mine.lo, from);
+    const int hi1 = SPLIT ? min(__shfl(mine.hi, from), j1) : __shfl(mine.hi, from);
     const int64_t at1 = at - (lane & 31) + from;
-    const Soft x = row_forward(a, b, tt, hh, SPLIT ? max(lo1, j0) : lo1, SPLIT ? min(hi1, j1) : hi1);
+    if (lo1 < hi1 && nan_throughout(row_of(a.v, b, lo1, hk), a.D)) continue;
+    const Soft x = row_forward(a, b, tt, hh, lo1, hi1);
     if (SPLIT) {
       x.o.store(part.o + at1 * a.D, a.D);
       if (lane == 0) part.ml[2 * at1] = x.m, part.ml[2 * at1 + 1] = x.l;
@@ -566,8 +570,8 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
       }
   }
   if (rg == 1) return;
-  const float odd = odd_of(dk) + odd_of(dv);
-  uint64_t again = __ballot(live && odd != 0.0f);
+  uint64_t odd_k = __ballot(live && odd_of(dk) != 0.0f), odd_v = __ballot(live && odd_of(dv) != 0.0f);
+  odd_k |= odd_k >> 32, odd_v |= odd_v >> 32;
   float* to = PARTS ? sums + (((int64_t)part * all_keys + (int64_t)job.pair * a.Tk + key) * 2) * a.D : nullptr;
   if (live && !PARTS) {
     store_columns(row_of_out(a.dk, b, j, hk), dk, a.scale, a.D, half);
@@ -576,10 +580,15 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     store_sums(to, dk, a.D, half);
     store_sums(to + a.D, dv, a.D, half);
   }
-  for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
-    const int from = __builtin_ctzll(again), jj = __shfl(j, from), lo = __shfl(rlo, from), hi = __shfl(rhi, from);
+  for (uint64_t again = (odd_k | odd_v) & 0xffffffffu; again != 0; again &= again - 1) {
+    const int from = __builtin_ctzll(again), jj = __shfl(j, from);
+    const int lo = PARTS ? max(__shfl(rlo, from), all.lo) : __shfl(rlo, from);
+    const int hi = PARTS ? min(__shfl(rhi, from), all.hi) : __shfl(rhi, from);
+    const bool k_odd = odd_k >> from & 1, v_odd = odd_v >> from & 1;
+    const NanRows nan = nan_rows(a, b, hk, lo, hi, v_odd);
+    if ((nan.dk || !k_odd) && (nan.dv || !v_odd)) continue;
     RowSum xk, xv;
-    row_dkv(a, b, jj, hk, PARTS ? max(lo, all.lo) : lo, PARTS ? min(hi, all.hi) : hi, xk, xv);
+    row_dkv(a, b, jj, hk, lo, hi, xk, xv);
     if (PARTS) {
       float* row = to + 2 * (int64_t)(from - (lane & 31)) * a.D;
       xk.store(row, a.D);
@@ -673,8 +682,9 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
     tile(j, lds.s0, lds.s1);
     if (j + kKeys < all.hi) tile(j + kKeys, lds.s1, lds.s0);
   }
-  const float odd = odd_of(dq);
-  uint64_t again = __ballot(live && odd != 0.0f);
+  // NaN throughout anyway: where a row's lse or delta is, and it sees a key
+  const bool lost = mine.lo < mine.hi && (nl != nl || nd != nd);
+  uint64_t again = __ballot(live && odd_of(dq) != 0.0f && !lost);
   float* to = PARTS ? sums + (((int64_t)part * a.pairs + job.pair) * rows + r) * a.D : nullptr;
   if (live && !PARTS) store_columns(row_of_out(a.dq, b, t, h), dq, a.scale, a.D, half);
   if (live && PARTS) store_sums(to, dq, a.D, half);

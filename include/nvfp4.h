@@ -478,8 +478,9 @@ int nvfp4_qk_norm_rope_grad(const nvfp4_rope* r, const nvfp4_heads* dq, const nv
  * results are zeros.  Values of cu that do not ascend or exceed Tq, Tk give unspecified
  * results, without an access outside the operands.
  * What a query does not see (infinities, NaN) does not reach its results, nor its
- * gradients those of the keys that it does not see.  Rows and keys whose results are not
- * finite are formed one by one, at a hundredth of the speed.
+ * gradients those of the keys that it does not see.  Rows and keys whose results are not finite
+ * are formed again one by one, some 500 times slower than others, unless a NaN among their scores or
+ * a row of v or dout that is NaN throughout tells that they are NaN throughout (a step that has diverged).
  * Results may not overlap operands or each other.
  * q, k, v, out and gradients BF16, 16-byte aligned with strides that are multiples of 8 (token
  * strides below 2^22, the heads of a group within 2^29 elements);

@@ -1,5 +1,6 @@
 """Values that are not finite, against the definition taken pair by pair: what a query sees makes its results
-NaN or infinite as the formulas do, what it does not see changes nothing."""
+NaN or infinite as the formulas do, what it does not see changes nothing, and a step of such values takes no
+longer than a small multiple of an ordinary one."""
 import pytest
 import torch
 
@@ -110,3 +111,38 @@ def test_few_queries(Tk, which):
         clean = [x.clone() for x in (q, k, v, dout)]
         (k, v)[which - 1][bad] = NAN
         _check(q, k, v, dout, clean, ref.seen_mask(Tq, Tk, True, 0), Tq, causal=True)
+
+
+def _us(f):
+    f()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+    a.record()
+    f()
+    b.record()
+    b.synchronize()
+    return a.elapsed_time(b) * 1e3
+
+
+@pytest.mark.parametrize("which", ["qkv", "q", "k", "v", "dout", "token"])
+def test_a_diverged_step_ends_soon(which):
+    """Ordinary work of 4096 tokens takes some 100 us; formed pair by pair it would be hundreds of times that.
+    Twenty times leaves room for the card's clocks."""
+    say("attention diverged", which)
+    g = torch.Generator().manual_seed(3)
+    ops = dict(q=_rand(g, 4096, 8, 128), k=_rand(g, 4096, 2, 128), v=_rand(g, 4096, 2, 128),
+               dout=_rand(g, 4096, 8, 128))
+
+    def times(q, k, v, dout):
+        out, lse = nv.attention(q, k, v, causal=True)
+        return (_us(lambda: nv.attention(q, k, v, causal=True)),
+                _us(lambda: nv.attention_grad(dout, q, k, v, out, lse, causal=True)))
+
+    usual = times(**ops)
+    for name, x in ops.items():
+        if name in which:
+            x.fill_(NAN)
+        elif which == "token" and name in "qkv":
+            x[100] = NAN
+    for got, was in zip(times(**ops), usual):
+        assert got <= 20 * max(was, 50.0), (got, was)

@@ -109,16 +109,22 @@ __device__ __forceinline__ Range keys_of(const Args& a, int t) {
   return Range{lo, hi};
 }
 
-// The query tokens that see key j.  All lanes call.
-__device__ __forceinline__ Range queries_of(const Args& a, int j) {
+// The query tokens that see key j; those before `more` see no other key.  All lanes call.
+struct Seers {
+  int lo, more, hi;
+};
+__device__ __forceinline__ Seers queries_of(const Args& a, int j) {
   Span s{0, a.Tq, 0, a.Tk};
   if (a.cu_q != nullptr) s = span_of(a, sequence_by_wave(a.cu_k, a.wide_cu, a.batch, j, a.Tk));
-  if (j >= a.Tk || j < s.k0 || j >= s.k1 || s.q1 <= s.q0) return Range{0, 0};
-  if (!a.causal) return Range{s.q0, s.q1};
+  if (j >= a.Tk || j < s.k0 || j >= s.k1 || s.q1 <= s.q0) return Seers{0, 0, 0};
+  const bool one = s.k1 - s.k0 == 1;
+  if (!a.causal) return Seers{s.q0, one ? s.q1 : s.q0, s.q1};
   const int64_t first = (int64_t)(j - s.k0) - ((s.k1 - s.k0) - (s.q1 - s.q0));
   const int lo = s.q0 + clamp64(first, 0, s.q1 - s.q0);
   const int hi = a.window > 0 ? s.q0 + clamp64(first + a.window, 0, s.q1 - s.q0) : s.q1;
-  return Range{lo, hi};
+  // the query whose last key is the sequence's first sees it alone
+  const int more = one || a.window == 1 ? hi : j == s.k0 && first >= 0 ? min(lo + 1, hi) : lo;
+  return Seers{lo, more, hi};
 }
 
 __device__ __forceinline__ int64_t stat_at(const Args& a, int b, int t, int h) {
@@ -262,15 +268,17 @@ __device__ inline NanRows nan_rows(const Args& a, int b, int hk, int64_t lo, int
   return is;
 }
 
-// Query rows lo .. hi - 1 (token * G + head of the group), added to dk and dv.
-__device__ inline void row_dkv(const Args& a, int b, int j, int hk, int64_t lo, int64_t hi, RowSum& dk,
-                               RowSum& dv) {
+// Query rows lo .. hi - 1 (token * G + head of the group), added to dk and dv; those before `more` see
+// no other key.
+__device__ inline void row_dkv(const Args& a, int b, int j, int hk, int64_t lo, int64_t more, int64_t hi,
+                               RowSum& dk, RowSum& dv) {
   const int lane = threadIdx.x & 63;
   for (int64_t r0 = lo; r0 < hi; r0 += 64) {
     const int64_t r = r0 + lane;
     const int n = (int)min((int64_t)64, hi - r0);
     float p = 0.0f, ds = 0.0f;
     if (r < hi) pair_grad(a, b, (int)(r / a.G), hk * a.G + (int)(r % a.G), j, p, ds);
+    if (r < more) ds *= 0.0f;
     for (int i = 0; i < n; ++i) {
       const int t = (int)((r0 + i) / a.G), h = hk * a.G + (int)((r0 + i) % a.G);
       dv.add(row_of(a.dout, b, t, h), a.D, __shfl(p, i));
@@ -454,20 +462,23 @@ struct RowLoader {
 };
 
 // The range that any of the rows (or keys) of a wave reaches, and the one that all
-// reach; rows that do not exist reach all.
+// reach; rows that do not exist reach all.  What a row reaches before `plain` is a case of its own: the
+// range of all begins behind it, and it ends at `apart` in the wave (0: none has any).
 struct Reach {
-  int lo, hi, all_lo, all_hi;
+  int lo, hi, all_lo, all_hi, apart;
 };
-__device__ __forceinline__ Reach reach_of(bool live, int lo, int hi) {
-  Reach r{lo < hi ? lo : 0x7fffffff, lo < hi ? hi : 0, live ? lo : 0, live ? hi : 0x7fffffff};
+__device__ __forceinline__ Reach reach_of(bool live, int lo, int plain, int hi) {
+  Reach r{lo < hi ? lo : 0x7fffffff, lo < hi ? hi : 0, live ? plain : 0, live ? hi : 0x7fffffff,
+          lo < plain ? plain : 0};
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
     r.lo = min(r.lo, __shfl_xor(r.lo, m));
     r.hi = max(r.hi, __shfl_xor(r.hi, m));
     r.all_lo = max(r.all_lo, __shfl_xor(r.all_lo, m));
     r.all_hi = min(r.all_hi, __shfl_xor(r.all_hi, m));
+    r.apart = max(r.apart, __shfl_xor(r.apart, m));
   }
-  return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi)};
+  return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi), uniform(r.apart)};
 }
 // The reach of WAVES waves, {0, 0} if none reaches anything; lds is free before and after.
 template <int WAVES>

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256 * KH, 2) void k_attn(Args a, int pairs, int til
   const Range mine = keys_of<true>(a, t);
 
   const bool some = mine.lo < mine.hi;
-  const Reach reach = reach_of(live, mine.lo, mine.hi);
+  const Reach reach = reach_of(live, mine.lo, mine.lo, mine.hi);
   const int lo = reach.lo, hi = reach.hi, all_lo = reach.all_lo, all_hi = reach.all_hi;
   const Range all = reach_of_all<4>(lds, reach, wave);   // both halves write the same
   int j0 = all.lo, j1 = all.hi;
@@ -453,9 +453,9 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   const int64_t key = (int64_t)job.tile * 128 + kg * 32 + (lane & 31);
   const bool live = key < a.Tk;
   const int j = live ? (int)key : a.Tk;
-  const Range seen = queries_of(a, j);
-  const int rlo = seen.lo * a.G, rhi = seen.hi * a.G;
-  const Reach reach = reach_of(live, rlo, rhi);
+  const Seers seen = queries_of(a, j);
+  const int rlo = seen.lo * a.G, rmore = seen.more * a.G, rhi = seen.hi * a.G;
+  const Reach reach = reach_of(live, rlo, rmore, rhi);
   Range all = reach_of_all<8>(lds.s0, reach, wave);
   if (PARTS) {
     const int per = ((all.hi - all.lo + 63) / 64 + parts - 1) / parts * 64;
@@ -520,6 +520,12 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
     }
     if (r0 < reach.all_lo || r0 + 32 > min(reach.all_hi, all.hi)) {
       const uint32_t first = (uint32_t)(r0 + 4 * half - rlo), n = (uint32_t)max(min(rhi, all.hi) - rlo, 0);
+      if (r0 < reach.apart) {   // of a row that sees one key, dp - delta is 0, where their sums leave a rounding
+        const uint32_t alone = (uint32_t)(rmore - rlo);
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (first + acc_row(v) < alone) dp[v] *= 0.0f;
+      }
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         if (first + acc_row(v) >= n) s[v] = dp[v] = 0.0f;
@@ -583,12 +589,12 @@ __device__ __forceinline__ void grad_keys(const Args& a, const GradLds<DP>& lds,
   for (uint64_t again = (odd_k | odd_v) & 0xffffffffu; again != 0; again &= again - 1) {
     const int from = __builtin_ctzll(again), jj = __shfl(j, from);
     const int lo = PARTS ? max(__shfl(rlo, from), all.lo) : __shfl(rlo, from);
-    const int hi = PARTS ? min(__shfl(rhi, from), all.hi) : __shfl(rhi, from);
+    const int hi = PARTS ? min(__shfl(rhi, from), all.hi) : __shfl(rhi, from), more = __shfl(rmore, from);
     const bool k_odd = odd_k >> from & 1, v_odd = odd_v >> from & 1;
     const NanRows nan = nan_rows(a, b, hk, lo, hi, v_odd);
     if ((nan.dk || !k_odd) && (nan.dv || !v_odd)) continue;
     RowSum xk, xv;
-    row_dkv(a, b, jj, hk, lo, hi, xk, xv);
+    row_dkv(a, b, jj, hk, lo, more, hi, xk, xv);
     if (PARTS) {
       float* row = to + 2 * (int64_t)(from - (lane & 31)) * a.D;
       xk.store(row, a.D);
@@ -615,7 +621,7 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   const bool live = r < rows;
   const int t = live ? (int)((uint32_t)r / (uint32_t)a.G) : a.Tq, h = hk * a.G + (live ? (int)r - t * a.G : 0);
   const Range mine = keys_of<true>(a, t);
-  const Reach reach = reach_of(live, mine.lo, mine.hi);
+  const Reach reach = reach_of(live, mine.lo, mine.lo, mine.hi);
   Range all = reach_of_all<8>(lds.s0, reach, wave);
   if (PARTS) {
     const int per = ((all.hi - all.lo + kKeys - 1) / kKeys + parts - 1) / parts * kKeys;
@@ -682,6 +688,12 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
     tile(j, lds.s0, lds.s1);
     if (j + kKeys < all.hi) tile(j + kKeys, lds.s1, lds.s0);
   }
+  // the dq of a row that sees one key is 0 (as in grad_keys), or NaN
+  const float f = mine.hi - mine.lo == 1 ? 0.0f : 1.0f;
+  if (__any(f == 0.0f)) {
+#pragma unroll
+    for (int db = 0; db < T::kBlocks; ++db) dq[db] *= f;
+  }
   // NaN throughout anyway: where a row's lse or delta is, and it sees a key
   const bool lost = mine.lo < mine.hi && (nl != nl || nd != nd);
   uint64_t again = __ballot(live && odd_of(dq) != 0.0f && !lost);
@@ -691,7 +703,8 @@ __device__ __forceinline__ void grad_queries(const Args& a, const GradLds<DP>& l
   for (again |= again >> 32, again &= 0xffffffffu; again != 0; again &= again - 1) {
     const int from = __builtin_ctzll(again), tt = __shfl(t, from), hh = __shfl(h, from);
     const int lo = __shfl(mine.lo, from), hi = __shfl(mine.hi, from);
-    const RowSum x = row_dq(a, b, tt, hh, PARTS ? max(lo, all.lo) : lo, PARTS ? min(hi, all.hi) : hi);
+    RowSum x = row_dq(a, b, tt, hh, PARTS ? max(lo, all.lo) : lo, PARTS ? min(hi, all.hi) : hi);
+    if (hi - lo == 1) x.x0 *= 0.0f, x.x1 *= 0.0f;
     if (PARTS)
       x.store(to + (int64_t)(from - (lane & 31)) * a.D, a.D);
     else

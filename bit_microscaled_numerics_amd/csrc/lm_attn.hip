@@ -5,11 +5,13 @@
 // forms the probabilities again from lse, twice: once with the sums of dk and dv in registers, once with
 // those of dq (7 products where 5 would do with dq added up by atomics in memory: those
 // would change their order from run to run, and 64 key tiles adding to 21 MB of dq for each
-// key head pass the L2).  Long products are bound by power: at 8192 tokens, 40 heads of 128 over 8
-// key heads, causal, the clock is at 1.7 - 1.9 GHz with the matrix cores busy for 53 - 55% (zeros
-// as data: 2.2 GHz and three quarters of the time); 680 - 740 us forward (0.93 - 1.0 PFLOP/s), 2100 - 2200
-// the gradient (1.1 PFLOP/s with what is formed again).  Heads of 64 are bound by the
-// exponentials and sums on the vector units, small calls by launches and the chain of a tile's steps.
+// key head pass the L2).  In long products a wave's exponentials run with no product of its own beside
+// them: at 8192 tokens, 40 heads of 128 over 8 key heads, causal, the matrix cores are busy for 53% of the forward
+// kernel and 59% of the gradient, the vector units for 47% and 35%, and waves wait to issue for 40% of
+// their time.  Power takes the rest: 1.7 - 1.9 GHz, where zeros as data run at 2.2 GHz in three quarters of the
+// time.  640 - 730 us forward (0.94 - 1.07 PFLOP/s), 2050 - 2350 the gradient (1.0 - 1.2 PFLOP/s with what is
+// formed again).  Heads of 64 have half the products to an exponential (36% and 58% busy forward, 43% and 40% in
+// the gradient); small calls are bound by launches and the chain of a tile's steps.
 #include <hip/hip_runtime.h>
 
 #include "lm_attn.h"
@@ -787,10 +789,14 @@ using namespace attn;
 
 namespace {
 
-// Keys of a sequence, on average.
+// Keys of a sequence, on average.  A tile of packed rows walks the keys of all sequences in it, which are as many
+// as the rows have queries where the queries are the keys' own tokens.  Few queries over long keys of their own
+// are taken for less work than they are: 32 sequences of one query over 512 keys each (32/8 heads of 128) are 8
+// workgroups of 256 tiles, 256 us; the same as a batch of sequences of one length takes 17.
 int64_t keys_in(const nvfp4_attn& a) { return a.cu_q == nullptr || a.batch < 2 ? a.Tk : a.Tk / a.batch; }
 
-// The n of at most `most` with the least chain / n + 8 + 1.3 n part (us).
+// The n of at most `most` with the least chain / n + 8 + 1.3 n part (us).  Parts are whole tiles: of 65 tiles in 32
+// parts, 22 have three and the others none.
 int least_parts(double chain, double part, int64_t most) {
   int best = 1;
   double least = chain;
@@ -881,9 +887,10 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
   const int tiles = (int)(((int64_t)a.Tq * a.G + kRowsWG - 1) / kRowsWG);
   Part part{nullptr, nullptr, parts_of(c.a)};
   const int64_t n = (int64_t)pairs * tiles;
-  // Eight waves a workgroup where there is at most one for each compute unit and its keys
-  // are many tiles (188 of 24 tiles of width 64: 30 -> 26 us; 128 of 32 of width 128: 47 -> 41; 96
-  // of 5: 17 -> 18; 512 of 64: 45 -> 57).
+  // Eight waves a workgroup where there is at most one for each compute unit and its keys are many
+  // tiles (calls, one set of four waves and two: 188 workgroups of 24 tiles of width 64, 23.5 and 19.8 us; 128 of 32
+  // of width 128, 38.5 and 34.0; 96 of 5, 11.6 and 11.5).  Up to two for each compute unit would gain as well (512
+  // of 64 tiles of width 64: 16/16 heads 80 and 54, 16/4 80 and 70; of width 128 111 and 84), four no more.
   const bool halves = part.n == 1 && n <= num_cus() && keys_in(c.a) >= 8 * kKeys;
   if (part.n > 1) {
     part.o = static_cast<float*>(c.ws);

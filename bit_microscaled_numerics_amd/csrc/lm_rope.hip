@@ -2,12 +2,15 @@
 // the same pass, and the gradient (internal to libnvfp4.so).
 //
 // A row of D values is taken as D/2 pairs: the rot/2 rotated ones, then the rest of the
-// row as the pairs of its halves, which are not rotated.  A lane owns 4 pairs; 1 .. 64
-// lanes make a row, so that a rotation needs no exchange and a norm a few shuffles.
+// row as the pairs of its halves, which are not rotated.  A lane owns 8 pairs, in the
+// gradient 4; 1 .. 64 lanes make a row, so that a rotation needs no exchange and a norm a few shuffles.
 // A wave takes all heads of a token (several tokens, where they are few): the
 // sines and cosines of a lane's pairs are formed once for all of them.
 //
-// Bound by HBM: 4 bytes per value (BF16), 6 in the gradient.
+// Bound by HBM: 4 bytes per value (BF16), 6 in the gradient; there the vector units are as busy (71%) as in the
+// forward kernel, and two dependent sums a row leave the waves waiting for 56% of their time (forward 48%): 4.5
+// TB/s of 5.9, where the forward kernel has 5.5.  Widths whose pairs are no multiple of 8 (4 in the gradient)
+// load value by value: 8192 tokens of 48 heads of 72, 53 us where the bytes take 19.
 #include <hip/hip_runtime.h>
 
 #include "lm_attn_kernels.h"
@@ -118,8 +121,8 @@ __device__ __forceinline__ void place(const Args& k, int s, int& a, int& b) {
   }
 }
 
-// A lane's pairs: 4 consecutive ones (VEC: all rotated or none, 8-byte pieces of a BF16
-// row), or 4 that lie a row's lanes apart.
+// A lane's N pairs: consecutive ones (VEC: all rotated or none, pieces of 2 N bytes of a BF16
+// row), or such that lie a row's lanes apart.
 template <bool IL, bool VEC, int N>
 struct Lane {
   const Args& k;
@@ -456,8 +459,8 @@ __global__ __launch_bounds__(1024) void k_rope_dw(const float* partials, int row
     store1(static_cast<bf16_t*>(to) + col, (float)sum);
 }
 
-// Pairs of a lane.  Forward 8, 16-byte loads of BF16 (38 us for 8192 tokens of 48 heads of 128, 43 with 4); the
-// gradient, which holds three times the registers, 4 (8 need 166: 110 us instead of 94).
+// Pairs of a lane.  Forward 8, 16-byte loads of BF16 (kernel of 8192 tokens of 48 heads of 128: 36.7 us, 38.0 with
+// 4); the gradient, which holds three times the registers, 4 (67.2 us, 78.4 with 8).
 constexpr int kForward = 8, kGradient = 4;
 
 // Lanes of a row; heads of a token side by side in a wave, and tokens side by side.

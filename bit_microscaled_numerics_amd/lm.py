@@ -408,7 +408,8 @@ class SelfAttention(torch.nn.Module):
     def forward(self, qkv: torch.Tensor, positions: Optional[torch.Tensor] = None,
                 cu: Optional[torch.Tensor] = None) -> torch.Tensor:
         """qkv [sequences, tokens, ..] or [tokens, ..]; cu (int32 or int64, on the GPU): where
-        the sequences of one row of tokens begin, and the end.  positions: of the tokens,
+        the sequences of one row of tokens begin, and the end; tokens before and behind may hold anything,
+        their rows and gradients are zeros.  positions: of the tokens,
         broadcast to qkv's leading dimensions (None: counted from each sequence's start)."""
         heads, kv_heads, dim = self.how[:3]
         if qkv.shape[-1] != (heads + 2 * kv_heads) * dim or qkv.dim() not in (2, 3):

@@ -8,8 +8,8 @@
 // key head pass the L2).  In long products a wave's exponentials run with no product of its own beside
 // them: at 8192 tokens, 40 heads of 128 over 8 key heads, causal, the matrix cores are busy for 53% of the forward
 // kernel and 59% of the gradient, the vector units for 47% and 35%, and waves wait to issue for 40% of
-// their time.  Power takes the rest: 1.7 - 1.9 GHz, where zeros as data run at 2.2 GHz in three quarters of the
-// time.  640 - 730 us forward (0.94 - 1.07 PFLOP/s), 2050 - 2350 the gradient (1.0 - 1.2 PFLOP/s with what is
+// their time.  Power costs about a quarter besides: the clock is at 1.7 - 1.9 GHz, with zeros as data at 2.2.
+// 640 - 730 us forward (0.94 - 1.07 PFLOP/s), 2050 - 2350 the gradient (1.0 - 1.2 PFLOP/s with what is
 // formed again).  Heads of 64 have half the products to an exponential (36% and 58% busy forward, 43% and 40% in
 // the gradient); small calls are bound by launches and the chain of a tile's steps.
 #include <hip/hip_runtime.h>
@@ -789,9 +789,9 @@ using namespace attn;
 
 namespace {
 
-// Keys of a sequence, on average.  A tile of packed rows walks the keys of all sequences in it, which are as many
-// as the rows have queries where the queries are the keys' own tokens.  Few queries over long keys of their own
-// are taken for less work than they are: 32 sequences of one query over 512 keys each (32/8 heads of 128) are 8
+// Keys of a sequence, on average.  A tile of packed rows walks the keys of all sequences in it: about as many as it
+// has queries, or one sequence's, where queries and keys are the same tokens.  Few queries over long keys of
+// their own are taken for less work than they are: 32 sequences of one query over 512 keys each (32/8 heads of 128) are 8
 // workgroups of 256 tiles, 256 us; the same as a batch of sequences of one length takes 17.
 int64_t keys_in(const nvfp4_attn& a) { return a.cu_q == nullptr || a.batch < 2 ? a.Tk : a.Tk / a.batch; }
 
@@ -890,7 +890,7 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t s) {
   // Eight waves a workgroup where there is at most one for each compute unit and its keys are many
   // tiles (calls, one set of four waves and two: 188 workgroups of 24 tiles of width 64, 23.5 and 19.8 us; 128 of 32
   // of width 128, 38.5 and 34.0; 96 of 5, 11.6 and 11.5).  Up to two for each compute unit would gain as well (512
-  // of 64 tiles of width 64: 16/16 heads 80 and 54, 16/4 80 and 70; of width 128 111 and 84), four no more.
+  // of 64 tiles of width 64: 16/16 heads 80 and 54, 16/4 80 and 70; of width 128 111 and 84); at four it makes no difference.
   const bool halves = part.n == 1 && n <= num_cus() && keys_in(c.a) >= 8 * kKeys;
   if (part.n > 1) {
     part.o = static_cast<float*>(c.ws);
